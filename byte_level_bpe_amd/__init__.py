@@ -48,7 +48,10 @@ EXPORTS = ["bbpe_load_ranks", "bbpe_load_ranks_tiktoken_file", "bbpe_upload_tabl
            "bbpe_stream_decoder_reset", "bbpe_stream_decode_device", "bbpe_word_cache_clear",
            "bbpe_word_cache_info", "bbpe_error_detail",
            "bbpe_table_info", "bbpe_set_timing", "bbpe_timing_report", "bbpe_timing_reset",
-           "bbpe_free", "bbpe_status_str"]
+           "bbpe_free", "bbpe_status_str",
+           "bbpe_block_tables_workspace_bytes", "bbpe_block_tables", "bbpe_qk_norm_rope",
+           "bbpe_qk_norm_rope_backward_workspace_bytes", "bbpe_qk_norm_rope_backward",
+           "bbpe_tree_attention_workspace_bytes", "bbpe_tree_attention"]
 
 _lib = None
 
@@ -597,3 +600,18 @@ def encode_segments(tok: Tokenizer, segments, tiktoken_safe: bool = True, device
 
 def decode(tok: Tokenizer, ids) -> bytes:
     return tok.decode(ids)
+
+
+# The operators on what an encode call leaves on the device live in serving.py,
+# which needs torch at import; they load with their first use.
+_SERVING = ("BlockTables", "PagedCache", "block_tables", "qk_norm_rope", "qk_norm_rope_backward",
+            "tree_attention", "tree_attention_workspace_bytes")
+
+
+def __getattr__(name):
+    if name in _SERVING:
+        from . import serving
+        for n in _SERVING:
+            globals()[n] = getattr(serving, n)
+        return globals()[name]
+    raise AttributeError("module %r has no attribute %r" % (__name__, name))

@@ -1,0 +1,675 @@
+// Attention of new tokens (a tree of drafts, a chain, one token) over a paged
+// key/value cache.
+//
+//   o_i = sum_j p_ij v_j / sum_j p_ij,  p_ij = exp2(s_ij - m_i),
+//   s_ij = scale * log2(e) * q_i . k_j  over the keys j that row i sees.
+//
+// Rows.  The query heads that share a key/value head are rows of one product:
+// a row tile holds M rows, a power of two of tokens times the group's heads.
+//
+// Split.  A unit is one row tile times KT keys.  For every key/value head the
+// units of all requests, row tile after row tile, are laid in one line and cut
+// into equal runs, one a workgroup: long and short requests, few and many rows
+// keep the card equally busy, and no length has to be known on the host.  A
+// row tile cut by a run's end leaves its parts (sums relative to their own
+// maximum) in the workspace, and k_attn_join adds them in order: which parts
+// there are depends on the lengths alone.
+//
+// Product.  Transposed, so that nothing moves between lanes: S^T = K Q^T has a
+// row's scores in one column of lanes (4 lanes, 8 keys each, of every 32),
+// which is just how the second product, O^T = V^T P^T, reads P.  K's fragment
+// is 16 bytes of one key a lane.  V's needs eight keys of one element: a lane
+// loads D/16 elements of eight keys and turns that block over in registers
+// (one byte permute for two elements).  Keys and values go from HBM to
+// registers without a stop in LDS; the running maximum is one per lane and
+// wave, and the waves join at the end of a run.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+
+#include "../../include/bbpe.h"
+#include "bbpe_device.h"
+#include "bbpe_float.h"
+
+namespace bbpe {
+namespace {
+
+constexpr uint32_t AT_BLOCK = 256, AT_WAVES = 4;
+constexpr uint32_t AT_REQ = 2048;    // requests of one launch (their units' sums lie in LDS)
+constexpr uint32_t AT_TILE = 32;     // keys a wave takes at once
+constexpr uint32_t AT_KT_LOG = 7;    // log2 of a unit's keys (AT_WAVES tiles)
+constexpr uint32_t AT_RUNS = 512;    // workgroups of a launch, over all heads
+
+struct AttnArgs {
+  const void *q;
+  int64_t q_ts, q_hs;
+  const char *kc, *vc;
+  int64_t page_stride, head_stride, token_stride;
+  uint64_t n_pages;
+  uint32_t page_shift;
+  const int32_t *table;
+  uint64_t table_stride;
+  uint32_t cap;            // keys that a table row can hold
+  const int64_t *q_off;
+  const int32_t *ctx;
+  uint32_t n_req;
+  const uint64_t *mask;    // null: a chain
+  uint32_t words;
+  float scale2;            // scale * log2(e)
+  void *out;
+  int64_t out_ts, out_hs;
+  float *lse;
+  uint64_t n_tok;
+  uint32_t hq, hk, grp;
+  uint32_t tok_log;        // log2 of a row tile's tokens
+  uint32_t runs;           // workgroups of one head
+  uint32_t q_vec, out_vec; // rows 16-byte aligned
+  uint32_t *meta;          // [hk][runs][4]: the row tile that begins in a run and ends in a later one
+  float *part;             // [hk][runs][2][M][D + 2]: its parts
+};
+
+// One request's lengths, as the kernels use them.
+struct Lengths {
+  int64_t first;  // its first token
+  uint32_t n;     // new tokens
+  uint32_t ctx;   // context; past the table's row: the row's keys
+  uint32_t klen;  // keys in all, within the table's row
+};
+__device__ __forceinline__ Lengths lengths_of(const AttnArgs &a, uint32_t r) {
+  Lengths L;
+  const int64_t lo = a.q_off[r], hi = a.q_off[r + 1];
+  const bool ok = lo >= 0 && hi >= lo && uint64_t(hi) <= a.n_tok;
+  L.first = lo;
+  L.n = ok ? uint32_t(hi - lo) : 0;
+  const int32_t c = max(a.ctx[r], 0);
+  L.ctx = uint32_t(c);
+  L.klen = uint32_t(min(int64_t(c) + L.n, int64_t(a.cap)));
+  return L;
+}
+
+// sum over j = 1..n of ceil(j / 2^q)
+__device__ __forceinline__ uint64_t ceil_sum(uint64_t n, uint32_t q) {
+  const uint64_t a = n >> q, b = n & ((uint64_t(1) << q) - 1);
+  return ((a * (a + 1) / 2) << q) + b * (a + 1);
+}
+
+// Units of a request's first t row tiles.  Masks: every row tile spans all
+// keys.  A chain: tile i ends at key ctx + (i + 1) * tokens, tokens = 2^tok_log.
+template <uint32_t KT_LOG>
+__device__ __forceinline__ uint64_t units_before(const AttnArgs &a, const Lengths &L, uint32_t t) {
+  constexpr uint32_t KT = 1u << KT_LOG;
+  if (a.mask) return uint64_t(t) * ((L.klen + KT - 1) >> KT_LOG);
+  const uint32_t base = min(L.ctx, a.cap), whole = base >> KT_LOG, rest = base & (KT - 1);
+  if (a.tok_log <= KT_LOG) {
+    const uint32_t s = (rest + (1u << a.tok_log) - 1) >> a.tok_log, q = KT_LOG - a.tok_log;
+    return uint64_t(t) * whole + ceil_sum(s + t, q) - ceil_sum(s, q);
+  }
+  const uint64_t steps = uint64_t(t) * (t + 1) / 2;
+  return uint64_t(t) * (whole + (rest ? 1 : 0)) + (steps << (a.tok_log - KT_LOG));
+}
+__device__ __forceinline__ uint32_t row_tiles(const AttnArgs &a, uint32_t n) {
+  return uint32_t((uint64_t(n) + (1u << a.tok_log) - 1) >> a.tok_log);
+}
+
+// Sums of the requests' units up to and with each, into LDS; returns the total.
+template <uint32_t KT_LOG>
+__device__ __forceinline__ uint64_t scan_units(const AttnArgs &a, uint64_t *incl, uint64_t *sh) {
+  constexpr uint32_t PER = AT_REQ / AT_BLOCK;
+  const uint32_t k = (a.n_req + AT_BLOCK - 1) / AT_BLOCK, r0 = threadIdx.x * k;
+  uint64_t u[PER], mine = 0;
+#pragma unroll
+  for (uint32_t j = 0; j < PER; ++j) {
+    u[j] = 0;
+    if (j < k && r0 + j < a.n_req) {
+      const Lengths L = lengths_of(a, r0 + j);
+      u[j] = units_before<KT_LOG>(a, L, row_tiles(a, L.n));
+    }
+    mine += u[j];
+  }
+  uint64_t total;
+  uint64_t at = block_incl_scan<AT_BLOCK, uint64_t>(mine, 0, [](uint64_t x, uint64_t y) { return x + y; }, sh, total) - mine;
+#pragma unroll
+  for (uint32_t j = 0; j < PER; ++j) {
+    at += u[j];
+    if (j < k && r0 + j < a.n_req) incl[r0 + j] = at;
+  }
+  __syncthreads();
+  return total;
+}
+
+template <typename T> struct Mma;
+template <> struct Mma<__bf16> {
+  static __device__ __forceinline__ f32x4 mul(bf16x8 x, bf16x8 y, f32x4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(x, y, c, 0, 0, 0);
+  }
+  static constexpr uint32_t EXP = 0x7F80;  // exponent of infinities and NaN
+  static constexpr uint32_t ONE = 0x3F80;
+};
+template <> struct Mma<_Float16> {
+  static __device__ __forceinline__ f32x4 mul(f16x8 x, f16x8 y, f32x4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(x, y, c, 0, 0, 0);
+  }
+  static constexpr uint32_t EXP = 0x7C00;
+  static constexpr uint32_t ONE = 0x3C00;
+};
+
+__device__ __forceinline__ float sum8(f32x8 a) {
+  return ((a[0] + a[1]) + (a[2] + a[3])) + ((a[4] + a[5]) + (a[6] + a[7]));
+}
+
+// The larger of the four lanes 16 apart, in all four.
+__device__ __forceinline__ float max_quarters(float x) {
+  x = fmaxf(x, __shfl_xor(x, 16, 64));
+  return fmaxf(x, __shfl_xor(x, 32, 64));
+}
+__device__ __forceinline__ float sum_quarters(float x) {
+  x += __shfl_xor(x, 16, 64);
+  return x + __shfl_xor(x, 32, 64);
+}
+
+// The low min(n, 8) bits (none for n <= 0).
+__device__ __forceinline__ uint32_t low_bits(int64_t n) {
+  return n <= 0 ? 0u : n >= 8 ? 0xFFu : (1u << uint32_t(n)) - 1u;
+}
+
+// Which of the eight keys from kb a row sees: below klim, and of the new ones
+// (from ctx on) those of its mask, or up to itself.
+__device__ __forceinline__ uint32_t seen8(const AttnArgs &a, const Lengths &L, uint32_t klim, uint32_t kb, uint32_t token) {
+  const uint32_t within = low_bits(int64_t(klim) - kb);
+  if (!a.mask) return within & low_bits(int64_t(L.ctx) + token + 1 - kb);
+  const uint32_t old = low_bits(int64_t(L.ctx) - kb);
+  if (old == 0xFFu) return within;
+  const int64_t j0 = int64_t(kb) - L.ctx;
+  const uint64_t *row = a.mask + (uint64_t(L.first) + token) * a.words;
+  uint64_t w = 0;
+  if (j0 < 0) {
+    w = a.words ? row[0] << uint32_t(-j0) : 0;
+  } else {
+    const uint32_t at = uint32_t(j0 >> 6), sh = uint32_t(j0 & 63);
+    if (at < a.words) w = row[at] >> sh;
+    if (sh > 56 && at + 1 < a.words) w |= row[at + 1] << (64 - sh);
+  }
+  return within & (old | (uint32_t(w) & 0xFFu & ~old));
+}
+
+// N elements of one output row from d on, from the sums o relative to the
+// maximum `top` and the softmax sum.  A row that saw nothing: zeros, -inf.
+template <typename T, uint32_t N>
+__device__ __forceinline__ void finish(const AttnArgs &a, int64_t token, uint32_t h, uint32_t d, const float *o, float top,
+                                       float sum, bool with_lse) {
+  const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+  T *p = static_cast<T *>(a.out) + token * a.out_ts + int64_t(h) * a.out_hs + d;
+  typedef T TN __attribute__((ext_vector_type(N)));
+  TN x;
+#pragma unroll
+  for (uint32_t j = 0; j < N; ++j) x[j] = T(sum == 0.0f ? 0.0f : o[j] * inv);
+  if (a.out_vec) {
+    *reinterpret_cast<TN *>(p) = x;
+  } else {
+#pragma unroll
+    for (uint32_t j = 0; j < N; ++j) p[j] = x[j];
+  }
+  if (with_lse && a.lse)
+    a.lse[token * a.hq + h] = sum == 0.0f ? -INFINITY : (top + __builtin_amdgcn_logf(sum)) * 0.69314718055994530942f;
+}
+
+template <typename T, uint32_t D, uint32_t MT>
+__global__ __launch_bounds__(AT_BLOCK, (D * MT <= 128 ? 3 : D * MT <= 256 ? 2 : 1)) void k_attn_rows(AttnArgs a) {
+  typedef typename Vec8<T>::type T8;
+  constexpr uint32_t NS = D / 32;          // steps of the first product
+  constexpr uint32_t VD = D / 16;          // a lane's elements of one value row
+  constexpr uint32_t M = 16 * MT;
+  constexpr uint32_t JC = VD < 8 ? VD : 8; // elements joined at once
+  constexpr uint32_t PAD = 16 * JC + 4;
+  __shared__ uint64_t s_incl[AT_REQ];
+  __shared__ uint64_t s_scan[2 * AT_BLOCK / 64 + 1];
+  __shared__ float s_o[AT_WAVES][16][PAD];
+  __shared__ float s_m[AT_WAVES][M], s_l[AT_WAVES][M];
+
+  const uint32_t head = blockIdx.x, run = blockIdx.y;
+  const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6, n16 = lane & 15, g = lane >> 4;
+  const uint64_t total = scan_units<AT_KT_LOG>(a, s_incl, s_scan);
+  const uint64_t per = (total + a.runs - 1) / a.runs;
+  const uint64_t u_end = min(total, (uint64_t(run) + 1) * per);
+  uint64_t u = uint64_t(run) * per;
+  uint32_t *meta = a.meta + (uint64_t(head) * a.runs + run) * 4;
+  bool left_open = false;  // a row tile begins here and ends in a later run
+
+  const char *kc = a.kc + int64_t(head) * a.head_stride * int64_t(sizeof(T));
+  const char *vc = a.vc + int64_t(head) * a.head_stride * int64_t(sizeof(T));
+
+  while (u < u_end) {
+    // request, row tile and first unit of the run's next segment
+    uint32_t lo = 0, hi = a.n_req - 1;
+    while (lo < hi) {
+      const uint32_t mid = (lo + hi) / 2;
+      if (s_incl[mid] > u) hi = mid;
+      else lo = mid + 1;
+    }
+    const uint32_t r = __builtin_amdgcn_readfirstlane(lo);
+    const Lengths L = lengths_of(a, r);
+    const uint64_t local = u - (r ? s_incl[r - 1] : 0);
+    uint32_t t = 0, t_hi = row_tiles(a, L.n) - 1;
+    while (t < t_hi) {  // the last tile that begins at or before `local`
+      const uint32_t mid = (t + t_hi + 1) / 2;
+      if (units_before<AT_KT_LOG>(a, L, mid) <= local) t = mid;
+      else t_hi = mid - 1;
+    }
+    const uint64_t tile_u = units_before<AT_KT_LOG>(a, L, t);
+    const uint32_t n_units = uint32_t(units_before<AT_KT_LOG>(a, L, t + 1) - tile_u);
+    const uint32_t first = uint32_t(local - tile_u);
+    const uint32_t count = uint32_t(min(uint64_t(n_units - first), u_end - u));
+    const uint32_t token0 = t << a.tok_log;
+    // keys that any row of the tile sees, and those that all of them see
+    const uint32_t klim = a.mask ? L.klen : uint32_t(min(uint64_t(L.klen), uint64_t(L.ctx) + token0 + (1u << a.tok_log)));
+    const uint32_t open = min(L.ctx, klim);
+    const int32_t *pages = a.table + uint64_t(r) * a.table_stride;
+
+    // queries: row 16 * i + n16 of the tile
+    T8 q[MT][NS];
+    uint32_t token[MT];
+#pragma unroll
+    for (uint32_t i = 0; i < MT; ++i) {
+      const uint32_t row = 16 * i + n16, tl = row / a.grp;
+      token[i] = token0 + tl;
+      const bool live = tl < (1u << a.tok_log) && token[i] < L.n;
+      token[i] = min(token[i], L.n - 1);
+      const T *p = static_cast<const T *>(a.q) + (L.first + token[i]) * a.q_ts + int64_t(head * a.grp + row % a.grp) * a.q_hs;
+#pragma unroll
+      for (uint32_t s = 0; s < NS; ++s) {
+        q[i][s] = T8{};
+        if (live) q[i][s] = load8_raw(p + s * 32 + g * 8, a.q_vec);
+      }
+    }
+    f32x4 acc[MT][VD];
+    float m[MT], l[MT];
+#pragma unroll
+    for (uint32_t i = 0; i < MT; ++i) {
+      m[i] = -INFINITY;
+      l[i] = 0.0f;
+#pragma unroll
+      for (uint32_t j = 0; j < VD; ++j) acc[i][j] = f32x4{};
+    }
+
+    for (uint32_t unit = first; unit < first + count; ++unit) {
+      const uint32_t key0 = (unit << AT_KT_LOG) + wave * AT_TILE;
+      if (key0 >= klim) break;
+      // the pages of this lane's eight values (keys kb..) and of its two keys (8 * (n16 / 4) + n16 % 4, and + 4)
+      const uint32_t kb = key0 + 8 * g, kk = key0 + 8 * (n16 >> 2);
+      const int32_t pv = pages[min(kb, klim - 1) >> a.page_shift];
+      const int32_t pk = pages[min(kk, klim - 1) >> a.page_shift];
+      const uint32_t in_page = (1u << a.page_shift) - 1;
+      const bool v_ok = uint32_t(pv) < a.n_pages, k_ok = uint32_t(pk) < a.n_pages;
+      const char *kp = kc + (int64_t(k_ok ? pk : 0) * a.page_stride + int64_t((kk & in_page) + (n16 & 3)) * a.token_stride) * int64_t(sizeof(T)) + g * 16;
+      const char *vp = vc + (int64_t(v_ok ? pv : 0) * a.page_stride + int64_t(kb & in_page) * a.token_stride) * int64_t(sizeof(T)) + n16 * (VD * sizeof(T));
+      T8 ka[NS], kb8[NS];
+#pragma unroll
+      for (uint32_t s = 0; s < NS; ++s) {
+        ka[s] = *reinterpret_cast<const T8 *>(kp + s * 64);
+        kb8[s] = *reinterpret_cast<const T8 *>(kp + 4 * a.token_stride * int64_t(sizeof(T)) + s * 64);
+      }
+      uint32_t v[8][VD / 2];
+#pragma unroll
+      for (uint32_t e = 0; e < 8; ++e) {
+        const char *p = vp + int64_t(e) * a.token_stride * int64_t(sizeof(T));
+        if constexpr (VD == 4) {
+          const uint2 x = *reinterpret_cast<const uint2 *>(p);
+          v[e][0] = x.x;
+          v[e][1] = x.y;
+        } else {
+#pragma unroll
+          for (uint32_t c = 0; c < VD / 8; ++c) {
+            const u32x4 x = *reinterpret_cast<const u32x4 *>(p + 16 * c);
+#pragma unroll
+            for (uint32_t w = 0; w < 4; ++w) v[e][4 * c + w] = x[w];
+          }
+        }
+      }
+      // tiles in which some row does not see some key
+      const bool part = key0 + AT_TILE > open || __any(!v_ok);
+      bool odd = false;  // masked places with infinities or NaN among the values
+      if (part) {
+        uint32_t bad = 0;
+#pragma unroll
+        for (uint32_t e = 0; e < 8; ++e)
+#pragma unroll
+          for (uint32_t w = 0; w < VD / 2; ++w) {
+            const uint32_t x = v[e][w];
+            bad |= uint32_t((x & Mma<T>::EXP) == Mma<T>::EXP) | uint32_t((x >> 16 & Mma<T>::EXP) == Mma<T>::EXP);
+          }
+        odd = __any(bad != 0);
+      }
+      T8 pf[MT];
+      uint32_t seen[MT];
+#pragma unroll
+      for (uint32_t i = 0; i < MT; ++i) {
+        f32x4 sa{}, sb{};
+#pragma unroll
+        for (uint32_t s = 0; s < NS; ++s) {
+          sa = Mma<T>::mul(ka[s], q[i][s], sa);
+          sb = Mma<T>::mul(kb8[s], q[i][s], sb);
+        }
+        float x[8];
+#pragma unroll
+        for (uint32_t e = 0; e < 4; ++e) {
+          x[e] = sa[e] * a.scale2;
+          x[4 + e] = sb[e] * a.scale2;
+        }
+        seen[i] = 0xFF;
+        if (part) {
+          seen[i] = v_ok ? seen8(a, L, klim, kb, token[i]) : 0;
+#pragma unroll
+          for (uint32_t e = 0; e < 8; ++e) x[e] = (seen[i] >> e & 1) ? x[e] : -INFINITY;
+        }
+        float top = x[0];
+#pragma unroll
+        for (uint32_t e = 1; e < 8; ++e) top = fmaxf(top, x[e]);
+        top = max_quarters(top);
+        if (__any(top > m[i])) {
+          const float m_new = fmaxf(m[i], top);
+          const float f = m_new == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(m[i] - m_new);
+          m[i] = m_new;
+          l[i] *= f;
+#pragma unroll
+          for (uint32_t j = 0; j < VD; ++j) acc[i][j] *= f;
+        }
+        const float base = m[i] == -INFINITY ? 0.0f : m[i];
+        f32x8 p;
+#pragma unroll
+        for (uint32_t e = 0; e < 8; ++e) p[e] = __builtin_amdgcn_exp2f(x[e] - base);
+        l[i] += sum8(p);
+        // rounded once to the cache's type: the matrix product's operand
+        pf[i] = from_float<T>(p);
+      }
+      // values turned over, two elements of eight keys at a time
+#pragma unroll
+      for (uint32_t w = 0; w < VD / 2; ++w) {
+        u32x4 f0, f1;
+#pragma unroll
+        for (uint32_t e = 0; e < 4; ++e) {
+          f0[e] = __builtin_amdgcn_perm(v[2 * e + 1][w], v[2 * e][w], 0x05040100);
+          f1[e] = __builtin_amdgcn_perm(v[2 * e + 1][w], v[2 * e][w], 0x07060302);
+        }
+#pragma unroll
+        for (uint32_t half = 0; half < 2; ++half) {
+          u32x4 f = half ? f1 : f0;
+          if (odd) {
+            // 0 * inf is NaN: such values leave the product, and come back as
+            // what they add to the rows that see them
+            u32x4 up{}, down{};
+#pragma unroll
+            for (uint32_t e = 0; e < 4; ++e)
+#pragma unroll
+              for (uint32_t h = 0; h < 32; h += 16) {
+                const uint32_t b = f[e] >> h & 0xFFFF, body = b & 0x7FFF;
+                if (body >= Mma<T>::EXP) {
+                  const bool nan = body > Mma<T>::EXP;
+                  if (nan || !(b & 0x8000)) up[e] |= Mma<T>::ONE << h;
+                  if (nan || (b & 0x8000)) down[e] |= Mma<T>::ONE << h;
+                  f[e] &= ~(0xFFFFu << h);
+                }
+              }
+#pragma unroll
+            for (uint32_t i = 0; i < MT; ++i) {
+              u32x4 vis;
+#pragma unroll
+              for (uint32_t e = 0; e < 4; ++e)
+                vis[e] = ((seen[i] >> (2 * e) & 1) ? Mma<T>::ONE : 0) | ((seen[i] >> (2 * e + 1) & 1) ? Mma<T>::ONE << 16 : 0);
+              const f32x4 plus = Mma<T>::mul(__builtin_bit_cast(T8, up), __builtin_bit_cast(T8, vis), f32x4{});
+              const f32x4 minus = Mma<T>::mul(__builtin_bit_cast(T8, down), __builtin_bit_cast(T8, vis), f32x4{});
+#pragma unroll
+              for (uint32_t e = 0; e < 4; ++e) {
+                if (plus[e] > 0.0f) acc[i][2 * w + half][e] += INFINITY;
+                if (minus[e] > 0.0f) acc[i][2 * w + half][e] -= INFINITY;
+              }
+            }
+          }
+#pragma unroll
+          for (uint32_t i = 0; i < MT; ++i)
+            acc[i][2 * w + half] = Mma<T>::mul(__builtin_bit_cast(T8, f), pf[i], acc[i][2 * w + half]);
+        }
+      }
+    }
+
+    // the waves' sums join: [wave][row][element]
+    const bool whole = first == 0 && count == n_units;
+    float *part = a.part + ((uint64_t(head) * a.runs + run) * 2 + (first == 0 ? 1 : 0)) * (M * (D + 2));
+#pragma unroll
+    for (uint32_t i = 0; i < MT; ++i) {
+      l[i] = sum_quarters(l[i]);
+      if (g == 0) {
+        s_m[wave][16 * i + n16] = m[i];
+        s_l[wave][16 * i + n16] = l[i];
+      }
+    }
+    const uint32_t jr = threadIdx.x >> 4, jd = threadIdx.x & 15;  // a thread's row and run of elements in the join
+#pragma unroll
+    for (uint32_t i = 0; i < MT; ++i) {
+#pragma unroll
+      for (uint32_t j0 = 0; j0 < VD; j0 += JC) {
+        __syncthreads();
+#pragma unroll
+        for (uint32_t e = 0; e < 4; ++e)
+#pragma unroll
+          for (uint32_t j = 0; j < JC; ++j) s_o[wave][n16][(4 * g + e) * JC + j] = acc[i][j0 + j][e];
+        __syncthreads();
+        const uint32_t row = 16 * i + jr;
+        float top = s_m[0][row];
+#pragma unroll
+        for (uint32_t w = 1; w < AT_WAVES; ++w) top = fmaxf(top, s_m[w][row]);
+        const float base = top == -INFINITY ? 0.0f : top;
+        float sum = 0.0f, o[JC];
+#pragma unroll
+        for (uint32_t j = 0; j < JC; ++j) o[j] = 0.0f;
+#pragma unroll
+        for (uint32_t w = 0; w < AT_WAVES; ++w) {
+          const float f = __builtin_amdgcn_exp2f(s_m[w][row] - base);
+          sum += s_l[w][row] * f;
+#pragma unroll
+          for (uint32_t j = 0; j < JC; ++j) o[j] += s_o[w][jr][jd * JC + j] * f;
+        }
+        const uint32_t tl = row / a.grp, tok = token0 + tl, d = jd * VD + j0;
+        if (tl >= (1u << a.tok_log) || tok >= L.n) continue;
+        if (whole) {
+          const uint32_t h = head * a.grp + row % a.grp;
+          finish<T, JC>(a, L.first + tok, h, d, o, top, sum, d == 0);
+        } else {
+#pragma unroll
+          for (uint32_t j = 0; j < JC; ++j) part[row * D + d + j] = o[j];
+          if (d == 0) {
+            part[M * D + row] = top;
+            part[M * D + M + row] = sum;
+          }
+        }
+      }
+    }
+    __syncthreads();  // s_m, s_l and s_o are free again
+    if (first == 0 && !whole) {
+      left_open = true;
+      if (threadIdx.x == 0) {
+        meta[0] = uint32_t((u + n_units - 1) / per) - run + 1;  // parts
+        meta[1] = r;
+        meta[2] = token0;
+      }
+    }
+    u += count;
+  }
+  if (!left_open && threadIdx.x == 0) meta[0] = 0;
+}
+
+// Adds up the parts of the row tiles that were cut: a wave for each row of the
+// tile that begins in run blockIdx.y, a lane for every 64th of the row.
+template <typename T, uint32_t D, uint32_t M>
+__global__ __launch_bounds__(AT_BLOCK) void k_attn_join(AttnArgs a) {
+  constexpr uint32_t N = D / 64;
+  const uint32_t head = blockIdx.x, run = blockIdx.y, lane = threadIdx.x & 63;
+  const uint32_t row = blockIdx.z * AT_WAVES + (threadIdx.x >> 6);
+  const uint32_t *meta = a.meta + (uint64_t(head) * a.runs + run) * 4;
+  const uint32_t n = meta[0];
+  if (n == 0) return;
+  const Lengths L = lengths_of(a, meta[1]);
+  const uint32_t tl = row / a.grp, tok = meta[2] + tl;
+  if (tl >= (1u << a.tok_log) || tok >= L.n) return;
+  // the first part is this run's second place, the others the first places of the runs after it
+  constexpr uint64_t SIZE = M * (D + 2);
+  const float *base = a.part + (uint64_t(head) * a.runs + run) * 2 * SIZE;
+  const auto at = [&](uint32_t p) { return base + (p == 0 ? SIZE : uint64_t(p) * 2 * SIZE); };
+  float top = -INFINITY;
+  for (uint32_t p = lane; p < n; p += 64) top = fmaxf(top, at(p)[M * D + row]);
+  for (int d = 32; d; d >>= 1) top = fmaxf(top, __shfl_xor(top, d, 64));
+  const float from = top == -INFINITY ? 0.0f : top;
+  float o[N], sum = 0.0f;
+#pragma unroll
+  for (uint32_t j = 0; j < N; ++j) o[j] = 0.0f;
+  for (uint32_t p0 = 0; p0 < n; p0 += 64) {
+    float f = 0.0f, l = 0.0f;
+    if (p0 + lane < n) {
+      f = __builtin_amdgcn_exp2f(at(p0 + lane)[M * D + row] - from);
+      l = at(p0 + lane)[M * D + M + row] * f;
+    }
+    for (int d = 32; d; d >>= 1) l += __shfl_xor(l, d, 64);
+    sum += l;
+    const uint32_t here = min(64u, n - p0);
+    for (uint32_t p = 0; p < here; p += 8) {  // eight loads in flight; lanes past the last part hold f = 0
+      float x[8][N];
+#pragma unroll
+      for (uint32_t e = 0; e < 8; ++e) {
+        const float *src = at(p0 + min(p + e, here - 1)) + row * D + lane * N;
+#pragma unroll
+        for (uint32_t j = 0; j < N; ++j) x[e][j] = src[j];
+      }
+#pragma unroll
+      for (uint32_t e = 0; e < 8; ++e) {
+        const float w = __shfl(f, int(p + e), 64);
+        if (p + e < here) {
+#pragma unroll
+          for (uint32_t j = 0; j < N; ++j) o[j] += x[e][j] * w;
+        }
+      }
+    }
+  }
+  finish<T, N>(a, L.first + tok, head * a.grp + row % a.grp, lane * N, o, top, sum, lane == 0);
+}
+
+uintptr_t addr(const void *p) { return reinterpret_cast<uintptr_t>(p); }
+
+// Row tiles of 16 * mt rows: 32 where a request has more than 16 rows for a
+// key/value head on average, or a group is wider than 16 heads.
+uint32_t tiles_of_16(uint64_t n_tok, uint32_t n_req, uint32_t grp) {
+  return grp > 16 || n_tok * grp > 16 * uint64_t(n_req) ? 2 : 1;
+}
+
+struct Plan {
+  uint32_t mt, runs;
+  uint64_t meta_bytes, bytes;
+};
+Plan plan_of(uint64_t n_tok, uint32_t n_req, uint32_t hq, uint32_t hk, uint32_t dim) {
+  Plan p;
+  p.mt = tiles_of_16(n_tok, n_req, hq / hk);
+  p.runs = std::max(1u, AT_RUNS / hk);
+  p.meta_bytes = (uint64_t(hk) * p.runs * 16 + 255) / 256 * 256;
+  p.bytes = p.meta_bytes + uint64_t(hk) * p.runs * 2 * (16 * p.mt) * (dim + 2) * sizeof(float);
+  return p;
+}
+
+bool good_cache(const bbpe_paged_cache *c) {
+  return c && (c->dtype == BBPE_BF16 || c->dtype == BBPE_F16) && (c->head_dim == 64 || c->head_dim == 128 || c->head_dim == 256) &&
+         c->n_kv_heads >= 1 && c->n_kv_heads <= 4096 && c->page_size >= 8 && c->page_size <= 65536 &&
+         (c->page_size & (c->page_size - 1)) == 0 && c->n_pages >= 1 && c->n_pages <= 0x7FFFFFFFull && c->k && c->v &&
+         ((addr(c->k) | addr(c->v)) & 15) == 0 && ((c->page_stride | c->head_stride | c->token_stride) & 7) == 0;
+}
+bool good_heads(uint32_t hq, const bbpe_paged_cache *c) {
+  return hq >= 1 && hq % c->n_kv_heads == 0 && hq / c->n_kv_heads <= 32;
+}
+
+template <typename T, uint32_t D, uint32_t MT>
+void launch(const AttnArgs &a, hipStream_t st) {
+  k_attn_rows<T, D, MT><<<dim3(a.hk, a.runs), AT_BLOCK, 0, st>>>(a);
+  k_attn_join<T, D, 16 * MT><<<dim3(a.hk, a.runs, 16 * MT / AT_WAVES), AT_BLOCK, 0, st>>>(a);
+}
+template <typename T, uint32_t D>
+void launch_mt(const AttnArgs &a, uint32_t mt, hipStream_t st) {
+  mt == 1 ? launch<T, D, 1>(a, st) : launch<T, D, 2>(a, st);
+}
+template <typename T>
+void launch_dim(const AttnArgs &a, uint32_t dim, uint32_t mt, hipStream_t st) {
+  dim == 64 ? launch_mt<T, 64>(a, mt, st) : dim == 128 ? launch_mt<T, 128>(a, mt, st) : launch_mt<T, 256>(a, mt, st);
+}
+
+}  // namespace
+}  // namespace bbpe
+
+using namespace bbpe;
+
+extern "C" {
+
+int bbpe_tree_attention_workspace_bytes(uint64_t n_tokens, uint32_t n_req, uint32_t n_q_heads,
+                                        const bbpe_paged_cache *cache, uint64_t *out_bytes) {
+  if (!out_bytes || !good_cache(cache) || !good_heads(n_q_heads, cache)) return BBPE_E_INVALID_ARG;
+  *out_bytes = plan_of(n_tokens, n_req, n_q_heads, cache->n_kv_heads, cache->head_dim).bytes;
+  return BBPE_OK;
+}
+
+int bbpe_tree_attention(const void *q, int64_t q_ts, int64_t q_hs, uint64_t n_tokens,
+                        uint32_t n_q_heads, const bbpe_paged_cache *cache, const int32_t *d_table,
+                        uint64_t table_stride, uint32_t table_width, const int64_t *d_q_off,
+                        const int32_t *d_ctx_len, uint32_t n_req, const uint64_t *d_tree_mask,
+                        uint32_t mask_words, float scale, void *out, int64_t out_ts,
+                        int64_t out_hs, float *d_lse, void *d_workspace, uint64_t workspace_bytes,
+                        void *hip_stream) {
+  if (!good_cache(cache) || !good_heads(n_q_heads, cache)) return BBPE_E_INVALID_ARG;
+  if (n_tokens > 0x7FFFFFFFull || !std::isfinite(scale) || (n_req > 1 && table_stride < table_width) ||
+      uint64_t(table_width) * cache->page_size > 0x7FFFFFFFull)
+    return BBPE_E_INVALID_ARG;
+  if (n_tokens == 0 || n_req == 0) return BBPE_OK;
+  if (!q || !out || !d_table || table_width == 0 || !d_q_off || !d_ctx_len || (d_tree_mask && mask_words == 0))
+    return BBPE_E_INVALID_ARG;
+  if ((addr(q) & 1) || (addr(out) & 1) || (addr(d_table) & 3) || (addr(d_q_off) & 7) || (addr(d_ctx_len) & 3) ||
+      (addr(d_tree_mask) & 7) || (addr(d_lse) & 3))
+    return BBPE_E_INVALID_ARG;
+  const Plan p = plan_of(n_tokens, n_req, n_q_heads, cache->n_kv_heads, cache->head_dim);
+  if (!d_workspace || (addr(d_workspace) & 255) || workspace_bytes < p.bytes) return BBPE_E_WORKSPACE;
+  AttnArgs a{};
+  a.q = q;
+  a.q_ts = q_ts;
+  a.q_hs = q_hs;
+  a.kc = static_cast<const char *>(cache->k);
+  a.vc = static_cast<const char *>(cache->v);
+  a.page_stride = cache->page_stride;
+  a.head_stride = cache->head_stride;
+  a.token_stride = cache->token_stride;
+  a.n_pages = cache->n_pages;
+  a.page_shift = uint32_t(__builtin_ctz(cache->page_size));
+  a.table_stride = table_stride;
+  a.cap = table_width * cache->page_size;
+  a.mask = d_tree_mask;
+  a.words = mask_words;
+  a.scale2 = scale * 1.44269504088896340736f;
+  a.out = out;
+  a.out_ts = out_ts;
+  a.out_hs = out_hs;
+  a.lse = d_lse;
+  a.n_tok = n_tokens;
+  a.hq = n_q_heads;
+  a.hk = cache->n_kv_heads;
+  a.grp = a.hq / a.hk;
+  a.tok_log = uint32_t(31 - __builtin_clz(16 * p.mt / a.grp));
+  a.runs = p.runs;
+  a.q_vec = ((addr(q) | uint64_t(q_ts * 2) | uint64_t(q_hs * 2)) & 15) == 0;
+  a.out_vec = ((addr(out) | uint64_t(out_ts * 2) | uint64_t(out_hs * 2)) & 15) == 0;
+  a.meta = static_cast<uint32_t *>(d_workspace);
+  a.part = reinterpret_cast<float *>(static_cast<char *>(d_workspace) + p.meta_bytes);
+  const hipStream_t st = static_cast<hipStream_t>(hip_stream);
+  for (uint32_t r0 = 0; r0 < n_req; r0 += AT_REQ) {
+    a.table = d_table + r0 * table_stride;
+    a.q_off = d_q_off + r0;
+    a.ctx = d_ctx_len + r0;
+    a.n_req = std::min(AT_REQ, n_req - r0);
+    if (cache->dtype == BBPE_BF16) launch_dim<__bf16>(a, cache->head_dim, p.mt, st);
+    else launch_dim<_Float16>(a, cache->head_dim, p.mt, st);
+  }
+  return hipGetLastError() == hipSuccess ? BBPE_OK : BBPE_E_HIP;
+}
+
+}  // extern "C"

@@ -1,0 +1,375 @@
+// Block tables and slot maps built on the device from request lengths: the
+// pages that a serving step's new tokens need are handed out from a free list,
+// and every token gets its cache slot and its position.
+//
+// Request r with c = ctx[r] cached and n = q_off[r+1] - q_off[r] new tokens
+// holds ceil(c/P) pages and needs ceil((c+n)/P) - ceil(c/P) more; its first is
+// entry (sum of the needs before r) of the free list.  Token i of it sits at
+// place p = c + i, so in entry p / P of the row, at p % P of that page.
+//
+// The work is stores (16 to 20 bytes a token, 4 a table entry) behind one scan
+// over the requests.  Up to FOLD requests every workgroup makes that scan for
+// itself and one launch does everything; beyond, a one-workgroup scan goes
+// first.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+
+#include "../../include/bbpe.h"
+#include "bbpe_device.h"
+
+namespace bbpe {
+namespace {
+
+constexpr uint32_t PG_BLOCK = 512;
+// Requests that every workgroup scans for itself (8 a thread).
+constexpr uint32_t PG_FOLD = 4096, PG_ITEMS = PG_FOLD / PG_BLOCK;
+constexpr uint32_t PG_TOKENS = 4;                    // a thread's tokens in one round
+constexpr uint32_t PG_TILE = PG_BLOCK * PG_TOKENS;   // a workgroup's tokens in one round
+constexpr uint32_t PG_PIECE = 2048;                  // table entries of one wave's piece
+constexpr uint32_t PG_FAILED = 0xFFFFFFFFu;          // start of a request that failed
+constexpr uint32_t PG_GRID = 512;                    // workgroups at most (two a compute unit)
+
+struct TableArgs {
+  const int64_t *q_off;
+  const int32_t *ctx;
+  const int32_t *free_pages;
+  int32_t *table;
+  const int32_t *depth;
+  int64_t *slots;
+  int32_t *pos, *req, *seq;
+  int64_t *status;
+  uint32_t *start;      // [n_req] more than PG_FOLD requests: first free-list entry, or PG_FAILED
+  uint32_t *n_good;     // [1] requests before the first broken offset
+  uint64_t table_stride, n_free, n_tok;
+  uint32_t n_req, width, page, page_shift;  // page_shift: 32 if the page size is no power of two
+  uint32_t vec_tok, vec_table;              // outputs 16-byte aligned: vector stores
+};
+
+__device__ __forceinline__ uint32_t page_of(const TableArgs &a, uint32_t p) {
+  return a.page_shift < 32 ? p >> a.page_shift : p / a.page;
+}
+// ceil(x / P) for x up to 2^31
+__device__ __forceinline__ uint32_t pages_for(const TableArgs &a, uint32_t x) {
+  return x ? page_of(a, x - 1) + 1 : 0;
+}
+
+// offsets that cannot be followed
+__device__ __forceinline__ bool off_broken(const TableArgs &a, int64_t lo, int64_t hi) {
+  return lo < 0 || hi < lo || uint64_t(hi) > a.n_tok;
+}
+
+struct Request {
+  int64_t lo, hi;
+  int32_t ctx;
+};
+__device__ __forceinline__ Request read_request(const TableArgs &a, uint32_t r) {
+  return Request{a.q_off[r], a.q_off[r + 1], a.ctx[r]};
+}
+
+// Pages that request q needs, and its code before the free list is looked at.
+__device__ __forceinline__ uint32_t need_of(const TableArgs &a, const Request &q, bool broken, int &code) {
+  code = BBPE_OK;
+  if (broken || q.ctx < 0 || q.hi - q.lo + q.ctx > 0x7FFFFFFFll) {
+    code = BBPE_E_INVALID_ARG;
+    return 0;
+  }
+  const uint32_t n = uint32_t(q.hi - q.lo), old = pages_for(a, uint32_t(q.ctx));
+  const uint32_t end = pages_for(a, uint32_t(q.ctx) + n);
+  if (end > a.width) {
+    code = BBPE_E_CAPACITY;
+    return 0;
+  }
+  return n ? end - old : 0;
+}
+
+// What a run of requests adds to the status record.
+struct Tally {
+  uint32_t first;  // first failed request (~0: none)
+  int code;
+  uint64_t pages, tokens;
+};
+__device__ __forceinline__ void settle(const TableArgs &a, const Request &q, uint32_t r, uint32_t need, int code,
+                                       uint64_t start, bool write, uint32_t &kept, Tally &t) {
+  if (code == BBPE_OK && need && start + need > a.n_free) code = BBPE_E_CAPACITY;
+  kept = code == BBPE_OK ? uint32_t(start < PG_FAILED ? start : PG_FAILED - 1) : PG_FAILED;
+  if (code == BBPE_OK) {
+    t.pages += need;
+    t.tokens += uint64_t(q.hi - q.lo);
+  } else if (r < t.first) {
+    t.first = r;
+    t.code = code;
+  }
+  if (write) a.seq[r] = code == BBPE_OK ? int32_t(q.ctx + (q.hi - q.lo)) : max(q.ctx, 0);
+}
+
+// Minimum over the block (sh: one word a wave).
+__device__ __forceinline__ uint32_t block_min(uint32_t v, uint32_t *sh, uint32_t waves) {
+  for (int d = 32; d; d >>= 1) v = min(v, uint32_t(__shfl_xor(int(v), d, 64)));
+  __syncthreads();
+  if ((threadIdx.x & 63) == 0) sh[threadIdx.x >> 6] = v;
+  __syncthreads();
+  uint32_t m = sh[0];
+  for (uint32_t w = 1; w < waves; ++w) m = min(m, sh[w]);
+  return m;
+}
+__device__ __forceinline__ uint64_t block_sum(uint64_t v, uint64_t *sh, uint32_t waves) {
+  for (int d = 32; d; d >>= 1) v += uint64_t(__shfl_xor((unsigned long long)v, d, 64));
+  __syncthreads();
+  if ((threadIdx.x & 63) == 0) sh[threadIdx.x >> 6] = v;
+  __syncthreads();
+  uint64_t m = 0;
+  for (uint32_t w = 0; w < waves; ++w) m += sh[w];
+  return m;
+}
+
+__device__ __forceinline__ void write_status(const TableArgs &a, Tally t, uint32_t *sh32, uint64_t *sh64, uint32_t waves) {
+  const uint32_t first = block_min(t.first, sh32, waves);
+  const uint64_t pages = block_sum(t.pages, sh64, waves), tokens = block_sum(t.tokens, sh64, waves);
+  if (threadIdx.x == 0) {
+    a.status[2] = int64_t(pages);
+    a.status[3] = int64_t(tokens);
+    if (first == 0xFFFFFFFFu) {
+      a.status[0] = BBPE_OK;
+      a.status[1] = -1;
+    }
+  }
+  if (first != 0xFFFFFFFFu && t.first == first) {
+    a.status[0] = t.code;
+    a.status[1] = int64_t(first);
+  }
+}
+
+// The scan for more than PG_FOLD requests: one workgroup, 1,024 requests a round.
+__global__ __launch_bounds__(1024) void k_page_scan(TableArgs a) {
+  constexpr uint32_t NT = 1024;
+  __shared__ uint64_t sh[2 * NT / 64 + 1];
+  __shared__ uint32_t shm[NT / 64];
+  uint64_t base = 0;
+  uint32_t good = a.n_req;
+  Tally t{0xFFFFFFFFu, BBPE_OK, 0, 0};
+  for (uint32_t r0 = 0; r0 < a.n_req; r0 += NT) {
+    const uint32_t r = r0 + threadIdx.x;
+    Request q{0, 0, 0};
+    if (r < a.n_req) q = read_request(a, r);
+    const bool mine = r < a.n_req && off_broken(a, q.lo, q.hi);
+    good = min(good, block_min(mine ? r : 0xFFFFFFFFu, shm, NT / 64));
+    int code = BBPE_OK;
+    const uint32_t need = r < a.n_req ? need_of(a, q, r >= good, code) : 0;
+    uint64_t total;
+    const uint64_t incl = block_incl_scan<NT, uint64_t>(need, 0, [](uint64_t x, uint64_t y) { return x + y; }, sh, total);
+    if (r < a.n_req) {
+      uint32_t kept;
+      settle(a, q, r, need, code, base + incl - need, true, kept, t);
+      a.start[r] = kept;
+    }
+    base += total;
+  }
+  write_status(a, t, shm, sh, NT / 64);
+  if (threadIdx.x == 0) *a.n_good = good;
+}
+
+template <bool FOLDED>
+__global__ __launch_bounds__(PG_BLOCK) void k_page_tables(TableArgs a) {
+  __shared__ uint64_t sh[2 * PG_BLOCK / 64 + 1];
+  __shared__ uint32_t shm[PG_BLOCK / 64];
+  __shared__ uint32_t s_off[FOLDED ? PG_FOLD + 1 : 1], s_start[FOLDED ? PG_FOLD : 1];
+  uint32_t good;
+  if (FOLDED) {
+    // thread t scans requests t*k .. t*k+k-1
+    const uint32_t k = (a.n_req + PG_BLOCK - 1) / PG_BLOCK, r0 = threadIdx.x * k;
+    Request q[PG_ITEMS];
+    uint32_t first = a.n_req;
+#pragma unroll
+    for (uint32_t j = 0; j < PG_ITEMS; ++j)
+      if (j < k && r0 + j < a.n_req) q[j] = read_request(a, r0 + j);
+#pragma unroll
+    for (uint32_t j = 0; j < PG_ITEMS; ++j)
+      if (j < k && r0 + j < a.n_req && off_broken(a, q[j].lo, q[j].hi)) first = min(first, r0 + j);
+    good = block_min(first, shm, PG_BLOCK / 64);
+    uint32_t need[PG_ITEMS];
+    int code[PG_ITEMS];
+    uint64_t mine = 0;
+#pragma unroll
+    for (uint32_t j = 0; j < PG_ITEMS; ++j) {
+      need[j] = 0;
+      if (j < k && r0 + j < a.n_req) need[j] = need_of(a, q[j], r0 + j >= good, code[j]);
+      mine += need[j];
+    }
+    uint64_t total;
+    uint64_t at = block_incl_scan<PG_BLOCK, uint64_t>(mine, 0, [](uint64_t x, uint64_t y) { return x + y; }, sh, total) - mine;
+    Tally t{0xFFFFFFFFu, BBPE_OK, 0, 0};
+#pragma unroll
+    for (uint32_t j = 0; j < PG_ITEMS; ++j) {
+      if (j < k && r0 + j < a.n_req) {
+        settle(a, q[j], r0 + j, need[j], code[j], at, blockIdx.x == 0, s_start[r0 + j], t);
+        if (r0 + j < good) {  // offsets within n_tok, so within 32 bits
+          s_off[r0 + j] = uint32_t(q[j].lo);
+          if (r0 + j + 1 == good) s_off[good] = uint32_t(q[j].hi);
+        }
+      }
+      at += need[j];
+    }
+    if (blockIdx.x == 0) write_status(a, t, shm, sh, PG_BLOCK / 64);
+    __syncthreads();
+  } else {
+    good = *a.n_good;
+  }
+  const auto off = [&](uint32_t r) -> uint32_t { return FOLDED ? s_off[r] : uint32_t(a.q_off[r]); };
+  const auto start_of = [&](uint32_t r) -> uint32_t { return FOLDED ? s_start[r] : a.start[r]; };
+
+  const uint32_t tiles = uint32_t((a.n_tok + PG_TILE - 1) / PG_TILE);
+  const uint32_t per_row = (a.width + PG_PIECE - 1) / PG_PIECE;
+  const uint64_t pieces = uint64_t(a.n_req) * per_row;
+  const uint64_t items = tiles + (pieces + PG_BLOCK / 64 - 1) / (PG_BLOCK / 64);
+  for (uint64_t item = blockIdx.x; item < items; item += gridDim.x) {
+    if (item < tiles) {
+      const uint64_t i0 = item * PG_TILE + threadIdx.x * PG_TOKENS;
+      if (i0 >= a.n_tok) continue;
+      // the last request that begins at or before i0 (good: past them all; ~0: before the first)
+      uint32_t lo = 0, hi = good + 1;  // off(lo - 1) <= i0 < off(hi)
+      if (good == 0) hi = 0;
+      while (lo < hi) {
+        const uint32_t mid = (lo + hi) / 2;
+        if (off(mid) <= i0) lo = mid + 1;
+        else hi = mid;
+      }
+      uint32_t r = lo - 1;  // ~0u if none
+      int64_t slot[PG_TOKENS];
+      int32_t pos[PG_TOKENS], req[PG_TOKENS];
+      uint32_t last_b = 0xFFFFFFFFu, last_r = 0xFFFFFFFFu;
+      int32_t page = -1;
+#pragma unroll
+      for (uint32_t j = 0; j < PG_TOKENS; ++j) {
+        const uint64_t i = i0 + j;
+        slot[j] = -1;
+        pos[j] = 0;
+        req[j] = -1;
+        if (i >= a.n_tok || good == 0) continue;
+        while (r + 1 <= good && off(r + 1) <= i) ++r;  // r == ~0u wraps to request 0
+        if (r >= good) continue;
+        const uint32_t s = start_of(r);
+        if (s == PG_FAILED) continue;
+        const uint32_t c = uint32_t(a.ctx[r]), p = c + uint32_t(i - off(r)), b = page_of(a, p);
+        if (b != last_b || r != last_r) {
+          const uint32_t old = pages_for(a, c);
+          page = b < old ? a.table[r * a.table_stride + b] : a.free_pages[s + (b - old)];
+          last_b = b;
+          last_r = r;
+        }
+        slot[j] = page < 0 ? -1 : int64_t(page) * a.page + (p - b * a.page);
+        pos[j] = int32_t(a.depth ? c + uint32_t(a.depth[i]) : p);
+        req[j] = int32_t(r);
+      }
+      if (a.vec_tok && i0 + PG_TOKENS <= a.n_tok) {
+        reinterpret_cast<int4 *>(a.pos)[i0 / 4] = make_int4(pos[0], pos[1], pos[2], pos[3]);
+        if (a.req) reinterpret_cast<int4 *>(a.req)[i0 / 4] = make_int4(req[0], req[1], req[2], req[3]);
+        reinterpret_cast<longlong2 *>(a.slots)[i0 / 2] = make_longlong2(slot[0], slot[1]);
+        reinterpret_cast<longlong2 *>(a.slots)[i0 / 2 + 1] = make_longlong2(slot[2], slot[3]);
+      } else {
+#pragma unroll
+        for (uint32_t j = 0; j < PG_TOKENS; ++j)
+          if (i0 + j < a.n_tok) {
+            a.slots[i0 + j] = slot[j];
+            a.pos[i0 + j] = pos[j];
+            if (a.req) a.req[i0 + j] = req[j];
+          }
+      }
+    } else {
+      const uint64_t piece = (item - tiles) * (PG_BLOCK / 64) + (threadIdx.x >> 6);
+      if (piece >= pieces) continue;
+      const uint32_t r = uint32_t(piece / per_row), lane = threadIdx.x & 63;
+      const uint32_t from = uint32_t(piece - uint64_t(r) * per_row) * PG_PIECE, to = min(a.width, from + PG_PIECE);
+      const uint32_t s = start_of(r);
+      const int32_t c = max(a.ctx[r], 0);
+      const uint32_t old = min(pages_for(a, uint32_t(c)), a.width);
+      uint32_t end = old;  // a failed request, or one without new tokens, takes none
+      if (s != PG_FAILED && off(r + 1) != off(r)) end = pages_for(a, uint32_t(c) + (off(r + 1) - off(r)));
+      int32_t *row = a.table + r * a.table_stride;
+      const auto entry = [&](uint32_t b) -> int32_t { return b < end ? a.free_pages[s + (b - old)] : -1; };
+      if (a.vec_table) {
+        for (uint32_t b = max(from, old & ~3u) + lane * 4; b < to; b += 256) {
+          if (b >= old && b + 4 <= to) {
+            *reinterpret_cast<int4 *>(row + b) = make_int4(entry(b), entry(b + 1), entry(b + 2), entry(b + 3));
+          } else {
+            for (uint32_t e = max(b, old); e < min(b + 4, to); ++e) row[e] = entry(e);
+          }
+        }
+      } else {
+        for (uint32_t b = max(from, old) + lane; b < to; b += 64) row[b] = entry(b);
+      }
+    }
+  }
+}
+
+}  // namespace
+}  // namespace bbpe
+
+using namespace bbpe;
+
+extern "C" {
+
+int bbpe_block_tables_workspace_bytes(uint32_t n_req, uint64_t *out_bytes) {
+  if (!out_bytes) return BBPE_E_INVALID_ARG;
+  *out_bytes = n_req > PG_FOLD ? 256 + 4 * uint64_t(n_req) : 0;
+  return BBPE_OK;
+}
+
+int bbpe_block_tables(const int64_t *d_q_off, const int32_t *d_ctx_len, uint32_t n_req,
+                      const int32_t *d_free_pages, uint64_t n_free, int32_t *d_table,
+                      uint64_t table_stride, uint32_t table_width, uint32_t page_size,
+                      uint64_t n_tokens, const int32_t *d_depth, int64_t *d_slots,
+                      int32_t *d_positions, int32_t *d_requests, int32_t *d_seq_len,
+                      int64_t *d_status, void *d_workspace, uint64_t workspace_bytes,
+                      void *hip_stream) {
+  const auto addr = [](const void *p) { return reinterpret_cast<uintptr_t>(p); };
+  if (!d_q_off || !d_status || (n_req && (!d_ctx_len || !d_seq_len)) || (n_free && !d_free_pages) ||
+      (n_req && table_width && !d_table) || (n_tokens && (!d_slots || !d_positions)))
+    return BBPE_E_INVALID_ARG;
+  if (page_size == 0 || page_size > (1u << 30) || table_width > 0x7FFFFFFFu || n_req > (1u << 24) ||
+      n_free > 0x7FFFFFFFull || n_tokens > 0x7FFFFFFFull || (n_req > 1 && table_stride < table_width))
+    return BBPE_E_INVALID_ARG;
+  if ((addr(d_q_off) & 7) || (addr(d_slots) & 7) || (addr(d_status) & 7) || (addr(d_ctx_len) & 3) ||
+      (addr(d_free_pages) & 3) || (addr(d_table) & 3) || (addr(d_depth) & 3) || (addr(d_positions) & 3) ||
+      (addr(d_requests) & 3) || (addr(d_seq_len) & 3))
+    return BBPE_E_INVALID_ARG;
+  const bool folded = n_req <= PG_FOLD;
+  if (!folded && (!d_workspace || (addr(d_workspace) & 255) || workspace_bytes < 256 + 4 * uint64_t(n_req)))
+    return BBPE_E_WORKSPACE;
+  TableArgs a{};
+  a.q_off = d_q_off;
+  a.ctx = d_ctx_len;
+  a.free_pages = d_free_pages;
+  a.table = d_table;
+  a.depth = d_depth;
+  a.slots = d_slots;
+  a.pos = d_positions;
+  a.req = d_requests;
+  a.seq = d_seq_len;
+  a.status = d_status;
+  a.table_stride = table_stride;
+  a.n_free = n_free;
+  a.n_tok = n_tokens;
+  a.n_req = n_req;
+  a.width = table_width;
+  a.page = page_size;
+  a.page_shift = (page_size & (page_size - 1)) == 0 ? uint32_t(__builtin_ctz(page_size)) : 32u;
+  a.vec_tok = ((addr(d_slots) | addr(d_positions) | addr(d_requests)) & 15) == 0;
+  a.vec_table = (addr(d_table) & 15) == 0 && (table_stride & 3) == 0;
+  const uint64_t tiles = (n_tokens + PG_TILE - 1) / PG_TILE;
+  const uint64_t pieces = uint64_t(n_req) * ((table_width + PG_PIECE - 1) / PG_PIECE);
+  const uint64_t items = tiles + (pieces + PG_BLOCK / 64 - 1) / (PG_BLOCK / 64);
+  const dim3 grid(uint32_t(std::max<uint64_t>(1, std::min<uint64_t>(PG_GRID, items))));
+  const hipStream_t st = static_cast<hipStream_t>(hip_stream);
+  if (folded) {
+    k_page_tables<true><<<grid, PG_BLOCK, 0, st>>>(a);
+  } else {
+    a.n_good = static_cast<uint32_t *>(d_workspace);
+    a.start = a.n_good + 64;
+    k_page_scan<<<1, 1024, 0, st>>>(a);
+    k_page_tables<false><<<grid, PG_BLOCK, 0, st>>>(a);
+  }
+  return hipGetLastError() == hipSuccess ? BBPE_OK : BBPE_E_HIP;
+}
+
+}  // extern "C"

@@ -364,6 +364,157 @@ int bbpe_timing_reset(bbpe_tokenizer *tok);
 
 void bbpe_free(bbpe_tokenizer *tok);
 
+/* --------------------------------------------------------------------------
+ * From ids to attention.  The operators below take what an encode call leaves
+ * on the device (d_id_off, the ids' count) and do what a serving or training
+ * program does around its model's matrix products: place new tokens in a
+ * paged key/value cache, normalise and rotate queries and keys, and attend
+ * over the cache.  They use no tokenizer handle and share no state: host
+ * threads may call them at once.  Each one enqueues its kernels on hip_stream
+ * and returns without synchronising, allocates nothing, records no memset, and
+ * may be captured into a HIP graph.  Arguments are checked on the host before
+ * anything is enqueued (BBPE_E_INVALID_ARG, BBPE_E_WORKSPACE); values that
+ * live on the device (lengths, pages, slots, masks) are checked by the kernels,
+ * which read and write nothing outside the buffers whatever they hold.
+ * Workspaces are 256-byte aligned device scratch; calls that may overlap (on
+ * different streams) need their own.
+ * -------------------------------------------------------------------------- */
+
+/* element types of queries, keys, values, weights and caches */
+enum { BBPE_BF16 = 0, BBPE_F16 = 1, BBPE_F32 = 2 };
+
+/* A paged key/value cache: n_pages pages, each holding page_size tokens of
+ * every key/value head.  Token o of page p, head h: the head_dim elements at
+ * p * page_stride + h * head_stride + o * token_stride of k and of v (strides
+ * in elements, multiples of 8; k and v 16-byte aligned).  dtype BBPE_BF16 or
+ * BBPE_F16.  Slot s of the cache is token s % page_size of page s / page_size. */
+typedef struct bbpe_paged_cache {
+  void *k, *v;
+  uint64_t n_pages;
+  uint32_t page_size, n_kv_heads, head_dim;
+  int32_t dtype;
+  int64_t page_stride, head_stride, token_stride;
+} bbpe_paged_cache;
+
+/* Block tables and slot maps from request lengths, on the device.
+ *
+ *   d_q_off[n_req+1]:  the new tokens of request r are [d_q_off[r], d_q_off[r+1])
+ *                      (an encode call's d_id_off);
+ *   d_ctx_len[n_req]:  tokens of r that the cache holds already, in the first
+ *                      ceil(ctx/page_size) pages of its table row;
+ *   d_free_pages[n_free]: pages to hand out, in this order;
+ *   d_table:           int32 [n_req][table_width], rows table_stride apart, in
+ *                      and out: row r keeps its held entries, its new pages
+ *                      follow, the rest of the row becomes -1;
+ *   n_tokens:          length of the per-token outputs;
+ *   d_depth[n_tokens]: optional: a drafted token's depth in its tree;
+ *   d_slots[n_tokens] (int64): the token's cache slot;
+ *   d_positions[n_tokens] (int32): ctx + index in the request, or ctx + depth;
+ *   d_requests[n_tokens] (int32), optional: the token's request;
+ *   d_seq_len[n_req]:  ctx + new tokens;
+ *   d_status[4] (int64): code of the first request that failed (BBPE_OK if
+ *                      none), its index (-1), pages handed out, tokens placed.
+ *
+ * Requests are served in order.  One fails with BBPE_E_INVALID_ARG when its
+ * context is negative, its length passes 2^31 - 1, or its or an earlier
+ * request's offsets are negative, decrease or pass n_tokens; with
+ * BBPE_E_CAPACITY when its pages pass table_width or the free list ends.  A
+ * failed request takes no page; its new tokens, and tokens of no request, get
+ * slot -1, position 0, request -1; its seq_len is its context (0 if negative).
+ * A token on a held entry outside 0 .. 2^31-1 gets slot -1.  The library's
+ * status codes are returned as usual for host-side errors only. */
+int bbpe_block_tables_workspace_bytes(uint32_t n_req, uint64_t *out_bytes);
+int bbpe_block_tables(const int64_t *d_q_off, const int32_t *d_ctx_len, uint32_t n_req,
+                      const int32_t *d_free_pages, uint64_t n_free, int32_t *d_table,
+                      uint64_t table_stride, uint32_t table_width, uint32_t page_size,
+                      uint64_t n_tokens, const int32_t *d_depth, int64_t *d_slots,
+                      int32_t *d_positions, int32_t *d_requests, int32_t *d_seq_len,
+                      int64_t *d_status, void *d_workspace, uint64_t workspace_bytes,
+                      void *hip_stream);
+
+/* Per-head RMS norm of queries and keys with the position rotation, in one
+ * pass over each.  For every row x of head_dim elements (one head of one
+ * token): y = x / sqrt(mean(x^2) + eps) * w, then for j < rot_dim / 2 the pair
+ * (y_j, y_{j+rot_dim/2}) -- interleaved: (y_2j, y_2j+1) -- turns by the angle
+ * positions * inv_freq[j]; elements from rot_dim on stay y.  Angles are
+ * products in 64 bits, sums are in 32, and there is one rounding, at the end.
+ *
+ *   dtype:             of q, k, v, the weights and the outputs;
+ *   q, k, v:           [n_tokens][heads][head_dim], the last dimension
+ *                      contiguous, token and head strides (_ts, _hs) in elements;
+ *   w_q, w_k:          [head_dim], 16-byte aligned; null: ones;
+ *   d_positions[n_tokens] (int32), d_inv_freq[rot_dim/2] (float);
+ *   q_out:             rotated queries (may be q itself);
+ *   k_out:             rotated keys, or null (may be k itself);
+ *   cache, d_slots:    serving form: rotated keys and the values v are stored at
+ *                      the token's slot (int64; a slot outside the cache is
+ *                      skipped); null for none.  v is read only with a cache.
+ *
+ * head_dim a multiple of 16 up to 256; rot_dim a multiple of 16 up to head_dim
+ * (0: no rotation).  16-byte aligned rows are faster than others. */
+int bbpe_qk_norm_rope(int dtype, uint64_t n_tokens, uint32_t n_q_heads, uint32_t n_kv_heads,
+                      uint32_t head_dim, uint32_t rot_dim, int interleaved, float eps,
+                      const void *q, int64_t q_ts, int64_t q_hs, const void *k, int64_t k_ts,
+                      int64_t k_hs, const void *v, int64_t v_ts, int64_t v_hs, const void *w_q,
+                      const void *w_k, const int32_t *d_positions, const float *d_inv_freq,
+                      void *q_out, int64_t qo_ts, int64_t qo_hs, void *k_out, int64_t ko_ts,
+                      int64_t ko_hs, const bbpe_paged_cache *cache, const int64_t *d_slots,
+                      void *hip_stream);
+
+/* Its backward pass: from the gradients g_q, g_k of the rotated rows and the
+ * rows q, k that went in, the gradients d_q, d_k of those rows (dtype, written
+ * once) and d_wq, d_wk of the weights (float [head_dim], summed over tokens and
+ * heads in a fixed order; null: not wanted).  d_q may be g_q and d_k may be g_k. */
+int bbpe_qk_norm_rope_backward_workspace_bytes(uint64_t n_tokens, uint32_t head_dim,
+                                               uint64_t *out_bytes);
+int bbpe_qk_norm_rope_backward(int dtype, uint64_t n_tokens, uint32_t n_q_heads,
+                               uint32_t n_kv_heads, uint32_t head_dim, uint32_t rot_dim,
+                               int interleaved, float eps, const void *g_q, int64_t gq_ts,
+                               int64_t gq_hs, const void *g_k, int64_t gk_ts, int64_t gk_hs,
+                               const void *q, int64_t q_ts, int64_t q_hs, const void *k,
+                               int64_t k_ts, int64_t k_hs, const void *w_q, const void *w_k,
+                               const int32_t *d_positions, const float *d_inv_freq, void *d_q,
+                               int64_t dq_ts, int64_t dq_hs, void *d_k, int64_t dk_ts,
+                               int64_t dk_hs, float *d_wq, float *d_wk, void *d_workspace,
+                               uint64_t workspace_bytes, void *hip_stream);
+
+/* Attention of new tokens over a paged cache that holds their keys and values
+ * already: a tree of drafted tokens, a chain (a prompt or a part of one), or
+ * one token.
+ *
+ *   q:                 [n_tokens][n_q_heads][head_dim] of the cache's type,
+ *                      strides in elements; query head h reads key/value head
+ *                      h / (n_q_heads / cache->n_kv_heads);
+ *   d_q_off[n_req+1], d_ctx_len[n_req], d_table (rows table_stride apart,
+ *                      table_width entries): as in bbpe_block_tables;
+ *   d_tree_mask:       uint64 [n_tokens][mask_words], or null.  Bit j of row i:
+ *                      token i sees new token j of its request (its ancestors
+ *                      and, normally, itself); tokens past 64 * mask_words are
+ *                      seen by none.  Null: token i sees new tokens 0 .. i;
+ *   out:               [n_tokens][n_q_heads][head_dim], same type;
+ *   d_lse:             float [n_tokens][n_q_heads], or null: the natural
+ *                      logarithm of the sum of exp(scale * score).
+ *
+ * Every token sees the whole context of its request, the first d_ctx_len[r]
+ * positions.  A token that sees nothing, or only scores of minus infinity,
+ * gives zeros and -inf.  Masked places contribute nothing whatever they hold.
+ * Table entries outside the cache, and positions past the row's end, are
+ * masked.  Scores, statistics and sums are float; the softmax weights are
+ * rounded to the cache's type for the product with the values.  Rows of out
+ * and d_lse whose token is in no request are not written.
+ *
+ * head_dim 64, 128 or 256; n_q_heads / n_kv_heads a whole number up to 32;
+ * page_size a power of two from 8 to 65536; table_width * page_size below 2^31. */
+int bbpe_tree_attention_workspace_bytes(uint64_t n_tokens, uint32_t n_req, uint32_t n_q_heads,
+                                        const bbpe_paged_cache *cache, uint64_t *out_bytes);
+int bbpe_tree_attention(const void *q, int64_t q_ts, int64_t q_hs, uint64_t n_tokens,
+                        uint32_t n_q_heads, const bbpe_paged_cache *cache, const int32_t *d_table,
+                        uint64_t table_stride, uint32_t table_width, const int64_t *d_q_off,
+                        const int32_t *d_ctx_len, uint32_t n_req, const uint64_t *d_tree_mask,
+                        uint32_t mask_words, float scale, void *out, int64_t out_ts,
+                        int64_t out_hs, float *d_lse, void *d_workspace, uint64_t workspace_bytes,
+                        void *hip_stream);
+
 /* A static English description of a status code. */
 const char *bbpe_status_str(int status);
 
