@@ -36,7 +36,7 @@ namespace bbpe {
 namespace {
 
 constexpr uint32_t AT_BLOCK = 256, AT_WAVES = 4;
-constexpr uint32_t AT_REQ = 2048;    // requests of one launch (their units' sums lie in LDS)
+constexpr uint32_t AT_REQ = 1024;    // requests of one launch (their units' sums lie in LDS)
 constexpr uint32_t AT_TILE = 32;     // keys a wave takes at once
 constexpr uint32_t AT_KT_LOG = 7;    // log2 of a unit's keys (AT_WAVES tiles)
 constexpr uint32_t AT_RUNS = 512;    // workgroups of a launch, over all heads
@@ -56,7 +56,8 @@ struct AttnArgs {
   uint32_t n_req;
   const uint64_t *mask;    // null: a chain
   uint32_t words;
-  float scale2;            // scale * log2(e)
+  float scale2;            // |scale| * log2(e)
+  uint32_t flip;           // a negative scale: the queries' signs are flipped
   void *out;
   int64_t out_ts, out_hs;
   float *lse;
@@ -138,6 +139,41 @@ __device__ __forceinline__ uint64_t scan_units(const AttnArgs &a, uint64_t *incl
   return total;
 }
 
+// The run's segments one after the other: which request, row tile and units.
+struct Segment {
+  Lengths L;
+  uint32_t r, token0;      // request, the row tile's first token in it
+  uint32_t n_units, first, count;
+  uint32_t klim, open;     // keys that any row of the tile sees, and those that all of them see
+};
+template <uint32_t KT_LOG>
+__device__ __forceinline__ Segment segment_at(const AttnArgs &a, const uint64_t *incl, uint64_t u, uint64_t u_end) {
+  Segment s;
+  uint32_t lo = 0, hi = a.n_req - 1;
+  while (lo < hi) {
+    const uint32_t mid = (lo + hi) / 2;
+    if (incl[mid] > u) hi = mid;
+    else lo = mid + 1;
+  }
+  s.r = __builtin_amdgcn_readfirstlane(lo);
+  s.L = lengths_of(a, s.r);
+  const uint64_t local = u - (s.r ? incl[s.r - 1] : 0);
+  uint32_t t = 0, t_hi = row_tiles(a, s.L.n) - 1;
+  while (t < t_hi) {  // the last tile that begins at or before `local`
+    const uint32_t mid = (t + t_hi + 1) / 2;
+    if (units_before<KT_LOG>(a, s.L, mid) <= local) t = mid;
+    else t_hi = mid - 1;
+  }
+  const uint64_t tile_u = units_before<KT_LOG>(a, s.L, t);
+  s.n_units = uint32_t(units_before<KT_LOG>(a, s.L, t + 1) - tile_u);
+  s.first = uint32_t(local - tile_u);
+  s.count = uint32_t(min(uint64_t(s.n_units - s.first), u_end - u));
+  s.token0 = t << a.tok_log;
+  s.klim = a.mask ? s.L.klen : uint32_t(min(uint64_t(s.L.klen), uint64_t(s.L.ctx) + s.token0 + (1u << a.tok_log)));
+  s.open = min(s.L.ctx, s.klim);
+  return s;
+}
+
 template <typename T> struct Mma;
 template <> struct Mma<__bf16> {
   static __device__ __forceinline__ f32x4 mul(bf16x8 x, bf16x8 y, f32x4 c) {
@@ -158,14 +194,23 @@ __device__ __forceinline__ float sum8(f32x8 a) {
   return ((a[0] + a[1]) + (a[2] + a[3])) + ((a[4] + a[5]) + (a[6] + a[7]));
 }
 
-// The larger of the four lanes 16 apart, in all four.
+// The larger, and the sum, of the four lanes 16 apart, in all four.
+__device__ __forceinline__ float max3(float x, float y, float z) {
+  float r;
+  asm("v_max3_f32 %0, %1, %2, %3" : "=v"(r) : "v"(x), "v"(y), "v"(z));
+  return r;
+}
 __device__ __forceinline__ float max_quarters(float x) {
-  x = fmaxf(x, __shfl_xor(x, 16, 64));
-  return fmaxf(x, __shfl_xor(x, 32, 64));
+  const auto p = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  x = fmaxf(__uint_as_float(p[0]), __uint_as_float(p[1]));
+  const auto q = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return fmaxf(__uint_as_float(q[0]), __uint_as_float(q[1]));
 }
 __device__ __forceinline__ float sum_quarters(float x) {
-  x += __shfl_xor(x, 16, 64);
-  return x + __shfl_xor(x, 32, 64);
+  const auto p = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  x = __uint_as_float(p[0]) + __uint_as_float(p[1]);
+  const auto q = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return __uint_as_float(q[0]) + __uint_as_float(q[1]);
 }
 
 // The low min(n, 8) bits (none for n <= 0).
@@ -214,6 +259,51 @@ __device__ __forceinline__ void finish(const AttnArgs &a, int64_t token, uint32_
     a.lse[token * a.hq + h] = sum == 0.0f ? -INFINITY : (top + __builtin_amdgcn_logf(sum)) * 0.69314718055994530942f;
 }
 
+// Two transposing reads: four elements of the row that this lane and the three
+// beside it name become four rows' elements at this lane's place among 16.
+template <typename T>
+__device__ __forceinline__ u32x4 turned(const T *p0, const T *p1) {
+  typedef short s16x4 __attribute__((ext_vector_type(4)));
+  typedef __attribute__((address_space(3))) s16x4 *lds;
+  const s16x4 x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds)(p0)), y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds)(p1));
+  const uint2 u = __builtin_bit_cast(uint2, x), v = __builtin_bit_cast(uint2, y);
+  return u32x4{u.x, u.y, v.x, v.y};
+}
+
+// Values that masked places may hold.  0 * inf is NaN, so infinities and NaN of
+// a tile with masked places leave the product, as flags (up: +inf or NaN, down:
+// -inf or NaN), and come back as what they add to the rows that see them.
+template <typename T>
+__device__ __forceinline__ uint32_t apart_bits(uint32_t f) {  // bit 15 of each half: infinity or NaN
+  return ((f & 0x7FFF7FFFu) + (0x8000u - Mma<T>::EXP) * 0x10001u) & 0x80008000u;
+}
+template <typename T>
+__device__ __forceinline__ void set_apart(u32x4 &f, u32x4 &up, u32x4 &down) {
+#pragma unroll
+  for (uint32_t e = 0; e < 4; ++e) {
+    const uint32_t bad = apart_bits<T>(f[e]) >> 15, neg = f[e] >> 15 & 0x10001u;
+    const uint32_t nan = (((f[e] & 0x7FFF7FFFu) + (0x7FFFu - Mma<T>::EXP) * 0x10001u) & 0x80008000u) >> 15;
+    up[e] = (nan | (bad & ~neg)) * Mma<T>::ONE;
+    down[e] = (nan | (bad & neg)) * Mma<T>::ONE;
+    f[e] &= ~(bad * 0xFFFFu);
+  }
+}
+// seen: bits of the eight keys of this lane
+template <typename T>
+__device__ __forceinline__ void add_apart(u32x4 up, u32x4 down, uint32_t seen, f32x4 &acc) {
+  typedef typename Vec8<T>::type T8;
+  u32x4 vis;
+#pragma unroll
+  for (uint32_t e = 0; e < 4; ++e) vis[e] = ((seen >> (2 * e) & 1) ? Mma<T>::ONE : 0) | ((seen >> (2 * e + 1) & 1) ? Mma<T>::ONE << 16 : 0);
+  const f32x4 plus = Mma<T>::mul(__builtin_bit_cast(T8, up), __builtin_bit_cast(T8, vis), f32x4{});
+  const f32x4 minus = Mma<T>::mul(__builtin_bit_cast(T8, down), __builtin_bit_cast(T8, vis), f32x4{});
+#pragma unroll
+  for (uint32_t e = 0; e < 4; ++e) {
+    if (plus[e] > 0.0f) acc[e] += INFINITY;
+    if (minus[e] > 0.0f) acc[e] -= INFINITY;
+  }
+}
+
 template <typename T, uint32_t D, uint32_t MT>
 __global__ __launch_bounds__(AT_BLOCK, (D * MT <= 128 ? 3 : D * MT <= 256 ? 2 : 1)) void k_attn_rows(AttnArgs a) {
   typedef typename Vec8<T>::type T8;
@@ -240,30 +330,10 @@ __global__ __launch_bounds__(AT_BLOCK, (D * MT <= 128 ? 3 : D * MT <= 256 ? 2 : 
   const char *vc = a.vc + int64_t(head) * a.head_stride * int64_t(sizeof(T));
 
   while (u < u_end) {
-    // request, row tile and first unit of the run's next segment
-    uint32_t lo = 0, hi = a.n_req - 1;
-    while (lo < hi) {
-      const uint32_t mid = (lo + hi) / 2;
-      if (s_incl[mid] > u) hi = mid;
-      else lo = mid + 1;
-    }
-    const uint32_t r = __builtin_amdgcn_readfirstlane(lo);
-    const Lengths L = lengths_of(a, r);
-    const uint64_t local = u - (r ? s_incl[r - 1] : 0);
-    uint32_t t = 0, t_hi = row_tiles(a, L.n) - 1;
-    while (t < t_hi) {  // the last tile that begins at or before `local`
-      const uint32_t mid = (t + t_hi + 1) / 2;
-      if (units_before<AT_KT_LOG>(a, L, mid) <= local) t = mid;
-      else t_hi = mid - 1;
-    }
-    const uint64_t tile_u = units_before<AT_KT_LOG>(a, L, t);
-    const uint32_t n_units = uint32_t(units_before<AT_KT_LOG>(a, L, t + 1) - tile_u);
-    const uint32_t first = uint32_t(local - tile_u);
-    const uint32_t count = uint32_t(min(uint64_t(n_units - first), u_end - u));
-    const uint32_t token0 = t << a.tok_log;
-    // keys that any row of the tile sees, and those that all of them see
-    const uint32_t klim = a.mask ? L.klen : uint32_t(min(uint64_t(L.klen), uint64_t(L.ctx) + token0 + (1u << a.tok_log)));
-    const uint32_t open = min(L.ctx, klim);
+    const Segment sg = segment_at<AT_KT_LOG>(a, s_incl, u, u_end);
+    const Lengths &L = sg.L;
+    const uint32_t r = sg.r, n_units = sg.n_units, first = sg.first, count = sg.count, token0 = sg.token0;
+    const uint32_t klim = sg.klim, open = sg.open;
     const int32_t *pages = a.table + uint64_t(r) * a.table_stride;
 
     // queries: row 16 * i + n16 of the tile
@@ -279,7 +349,7 @@ __global__ __launch_bounds__(AT_BLOCK, (D * MT <= 128 ? 3 : D * MT <= 256 ? 2 : 
 #pragma unroll
       for (uint32_t s = 0; s < NS; ++s) {
         q[i][s] = T8{};
-        if (live) q[i][s] = load8_raw(p + s * 32 + g * 8, a.q_vec);
+        if (live) q[i][s] = __builtin_bit_cast(T8, __builtin_bit_cast(u32x4, load8_raw(p + s * 32 + g * 8, a.q_vec)) ^ a.flip);
       }
     }
     f32x4 acc[MT][VD];
@@ -334,10 +404,7 @@ __global__ __launch_bounds__(AT_BLOCK, (D * MT <= 128 ? 3 : D * MT <= 256 ? 2 : 
 #pragma unroll
         for (uint32_t e = 0; e < 8; ++e)
 #pragma unroll
-          for (uint32_t w = 0; w < VD / 2; ++w) {
-            const uint32_t x = v[e][w];
-            bad |= uint32_t((x & Mma<T>::EXP) == Mma<T>::EXP) | uint32_t((x >> 16 & Mma<T>::EXP) == Mma<T>::EXP);
-          }
+          for (uint32_t w = 0; w < VD / 2; ++w) bad |= apart_bits<T>(v[e][w]);
         odd = __any(bad != 0);
       }
       T8 pf[MT];
@@ -350,34 +417,26 @@ __global__ __launch_bounds__(AT_BLOCK, (D * MT <= 128 ? 3 : D * MT <= 256 ? 2 : 
           sa = Mma<T>::mul(ka[s], q[i][s], sa);
           sb = Mma<T>::mul(kb8[s], q[i][s], sb);
         }
-        float x[8];
-#pragma unroll
-        for (uint32_t e = 0; e < 4; ++e) {
-          x[e] = sa[e] * a.scale2;
-          x[4 + e] = sb[e] * a.scale2;
-        }
+        float x[8] = {sa[0], sa[1], sa[2], sa[3], sb[0], sb[1], sb[2], sb[3]};
         seen[i] = 0xFF;
         if (part) {
           seen[i] = v_ok ? seen8(a, L, klim, kb, token[i]) : 0;
 #pragma unroll
           for (uint32_t e = 0; e < 8; ++e) x[e] = (seen[i] >> e & 1) ? x[e] : -INFINITY;
         }
-        float top = x[0];
-#pragma unroll
-        for (uint32_t e = 1; e < 8; ++e) top = fmaxf(top, x[e]);
-        top = max_quarters(top);
+        const float top = max_quarters(max3(max3(x[0], x[1], x[2]), max3(x[3], x[4], x[5]), fmaxf(x[6], x[7])));
         if (__any(top > m[i])) {
           const float m_new = fmaxf(m[i], top);
-          const float f = m_new == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(m[i] - m_new);
+          const float f = m_new == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f((m[i] - m_new) * a.scale2);
           m[i] = m_new;
           l[i] *= f;
 #pragma unroll
           for (uint32_t j = 0; j < VD; ++j) acc[i][j] *= f;
         }
-        const float base = m[i] == -INFINITY ? 0.0f : m[i];
+        const float base = m[i] == -INFINITY ? 0.0f : m[i] * a.scale2;
         f32x8 p;
 #pragma unroll
-        for (uint32_t e = 0; e < 8; ++e) p[e] = __builtin_amdgcn_exp2f(x[e] - base);
+        for (uint32_t e = 0; e < 8; ++e) p[e] = __builtin_amdgcn_exp2f(__builtin_fmaf(x[e], a.scale2, -base));
         l[i] += sum8(p);
         // rounded once to the cache's type: the matrix product's operand
         pf[i] = from_float<T>(p);
@@ -395,35 +454,10 @@ __global__ __launch_bounds__(AT_BLOCK, (D * MT <= 128 ? 3 : D * MT <= 256 ? 2 : 
         for (uint32_t half = 0; half < 2; ++half) {
           u32x4 f = half ? f1 : f0;
           if (odd) {
-            // 0 * inf is NaN: such values leave the product, and come back as
-            // what they add to the rows that see them
-            u32x4 up{}, down{};
+            u32x4 up, down;
+            set_apart<T>(f, up, down);
 #pragma unroll
-            for (uint32_t e = 0; e < 4; ++e)
-#pragma unroll
-              for (uint32_t h = 0; h < 32; h += 16) {
-                const uint32_t b = f[e] >> h & 0xFFFF, body = b & 0x7FFF;
-                if (body >= Mma<T>::EXP) {
-                  const bool nan = body > Mma<T>::EXP;
-                  if (nan || !(b & 0x8000)) up[e] |= Mma<T>::ONE << h;
-                  if (nan || (b & 0x8000)) down[e] |= Mma<T>::ONE << h;
-                  f[e] &= ~(0xFFFFu << h);
-                }
-              }
-#pragma unroll
-            for (uint32_t i = 0; i < MT; ++i) {
-              u32x4 vis;
-#pragma unroll
-              for (uint32_t e = 0; e < 4; ++e)
-                vis[e] = ((seen[i] >> (2 * e) & 1) ? Mma<T>::ONE : 0) | ((seen[i] >> (2 * e + 1) & 1) ? Mma<T>::ONE << 16 : 0);
-              const f32x4 plus = Mma<T>::mul(__builtin_bit_cast(T8, up), __builtin_bit_cast(T8, vis), f32x4{});
-              const f32x4 minus = Mma<T>::mul(__builtin_bit_cast(T8, down), __builtin_bit_cast(T8, vis), f32x4{});
-#pragma unroll
-              for (uint32_t e = 0; e < 4; ++e) {
-                if (plus[e] > 0.0f) acc[i][2 * w + half][e] += INFINITY;
-                if (minus[e] > 0.0f) acc[i][2 * w + half][e] -= INFINITY;
-              }
-            }
+            for (uint32_t i = 0; i < MT; ++i) add_apart<T>(up, down, seen[i], acc[i][2 * w + half]);
           }
 #pragma unroll
           for (uint32_t i = 0; i < MT; ++i)
@@ -439,7 +473,7 @@ __global__ __launch_bounds__(AT_BLOCK, (D * MT <= 128 ? 3 : D * MT <= 256 ? 2 : 
     for (uint32_t i = 0; i < MT; ++i) {
       l[i] = sum_quarters(l[i]);
       if (g == 0) {
-        s_m[wave][16 * i + n16] = m[i];
+        s_m[wave][16 * i + n16] = m[i] == -INFINITY ? m[i] : m[i] * a.scale2;
         s_l[wave][16 * i + n16] = l[i];
       }
     }
@@ -494,6 +528,263 @@ __global__ __launch_bounds__(AT_BLOCK, (D * MT <= 128 ? 3 : D * MT <= 256 ? 2 : 
       }
     }
     u += count;
+  }
+  if (!left_open && threadIdx.x == 0) meta[0] = 0;
+}
+
+// Row tiles of 64 * MT rows.  With this many rows the products, not the cache,
+// take the time, and what counts is how often K and V pass from memory to the
+// registers: a workgroup's waves take 16 * MT rows each of one row tile and
+// share its tiles of KT keys in LDS, two of them: while one is read, the next
+// one's rows are on their way through registers, first K's, then V's.  The products are
+// k_attn_rows'; V's fragment comes turned over from LDS by the transposing
+// reads.  16-byte chunks of a row are stored at (chunk XOR a function of the
+// row), so that 16 rows at one chunk, and 16 rows by four, fall on different
+// banks.
+template <uint32_t D>
+__device__ __forceinline__ uint32_t k_chunk(uint32_t row, uint32_t c) {
+  return D == 64 ? c ^ (row >> 1 & 7) : c ^ (row & 15);
+}
+template <uint32_t D>
+__device__ __forceinline__ uint32_t v_chunk(uint32_t row, uint32_t c) {
+  return D == 64 ? c ^ ((row >> 1 & 3) << 1) : c ^ ((row & 7) << 1);
+}
+
+template <typename T, uint32_t D, uint32_t MT>
+__global__ __launch_bounds__(AT_BLOCK, 2) void k_attn_tiles(AttnArgs a) {
+  typedef typename Vec8<T>::type T8;
+  constexpr uint32_t KT_LOG = D == 256 ? 5 : 6, KT = 1u << KT_LOG;  // keys of a tile
+  constexpr uint32_t NS = D / 32, ND = D / 16;
+  constexpr uint32_t CH = D / 8;             // 16-byte chunks of a row
+  constexpr uint32_t RPI = 64 / CH;          // rows of one load to LDS (1 KiB)
+  constexpr uint32_t ROWS = KT / AT_WAVES;   // rows that a wave fetches, in groups of 8 (of one page each)
+  constexpr uint32_t GROUPS = ROWS / 8, LPG = 8 / RPI;
+  constexpr uint32_t M = 64 * MT;
+  __shared__ __attribute__((aligned(1024))) T s_k[2][KT * D];
+  __shared__ __attribute__((aligned(1024))) T s_v[2][KT * D];
+  __shared__ uint64_t s_incl[AT_REQ];
+  __shared__ uint64_t s_scan[2 * AT_BLOCK / 64 + 1];
+
+  const uint32_t head = blockIdx.x, run = blockIdx.y;
+  const uint32_t lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), n16 = lane & 15, g = lane >> 4;
+  const uint64_t total = scan_units<KT_LOG>(a, s_incl, s_scan);
+  const uint64_t per = (total + a.runs - 1) / a.runs;
+  const uint64_t u_end = min(total, (uint64_t(run) + 1) * per);
+  uint64_t u = uint64_t(run) * per;
+  uint32_t *meta = a.meta + (uint64_t(head) * a.runs + run) * 4;
+  bool left_open = false;
+  const char *kc = a.kc + int64_t(head) * a.head_stride * int64_t(sizeof(T));
+  const char *vc = a.vc + int64_t(head) * a.head_stride * int64_t(sizeof(T));
+  const uint32_t in_page = (1u << a.page_shift) - 1;
+  // a lane's rows and chunk in its loads: row i * RPI + lane / CH of a group of eight
+  int64_t off[LPG];
+#pragma unroll
+  for (uint32_t i = 0; i < LPG; ++i) off[i] = int64_t(i * RPI + lane / CH) * a.token_stride * int64_t(sizeof(T)) + 16 * (lane % CH);
+
+  while (u < u_end) {
+    const Segment sg = segment_at<KT_LOG>(a, s_incl, u, u_end);
+    const Lengths &L = sg.L;
+    const int32_t *pages = a.table + uint64_t(sg.r) * a.table_stride;
+    T8 q[MT][NS];
+    uint32_t token[MT];
+    bool any = false;  // a row of this wave's is one of the tile's
+#pragma unroll
+    for (uint32_t i = 0; i < MT; ++i) {
+      const uint32_t row = 16 * (wave * MT + i) + n16, tl = row / a.grp;
+      token[i] = sg.token0 + tl;
+      const bool live = tl < (1u << a.tok_log) && token[i] < L.n;
+      any |= live;
+      token[i] = min(token[i], L.n - 1);
+      const T *p = static_cast<const T *>(a.q) + (L.first + token[i]) * a.q_ts + int64_t(head * a.grp + row % a.grp) * a.q_hs;
+#pragma unroll
+      for (uint32_t s = 0; s < NS; ++s) {
+        q[i][s] = T8{};
+        if (live) q[i][s] = __builtin_bit_cast(T8, __builtin_bit_cast(u32x4, load8_raw(p + s * 32 + g * 8, a.q_vec)) ^ a.flip);
+      }
+    }
+    any = __any(any);
+    f32x4 acc[MT][ND];
+    float m[MT], l[MT];
+#pragma unroll
+    for (uint32_t i = 0; i < MT; ++i) {
+      m[i] = -INFINITY;
+      l[i] = 0.0f;
+#pragma unroll
+      for (uint32_t j = 0; j < ND; ++j) acc[i][j] = f32x4{};
+    }
+    const uint32_t unit_end = min(sg.first + sg.count, (sg.klim + KT - 1) >> KT_LOG);
+
+    // the tile's pages, one a lane (of its KT / 8 groups); a page outside the cache reads page 0 and is masked
+    const auto pages_of = [&](uint32_t unit) -> int32_t {
+      const uint32_t key = (unit << KT_LOG) + 8 * (lane & (KT / 8 - 1));
+      return pages[min(key, sg.klim - 1) >> a.page_shift];
+    };
+    // its rows of K or of V on their way: global memory to registers, registers to LDS
+    u32x4 way[GROUPS * LPG];
+    const auto fetch = [&](const char *base, uint32_t unit, int32_t page) {
+#pragma unroll
+      for (uint32_t gi = 0; gi < GROUPS; ++gi) {
+        const uint32_t group = wave * GROUPS + gi, key = (unit << KT_LOG) + 8 * group;
+        const uint32_t p = uint32_t(__builtin_amdgcn_readlane(page, int(group)));
+        const char *at = base + (int64_t(p < a.n_pages ? p : 0) * a.page_stride + int64_t(key & in_page) * a.token_stride) * int64_t(sizeof(T));
+#pragma unroll
+        for (uint32_t i = 0; i < LPG; ++i) way[gi * LPG + i] = *reinterpret_cast<const u32x4 *>(at + off[i]);
+      }
+    };
+    const auto place_k = [&](uint32_t buf) {
+#pragma unroll
+      for (uint32_t i = 0; i < GROUPS * LPG; ++i) {
+        const uint32_t row = wave * ROWS + i * RPI + lane / CH;
+        *reinterpret_cast<u32x4 *>(s_k[buf] + row * D + 8 * k_chunk<D>(row, lane % CH)) = way[i];
+      }
+    };
+    const auto place_v = [&](uint32_t buf) {
+#pragma unroll
+      for (uint32_t i = 0; i < GROUPS * LPG; ++i) {
+        const uint32_t row = wave * ROWS + i * RPI + lane / CH;
+        *reinterpret_cast<u32x4 *>(s_v[buf] + row * D + 8 * v_chunk<D>(row, lane % CH)) = way[i];
+      }
+    };
+    int32_t page = 0;
+    uint32_t hidden_next = 0;  // groups of eight keys whose page is not in the cache
+    const auto hidden_of = [&](int32_t p) { return ~uint32_t(__ballot(uint32_t(p) < a.n_pages)) & ((1u << (KT / 8)) - 1); };
+    if (sg.first < unit_end) {
+      page = pages_of(sg.first);
+      fetch(kc, sg.first, page);
+      place_k(0);
+      fetch(vc, sg.first, page);
+      place_v(0);
+      hidden_next = hidden_of(page);
+      if (sg.first + 1 < unit_end) page = pages_of(sg.first + 1);
+    }
+    for (uint32_t unit = sg.first; unit < unit_end; ++unit) {
+      const uint32_t buf = (unit - sg.first) & 1;
+      const bool more = unit + 1 < unit_end;
+      const uint32_t hidden = hidden_next;
+      __syncthreads();  // this tile is there, and every wave is done with the other
+      if (more) fetch(kc, unit + 1, page);
+      const uint32_t key0 = unit << KT_LOG;
+      const bool part = key0 + KT > sg.open || hidden;
+      f32x4 s[MT][KT / 16];
+      uint64_t seen[MT];
+      if (any) {
+#pragma unroll
+        for (uint32_t k = 0; k < KT / 16; ++k) {
+#pragma unroll
+          for (uint32_t i = 0; i < MT; ++i) s[i][k] = f32x4{};
+#pragma unroll
+          for (uint32_t e = 0; e < NS; ++e) {
+            const uint32_t row = 16 * k + n16;
+            const T8 f = *reinterpret_cast<const T8 *>(s_k[buf] + row * D + 8 * k_chunk<D>(row, 4 * e + g));
+#pragma unroll
+            for (uint32_t i = 0; i < MT; ++i) s[i][k] = Mma<T>::mul(f, q[i][e], s[i][k]);
+          }
+        }
+#pragma unroll
+        for (uint32_t i = 0; i < MT; ++i) {
+          seen[i] = 0;
+          if (part) {
+            // a lane's keys are 16 k + 4 g ..+3: its bits are gathered four at a time
+#pragma unroll
+            for (uint32_t k = 0; k < KT / 16; ++k) {
+              const uint32_t at = 16 * k + 8 * (g >> 1);
+              const uint32_t b = (hidden >> (at >> 3) & 1) ? 0 : seen8(a, L, sg.klim, key0 + at, token[i]);
+              seen[i] |= uint64_t(b >> (4 * (g & 1)) & 15) << (4 * k);
+            }
+#pragma unroll
+            for (uint32_t k = 0; k < KT / 16; ++k)
+#pragma unroll
+              for (uint32_t e = 0; e < 4; ++e) s[i][k][e] = (seen[i] >> (4 * k + e) & 1) ? s[i][k][e] : -INFINITY;
+          }
+          float top = fmaxf(s[i][0][0], s[i][0][1]);
+#pragma unroll
+          for (uint32_t e = 2; e < KT / 4; e += 2) top = max3(top, s[i][e / 4][e % 4], s[i][e / 4][e % 4 + 1]);
+          top = max_quarters(top);
+          if (__any(top > m[i])) {
+            const float m_new = fmaxf(m[i], top);
+            const float f = m_new == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f((m[i] - m_new) * a.scale2);
+            m[i] = m_new;
+            l[i] *= f;
+#pragma unroll
+            for (uint32_t j = 0; j < ND; ++j) acc[i][j] *= f;
+          }
+          const float base = m[i] == -INFINITY ? 0.0f : m[i] * a.scale2;
+#pragma unroll
+          for (uint32_t k = 0; k < KT / 16; ++k) {
+#pragma unroll
+            for (uint32_t e = 0; e < 4; ++e) s[i][k][e] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i][k][e], a.scale2, -base));
+            l[i] += (s[i][k][0] + s[i][k][1]) + (s[i][k][2] + s[i][k][3]);
+          }
+        }
+      }
+      if (more) {
+        place_k(buf ^ 1);
+        fetch(vc, unit + 1, page);
+        hidden_next = hidden_of(page);
+        if (unit + 2 < unit_end) page = pages_of(unit + 2);
+      }
+      if (any) {
+#pragma unroll
+        for (uint32_t k = 0; k < KT / 32; ++k) {
+          T8 pf[MT];
+#pragma unroll
+          for (uint32_t i = 0; i < MT; ++i) {
+            const f32x4 x = s[i][2 * k], y = s[i][2 * k + 1];
+            pf[i] = from_float<T>(f32x8{x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]});
+          }
+#pragma unroll
+          for (uint32_t j = 0; j < ND; ++j) {
+            // values 32 k + 4 g ..+3 and + 16 of elements 16 j ..+15: four lanes read a row's 32 bytes
+            const uint32_t row = 32 * k + 4 * g + (n16 >> 2), c = 2 * j + (n16 >> 1 & 1);
+            const T *p = s_v[buf] + row * D + 4 * (n16 & 1);
+            u32x4 f = turned(p + 8 * v_chunk<D>(row, c), p + 16 * D + 8 * v_chunk<D>(row + 16, c));
+            if (part && __any((apart_bits<T>(f[0]) | apart_bits<T>(f[1]) | apart_bits<T>(f[2]) | apart_bits<T>(f[3])) != 0)) {
+              u32x4 up, down;
+              set_apart<T>(f, up, down);
+#pragma unroll
+              for (uint32_t i = 0; i < MT; ++i) add_apart<T>(up, down, uint32_t(seen[i] >> (8 * k)) & 0xFF, acc[i][j]);
+            }
+#pragma unroll
+            for (uint32_t i = 0; i < MT; ++i) acc[i][j] = Mma<T>::mul(__builtin_bit_cast(T8, f), pf[i], acc[i][j]);
+          }
+        }
+      }
+      if (more) place_v(buf ^ 1);
+    }
+    __syncthreads();  // the next segment's first tile goes to the first buffer
+
+    const bool whole = sg.first == 0 && sg.count == sg.n_units;
+    float *part = a.part + ((uint64_t(head) * a.runs + run) * 2 + (sg.first == 0 ? 1 : 0)) * (M * (D + 2));
+#pragma unroll
+    for (uint32_t i = 0; i < MT; ++i) {
+      const float sum = sum_quarters(l[i]);
+      const uint32_t row = 16 * (wave * MT + i) + n16, tl = row / a.grp, tok = sg.token0 + tl;
+      if (tl >= (1u << a.tok_log) || tok >= L.n) continue;
+      if (whole) {
+        const uint32_t h = head * a.grp + row % a.grp;
+#pragma unroll
+        for (uint32_t j = 0; j < ND; ++j) {
+          const float o[4] = {acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]};
+          finish<T, 4>(a, L.first + tok, h, 16 * j + 4 * g, o, m[i] == -INFINITY ? m[i] : m[i] * a.scale2, sum, j == 0 && g == 0);
+        }
+      } else {
+#pragma unroll
+        for (uint32_t j = 0; j < ND; ++j) *reinterpret_cast<f32x4 *>(part + row * D + 16 * j + 4 * g) = acc[i][j];
+        if (g == 0) {
+          part[M * D + row] = m[i] == -INFINITY ? m[i] : m[i] * a.scale2;
+          part[M * D + M + row] = sum;
+        }
+      }
+    }
+    if (sg.first == 0 && !whole) {
+      left_open = true;
+      if (threadIdx.x == 0) {
+        meta[0] = uint32_t((u + sg.n_units - 1) / per) - run + 1;
+        meta[1] = sg.r;
+        meta[2] = sg.token0;
+      }
+    }
+    u += sg.count;
   }
   if (!left_open && threadIdx.x == 0) meta[0] = 0;
 }
@@ -554,22 +845,23 @@ __global__ __launch_bounds__(AT_BLOCK) void k_attn_join(AttnArgs a) {
 
 uintptr_t addr(const void *p) { return reinterpret_cast<uintptr_t>(p); }
 
-// Row tiles of 16 * mt rows: 32 where a request has more than 16 rows for a
-// key/value head on average, or a group is wider than 16 heads.
-uint32_t tiles_of_16(uint64_t n_tok, uint32_t n_req, uint32_t grp) {
-  return grp > 16 || n_tok * grp > 16 * uint64_t(n_req) ? 2 : 1;
+// Rows of a row tile, by the rows that a request has for one key/value head on
+// average: 16 or 32 of k_attn_rows, 64 or 128 of k_attn_tiles.
+uint32_t tile_rows(uint64_t n_tok, uint32_t n_req, uint32_t grp) {
+  const uint64_t rows = std::max<uint64_t>(grp, n_tok * grp / std::max(1u, n_req));
+  return rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128;
 }
 
 struct Plan {
-  uint32_t mt, runs;
+  uint32_t rows, runs;
   uint64_t meta_bytes, bytes;
 };
 Plan plan_of(uint64_t n_tok, uint32_t n_req, uint32_t hq, uint32_t hk, uint32_t dim) {
   Plan p;
-  p.mt = tiles_of_16(n_tok, n_req, hq / hk);
+  p.rows = tile_rows(n_tok, n_req, hq / hk);
   p.runs = std::max(1u, AT_RUNS / hk);
   p.meta_bytes = (uint64_t(hk) * p.runs * 16 + 255) / 256 * 256;
-  p.bytes = p.meta_bytes + uint64_t(hk) * p.runs * 2 * (16 * p.mt) * (dim + 2) * sizeof(float);
+  p.bytes = p.meta_bytes + uint64_t(hk) * p.runs * 2 * p.rows * (dim + 2) * sizeof(float);
   return p;
 }
 
@@ -580,21 +872,23 @@ bool good_cache(const bbpe_paged_cache *c) {
          ((addr(c->k) | addr(c->v)) & 15) == 0 && ((c->page_stride | c->head_stride | c->token_stride) & 7) == 0;
 }
 bool good_heads(uint32_t hq, const bbpe_paged_cache *c) {
-  return hq >= 1 && hq % c->n_kv_heads == 0 && hq / c->n_kv_heads <= 32;
+  return hq >= 1 && hq % c->n_kv_heads == 0 && hq / c->n_kv_heads <= 128;
 }
 
-template <typename T, uint32_t D, uint32_t MT>
+template <typename T, uint32_t D, uint32_t M>
 void launch(const AttnArgs &a, hipStream_t st) {
-  k_attn_rows<T, D, MT><<<dim3(a.hk, a.runs), AT_BLOCK, 0, st>>>(a);
-  k_attn_join<T, D, 16 * MT><<<dim3(a.hk, a.runs, 16 * MT / AT_WAVES), AT_BLOCK, 0, st>>>(a);
+  const dim3 grid(a.hk, a.runs);
+  if constexpr (M <= 32) k_attn_rows<T, D, M / 16><<<grid, AT_BLOCK, 0, st>>>(a);
+  else k_attn_tiles<T, D, M / 64><<<grid, AT_BLOCK, 0, st>>>(a);
+  k_attn_join<T, D, M><<<dim3(a.hk, a.runs, M / AT_WAVES), AT_BLOCK, 0, st>>>(a);
 }
 template <typename T, uint32_t D>
-void launch_mt(const AttnArgs &a, uint32_t mt, hipStream_t st) {
-  mt == 1 ? launch<T, D, 1>(a, st) : launch<T, D, 2>(a, st);
+void launch_rows(const AttnArgs &a, uint32_t rows, hipStream_t st) {
+  rows == 16 ? launch<T, D, 16>(a, st) : rows == 32 ? launch<T, D, 32>(a, st) : rows == 64 ? launch<T, D, 64>(a, st) : launch<T, D, 128>(a, st);
 }
 template <typename T>
-void launch_dim(const AttnArgs &a, uint32_t dim, uint32_t mt, hipStream_t st) {
-  dim == 64 ? launch_mt<T, 64>(a, mt, st) : dim == 128 ? launch_mt<T, 128>(a, mt, st) : launch_mt<T, 256>(a, mt, st);
+void launch_dim(const AttnArgs &a, uint32_t dim, uint32_t rows, hipStream_t st) {
+  dim == 64 ? launch_rows<T, 64>(a, rows, st) : dim == 128 ? launch_rows<T, 128>(a, rows, st) : launch_rows<T, 256>(a, rows, st);
 }
 
 }  // namespace
@@ -645,7 +939,9 @@ int bbpe_tree_attention(const void *q, int64_t q_ts, int64_t q_hs, uint64_t n_to
   a.cap = table_width * cache->page_size;
   a.mask = d_tree_mask;
   a.words = mask_words;
-  a.scale2 = scale * 1.44269504088896340736f;
+  // 2^-120 for a scale of zero: every weight comes out one, and a masked score stays -inf
+  a.scale2 = scale == 0.0f ? 0x1p-120f : std::fabs(scale) * 1.44269504088896340736f;
+  a.flip = scale < 0.0f ? 0x80008000u : 0u;
   a.out = out;
   a.out_ts = out_ts;
   a.out_hs = out_hs;
@@ -654,7 +950,7 @@ int bbpe_tree_attention(const void *q, int64_t q_ts, int64_t q_hs, uint64_t n_to
   a.hq = n_q_heads;
   a.hk = cache->n_kv_heads;
   a.grp = a.hq / a.hk;
-  a.tok_log = uint32_t(31 - __builtin_clz(16 * p.mt / a.grp));
+  a.tok_log = uint32_t(31 - __builtin_clz(p.rows / a.grp));
   a.runs = p.runs;
   a.q_vec = ((addr(q) | uint64_t(q_ts * 2) | uint64_t(q_hs * 2)) & 15) == 0;
   a.out_vec = ((addr(out) | uint64_t(out_ts * 2) | uint64_t(out_hs * 2)) & 15) == 0;
@@ -666,8 +962,8 @@ int bbpe_tree_attention(const void *q, int64_t q_ts, int64_t q_hs, uint64_t n_to
     a.q_off = d_q_off + r0;
     a.ctx = d_ctx_len + r0;
     a.n_req = std::min(AT_REQ, n_req - r0);
-    if (cache->dtype == BBPE_BF16) launch_dim<__bf16>(a, cache->head_dim, p.mt, st);
-    else launch_dim<_Float16>(a, cache->head_dim, p.mt, st);
+    if (cache->dtype == BBPE_BF16) launch_dim<__bf16>(a, cache->head_dim, p.rows, st);
+    else launch_dim<_Float16>(a, cache->head_dim, p.rows, st);
   }
   return hipGetLastError() == hipSuccess ? BBPE_OK : BBPE_E_HIP;
 }

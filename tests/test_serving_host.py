@@ -98,7 +98,7 @@ def attn_call(c=None, **kw):
 
 
 @pytest.mark.parametrize("bad", [dict(q=None), dict(out=None), dict(table=None), dict(q_off=None), dict(ctx=None), dict(width=0),
-                                 dict(hq=3), dict(hq=0), dict(hq=66), dict(mask=X), dict(scale=float("inf")),
+                                 dict(hq=3), dict(hq=0), dict(hq=258), dict(mask=X), dict(scale=float("inf")),
                                  dict(scale=float("nan")), dict(stride=7), dict(width=1 << 27, stride=1 << 27), dict(q=X + 1),
                                  dict(lse=X + 2), dict(mask=X + 4, words=1), dict(cache=None), dict(n=1 << 31)])
 def test_attention_refuses(bad):
