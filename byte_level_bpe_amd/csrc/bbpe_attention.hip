@@ -4,8 +4,9 @@
 //   o_i = sum_j p_ij v_j / sum_j p_ij,  p_ij = exp2(s_ij - m_i),
 //   s_ij = scale * log2(e) * q_i . k_j  over the keys j that row i sees.
 //
-// Rows.  The query heads that share a key/value head are rows of one product:
-// a row tile holds M rows, a power of two of tokens times the group's heads.
+// Rows.  The query heads that share a key/value head are rows of one product,
+// M of them a row tile: the request's rows one after the other, or, in a chain,
+// where a tile ends with its last token's key, a power of two of whole tokens.
 //
 // Split.  A unit is one row tile times KT keys.  For every key/value head the
 // units of all requests, row tile after row tile, are laid in one line and cut
@@ -63,7 +64,8 @@ struct AttnArgs {
   float *lse;
   uint64_t n_tok;
   uint32_t hq, hk, grp;
-  uint32_t tok_log;        // log2 of a row tile's tokens
+  uint32_t tok_log;        // a chain: log2 of a row tile's tokens
+  uint32_t stride;         // rows of a row tile: M with masks, whole tokens in a chain
   uint32_t runs;           // workgroups of one head
   uint32_t q_vec, out_vec; // rows 16-byte aligned
   uint32_t *meta;          // [hk][runs][4]: the row tile that begins in a run and ends in a later one
@@ -110,7 +112,7 @@ __device__ __forceinline__ uint64_t units_before(const AttnArgs &a, const Length
   return uint64_t(t) * (whole + (rest ? 1 : 0)) + (steps << (a.tok_log - KT_LOG));
 }
 __device__ __forceinline__ uint32_t row_tiles(const AttnArgs &a, uint32_t n) {
-  return uint32_t((uint64_t(n) + (1u << a.tok_log) - 1) >> a.tok_log);
+  return (n * a.grp + a.stride - 1) / a.stride;
 }
 
 // Sums of the requests' units up to and with each, into LDS; returns the total.
@@ -142,7 +144,7 @@ __device__ __forceinline__ uint64_t scan_units(const AttnArgs &a, uint64_t *incl
 // The run's segments one after the other: which request, row tile and units.
 struct Segment {
   Lengths L;
-  uint32_t r, token0;      // request, the row tile's first token in it
+  uint32_t r, row0;        // request, the row tile's first row in it (row: token * group + head)
   uint32_t n_units, first, count;
   uint32_t klim, open;     // keys that any row of the tile sees, and those that all of them see
 };
@@ -168,10 +170,20 @@ __device__ __forceinline__ Segment segment_at(const AttnArgs &a, const uint64_t 
   s.n_units = uint32_t(units_before<KT_LOG>(a, s.L, t + 1) - tile_u);
   s.first = uint32_t(local - tile_u);
   s.count = uint32_t(min(uint64_t(s.n_units - s.first), u_end - u));
-  s.token0 = t << a.tok_log;
-  s.klim = a.mask ? s.L.klen : uint32_t(min(uint64_t(s.L.klen), uint64_t(s.L.ctx) + s.token0 + (1u << a.tok_log)));
+  s.row0 = t * a.stride;
+  s.klim = a.mask ? s.L.klen : uint32_t(min(uint64_t(s.L.klen), uint64_t(s.L.ctx) + (uint64_t(t + 1) << a.tok_log)));
   s.open = min(s.L.ctx, s.klim);
   return s;
+}
+
+// Row `row` of a segment's row tile: its token in the request and its head in the group.
+struct Row {
+  uint32_t token, h;
+  bool live;  // one of the tile's rows; else the tile's rows' last token stands in
+};
+__device__ __forceinline__ Row row_of(const AttnArgs &a, const Segment &s, uint32_t row) {
+  const uint32_t at = s.row0 + row, token = at / a.grp;
+  return Row{min(token, s.L.n - 1), at - token * a.grp, row < a.stride && token < s.L.n};
 }
 
 template <typename T> struct Mma;
@@ -180,31 +192,33 @@ template <> struct Mma<__bf16> {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(x, y, c, 0, 0, 0);
   }
   static constexpr uint32_t EXP = 0x7F80;  // exponent of infinities and NaN
-  static constexpr uint32_t ONE = 0x3F80;
 };
 template <> struct Mma<_Float16> {
   static __device__ __forceinline__ f32x4 mul(f16x8 x, f16x8 y, f32x4 c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_f16(x, y, c, 0, 0, 0);
   }
   static constexpr uint32_t EXP = 0x7C00;
-  static constexpr uint32_t ONE = 0x3C00;
 };
 
 __device__ __forceinline__ float sum8(f32x8 a) {
   return ((a[0] + a[1]) + (a[2] + a[3])) + ((a[4] + a[5]) + (a[6] + a[7]));
 }
 
-// The larger, and the sum, of the four lanes 16 apart, in all four.
-__device__ __forceinline__ float max3(float x, float y, float z) {
-  float r;
-  asm("v_max3_f32 %0, %1, %2, %3" : "=v"(r) : "v"(x), "v"(y), "v"(z));
-  return r;
+// The larger of two, as the middle of them and an infinity that the compiler
+// does not know for one: from fmaxf() it makes a maximum behind two more
+// instructions, which quiet a NaN in either.  (A NaN among the scores makes its
+// weight NaN, and with it the row, whatever the maximum is.)
+__device__ __forceinline__ float max2(float x, float y) {
+  float inf = INFINITY;
+  asm("" : "+s"(inf));
+  return __builtin_amdgcn_fmed3f(x, y, inf);
 }
+// The larger, and the sum, of the four lanes 16 apart, in all four.
 __device__ __forceinline__ float max_quarters(float x) {
   const auto p = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
-  x = fmaxf(__uint_as_float(p[0]), __uint_as_float(p[1]));
+  x = max2(__uint_as_float(p[0]), __uint_as_float(p[1]));
   const auto q = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
-  return fmaxf(__uint_as_float(q[0]), __uint_as_float(q[1]));
+  return max2(__uint_as_float(q[0]), __uint_as_float(q[1]));
 }
 __device__ __forceinline__ float sum_quarters(float x) {
   const auto p = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
@@ -270,38 +284,35 @@ __device__ __forceinline__ u32x4 turned(const T *p0, const T *p1) {
   return u32x4{u.x, u.y, v.x, v.y};
 }
 
-// Values that masked places may hold.  0 * inf is NaN, so infinities and NaN of
-// a tile with masked places leave the product, as flags (up: +inf or NaN, down:
-// -inf or NaN), and come back as what they add to the rows that see them.
+// Values that masked places may hold.  0 * inf is NaN, so infinities and NaN
+// leave the products of tiles with masked places (they become zeros), and
+// add_apart() adds them, at the end of a segment, to the rows that see them.
 template <typename T>
-__device__ __forceinline__ uint32_t apart_bits(uint32_t f) {  // bit 15 of each half: infinity or NaN
-  return ((f & 0x7FFF7FFFu) + (0x8000u - Mma<T>::EXP) * 0x10001u) & 0x80008000u;
+__device__ __forceinline__ uint32_t set_apart(uint32_t &f) {  // not 0: there were some
+  const uint32_t bad = ((f & 0x7FFF7FFFu) + (0x8000u - Mma<T>::EXP) * 0x10001u) & 0x80008000u;
+  f &= ~((bad >> 15) * 0xFFFFu);
+  return bad;
 }
-template <typename T>
-__device__ __forceinline__ void set_apart(u32x4 &f, u32x4 &up, u32x4 &down) {
+
+// place(v, seen) for each key of a tile: its values' row, and which of the
+// lane's rows (token[0..MT)) see it.
+template <typename T, uint32_t MT, typename F>
+__device__ void add_apart(const AttnArgs &a, const Segment &s, const char *vc, uint32_t from, uint32_t to, const uint32_t *token,
+                          F place) {
+  for (uint32_t key = from; key < to; ++key) {
+    const uint32_t page = uint32_t(a.table[uint64_t(s.r) * a.table_stride + (key >> a.page_shift)]);
+    if (page >= a.n_pages) continue;
+    const T *v = reinterpret_cast<const T *>(vc) + int64_t(page) * a.page_stride + int64_t(key & ((1u << a.page_shift) - 1)) * a.token_stride;
+    uint32_t seen = 0;
 #pragma unroll
-  for (uint32_t e = 0; e < 4; ++e) {
-    const uint32_t bad = apart_bits<T>(f[e]) >> 15, neg = f[e] >> 15 & 0x10001u;
-    const uint32_t nan = (((f[e] & 0x7FFF7FFFu) + (0x7FFFu - Mma<T>::EXP) * 0x10001u) & 0x80008000u) >> 15;
-    up[e] = (nan | (bad & ~neg)) * Mma<T>::ONE;
-    down[e] = (nan | (bad & neg)) * Mma<T>::ONE;
-    f[e] &= ~(bad * 0xFFFFu);
+    for (uint32_t i = 0; i < MT; ++i) seen |= (seen8(a, s.L, s.klim, key, token[i]) & 1) << i;
+    place(v, seen);
   }
 }
-// seen: bits of the eight keys of this lane
 template <typename T>
-__device__ __forceinline__ void add_apart(u32x4 up, u32x4 down, uint32_t seen, f32x4 &acc) {
-  typedef typename Vec8<T>::type T8;
-  u32x4 vis;
-#pragma unroll
-  for (uint32_t e = 0; e < 4; ++e) vis[e] = ((seen >> (2 * e) & 1) ? Mma<T>::ONE : 0) | ((seen >> (2 * e + 1) & 1) ? Mma<T>::ONE << 16 : 0);
-  const f32x4 plus = Mma<T>::mul(__builtin_bit_cast(T8, up), __builtin_bit_cast(T8, vis), f32x4{});
-  const f32x4 minus = Mma<T>::mul(__builtin_bit_cast(T8, down), __builtin_bit_cast(T8, vis), f32x4{});
-#pragma unroll
-  for (uint32_t e = 0; e < 4; ++e) {
-    if (plus[e] > 0.0f) acc[e] += INFINITY;
-    if (minus[e] > 0.0f) acc[e] -= INFINITY;
-  }
+__device__ __forceinline__ float apart(T v) {  // an infinity or NaN, or 0
+  const float x = float(v);
+  return (__builtin_bit_cast(uint16_t, v) & Mma<T>::EXP) == Mma<T>::EXP ? x : 0.0f;
 }
 
 template <typename T, uint32_t D, uint32_t MT>
@@ -332,7 +343,7 @@ __global__ __launch_bounds__(AT_BLOCK, (D * MT <= 128 ? 3 : D * MT <= 256 ? 2 : 
   while (u < u_end) {
     const Segment sg = segment_at<AT_KT_LOG>(a, s_incl, u, u_end);
     const Lengths &L = sg.L;
-    const uint32_t r = sg.r, n_units = sg.n_units, first = sg.first, count = sg.count, token0 = sg.token0;
+    const uint32_t r = sg.r, n_units = sg.n_units, first = sg.first, count = sg.count;
     const uint32_t klim = sg.klim, open = sg.open;
     const int32_t *pages = a.table + uint64_t(r) * a.table_stride;
 
@@ -341,11 +352,10 @@ __global__ __launch_bounds__(AT_BLOCK, (D * MT <= 128 ? 3 : D * MT <= 256 ? 2 : 
     uint32_t token[MT];
 #pragma unroll
     for (uint32_t i = 0; i < MT; ++i) {
-      const uint32_t row = 16 * i + n16, tl = row / a.grp;
-      token[i] = token0 + tl;
-      const bool live = tl < (1u << a.tok_log) && token[i] < L.n;
-      token[i] = min(token[i], L.n - 1);
-      const T *p = static_cast<const T *>(a.q) + (L.first + token[i]) * a.q_ts + int64_t(head * a.grp + row % a.grp) * a.q_hs;
+      const Row w = row_of(a, sg, 16 * i + n16);
+      const bool live = w.live;
+      token[i] = w.token;
+      const T *p = static_cast<const T *>(a.q) + (L.first + w.token) * a.q_ts + int64_t(head * a.grp + w.h) * a.q_hs;
 #pragma unroll
       for (uint32_t s = 0; s < NS; ++s) {
         q[i][s] = T8{};
@@ -362,6 +372,7 @@ __global__ __launch_bounds__(AT_BLOCK, (D * MT <= 128 ? 3 : D * MT <= 256 ? 2 : 
       for (uint32_t j = 0; j < VD; ++j) acc[i][j] = f32x4{};
     }
 
+    uint32_t odd_from = ~0u;  // this wave's first unit with infinities or NaN beside masked places
     for (uint32_t unit = first; unit < first + count; ++unit) {
       const uint32_t key0 = (unit << AT_KT_LOG) + wave * AT_TILE;
       if (key0 >= klim) break;
@@ -398,17 +409,15 @@ __global__ __launch_bounds__(AT_BLOCK, (D * MT <= 128 ? 3 : D * MT <= 256 ? 2 : 
       }
       // tiles in which some row does not see some key
       const bool part = key0 + AT_TILE > open || __any(!v_ok);
-      bool odd = false;  // masked places with infinities or NaN among the values
       if (part) {
         uint32_t bad = 0;
 #pragma unroll
         for (uint32_t e = 0; e < 8; ++e)
 #pragma unroll
-          for (uint32_t w = 0; w < VD / 2; ++w) bad |= apart_bits<T>(v[e][w]);
-        odd = __any(bad != 0);
+          for (uint32_t w = 0; w < VD / 2; ++w) bad |= set_apart<T>(v[e][w]);
+        if (__any(bad != 0)) odd_from = min(odd_from, unit);
       }
       T8 pf[MT];
-      uint32_t seen[MT];
 #pragma unroll
       for (uint32_t i = 0; i < MT; ++i) {
         f32x4 sa{}, sb{};
@@ -418,15 +427,14 @@ __global__ __launch_bounds__(AT_BLOCK, (D * MT <= 128 ? 3 : D * MT <= 256 ? 2 : 
           sb = Mma<T>::mul(kb8[s], q[i][s], sb);
         }
         float x[8] = {sa[0], sa[1], sa[2], sa[3], sb[0], sb[1], sb[2], sb[3]};
-        seen[i] = 0xFF;
         if (part) {
-          seen[i] = v_ok ? seen8(a, L, klim, kb, token[i]) : 0;
+          const uint32_t seen = v_ok ? seen8(a, L, klim, kb, token[i]) : 0;
 #pragma unroll
-          for (uint32_t e = 0; e < 8; ++e) x[e] = (seen[i] >> e & 1) ? x[e] : -INFINITY;
+          for (uint32_t e = 0; e < 8; ++e) x[e] = (seen >> e & 1) ? x[e] : -INFINITY;
         }
-        const float top = max_quarters(max3(max3(x[0], x[1], x[2]), max3(x[3], x[4], x[5]), fmaxf(x[6], x[7])));
+        const float top = max_quarters(max2(max2(max2(x[0], x[1]), max2(x[2], x[3])), max2(max2(x[4], x[5]), max2(x[6], x[7]))));
         if (__any(top > m[i])) {
-          const float m_new = fmaxf(m[i], top);
+          const float m_new = max2(m[i], top);
           const float f = m_new == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f((m[i] - m_new) * a.scale2);
           m[i] = m_new;
           l[i] *= f;
@@ -452,18 +460,28 @@ __global__ __launch_bounds__(AT_BLOCK, (D * MT <= 128 ? 3 : D * MT <= 256 ? 2 : 
         }
 #pragma unroll
         for (uint32_t half = 0; half < 2; ++half) {
-          u32x4 f = half ? f1 : f0;
-          if (odd) {
-            u32x4 up, down;
-            set_apart<T>(f, up, down);
-#pragma unroll
-            for (uint32_t i = 0; i < MT; ++i) add_apart<T>(up, down, seen[i], acc[i][2 * w + half]);
-          }
+          const u32x4 f = half ? f1 : f0;
 #pragma unroll
           for (uint32_t i = 0; i < MT; ++i)
             acc[i][2 * w + half] = Mma<T>::mul(__builtin_bit_cast(T8, f), pf[i], acc[i][2 * w + half]);
         }
       }
+    }
+
+    for (uint32_t unit = odd_from; unit < first + count; ++unit) {
+      const uint32_t key0 = (unit << AT_KT_LOG) + wave * AT_TILE;
+      if (key0 >= klim) break;
+      if (!__any(!(uint32_t(pages[min(key0 + 8 * g, klim - 1) >> a.page_shift]) < a.n_pages)) && key0 + AT_TILE <= open) continue;
+      add_apart<T, MT>(a, sg, vc, key0, min(key0 + AT_TILE, klim), token, [&](const T *v, uint32_t seen) {
+#pragma unroll
+        for (uint32_t j = 0; j < VD; ++j)
+#pragma unroll
+          for (uint32_t e = 0; e < 4; ++e) {
+            const float x = apart(v[(4 * g + e) * VD + j]);
+#pragma unroll
+            for (uint32_t i = 0; i < MT; ++i) acc[i][j][e] += (seen >> i & 1) ? x : 0.0f;
+          }
+      });
     }
 
     // the waves' sums join: [wave][row][element]
@@ -503,11 +521,11 @@ __global__ __launch_bounds__(AT_BLOCK, (D * MT <= 128 ? 3 : D * MT <= 256 ? 2 : 
 #pragma unroll
           for (uint32_t j = 0; j < JC; ++j) o[j] += s_o[w][jr][jd * JC + j] * f;
         }
-        const uint32_t tl = row / a.grp, tok = token0 + tl, d = jd * VD + j0;
-        if (tl >= (1u << a.tok_log) || tok >= L.n) continue;
+        const uint32_t d = jd * VD + j0;
+        const Row w = row_of(a, sg, row);
+        if (!w.live) continue;
         if (whole) {
-          const uint32_t h = head * a.grp + row % a.grp;
-          finish<T, JC>(a, L.first + tok, h, d, o, top, sum, d == 0);
+          finish<T, JC>(a, L.first + w.token, head * a.grp + w.h, d, o, top, sum, d == 0);
         } else {
 #pragma unroll
           for (uint32_t j = 0; j < JC; ++j) part[row * D + d + j] = o[j];
@@ -524,7 +542,7 @@ __global__ __launch_bounds__(AT_BLOCK, (D * MT <= 128 ? 3 : D * MT <= 256 ? 2 : 
       if (threadIdx.x == 0) {
         meta[0] = uint32_t((u + n_units - 1) / per) - run + 1;  // parts
         meta[1] = r;
-        meta[2] = token0;
+        meta[2] = sg.row0;
       }
     }
     u += count;
@@ -564,6 +582,7 @@ __global__ __launch_bounds__(AT_BLOCK, 2) void k_attn_tiles(AttnArgs a) {
   __shared__ __attribute__((aligned(1024))) T s_v[2][KT * D];
   __shared__ uint64_t s_incl[AT_REQ];
   __shared__ uint64_t s_scan[2 * AT_BLOCK / 64 + 1];
+  __shared__ uint32_t s_odd;  // the segment has infinities or NaN in tiles with masked places
 
   const uint32_t head = blockIdx.x, run = blockIdx.y;
   const uint32_t lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), n16 = lane & 15, g = lane >> 4;
@@ -580,6 +599,18 @@ __global__ __launch_bounds__(AT_BLOCK, 2) void k_attn_tiles(AttnArgs a) {
   int64_t off[LPG];
 #pragma unroll
   for (uint32_t i = 0; i < LPG; ++i) off[i] = int64_t(i * RPI + lane / CH) * a.token_stride * int64_t(sizeof(T)) + 16 * (lane % CH);
+  // its places in the fragments' reads of a tile: K's row 16 k + n16, V's rows
+  // 32 k + 4 g + n16 / 4 and + 16 (four lanes read 32 bytes of a row), both with
+  // chunks that repeat within the row steps
+  constexpr uint32_t VA = ND < 8 ? ND : 8;
+  uint32_t k_at[NS], v_at[VA];
+#pragma unroll
+  for (uint32_t e = 0; e < NS; ++e) k_at[e] = n16 * D + 8 * k_chunk<D>(n16, 4 * e + g);
+#pragma unroll
+  for (uint32_t j = 0; j < VA; ++j) {
+    const uint32_t row = 4 * g + (n16 >> 2);
+    v_at[j] = row * D + 8 * v_chunk<D>(row, 2 * j + (n16 >> 1 & 1)) + 4 * (n16 & 1);
+  }
 
   while (u < u_end) {
     const Segment sg = segment_at<KT_LOG>(a, s_incl, u, u_end);
@@ -590,12 +621,11 @@ __global__ __launch_bounds__(AT_BLOCK, 2) void k_attn_tiles(AttnArgs a) {
     bool any = false;  // a row of this wave's is one of the tile's
 #pragma unroll
     for (uint32_t i = 0; i < MT; ++i) {
-      const uint32_t row = 16 * (wave * MT + i) + n16, tl = row / a.grp;
-      token[i] = sg.token0 + tl;
-      const bool live = tl < (1u << a.tok_log) && token[i] < L.n;
+      const Row w = row_of(a, sg, 16 * (wave * MT + i) + n16);
+      const bool live = w.live;
       any |= live;
-      token[i] = min(token[i], L.n - 1);
-      const T *p = static_cast<const T *>(a.q) + (L.first + token[i]) * a.q_ts + int64_t(head * a.grp + row % a.grp) * a.q_hs;
+      token[i] = w.token;
+      const T *p = static_cast<const T *>(a.q) + (L.first + w.token) * a.q_ts + int64_t(head * a.grp + w.h) * a.q_hs;
 #pragma unroll
       for (uint32_t s = 0; s < NS; ++s) {
         q[i][s] = T8{};
@@ -638,7 +668,19 @@ __global__ __launch_bounds__(AT_BLOCK, 2) void k_attn_tiles(AttnArgs a) {
         *reinterpret_cast<u32x4 *>(s_k[buf] + row * D + 8 * k_chunk<D>(row, lane % CH)) = way[i];
       }
     };
-    const auto place_v = [&](uint32_t buf) {
+    const auto place_v = [&](uint32_t buf, bool part) {
+      if (part) {
+        uint32_t bad = 0;
+#pragma unroll
+        for (uint32_t i = 0; i < GROUPS * LPG; ++i)
+#pragma unroll
+          for (uint32_t e = 0; e < 4; ++e) {
+            uint32_t f = way[i][e];
+            bad |= set_apart<T>(f);
+            way[i][e] = f;
+          }
+        if (__any(bad != 0)) s_odd = 1;  // (every wave that finds some writes the same)
+      }
 #pragma unroll
       for (uint32_t i = 0; i < GROUPS * LPG; ++i) {
         const uint32_t row = wave * ROWS + i * RPI + lane / CH;
@@ -648,13 +690,17 @@ __global__ __launch_bounds__(AT_BLOCK, 2) void k_attn_tiles(AttnArgs a) {
     int32_t page = 0;
     uint32_t hidden_next = 0;  // groups of eight keys whose page is not in the cache
     const auto hidden_of = [&](int32_t p) { return ~uint32_t(__ballot(uint32_t(p) < a.n_pages)) & ((1u << (KT / 8)) - 1); };
+    // tiles in which some row does not see some key
+    const auto in_part = [&](uint32_t unit, uint32_t hidden) { return ((unit + 1) << KT_LOG) > sg.open || hidden; };
+    if (threadIdx.x == 0) s_odd = 0;
+    __syncthreads();
     if (sg.first < unit_end) {
       page = pages_of(sg.first);
       fetch(kc, sg.first, page);
       place_k(0);
       fetch(vc, sg.first, page);
-      place_v(0);
       hidden_next = hidden_of(page);
+      place_v(0, in_part(sg.first, hidden_next));
       if (sg.first + 1 < unit_end) page = pages_of(sg.first + 1);
     }
     for (uint32_t unit = sg.first; unit < unit_end; ++unit) {
@@ -664,9 +710,8 @@ __global__ __launch_bounds__(AT_BLOCK, 2) void k_attn_tiles(AttnArgs a) {
       __syncthreads();  // this tile is there, and every wave is done with the other
       if (more) fetch(kc, unit + 1, page);
       const uint32_t key0 = unit << KT_LOG;
-      const bool part = key0 + KT > sg.open || hidden;
+      const bool part = in_part(unit, hidden);
       f32x4 s[MT][KT / 16];
-      uint64_t seen[MT];
       if (any) {
 #pragma unroll
         for (uint32_t k = 0; k < KT / 16; ++k) {
@@ -674,40 +719,46 @@ __global__ __launch_bounds__(AT_BLOCK, 2) void k_attn_tiles(AttnArgs a) {
           for (uint32_t i = 0; i < MT; ++i) s[i][k] = f32x4{};
 #pragma unroll
           for (uint32_t e = 0; e < NS; ++e) {
-            const uint32_t row = 16 * k + n16;
-            const T8 f = *reinterpret_cast<const T8 *>(s_k[buf] + row * D + 8 * k_chunk<D>(row, 4 * e + g));
+            const T8 f = *reinterpret_cast<const T8 *>(s_k[buf] + k_at[e] + 16 * k * D);
 #pragma unroll
             for (uint32_t i = 0; i < MT; ++i) s[i][k] = Mma<T>::mul(f, q[i][e], s[i][k]);
           }
         }
+        if (part) {
 #pragma unroll
-        for (uint32_t i = 0; i < MT; ++i) {
-          seen[i] = 0;
-          if (part) {
-            // a lane's keys are 16 k + 4 g ..+3: its bits are gathered four at a time
+          for (uint32_t i = 0; i < MT; ++i)
 #pragma unroll
             for (uint32_t k = 0; k < KT / 16; ++k) {
+              // a lane's keys are 16 k + 4 g ..+3
               const uint32_t at = 16 * k + 8 * (g >> 1);
-              const uint32_t b = (hidden >> (at >> 3) & 1) ? 0 : seen8(a, L, sg.klim, key0 + at, token[i]);
-              seen[i] |= uint64_t(b >> (4 * (g & 1)) & 15) << (4 * k);
+              const uint32_t seen = ((hidden >> (at >> 3) & 1) ? 0 : seen8(a, L, sg.klim, key0 + at, token[i])) >> (4 * (g & 1));
+#pragma unroll
+              for (uint32_t e = 0; e < 4; ++e) s[i][k][e] = (seen >> e & 1) ? s[i][k][e] : -INFINITY;
             }
+        }
+        float top[MT];
+        bool more_top = false;
 #pragma unroll
-            for (uint32_t k = 0; k < KT / 16; ++k)
+        for (uint32_t i = 0; i < MT; ++i) {
+          top[i] = -INFINITY;
 #pragma unroll
-              for (uint32_t e = 0; e < 4; ++e) s[i][k][e] = (seen[i] >> (4 * k + e) & 1) ? s[i][k][e] : -INFINITY;
-          }
-          float top = fmaxf(s[i][0][0], s[i][0][1]);
+          for (uint32_t k = 0; k < KT / 16; ++k) top[i] = max2(top[i], max2(max2(s[i][k][0], s[i][k][1]), max2(s[i][k][2], s[i][k][3])));
+          top[i] = max_quarters(top[i]);
+          more_top |= top[i] > m[i];
+        }
+        if (__any(more_top)) {
 #pragma unroll
-          for (uint32_t e = 2; e < KT / 4; e += 2) top = max3(top, s[i][e / 4][e % 4], s[i][e / 4][e % 4 + 1]);
-          top = max_quarters(top);
-          if (__any(top > m[i])) {
-            const float m_new = fmaxf(m[i], top);
+          for (uint32_t i = 0; i < MT; ++i) {
+            const float m_new = max2(m[i], top[i]);
             const float f = m_new == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f((m[i] - m_new) * a.scale2);
             m[i] = m_new;
             l[i] *= f;
 #pragma unroll
             for (uint32_t j = 0; j < ND; ++j) acc[i][j] *= f;
           }
+        }
+#pragma unroll
+        for (uint32_t i = 0; i < MT; ++i) {
           const float base = m[i] == -INFINITY ? 0.0f : m[i] * a.scale2;
 #pragma unroll
           for (uint32_t k = 0; k < KT / 16; ++k) {
@@ -724,48 +775,58 @@ __global__ __launch_bounds__(AT_BLOCK, 2) void k_attn_tiles(AttnArgs a) {
         if (unit + 2 < unit_end) page = pages_of(unit + 2);
       }
       if (any) {
+        const auto weights = [&](uint32_t i, uint32_t k) {
+          const f32x4 x = s[i][2 * k], y = s[i][2 * k + 1];
+          return from_float<T>(f32x8{x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]});
+        };
+        const auto values = [&](uint32_t j, uint32_t k) {
+          const T *p = s_v[buf] + v_at[j % 8] + 128 * (j / 8) + 32 * k * D;
+          return turned(p, p + 16 * D);
+        };
 #pragma unroll
         for (uint32_t k = 0; k < KT / 32; ++k) {
           T8 pf[MT];
 #pragma unroll
-          for (uint32_t i = 0; i < MT; ++i) {
-            const f32x4 x = s[i][2 * k], y = s[i][2 * k + 1];
-            pf[i] = from_float<T>(f32x8{x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]});
-          }
+          for (uint32_t i = 0; i < MT; ++i) pf[i] = weights(i, k);
 #pragma unroll
           for (uint32_t j = 0; j < ND; ++j) {
-            // values 32 k + 4 g ..+3 and + 16 of elements 16 j ..+15: four lanes read a row's 32 bytes
-            const uint32_t row = 32 * k + 4 * g + (n16 >> 2), c = 2 * j + (n16 >> 1 & 1);
-            const T *p = s_v[buf] + row * D + 4 * (n16 & 1);
-            u32x4 f = turned(p + 8 * v_chunk<D>(row, c), p + 16 * D + 8 * v_chunk<D>(row + 16, c));
-            if (part && __any((apart_bits<T>(f[0]) | apart_bits<T>(f[1]) | apart_bits<T>(f[2]) | apart_bits<T>(f[3])) != 0)) {
-              u32x4 up, down;
-              set_apart<T>(f, up, down);
+            const T8 f = __builtin_bit_cast(T8, values(j, k));
 #pragma unroll
-              for (uint32_t i = 0; i < MT; ++i) add_apart<T>(up, down, uint32_t(seen[i] >> (8 * k)) & 0xFF, acc[i][j]);
-            }
-#pragma unroll
-            for (uint32_t i = 0; i < MT; ++i) acc[i][j] = Mma<T>::mul(__builtin_bit_cast(T8, f), pf[i], acc[i][j]);
+            for (uint32_t i = 0; i < MT; ++i) acc[i][j] = Mma<T>::mul(f, pf[i], acc[i][j]);
           }
         }
       }
-      if (more) place_v(buf ^ 1);
+      if (more) place_v(buf ^ 1, in_part(unit + 1, hidden_next));
     }
-    __syncthreads();  // the next segment's first tile goes to the first buffer
+    __syncthreads();  // s_odd is settled, and both buffers are free for the next segment
+    if (s_odd && any)
+      for (uint32_t unit = sg.first; unit < unit_end; ++unit)
+        if (in_part(unit, hidden_of(pages_of(unit))))
+          add_apart<T, MT>(a, sg, vc, unit << KT_LOG, min((unit + 1) << KT_LOG, sg.klim), token, [&](const T *v, uint32_t seen) {
+#pragma unroll
+            for (uint32_t j = 0; j < ND; ++j)
+#pragma unroll
+              for (uint32_t e = 0; e < 4; ++e) {
+                const float x = apart(v[16 * j + 4 * g + e]);
+#pragma unroll
+                for (uint32_t i = 0; i < MT; ++i) acc[i][j][e] += (seen >> i & 1) ? x : 0.0f;
+              }
+          });
+    __syncthreads();  // s_odd has been read
 
     const bool whole = sg.first == 0 && sg.count == sg.n_units;
     float *part = a.part + ((uint64_t(head) * a.runs + run) * 2 + (sg.first == 0 ? 1 : 0)) * (M * (D + 2));
 #pragma unroll
     for (uint32_t i = 0; i < MT; ++i) {
       const float sum = sum_quarters(l[i]);
-      const uint32_t row = 16 * (wave * MT + i) + n16, tl = row / a.grp, tok = sg.token0 + tl;
-      if (tl >= (1u << a.tok_log) || tok >= L.n) continue;
+      const uint32_t row = 16 * (wave * MT + i) + n16;
+      const Row w = row_of(a, sg, row);
+      if (!w.live) continue;
       if (whole) {
-        const uint32_t h = head * a.grp + row % a.grp;
 #pragma unroll
         for (uint32_t j = 0; j < ND; ++j) {
           const float o[4] = {acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]};
-          finish<T, 4>(a, L.first + tok, h, 16 * j + 4 * g, o, m[i] == -INFINITY ? m[i] : m[i] * a.scale2, sum, j == 0 && g == 0);
+          finish<T, 4>(a, L.first + w.token, head * a.grp + w.h, 16 * j + 4 * g, o, m[i] == -INFINITY ? m[i] : m[i] * a.scale2, sum, j == 0 && g == 0);
         }
       } else {
 #pragma unroll
@@ -781,7 +842,7 @@ __global__ __launch_bounds__(AT_BLOCK, 2) void k_attn_tiles(AttnArgs a) {
       if (threadIdx.x == 0) {
         meta[0] = uint32_t((u + sg.n_units - 1) / per) - run + 1;
         meta[1] = sg.r;
-        meta[2] = sg.token0;
+        meta[2] = sg.row0;
       }
     }
     u += sg.count;
@@ -799,9 +860,11 @@ __global__ __launch_bounds__(AT_BLOCK) void k_attn_join(AttnArgs a) {
   const uint32_t *meta = a.meta + (uint64_t(head) * a.runs + run) * 4;
   const uint32_t n = meta[0];
   if (n == 0) return;
-  const Lengths L = lengths_of(a, meta[1]);
-  const uint32_t tl = row / a.grp, tok = meta[2] + tl;
-  if (tl >= (1u << a.tok_log) || tok >= L.n) return;
+  Segment sg;
+  sg.L = lengths_of(a, meta[1]);
+  sg.row0 = meta[2];
+  const Row own = row_of(a, sg, row);
+  if (!own.live) return;
   // the first part is this run's second place, the others the first places of the runs after it
   constexpr uint64_t SIZE = M * (D + 2);
   const float *base = a.part + (uint64_t(head) * a.runs + run) * 2 * SIZE;
@@ -840,7 +903,7 @@ __global__ __launch_bounds__(AT_BLOCK) void k_attn_join(AttnArgs a) {
       }
     }
   }
-  finish<T, N>(a, L.first + tok, head * a.grp + row % a.grp, lane * N, o, top, sum, lane == 0);
+  finish<T, N>(a, sg.L.first + own.token, head * a.grp + own.h, lane * N, o, top, sum, lane == 0);
 }
 
 uintptr_t addr(const void *p) { return reinterpret_cast<uintptr_t>(p); }
@@ -913,7 +976,7 @@ int bbpe_tree_attention(const void *q, int64_t q_ts, int64_t q_hs, uint64_t n_to
                         int64_t out_hs, float *d_lse, void *d_workspace, uint64_t workspace_bytes,
                         void *hip_stream) {
   if (!good_cache(cache) || !good_heads(n_q_heads, cache)) return BBPE_E_INVALID_ARG;
-  if (n_tokens > 0x7FFFFFFFull || !std::isfinite(scale) || (n_req > 1 && table_stride < table_width) ||
+  if (n_tokens > 0x7FFFFFFFull || n_tokens * (n_q_heads / cache->n_kv_heads) > 0x7FFFFFFFull || !std::isfinite(scale) || (n_req > 1 && table_stride < table_width) ||
       uint64_t(table_width) * cache->page_size > 0x7FFFFFFFull)
     return BBPE_E_INVALID_ARG;
   if (n_tokens == 0 || n_req == 0) return BBPE_OK;
@@ -951,6 +1014,7 @@ int bbpe_tree_attention(const void *q, int64_t q_ts, int64_t q_hs, uint64_t n_to
   a.hk = cache->n_kv_heads;
   a.grp = a.hq / a.hk;
   a.tok_log = uint32_t(31 - __builtin_clz(p.rows / a.grp));
+  a.stride = d_tree_mask ? p.rows : a.grp << a.tok_log;
   a.runs = p.runs;
   a.q_vec = ((addr(q) | uint64_t(q_ts * 2) | uint64_t(q_hs * 2)) & 15) == 0;
   a.out_vec = ((addr(out) | uint64_t(out_ts * 2) | uint64_t(out_hs * 2)) & 15) == 0;
