@@ -172,7 +172,8 @@ __device__ __forceinline__ Segment segment_at(const AttnArgs &a, const uint64_t 
   s.count = uint32_t(min(uint64_t(s.n_units - s.first), u_end - u));
   s.row0 = t * a.stride;
   s.klim = a.mask ? s.L.klen : uint32_t(min(uint64_t(s.L.klen), uint64_t(s.L.ctx) + (uint64_t(t + 1) << a.tok_log)));
-  s.open = min(s.L.ctx, s.klim);
+  // (a chain's rows all see the keys up to the tile's first token's)
+  s.open = a.mask ? min(s.L.ctx, s.klim) : uint32_t(min(uint64_t(s.klim), uint64_t(s.L.ctx) + (uint64_t(t) << a.tok_log) + 1));
   return s;
 }
 
@@ -553,8 +554,10 @@ __global__ __launch_bounds__(AT_BLOCK, (D * MT <= 128 ? 3 : D * MT <= 256 ? 2 : 
 // Row tiles of 64 * MT rows.  With this many rows the products, not the cache,
 // take the time, and what counts is how often K and V pass from memory to the
 // registers: a workgroup's waves take 16 * MT rows each of one row tile and
-// share its tiles of KT keys in LDS, two of them: while one is read, the next
-// one's rows are on their way through registers, first K's, then V's.  The products are
+// share its tiles of KT keys in LDS, two of them, one read while the next is on
+// its way (from global memory to LDS without registers between; the two are
+// variables of their own, so that the compiler sees that reads of one need not
+// wait for the other).  The products are
 // k_attn_rows'; V's fragment comes turned over from LDS by the transposing
 // reads.  16-byte chunks of a row are stored at (chunk XOR a function of the
 // row), so that 16 rows at one chunk, and 16 rows by four, fall on different
@@ -578,8 +581,7 @@ __global__ __launch_bounds__(AT_BLOCK, 2) void k_attn_tiles(AttnArgs a) {
   constexpr uint32_t ROWS = KT / AT_WAVES;   // rows that a wave fetches, in groups of 8 (of one page each)
   constexpr uint32_t GROUPS = ROWS / 8, LPG = 8 / RPI;
   constexpr uint32_t M = 64 * MT;
-  __shared__ __attribute__((aligned(1024))) T s_k[2][KT * D];
-  __shared__ __attribute__((aligned(1024))) T s_v[2][KT * D];
+  __shared__ __attribute__((aligned(1024))) T s_k0[KT * D], s_k1[KT * D], s_v0[KT * D], s_v1[KT * D];
   __shared__ uint64_t s_incl[AT_REQ];
   __shared__ uint64_t s_scan[2 * AT_BLOCK / 64 + 1];
   __shared__ uint32_t s_odd;  // the segment has infinities or NaN in tiles with masked places
@@ -595,10 +597,17 @@ __global__ __launch_bounds__(AT_BLOCK, 2) void k_attn_tiles(AttnArgs a) {
   const char *kc = a.kc + int64_t(head) * a.head_stride * int64_t(sizeof(T));
   const char *vc = a.vc + int64_t(head) * a.head_stride * int64_t(sizeof(T));
   const uint32_t in_page = (1u << a.page_shift) - 1;
-  // a lane's rows and chunk in its loads: row i * RPI + lane / CH of a group of eight
-  int64_t off[LPG];
+  // a lane's sources in its loads to LDS, from a group of eight rows' first on:
+  // row i * RPI + lane / CH of the group, and the chunk whose place is lane % CH
+  uint32_t k_from[GROUPS][LPG], v_from[LPG];
 #pragma unroll
-  for (uint32_t i = 0; i < LPG; ++i) off[i] = int64_t(i * RPI + lane / CH) * a.token_stride * int64_t(sizeof(T)) + 16 * (lane % CH);
+  for (uint32_t i = 0; i < LPG; ++i) {
+    const uint32_t row = i * RPI + lane / CH;
+    v_from[i] = row * uint32_t(a.token_stride) * uint32_t(sizeof(T)) + 16 * v_chunk<D>(row, lane % CH);
+#pragma unroll
+    for (uint32_t gi = 0; gi < GROUPS; ++gi)
+      k_from[gi][i] = row * uint32_t(a.token_stride) * uint32_t(sizeof(T)) + 16 * k_chunk<D>(8 * (wave * GROUPS + gi) + row, lane % CH);
+  }
   // its places in the fragments' reads of a tile: K's row 16 k + n16, V's rows
   // 32 k + 4 g + n16 / 4 and + 16 (four lanes read 32 bytes of a row), both with
   // chunks that repeat within the row steps
@@ -649,43 +658,40 @@ __global__ __launch_bounds__(AT_BLOCK, 2) void k_attn_tiles(AttnArgs a) {
       const uint32_t key = (unit << KT_LOG) + 8 * (lane & (KT / 8 - 1));
       return pages[min(key, sg.klim - 1) >> a.page_shift];
     };
-    // its rows of K or of V on their way: global memory to registers, registers to LDS
-    u32x4 way[GROUPS * LPG];
-    const auto fetch = [&](const char *base, uint32_t unit, int32_t page) {
+    // this wave's rows of a tile, on their way to LDS
+    const auto fetch = [&](uint32_t unit, int32_t page, T *k_to, T *v_to) {
 #pragma unroll
       for (uint32_t gi = 0; gi < GROUPS; ++gi) {
         const uint32_t group = wave * GROUPS + gi, key = (unit << KT_LOG) + 8 * group;
         const uint32_t p = uint32_t(__builtin_amdgcn_readlane(page, int(group)));
-        const char *at = base + (int64_t(p < a.n_pages ? p : 0) * a.page_stride + int64_t(key & in_page) * a.token_stride) * int64_t(sizeof(T));
+        const int64_t at = (int64_t(p < a.n_pages ? p : 0) * a.page_stride + int64_t(key & in_page) * a.token_stride) * int64_t(sizeof(T));
 #pragma unroll
-        for (uint32_t i = 0; i < LPG; ++i) way[gi * LPG + i] = *reinterpret_cast<const u32x4 *>(at + off[i]);
+        for (uint32_t i = 0; i < LPG; ++i) {
+          typedef const __attribute__((address_space(1))) void *from;
+          typedef __attribute__((address_space(3))) void *to;
+          __builtin_amdgcn_global_load_lds((from)(kc + at + k_from[gi][i]), (to)(k_to + (8 * group + i * RPI) * D), 16, 0, 0);
+          __builtin_amdgcn_global_load_lds((from)(vc + at + v_from[i]), (to)(v_to + (8 * group + i * RPI) * D), 16, 0, 0);
+        }
       }
     };
-    const auto place_k = [&](uint32_t buf) {
+    // its rows of V in a tile with masked places, once they are there
+    const auto clean = [&](T *v) {
+      uint32_t bad = 0;
 #pragma unroll
-      for (uint32_t i = 0; i < GROUPS * LPG; ++i) {
-        const uint32_t row = wave * ROWS + i * RPI + lane / CH;
-        *reinterpret_cast<u32x4 *>(s_k[buf] + row * D + 8 * k_chunk<D>(row, lane % CH)) = way[i];
+      for (uint32_t i = 0; i < ROWS / RPI; ++i) {
+        u32x4 *p = reinterpret_cast<u32x4 *>(v + wave * ROWS * D) + 64 * i + lane;
+        u32x4 f = *p;
+        uint32_t here = 0;
+#pragma unroll
+        for (uint32_t e = 0; e < 4; ++e) {
+          uint32_t w = f[e];
+          here |= set_apart<T>(w);
+          f[e] = w;
+        }
+        if (here) *p = f;
+        bad |= here;
       }
-    };
-    const auto place_v = [&](uint32_t buf, bool part) {
-      if (part) {
-        uint32_t bad = 0;
-#pragma unroll
-        for (uint32_t i = 0; i < GROUPS * LPG; ++i)
-#pragma unroll
-          for (uint32_t e = 0; e < 4; ++e) {
-            uint32_t f = way[i][e];
-            bad |= set_apart<T>(f);
-            way[i][e] = f;
-          }
-        if (__any(bad != 0)) s_odd = 1;  // (every wave that finds some writes the same)
-      }
-#pragma unroll
-      for (uint32_t i = 0; i < GROUPS * LPG; ++i) {
-        const uint32_t row = wave * ROWS + i * RPI + lane / CH;
-        *reinterpret_cast<u32x4 *>(s_v[buf] + row * D + 8 * v_chunk<D>(row, lane % CH)) = way[i];
-      }
+      if (__any(bad != 0)) s_odd = 1;  // (every wave that finds some writes the same)
     };
     int32_t page = 0;
     uint32_t hidden_next = 0;  // groups of eight keys whose page is not in the cache
@@ -696,30 +702,32 @@ __global__ __launch_bounds__(AT_BLOCK, 2) void k_attn_tiles(AttnArgs a) {
     __syncthreads();
     if (sg.first < unit_end) {
       page = pages_of(sg.first);
-      fetch(kc, sg.first, page);
-      place_k(0);
-      fetch(vc, sg.first, page);
+      fetch(sg.first, page, s_k0, s_v0);
       hidden_next = hidden_of(page);
-      place_v(0, in_part(sg.first, hidden_next));
       if (sg.first + 1 < unit_end) page = pages_of(sg.first + 1);
     }
-    for (uint32_t unit = sg.first; unit < unit_end; ++unit) {
-      const uint32_t buf = (unit - sg.first) & 1;
-      const bool more = unit + 1 < unit_end;
+    const auto step = [&](uint32_t unit, const T *s_k, T *s_v, T *k_next, T *v_next) {
       const uint32_t hidden = hidden_next;
-      __syncthreads();  // this tile is there, and every wave is done with the other
-      if (more) fetch(kc, unit + 1, page);
+      __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0): this wave's rows are there
+      if (in_part(unit, hidden)) clean(s_v);
+      __syncthreads();                     // everybody's are, and everybody is done with the other tile
+      if (unit + 1 < unit_end) {
+        fetch(unit + 1, page, k_next, v_next);
+        hidden_next = hidden_of(page);
+        if (unit + 2 < unit_end) page = pages_of(unit + 2);
+      }
+      if (!any) return;
       const uint32_t key0 = unit << KT_LOG;
       const bool part = in_part(unit, hidden);
       f32x4 s[MT][KT / 16];
-      if (any) {
+      {
 #pragma unroll
         for (uint32_t k = 0; k < KT / 16; ++k) {
 #pragma unroll
           for (uint32_t i = 0; i < MT; ++i) s[i][k] = f32x4{};
 #pragma unroll
           for (uint32_t e = 0; e < NS; ++e) {
-            const T8 f = *reinterpret_cast<const T8 *>(s_k[buf] + k_at[e] + 16 * k * D);
+            const T8 f = *reinterpret_cast<const T8 *>(s_k + k_at[e] + 16 * k * D);
 #pragma unroll
             for (uint32_t i = 0; i < MT; ++i) s[i][k] = Mma<T>::mul(f, q[i][e], s[i][k]);
           }
@@ -768,19 +776,13 @@ __global__ __launch_bounds__(AT_BLOCK, 2) void k_attn_tiles(AttnArgs a) {
           }
         }
       }
-      if (more) {
-        place_k(buf ^ 1);
-        fetch(vc, unit + 1, page);
-        hidden_next = hidden_of(page);
-        if (unit + 2 < unit_end) page = pages_of(unit + 2);
-      }
-      if (any) {
+      {
         const auto weights = [&](uint32_t i, uint32_t k) {
           const f32x4 x = s[i][2 * k], y = s[i][2 * k + 1];
           return from_float<T>(f32x8{x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]});
         };
         const auto values = [&](uint32_t j, uint32_t k) {
-          const T *p = s_v[buf] + v_at[j % 8] + 128 * (j / 8) + 32 * k * D;
+          const T *p = s_v + v_at[j % 8] + 128 * (j / 8) + 32 * k * D;
           return turned(p, p + 16 * D);
         };
 #pragma unroll
@@ -796,7 +798,10 @@ __global__ __launch_bounds__(AT_BLOCK, 2) void k_attn_tiles(AttnArgs a) {
           }
         }
       }
-      if (more) place_v(buf ^ 1, in_part(unit + 1, hidden_next));
+    };
+    for (uint32_t unit = sg.first; unit < unit_end; unit += 2) {
+      step(unit, s_k0, s_v0, s_k1, s_v1);
+      if (unit + 1 < unit_end) step(unit + 1, s_k1, s_v1, s_k0, s_v0);
     }
     __syncthreads();  // s_odd is settled, and both buffers are free for the next segment
     if (s_odd && any)
@@ -932,7 +937,8 @@ bool good_cache(const bbpe_paged_cache *c) {
   return c && (c->dtype == BBPE_BF16 || c->dtype == BBPE_F16) && (c->head_dim == 64 || c->head_dim == 128 || c->head_dim == 256) &&
          c->n_kv_heads >= 1 && c->n_kv_heads <= 4096 && c->page_size >= 8 && c->page_size <= 65536 &&
          (c->page_size & (c->page_size - 1)) == 0 && c->n_pages >= 1 && c->n_pages <= 0x7FFFFFFFull && c->k && c->v &&
-         ((addr(c->k) | addr(c->v)) & 15) == 0 && ((c->page_stride | c->head_stride | c->token_stride) & 7) == 0;
+         ((addr(c->k) | addr(c->v)) & 15) == 0 && ((c->page_stride | c->head_stride | c->token_stride) & 7) == 0 &&
+         c->token_stride >= 0 && c->token_stride < (1 << 27);
 }
 bool good_heads(uint32_t hq, const bbpe_paged_cache *c) {
   return hq >= 1 && hq % c->n_kv_heads == 0 && hq / c->n_kv_heads <= 128;

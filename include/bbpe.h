@@ -504,7 +504,8 @@ int bbpe_qk_norm_rope_backward(int dtype, uint64_t n_tokens, uint32_t n_q_heads,
  * and d_lse whose token is in no request are not written.
  *
  * head_dim 64, 128 or 256; n_q_heads / n_kv_heads a whole number up to 128;
- * page_size a power of two from 8 to 65536; table_width * page_size below 2^31. */
+ * page_size a power of two from 8 to 65536; token_stride from 0 to 2^27 - 1;
+ * table_width * page_size below 2^31. */
 int bbpe_tree_attention_workspace_bytes(uint64_t n_tokens, uint32_t n_req, uint32_t n_q_heads,
                                         const bbpe_paged_cache *cache, uint64_t *out_bytes);
 int bbpe_tree_attention(const void *q, int64_t q_ts, int64_t q_hs, uint64_t n_tokens,
