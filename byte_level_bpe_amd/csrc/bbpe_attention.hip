@@ -116,10 +116,10 @@ __device__ __forceinline__ uint32_t row_tiles(const AttnArgs &a, uint32_t n) {
 }
 
 // Sums of the requests' units up to and with each, into LDS; returns the total.
-template <uint32_t KT_LOG>
+template <uint32_t KT_LOG, uint32_t NT>
 __device__ __forceinline__ uint64_t scan_units(const AttnArgs &a, uint64_t *incl, uint64_t *sh) {
-  constexpr uint32_t PER = AT_REQ / AT_BLOCK;
-  const uint32_t k = (a.n_req + AT_BLOCK - 1) / AT_BLOCK, r0 = threadIdx.x * k;
+  constexpr uint32_t PER = AT_REQ / NT;
+  const uint32_t k = (a.n_req + NT - 1) / NT, r0 = threadIdx.x * k;
   uint64_t u[PER], mine = 0;
 #pragma unroll
   for (uint32_t j = 0; j < PER; ++j) {
@@ -131,7 +131,7 @@ __device__ __forceinline__ uint64_t scan_units(const AttnArgs &a, uint64_t *incl
     mine += u[j];
   }
   uint64_t total;
-  uint64_t at = block_incl_scan<AT_BLOCK, uint64_t>(mine, 0, [](uint64_t x, uint64_t y) { return x + y; }, sh, total) - mine;
+  uint64_t at = block_incl_scan<NT, uint64_t>(mine, 0, [](uint64_t x, uint64_t y) { return x + y; }, sh, total) - mine;
 #pragma unroll
   for (uint32_t j = 0; j < PER; ++j) {
     at += u[j];
@@ -185,6 +185,7 @@ struct Row {
 __device__ __forceinline__ Row row_of(const AttnArgs &a, const Segment &s, uint32_t row) {
   const uint32_t at = s.row0 + row, token = at / a.grp;
   return Row{min(token, s.L.n - 1), at - token * a.grp, row < a.stride && token < s.L.n};
+  // (a row that is not live has a token and a head all the same: its products are not used)
 }
 
 template <typename T> struct Mma;
@@ -331,7 +332,7 @@ __global__ __launch_bounds__(AT_BLOCK, (D * MT <= 128 ? 3 : D * MT <= 256 ? 2 : 
 
   const uint32_t head = blockIdx.x, run = blockIdx.y;
   const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6, n16 = lane & 15, g = lane >> 4;
-  const uint64_t total = scan_units<AT_KT_LOG>(a, s_incl, s_scan);
+  const uint64_t total = scan_units<AT_KT_LOG, AT_BLOCK>(a, s_incl, s_scan);
   const uint64_t per = (total + a.runs - 1) / a.runs;
   const uint64_t u_end = min(total, (uint64_t(run) + 1) * per);
   uint64_t u = uint64_t(run) * per;
@@ -354,13 +355,11 @@ __global__ __launch_bounds__(AT_BLOCK, (D * MT <= 128 ? 3 : D * MT <= 256 ? 2 : 
 #pragma unroll
     for (uint32_t i = 0; i < MT; ++i) {
       const Row w = row_of(a, sg, 16 * i + n16);
-      const bool live = w.live;
       token[i] = w.token;
       const T *p = static_cast<const T *>(a.q) + (L.first + w.token) * a.q_ts + int64_t(head * a.grp + w.h) * a.q_hs;
 #pragma unroll
       for (uint32_t s = 0; s < NS; ++s) {
-        q[i][s] = T8{};
-        if (live) q[i][s] = __builtin_bit_cast(T8, __builtin_bit_cast(u32x4, load8_raw(p + s * 32 + g * 8, a.q_vec)) ^ a.flip);
+        q[i][s] = __builtin_bit_cast(T8, __builtin_bit_cast(u32x4, load8_raw(p + s * 32 + g * 8, a.q_vec)) ^ a.flip);
       }
     }
     f32x4 acc[MT][VD];
@@ -551,17 +550,15 @@ __global__ __launch_bounds__(AT_BLOCK, (D * MT <= 128 ? 3 : D * MT <= 256 ? 2 : 
   if (!left_open && threadIdx.x == 0) meta[0] = 0;
 }
 
-// Row tiles of 64 * MT rows.  With this many rows the products, not the cache,
-// take the time, and what counts is how often K and V pass from memory to the
-// registers: a workgroup's waves take 16 * MT rows each of one row tile and
-// share its tiles of KT keys in LDS, two of them, one read while the next is on
-// its way (from global memory to LDS without registers between; the two are
-// variables of their own, so that the compiler sees that reads of one need not
-// wait for the other).  The products are
-// k_attn_rows'; V's fragment comes turned over from LDS by the transposing
-// reads.  16-byte chunks of a row are stored at (chunk XOR a function of the
-// row), so that 16 rows at one chunk, and 16 rows by four, fall on different
-// banks.
+// Row tiles of 16 * MT rows for each of W waves.  With this many rows the
+// products, not the cache, take the time, and what counts is how often K and V
+// pass from memory to the registers: the waves of a workgroup share tiles of KT
+// keys in LDS, two of them, one read while the next is on its way (from global
+// memory to LDS without registers between; the two are variables of their own,
+// so that the compiler sees that reads of one need not wait for the other).  The products are k_attn_rows'; V's fragment comes turned over from
+// LDS by the transposing reads.  16-byte chunks of a row are stored at (chunk
+// XOR a function of the row), so that 16 rows at one chunk, and 16 rows by four
+// lanes, fall on different banks.
 template <uint32_t D>
 __device__ __forceinline__ uint32_t k_chunk(uint32_t row, uint32_t c) {
   return D == 64 ? c ^ (row >> 1 & 7) : c ^ (row & 15);
@@ -571,24 +568,52 @@ __device__ __forceinline__ uint32_t v_chunk(uint32_t row, uint32_t c) {
   return D == 64 ? c ^ ((row >> 1 & 3) << 1) : c ^ ((row & 7) << 1);
 }
 
-template <typename T, uint32_t D, uint32_t MT>
-__global__ __launch_bounds__(AT_BLOCK, 2) void k_attn_tiles(AttnArgs a) {
+// Which of the 64 keys from key0 on a row sees (seen8's rules).
+__device__ __forceinline__ uint64_t low_bits64(int64_t n) {
+  return n <= 0 ? 0 : n >= 64 ? ~uint64_t(0) : (uint64_t(1) << uint32_t(n)) - 1;
+}
+__device__ __forceinline__ uint64_t seen64(const AttnArgs &a, const Lengths &L, uint32_t klim, uint32_t key0, uint32_t token) {
+  const uint64_t within = low_bits64(int64_t(klim) - key0);
+  if (!a.mask) return within & low_bits64(int64_t(L.ctx) + token + 1 - key0);
+  const uint64_t old = low_bits64(int64_t(L.ctx) - key0);
+  const int64_t j0 = int64_t(key0) - L.ctx;
+  if (j0 <= -64) return within;
+  const uint64_t *row = a.mask + (uint64_t(L.first) + token) * a.words;
+  uint64_t w = 0;
+  if (j0 < 0) {
+    w = row[0] << uint32_t(-j0);
+  } else {
+    const uint32_t at = uint32_t(j0 >> 6), sh = uint32_t(j0 & 63);
+    if (at < a.words) w = row[at] >> sh;
+    if (sh && at + 1 < a.words) w |= row[at + 1] << (64 - sh);
+  }
+  return within & (old | w);  // (w has no bits below the context's end)
+}
+
+// Waits for this wave's loads (s_waitcnt vmcnt(0), the other counters free).
+__device__ __forceinline__ void wait_loads() { __builtin_amdgcn_s_waitcnt(0x0F70); }
+
+template <typename T, uint32_t D, uint32_t W, uint32_t MT, uint32_t KT_LOG>
+__global__ __launch_bounds__(64 * W, 2) void k_attn_tiles(AttnArgs a) {
   typedef typename Vec8<T>::type T8;
-  constexpr uint32_t KT_LOG = D == 256 ? 5 : 6, KT = 1u << KT_LOG;  // keys of a tile
+  constexpr uint32_t KT = 1u << KT_LOG;      // keys of a tile
   constexpr uint32_t NS = D / 32, ND = D / 16;
   constexpr uint32_t CH = D / 8;             // 16-byte chunks of a row
   constexpr uint32_t RPI = 64 / CH;          // rows of one load to LDS (1 KiB)
-  constexpr uint32_t ROWS = KT / AT_WAVES;   // rows that a wave fetches, in groups of 8 (of one page each)
+  constexpr uint32_t ROWS = KT / W;          // rows that a wave fetches, in groups of 8 (of one page each)
   constexpr uint32_t GROUPS = ROWS / 8, LPG = 8 / RPI;
-  constexpr uint32_t M = 64 * MT;
-  __shared__ __attribute__((aligned(1024))) T s_k0[KT * D], s_k1[KT * D], s_v0[KT * D], s_v1[KT * D];
+  constexpr uint32_t LOADS = 2 * GROUPS * LPG;  // a wave's loads for one tile
+  constexpr uint32_t M = 16 * MT * W;
+  static_assert(ROWS % 8 == 0 && KT >= 32 && KT <= 64, "");
+  __shared__ __attribute__((aligned(1024))) T s_k0[KT * D], s_v0[KT * D], s_k1[KT * D], s_v1[KT * D];
   __shared__ uint64_t s_incl[AT_REQ];
-  __shared__ uint64_t s_scan[2 * AT_BLOCK / 64 + 1];
-  __shared__ uint32_t s_odd;  // the segment has infinities or NaN in tiles with masked places
+  __shared__ uint64_t s_scan[2 * W + 1];
+  __shared__ uint8_t s_hidden[2][8];     // a tile's groups of eight keys whose page is not in the cache
+  __shared__ uint32_t s_odd;               // the segment has infinities or NaN in tiles with masked places
 
   const uint32_t head = blockIdx.x, run = blockIdx.y;
   const uint32_t lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), n16 = lane & 15, g = lane >> 4;
-  const uint64_t total = scan_units<KT_LOG>(a, s_incl, s_scan);
+  const uint64_t total = scan_units<KT_LOG, 64 * W>(a, s_incl, s_scan);
   const uint64_t per = (total + a.runs - 1) / a.runs;
   const uint64_t u_end = min(total, (uint64_t(run) + 1) * per);
   uint64_t u = uint64_t(run) * per;
@@ -597,6 +622,7 @@ __global__ __launch_bounds__(AT_BLOCK, 2) void k_attn_tiles(AttnArgs a) {
   const char *kc = a.kc + int64_t(head) * a.head_stride * int64_t(sizeof(T));
   const char *vc = a.vc + int64_t(head) * a.head_stride * int64_t(sizeof(T));
   const uint32_t in_page = (1u << a.page_shift) - 1;
+  if (threadIdx.x < 16) (&s_hidden[0][0])[threadIdx.x] = 0;  // (a tile of 32 keys has four groups)
   // a lane's sources in its loads to LDS, from a group of eight rows' first on:
   // row i * RPI + lane / CH of the group, and the chunk whose place is lane % CH
   uint32_t k_from[GROUPS][LPG], v_from[LPG];
@@ -624,21 +650,61 @@ __global__ __launch_bounds__(AT_BLOCK, 2) void k_attn_tiles(AttnArgs a) {
   while (u < u_end) {
     const Segment sg = segment_at<KT_LOG>(a, s_incl, u, u_end);
     const Lengths &L = sg.L;
-    const int32_t *pages = a.table + uint64_t(sg.r) * a.table_stride;
+    // the table's row, read by scalar loads, whose counter the loads to LDS do not share
+    const __attribute__((address_space(4))) int32_t *pages =
+        (const __attribute__((address_space(4))) int32_t *)(a.table + uint64_t(sg.r) * a.table_stride);
+    const uint32_t unit_end = min(sg.first + sg.count, (sg.klim + KT - 1) >> KT_LOG);
+
+    uint32_t page[GROUPS];  // of this wave's groups in the next tile to fetch
+    const auto look = [&](uint32_t unit) {
+#pragma unroll
+      for (uint32_t gi = 0; gi < GROUPS; ++gi)
+        page[gi] = uint32_t(pages[min((unit << KT_LOG) + 8 * (wave * GROUPS + gi), sg.klim - 1) >> a.page_shift]);
+    };
+    // this wave's rows of a tile, on their way to LDS: load n of LOADS, K's first.
+    // (A page outside the cache reads page 0 and is masked.)
+    int64_t from_at[GROUPS];
+    const auto aim = [&](uint32_t unit, uint32_t stage) {
+#pragma unroll
+      for (uint32_t gi = 0; gi < GROUPS; ++gi) {
+        const uint32_t group = wave * GROUPS + gi, key = (unit << KT_LOG) + 8 * group;
+        const bool ok = page[gi] < a.n_pages;
+        from_at[gi] = (int64_t(ok ? page[gi] : 0) * a.page_stride + int64_t(key & in_page) * a.token_stride) * int64_t(sizeof(T));
+        if (lane == 0) s_hidden[stage][group] = !ok;
+      }
+    };
+    const auto fetch = [&](uint32_t n, T *k_to, T *v_to) {
+      typedef const __attribute__((address_space(1))) void *from;
+      typedef __attribute__((address_space(3))) void *to;
+      const uint32_t gi = n % (LOADS / 2) / LPG, i = n % LPG, row = 8 * (wave * GROUPS + gi) + i * RPI;
+      if (n < LOADS / 2) __builtin_amdgcn_global_load_lds((from)(kc + from_at[gi] + k_from[gi][i]), (to)(k_to + row * D), 16, 0, 0);
+      else __builtin_amdgcn_global_load_lds((from)(vc + from_at[gi] + v_from[i]), (to)(v_to + row * D), 16, 0, 0);
+    };
+    const auto fetch_all = [&](uint32_t unit, T *k_to, T *v_to, uint32_t stage) {
+      aim(min(unit, unit_end - 1), stage);
+#pragma unroll
+      for (uint32_t n = 0; n < LOADS; ++n) fetch(n, k_to, v_to);
+      look(min(unit + 1, unit_end - 1));
+    };
+    if (threadIdx.x == 0) s_odd = 0;
+    __syncthreads();
+    if (sg.first < unit_end) {
+      look(sg.first);
+      fetch_all(sg.first, s_k0, s_v0, 0);
+    }
+
     T8 q[MT][NS];
     uint32_t token[MT];
     bool any = false;  // a row of this wave's is one of the tile's
 #pragma unroll
     for (uint32_t i = 0; i < MT; ++i) {
       const Row w = row_of(a, sg, 16 * (wave * MT + i) + n16);
-      const bool live = w.live;
-      any |= live;
+      any |= w.live;
       token[i] = w.token;
       const T *p = static_cast<const T *>(a.q) + (L.first + w.token) * a.q_ts + int64_t(head * a.grp + w.h) * a.q_hs;
 #pragma unroll
       for (uint32_t s = 0; s < NS; ++s) {
-        q[i][s] = T8{};
-        if (live) q[i][s] = __builtin_bit_cast(T8, __builtin_bit_cast(u32x4, load8_raw(p + s * 32 + g * 8, a.q_vec)) ^ a.flip);
+        q[i][s] = __builtin_bit_cast(T8, __builtin_bit_cast(u32x4, load8_raw(p + s * 32 + g * 8, a.q_vec)) ^ a.flip);
       }
     }
     any = __any(any);
@@ -651,34 +717,14 @@ __global__ __launch_bounds__(AT_BLOCK, 2) void k_attn_tiles(AttnArgs a) {
 #pragma unroll
       for (uint32_t j = 0; j < ND; ++j) acc[i][j] = f32x4{};
     }
-    const uint32_t unit_end = min(sg.first + sg.count, (sg.klim + KT - 1) >> KT_LOG);
 
-    // the tile's pages, one a lane (of its KT / 8 groups); a page outside the cache reads page 0 and is masked
-    const auto pages_of = [&](uint32_t unit) -> int32_t {
-      const uint32_t key = (unit << KT_LOG) + 8 * (lane & (KT / 8 - 1));
-      return pages[min(key, sg.klim - 1) >> a.page_shift];
-    };
-    // this wave's rows of a tile, on their way to LDS
-    const auto fetch = [&](uint32_t unit, int32_t page, T *k_to, T *v_to) {
-#pragma unroll
-      for (uint32_t gi = 0; gi < GROUPS; ++gi) {
-        const uint32_t group = wave * GROUPS + gi, key = (unit << KT_LOG) + 8 * group;
-        const uint32_t p = uint32_t(__builtin_amdgcn_readlane(page, int(group)));
-        const int64_t at = (int64_t(p < a.n_pages ? p : 0) * a.page_stride + int64_t(key & in_page) * a.token_stride) * int64_t(sizeof(T));
-#pragma unroll
-        for (uint32_t i = 0; i < LPG; ++i) {
-          typedef const __attribute__((address_space(1))) void *from;
-          typedef __attribute__((address_space(3))) void *to;
-          __builtin_amdgcn_global_load_lds((from)(kc + at + k_from[gi][i]), (to)(k_to + (8 * group + i * RPI) * D), 16, 0, 0);
-          __builtin_amdgcn_global_load_lds((from)(vc + at + v_from[i]), (to)(v_to + (8 * group + i * RPI) * D), 16, 0, 0);
-        }
-      }
-    };
-    // its rows of V in a tile with masked places, once they are there
-    const auto clean = [&](T *v) {
+    // this wave's rows of V, once they are there: in a tile where some row does
+    // not see some key all of them, in others those of a group that is hidden
+    const auto clean = [&](T *v, bool all, uint64_t hidden) {
       uint32_t bad = 0;
 #pragma unroll
       for (uint32_t i = 0; i < ROWS / RPI; ++i) {
+        if (!all && !(hidden >> (8 * (wave * GROUPS + i / LPG)) & 1)) continue;
         u32x4 *p = reinterpret_cast<u32x4 *>(v + wave * ROWS * D) + 64 * i + lane;
         u32x4 f = *p;
         uint32_t here = 0;
@@ -691,139 +737,151 @@ __global__ __launch_bounds__(AT_BLOCK, 2) void k_attn_tiles(AttnArgs a) {
         if (here) *p = f;
         bad |= here;
       }
-      if (__any(bad != 0)) s_odd = 1;  // (every wave that finds some writes the same)
+      if (all && __any(bad != 0)) s_odd = 1;  // (every wave that finds some writes the same)
     };
-    int32_t page = 0;
-    uint32_t hidden_next = 0;  // groups of eight keys whose page is not in the cache
-    const auto hidden_of = [&](int32_t p) { return ~uint32_t(__ballot(uint32_t(p) < a.n_pages)) & ((1u << (KT / 8)) - 1); };
-    // tiles in which some row does not see some key
-    const auto in_part = [&](uint32_t unit, uint32_t hidden) { return ((unit + 1) << KT_LOG) > sg.open || hidden; };
-    if (threadIdx.x == 0) s_odd = 0;
-    __syncthreads();
-    if (sg.first < unit_end) {
-      page = pages_of(sg.first);
-      fetch(sg.first, page, s_k0, s_v0);
-      hidden_next = hidden_of(page);
-      if (sg.first + 1 < unit_end) page = pages_of(sg.first + 1);
-    }
-    const auto step = [&](uint32_t unit, const T *s_k, T *s_v, T *k_next, T *v_next) {
-      const uint32_t hidden = hidden_next;
-      __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0): this wave's rows are there
-      if (in_part(unit, hidden)) clean(s_v);
-      __syncthreads();                     // everybody's are, and everybody is done with the other tile
-      if (unit + 1 < unit_end) {
-        fetch(unit + 1, page, k_next, v_next);
-        hidden_next = hidden_of(page);
-        if (unit + 2 < unit_end) page = pages_of(unit + 2);
+
+    const auto step = [&](uint32_t unit, uint32_t stage, const T *s_k, T *s_v, T *k_free, T *v_free) {
+      wait_loads();  // this wave's rows of the tile are there
+      const bool ends = ((unit + 1) << KT_LOG) > sg.open;  // some row does not see some key
+      uint64_t hidden = *reinterpret_cast<const uint64_t *>(s_hidden[stage]);  // (this wave's groups: its own writes)
+      if (ends || hidden) clean(s_v, ends, hidden);
+      __syncthreads();  // everybody's are, and everybody is done with the tile before
+      // (past the segment's last tile, that one again: no branch cuts the products apart)
+      aim(min(unit + 1, unit_end - 1), stage ^ 1);
+#pragma unroll
+      for (uint32_t n = 0; n < LOADS; ++n) fetch(n, k_free, v_free);
+      if (!any) {
+        look(min(unit + 2, unit_end - 1));
+        return;
       }
-      if (!any) return;
+      hidden = *reinterpret_cast<const uint64_t *>(s_hidden[stage]);
       const uint32_t key0 = unit << KT_LOG;
-      const bool part = in_part(unit, hidden);
+      // Fragments are read a group ahead of the products that use them; left to
+      // itself the compiler puts each read right before its use.
+      T8 kf[2][NS];
+      const auto read_k = [&](uint32_t k) {
+#pragma unroll
+        for (uint32_t e = 0; e < NS; ++e) kf[k & 1][e] = *reinterpret_cast<const T8 *>(s_k + k_at[e] + 16 * k * D);
+      };
       f32x4 s[MT][KT / 16];
-      {
+      read_k(0);
+#pragma unroll
+      for (uint32_t k = 0; k < KT / 16; ++k) {
+        if (k + 1 < KT / 16) read_k(k + 1);
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (uint32_t i = 0; i < MT; ++i) s[i][k] = f32x4{};
+#pragma unroll
+        for (uint32_t e = 0; e < NS; ++e)
+#pragma unroll
+          for (uint32_t i = 0; i < MT; ++i) s[i][k] = Mma<T>::mul(kf[k & 1][e], q[i][e], s[i][k]);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      look(min(unit + 2, unit_end - 1));
+      constexpr uint32_t VG = ND < 4 ? ND : 4, VN = ND / VG * (KT / 32);  // V's fragments of a group; groups
+      T8 vf[2][VG];
+      const auto read_v = [&](uint32_t n) {
+#pragma unroll
+        for (uint32_t e = 0; e < VG; ++e) {
+          const uint32_t j = n * VG % ND + e, k = n * VG / ND;
+          const T *p = s_v + v_at[j % 8] + 128 * (j / 8) + 32 * k * D;
+          vf[n & 1][e] = __builtin_bit_cast(T8, turned(p, p + 16 * D));
+        }
+      };
+      read_v(0);
+      __builtin_amdgcn_sched_barrier(0);
+      if (ends || hidden) {
+        uint64_t shown = ~uint64_t(0);
+        for (uint32_t e = 0; e < KT / 8; ++e)
+          if (hidden >> (8 * e) & 1) shown &= ~(uint64_t(0xFF) << (8 * e));
+#pragma unroll
+        for (uint32_t i = 0; i < MT; ++i) {
+          const uint64_t seen = (seen64(a, L, sg.klim, key0, token[i]) & shown) >> (4 * g);  // a lane's keys are 16 k + 4 g ..+3
+#pragma unroll
+          for (uint32_t k = 0; k < KT / 16; ++k)
+#pragma unroll
+            for (uint32_t e = 0; e < 4; ++e) s[i][k][e] = (seen >> (16 * k + e) & 1) ? s[i][k][e] : -INFINITY;
+        }
+      }
+      float top[MT];
+      bool more_top = false;
+#pragma unroll
+      for (uint32_t i = 0; i < MT; ++i) {
+        top[i] = -INFINITY;
+#pragma unroll
+        for (uint32_t k = 0; k < KT / 16; ++k) top[i] = max2(top[i], max2(max2(s[i][k][0], s[i][k][1]), max2(s[i][k][2], s[i][k][3])));
+        top[i] = max_quarters(top[i]);
+        more_top |= top[i] > m[i];
+      }
+      if (__any(more_top)) {
+#pragma unroll
+        for (uint32_t i = 0; i < MT; ++i) {
+          const float m_new = max2(m[i], top[i]);
+          const float f = m_new == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f((m[i] - m_new) * a.scale2);
+          m[i] = m_new;
+          l[i] *= f;
+#pragma unroll
+          for (uint32_t j = 0; j < ND; ++j) acc[i][j] *= f;
+        }
+      }
+#pragma unroll
+      for (uint32_t i = 0; i < MT; ++i) {
+        const float base = m[i] == -INFINITY ? 0.0f : m[i] * a.scale2;
 #pragma unroll
         for (uint32_t k = 0; k < KT / 16; ++k) {
 #pragma unroll
-          for (uint32_t i = 0; i < MT; ++i) s[i][k] = f32x4{};
-#pragma unroll
-          for (uint32_t e = 0; e < NS; ++e) {
-            const T8 f = *reinterpret_cast<const T8 *>(s_k + k_at[e] + 16 * k * D);
-#pragma unroll
-            for (uint32_t i = 0; i < MT; ++i) s[i][k] = Mma<T>::mul(f, q[i][e], s[i][k]);
-          }
-        }
-        if (part) {
-#pragma unroll
-          for (uint32_t i = 0; i < MT; ++i)
-#pragma unroll
-            for (uint32_t k = 0; k < KT / 16; ++k) {
-              // a lane's keys are 16 k + 4 g ..+3
-              const uint32_t at = 16 * k + 8 * (g >> 1);
-              const uint32_t seen = ((hidden >> (at >> 3) & 1) ? 0 : seen8(a, L, sg.klim, key0 + at, token[i])) >> (4 * (g & 1));
-#pragma unroll
-              for (uint32_t e = 0; e < 4; ++e) s[i][k][e] = (seen >> e & 1) ? s[i][k][e] : -INFINITY;
-            }
-        }
-        float top[MT];
-        bool more_top = false;
-#pragma unroll
-        for (uint32_t i = 0; i < MT; ++i) {
-          top[i] = -INFINITY;
-#pragma unroll
-          for (uint32_t k = 0; k < KT / 16; ++k) top[i] = max2(top[i], max2(max2(s[i][k][0], s[i][k][1]), max2(s[i][k][2], s[i][k][3])));
-          top[i] = max_quarters(top[i]);
-          more_top |= top[i] > m[i];
-        }
-        if (__any(more_top)) {
-#pragma unroll
-          for (uint32_t i = 0; i < MT; ++i) {
-            const float m_new = max2(m[i], top[i]);
-            const float f = m_new == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f((m[i] - m_new) * a.scale2);
-            m[i] = m_new;
-            l[i] *= f;
-#pragma unroll
-            for (uint32_t j = 0; j < ND; ++j) acc[i][j] *= f;
-          }
-        }
-#pragma unroll
-        for (uint32_t i = 0; i < MT; ++i) {
-          const float base = m[i] == -INFINITY ? 0.0f : m[i] * a.scale2;
-#pragma unroll
-          for (uint32_t k = 0; k < KT / 16; ++k) {
-#pragma unroll
-            for (uint32_t e = 0; e < 4; ++e) s[i][k][e] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i][k][e], a.scale2, -base));
-            l[i] += (s[i][k][0] + s[i][k][1]) + (s[i][k][2] + s[i][k][3]);
-          }
+          for (uint32_t e = 0; e < 4; ++e) s[i][k][e] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i][k][e], a.scale2, -base));
+          l[i] += (s[i][k][0] + s[i][k][1]) + (s[i][k][2] + s[i][k][3]);
         }
       }
-      {
-        const auto weights = [&](uint32_t i, uint32_t k) {
+      T8 pf[MT][KT / 32];
+#pragma unroll
+      for (uint32_t k = 0; k < KT / 32; ++k)
+#pragma unroll
+        for (uint32_t i = 0; i < MT; ++i) {
+          // rounded once to the cache's type: the matrix product's operand
           const f32x4 x = s[i][2 * k], y = s[i][2 * k + 1];
-          return from_float<T>(f32x8{x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]});
-        };
-        const auto values = [&](uint32_t j, uint32_t k) {
-          const T *p = s_v + v_at[j % 8] + 128 * (j / 8) + 32 * k * D;
-          return turned(p, p + 16 * D);
-        };
-#pragma unroll
-        for (uint32_t k = 0; k < KT / 32; ++k) {
-          T8 pf[MT];
-#pragma unroll
-          for (uint32_t i = 0; i < MT; ++i) pf[i] = weights(i, k);
-#pragma unroll
-          for (uint32_t j = 0; j < ND; ++j) {
-            const T8 f = __builtin_bit_cast(T8, values(j, k));
-#pragma unroll
-            for (uint32_t i = 0; i < MT; ++i) acc[i][j] = Mma<T>::mul(f, pf[i], acc[i][j]);
-          }
+          pf[i][k] = from_float<T>(f32x8{x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]});
         }
+#pragma unroll
+      for (uint32_t n = 0; n < VN; ++n) {
+        if (n + 1 < VN) read_v(n + 1);
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (uint32_t e = 0; e < VG; ++e)
+#pragma unroll
+          for (uint32_t i = 0; i < MT; ++i) {
+            const uint32_t j = n * VG % ND + e;
+            acc[i][j] = Mma<T>::mul(vf[n & 1][e], pf[i][n * VG / ND], acc[i][j]);
+          }
+        __builtin_amdgcn_sched_barrier(0);
       }
     };
     for (uint32_t unit = sg.first; unit < unit_end; unit += 2) {
-      step(unit, s_k0, s_v0, s_k1, s_v1);
-      if (unit + 1 < unit_end) step(unit + 1, s_k1, s_v1, s_k0, s_v0);
+      step(unit, 0, s_k0, s_v0, s_k1, s_v1);
+      if (unit + 1 < unit_end) step(unit + 1, 1, s_k1, s_v1, s_k0, s_v0);
     }
-    __syncthreads();  // s_odd is settled, and both buffers are free for the next segment
+    wait_loads();     // nothing is on its way to LDS any more,
+    __syncthreads();  // s_odd is settled, and every stage is free for the next segment
     if (s_odd && any)
-      for (uint32_t unit = sg.first; unit < unit_end; ++unit)
-        if (in_part(unit, hidden_of(pages_of(unit))))
-          add_apart<T, MT>(a, sg, vc, unit << KT_LOG, min((unit + 1) << KT_LOG, sg.klim), token, [&](const T *v, uint32_t seen) {
+      for (uint32_t unit = max(sg.first, sg.open >> KT_LOG); unit < unit_end; ++unit)
+        add_apart<T, MT>(a, sg, vc, unit << KT_LOG, min((unit + 1) << KT_LOG, sg.klim), token, [&](const T *v, uint32_t seen) {
 #pragma unroll
-            for (uint32_t j = 0; j < ND; ++j)
+          for (uint32_t j = 0; j < ND; ++j)
 #pragma unroll
-              for (uint32_t e = 0; e < 4; ++e) {
-                const float x = apart(v[16 * j + 4 * g + e]);
+            for (uint32_t e = 0; e < 4; ++e) {
+              const float x = apart(v[16 * j + 4 * g + e]);
 #pragma unroll
-                for (uint32_t i = 0; i < MT; ++i) acc[i][j][e] += (seen >> i & 1) ? x : 0.0f;
-              }
-          });
+              for (uint32_t i = 0; i < MT; ++i) acc[i][j][e] += (seen >> i & 1) ? x : 0.0f;
+            }
+        });
     __syncthreads();  // s_odd has been read
 
     const bool whole = sg.first == 0 && sg.count == sg.n_units;
     float *part = a.part + ((uint64_t(head) * a.runs + run) * 2 + (sg.first == 0 ? 1 : 0)) * (M * (D + 2));
 #pragma unroll
     for (uint32_t i = 0; i < MT; ++i) {
-      const float sum = sum_quarters(l[i]);
+      const float sum = sum_quarters(l[i]), top = m[i] == -INFINITY ? m[i] : m[i] * a.scale2;
       const uint32_t row = 16 * (wave * MT + i) + n16;
       const Row w = row_of(a, sg, row);
       if (!w.live) continue;
@@ -831,13 +889,13 @@ __global__ __launch_bounds__(AT_BLOCK, 2) void k_attn_tiles(AttnArgs a) {
 #pragma unroll
         for (uint32_t j = 0; j < ND; ++j) {
           const float o[4] = {acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]};
-          finish<T, 4>(a, L.first + w.token, head * a.grp + w.h, 16 * j + 4 * g, o, m[i] == -INFINITY ? m[i] : m[i] * a.scale2, sum, j == 0 && g == 0);
+          finish<T, 4>(a, L.first + w.token, head * a.grp + w.h, 16 * j + 4 * g, o, top, sum, j == 0 && g == 0);
         }
       } else {
 #pragma unroll
         for (uint32_t j = 0; j < ND; ++j) *reinterpret_cast<f32x4 *>(part + row * D + 16 * j + 4 * g) = acc[i][j];
         if (g == 0) {
-          part[M * D + row] = m[i] == -INFINITY ? m[i] : m[i] * a.scale2;
+          part[M * D + row] = top;
           part[M * D + M + row] = sum;
         }
       }
@@ -915,9 +973,9 @@ uintptr_t addr(const void *p) { return reinterpret_cast<uintptr_t>(p); }
 
 // Rows of a row tile, by the rows that a request has for one key/value head on
 // average: 16 or 32 of k_attn_rows, 64 or 128 of k_attn_tiles.
-uint32_t tile_rows(uint64_t n_tok, uint32_t n_req, uint32_t grp) {
+uint32_t tile_rows(uint64_t n_tok, uint32_t n_req, uint32_t grp, uint32_t dim) {
   const uint64_t rows = std::max<uint64_t>(grp, n_tok * grp / std::max(1u, n_req));
-  return rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128;
+  return rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : rows <= 128 || dim == 256 ? 128 : 256;
 }
 
 struct Plan {
@@ -926,8 +984,8 @@ struct Plan {
 };
 Plan plan_of(uint64_t n_tok, uint32_t n_req, uint32_t hq, uint32_t hk, uint32_t dim) {
   Plan p;
-  p.rows = tile_rows(n_tok, n_req, hq / hk);
-  p.runs = std::max(1u, AT_RUNS / hk);
+  p.rows = tile_rows(n_tok, n_req, hq / hk, dim);
+  p.runs = std::max(1u, (p.rows > 128 || (dim == 256 && p.rows == 128) ? AT_RUNS / 2 : AT_RUNS) / hk);
   p.meta_bytes = (uint64_t(hk) * p.runs * 16 + 255) / 256 * 256;
   p.bytes = p.meta_bytes + uint64_t(hk) * p.runs * 2 * p.rows * (dim + 2) * sizeof(float);
   return p;
@@ -948,12 +1006,18 @@ template <typename T, uint32_t D, uint32_t M>
 void launch(const AttnArgs &a, hipStream_t st) {
   const dim3 grid(a.hk, a.runs);
   if constexpr (M <= 32) k_attn_rows<T, D, M / 16><<<grid, AT_BLOCK, 0, st>>>(a);
-  else k_attn_tiles<T, D, M / 64><<<grid, AT_BLOCK, 0, st>>>(a);
+  else if constexpr (D == 256 && M == 128) k_attn_tiles<T, D, 8, 1, 6><<<grid, 2 * AT_BLOCK, 0, st>>>(a);
+  else if constexpr (M <= 128) k_attn_tiles<T, D, 4, M / 64, (D == 256 ? 5 : 6)><<<grid, AT_BLOCK, 0, st>>>(a);
+  else k_attn_tiles<T, D, 8, M / 128, 6><<<grid, 2 * AT_BLOCK, 0, st>>>(a);
   k_attn_join<T, D, M><<<dim3(a.hk, a.runs, M / AT_WAVES), AT_BLOCK, 0, st>>>(a);
 }
 template <typename T, uint32_t D>
 void launch_rows(const AttnArgs &a, uint32_t rows, hipStream_t st) {
-  rows == 16 ? launch<T, D, 16>(a, st) : rows == 32 ? launch<T, D, 32>(a, st) : rows == 64 ? launch<T, D, 64>(a, st) : launch<T, D, 128>(a, st);
+  rows == 16    ? launch<T, D, 16>(a, st)
+  : rows == 32  ? launch<T, D, 32>(a, st)
+  : rows == 64  ? launch<T, D, 64>(a, st)
+  : rows == 128 || D == 256 ? launch<T, D, 128>(a, st)
+                : launch<T, D, (D == 256 ? 128 : 256)>(a, st);
 }
 template <typename T>
 void launch_dim(const AttnArgs &a, uint32_t dim, uint32_t rows, hipStream_t st) {
