@@ -1,15 +1,17 @@
 """Builds libbbpe.so (the C-ABI library) in this directory with hipcc for
-gfx950.  Usage: python -m byte_level_bpe_amd.build"""
+gfx950, and _serving.so, the binding's short way to it from torch.  Usage: python -m byte_level_bpe_amd.build"""
 from __future__ import annotations
 
 import concurrent.futures as cf
 import os
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 OUT = os.path.join(HERE, "libbbpe.so")
+SERVING = os.path.join(HERE, "_serving.so")
 BUILD = os.path.join(HERE, "_build")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = os.environ.get("BBPE_ARCH", "gfx950")
@@ -38,10 +40,28 @@ def _compile(src: str) -> str:
     return obj
 
 
+def _serving() -> None:
+    """bbpe_torch.cpp against the installed torch's headers and libraries."""
+    import torch
+    from torch.utils.cpp_extension import include_paths, library_paths
+    tmp = SERVING + ".tmp"
+    cmd = (["g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-w", "-D__HIP_PLATFORM_AMD__=1", "-DUSE_ROCM=1",
+            "-D_GLIBCXX_USE_CXX11_ABI=%d" % torch._C._GLIBCXX_USE_CXX11_ABI, os.path.join(CSRC, "bbpe_torch.cpp"),
+            "-I" + sysconfig.get_paths()["include"]] + ["-isystem" + p for p in include_paths(device_type="cuda")] +
+           ["-L" + p for p in library_paths(device_type="cuda")] +
+           ["-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_hip", "-o", tmp])
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError("compile failed: %s\n%s" % (" ".join(cmd), r.stderr))
+    os.replace(tmp, SERVING)
+
+
 def build(verbose: bool = False) -> str:
     os.makedirs(BUILD, exist_ok=True)
-    with cf.ThreadPoolExecutor(max_workers=min(8, len(SOURCES))) as ex:
+    with cf.ThreadPoolExecutor(max_workers=min(8, len(SOURCES) + 1)) as ex:
+        serving = ex.submit(_serving)
         objs = list(ex.map(_compile, SOURCES))
+        serving.result()
     tmp = OUT + ".tmp"
     # -z defs: a kernel declared but not defined fails the link here, not at load
     cmd = [HIPCC, "--offload-arch=" + ARCH, "-shared", "-fPIC", "-Wl,-z,defs", "-o", tmp] + objs

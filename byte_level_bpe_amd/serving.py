@@ -17,11 +17,13 @@ HIP graph.
 from __future__ import annotations
 
 import ctypes as C
+import importlib.util
+import os
 from typing import NamedTuple
 
 import torch
 
-from . import BBPEError, E_INVALID_ARG, OK, _load
+from . import BBPEError, E_INVALID_ARG, HERE, _load
 
 _DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}  # BBPE_BF16, BBPE_F16, BBPE_F32
 
@@ -58,6 +60,25 @@ def _lib():
             fn.restype, fn.argtypes = I, args
         _fns = lib
     return _fns
+
+
+def _short_way():
+    """The _serving extension (csrc/bbpe_torch.cpp), which takes plain calls in
+    one step and leaves the others, by NotImplemented, to the code here."""
+    path = os.path.join(HERE, "_serving.so")
+    if not os.path.exists(path):
+        raise ImportError("_serving.so is not built; run python -m byte_level_bpe_amd.build")
+    spec = importlib.util.spec_from_file_location(__package__ + "._serving", path)
+    mod = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(mod)
+    lib = _lib()
+    mod.bind(*(C.cast(getattr(lib, "bbpe_" + n), C.c_void_p).value for n in (
+        "block_tables", "qk_norm_rope", "qk_norm_rope_backward_workspace_bytes", "qk_norm_rope_backward",
+        "tree_attention_workspace_bytes", "tree_attention")))
+    return mod
+
+
+_short = _short_way()
 
 
 def _bad(what: str):
@@ -157,6 +178,10 @@ def block_tables(q_off, ctx_len, free_pages, table, page_size: int, n_tokens: in
     the per-token outputs; depth: int32 [n_tokens], a drafted token's depth in
     its tree; out: a BlockTables to write into; workspace: uint8, for more than
     4,096 requests."""
+    if out is None and workspace is None and stream is None:
+        got = _short.block_tables(q_off, ctx_len, free_pages, table, page_size, n_tokens, depth)
+        if got is not NotImplemented:
+            return tuple.__new__(BlockTables, got)
     dev = q_off.device
     n = ctx_len.shape[0] if ctx_len.dim() == 1 else -1
     with _On(dev, stream, "block_tables") as on:
@@ -241,6 +266,13 @@ def qk_norm_rope(q, k, q_weight, k_weight, positions, inv_freq, eps: float = 1e-
     With a PagedCache, v and slots (block_tables'), keys and values go to their
     slots, and k_out is None unless given.  Inputs may be strided over tokens
     and heads; q_out may be q and k_out k.  A weight of None is ones."""
+    if q_out is None and k_out is None and stream is None and (cache is not None or slots is None):
+        got = (_short.qk_norm_rope(q, k, q_weight, k_weight, positions, inv_freq, eps, interleaved, None, None, None, None)
+               if cache is None else
+               _short.qk_norm_rope(q, k, q_weight, k_weight, positions, inv_freq, eps, interleaved, v, slots, cache.k,
+                                   cache._p))
+        if got is not NotImplemented:
+            return got
     dev, dt = q.device, q.dtype
     with _On(dev, stream, "qk_norm_rope") as on:
         n, hq, hk, dim, rot, ws, pos, freq = _norm_args("qk_norm_rope", q, k, q_weight, k_weight, positions, inv_freq)
@@ -274,6 +306,10 @@ def qk_norm_rope_backward(grad_q, grad_k, q, k, q_weight, k_weight, positions, i
     """Gradients of qk_norm_rope's inputs from those of its outputs
     (bbpe_qk_norm_rope_backward): (dq, dk, dq_weight, dk_weight), the weights'
     in float32, None where the weight is None.  dq may be grad_q, dk grad_k."""
+    if dq is None and dk is None and workspace is None and stream is None:
+        got = _short.qk_norm_rope_backward(q, k, q_weight, k_weight, positions, inv_freq, eps, interleaved, grad_q, grad_k)
+        if got is not NotImplemented:
+            return got
     dev, dt = q.device, q.dtype
     with _On(dev, stream, "qk_norm_rope_backward") as on:
         n, hq, hk, dim, rot, ws, pos, freq = _norm_args("qk_norm_rope_backward", q, k, q_weight, k_weight, positions,
@@ -318,6 +354,11 @@ def tree_attention(q, cache: PagedCache, table, q_off, ctx_len, tree_mask=None, 
     tokens); tree_mask: int64 [n_tokens, words], bit j of row i set where token i
     sees new token j of its request; without it, tokens see themselves and those
     before; scale: dim ** -0.5 by default; lse: float32 [n_tokens, n_q_heads]."""
+    if out is None and lse is None and workspace is None and stream is None:
+        got = _short.tree_attention(q, cache.k, cache._p, table, q_off, ctx_len, tree_mask,
+                                    cache.head_dim ** -0.5 if scale is None else scale, return_lse)
+        if got is not NotImplemented:
+            return got if return_lse else got[0]
     dev, dt = q.device, q.dtype
     with _On(dev, stream, "tree_attention") as on:
         if q.dim() != 3 or dt is not cache.dtype or dev != cache.device or q.shape[2] != cache.head_dim:
