@@ -171,9 +171,12 @@ __global__ __launch_bounds__(1024) void k_page_scan(TableArgs a) {
 
 template <bool FOLDED>
 __global__ __launch_bounds__(PG_BLOCK) void k_page_tables(TableArgs a) {
-  __shared__ uint64_t sh[2 * PG_BLOCK / 64 + 1];
+  __shared__ uint64_t sh[PG_BLOCK / 64], s_tally[PG_BLOCK / 64][3];
   __shared__ uint32_t shm[PG_BLOCK / 64];
   __shared__ uint32_t s_off[FOLDED ? PG_FOLD + 1 : 1], s_start[FOLDED ? PG_FOLD : 1];
+  __shared__ int32_t s_ctx[FOLDED ? PG_FOLD : 1];
+  const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  constexpr uint32_t WAVES = PG_BLOCK / 64;
   uint32_t good;
   if (FOLDED) {
     // thread t scans requests t*k .. t*k+k-1
@@ -183,40 +186,93 @@ __global__ __launch_bounds__(PG_BLOCK) void k_page_tables(TableArgs a) {
 #pragma unroll
     for (uint32_t j = 0; j < PG_ITEMS; ++j)
       if (j < k && r0 + j < a.n_req) q[j] = read_request(a, r0 + j);
-#pragma unroll
-    for (uint32_t j = 0; j < PG_ITEMS; ++j)
-      if (j < k && r0 + j < a.n_req && off_broken(a, q[j].lo, q[j].hi)) first = min(first, r0 + j);
-    good = block_min(first, shm, PG_BLOCK / 64);
+    // (requests from the first broken offset on fail: what the sums of the others say does not depend on them)
     uint32_t need[PG_ITEMS];
     int code[PG_ITEMS];
     uint64_t mine = 0;
 #pragma unroll
     for (uint32_t j = 0; j < PG_ITEMS; ++j) {
       need[j] = 0;
-      if (j < k && r0 + j < a.n_req) need[j] = need_of(a, q[j], r0 + j >= good, code[j]);
+      if (j < k && r0 + j < a.n_req) {
+        const bool broken = off_broken(a, q[j].lo, q[j].hi);
+        if (broken) first = min(first, r0 + j);
+        need[j] = need_of(a, q[j], broken, code[j]);
+      }
       mine += need[j];
     }
-    uint64_t total;
-    uint64_t at = block_incl_scan<PG_BLOCK, uint64_t>(mine, 0, [](uint64_t x, uint64_t y) { return x + y; }, sh, total) - mine;
+    const uint64_t incl = wave_incl_scan(mine, uint64_t(0), [](uint64_t u, uint64_t v) { return u + v; });
+    first = wave_reduce(first, 0xFFFFFFFFu, [](uint32_t u, uint32_t v) { return min(u, v); });
+    if (lane == 63) {
+      sh[wave] = incl;
+      shm[wave] = first;
+    }
+    __syncthreads();
+    uint64_t at = incl - mine;
+    good = a.n_req;
+#pragma unroll
+    for (uint32_t w = 0; w < WAVES; ++w) {
+      good = min(good, shm[w]);
+      at += w < wave ? sh[w] : 0;
+    }
     Tally t{0xFFFFFFFFu, BBPE_OK, 0, 0};
 #pragma unroll
     for (uint32_t j = 0; j < PG_ITEMS; ++j) {
-      if (j < k && r0 + j < a.n_req) {
-        settle(a, q[j], r0 + j, need[j], code[j], at, blockIdx.x == 0, s_start[r0 + j], t);
-        if (r0 + j < good) {  // offsets within n_tok, so within 32 bits
-          s_off[r0 + j] = uint32_t(q[j].lo);
-          if (r0 + j + 1 == good) s_off[good] = uint32_t(q[j].hi);
+      const uint32_t r = r0 + j;
+      if (j < k && r < a.n_req) {
+        settle(a, q[j], r, need[j], r >= good ? BBPE_E_INVALID_ARG : code[j], at, blockIdx.x == 0, s_start[r], t);
+        s_ctx[r] = q[j].ctx;
+        if (r < good) {  // offsets within n_tok, so within 32 bits
+          s_off[r] = uint32_t(q[j].lo);
+          if (r + 1 == good) s_off[good] = uint32_t(q[j].hi);
         }
       }
       at += need[j];
     }
-    if (blockIdx.x == 0) write_status(a, t, shm, sh, PG_BLOCK / 64);
+    if (blockIdx.x == 0) {
+      // the first failed request with its code in one word, and the sums
+      const auto add = [](uint64_t u, uint64_t v) { return u + v; };
+      const uint64_t key = wave_reduce(uint64_t(t.first) << 8 | uint8_t(-t.code), ~uint64_t(0), [](uint64_t u, uint64_t v) { return u < v ? u : v; });
+      const uint64_t pages = wave_reduce(t.pages, uint64_t(0), add), tokens = wave_reduce(t.tokens, uint64_t(0), add);
+      if (lane == 0) {
+        s_tally[wave][0] = key;
+        s_tally[wave][1] = pages;
+        s_tally[wave][2] = tokens;
+      }
+    }
     __syncthreads();
+    if (blockIdx.x == 0 && threadIdx.x == 0) {
+      uint64_t key = ~uint64_t(0), pages = 0, tokens = 0;
+      for (uint32_t w = 0; w < WAVES; ++w) {
+        key = key < s_tally[w][0] ? key : s_tally[w][0];
+        pages += s_tally[w][1];
+        tokens += s_tally[w][2];
+      }
+      const bool fine = uint32_t(key >> 8) == 0xFFFFFFFFu;
+      a.status[0] = fine ? BBPE_OK : -int64_t(key & 0xFF);
+      a.status[1] = fine ? -1 : int64_t(uint32_t(key >> 8));
+      a.status[2] = int64_t(pages);
+      a.status[3] = int64_t(tokens);
+    }
   } else {
     good = *a.n_good;
   }
   const auto off = [&](uint32_t r) -> uint32_t { return FOLDED ? s_off[r] : uint32_t(a.q_off[r]); };
   const auto start_of = [&](uint32_t r) -> uint32_t { return FOLDED ? s_start[r] : a.start[r]; };
+  const auto ctx_of = [&](uint32_t r) -> int32_t { return FOLDED ? s_ctx[r] : a.ctx[r]; };
+  // The last request that begins at or before token i, the same i for the whole
+  // wave (~0: before the first; good: past them all): 64 offsets at a time.
+  const auto find = [&](uint32_t i) -> uint32_t {
+    if (good == 0 || off(good) <= i) return good;
+    uint32_t lo = 0, span = 1;
+    while (span * 64 < good) span *= 64;
+    for (; span; span /= 64) {
+      const uint32_t r = lo + lane * span;
+      const uint32_t c = uint32_t(__popcll(__ballot(r < good && off(r) <= i)));
+      if (c == 0) return 0xFFFFFFFFu;  // (at the first level only)
+      lo += (c - 1) * span;
+    }
+    return lo;
+  };
 
   const uint32_t tiles = uint32_t((a.n_tok + PG_TILE - 1) / PG_TILE);
   const uint32_t per_row = (a.width + PG_PIECE - 1) / PG_PIECE;
@@ -225,16 +281,19 @@ __global__ __launch_bounds__(PG_BLOCK) void k_page_tables(TableArgs a) {
   for (uint64_t item = blockIdx.x; item < items; item += gridDim.x) {
     if (item < tiles) {
       const uint64_t i0 = item * PG_TILE + threadIdx.x * PG_TOKENS;
-      if (i0 >= a.n_tok) continue;
-      // the last request that begins at or before i0 (good: past them all; ~0: before the first)
-      uint32_t lo = 0, hi = good + 1;  // off(lo - 1) <= i0 < off(hi)
-      if (good == 0) hi = 0;
-      while (lo < hi) {
-        const uint32_t mid = (lo + hi) / 2;
-        if (off(mid) <= i0) lo = mid + 1;
-        else hi = mid;
+      if (item * PG_TILE + wave * 64 * PG_TOKENS >= a.n_tok) continue;  // the wave's first token
+      // between the requests of the wave's first and last token
+      const uint32_t w0 = uint32_t(item * PG_TILE + wave * 64 * PG_TOKENS);
+      uint32_t r = find(w0), last = find(uint32_t(min(uint64_t(w0) + 64 * PG_TOKENS, a.n_tok) - 1));
+      if (good && r != last) {
+        uint32_t lo = r + 1, hi = min(last, good) + 1;  // off(lo - 1) <= i0 < off(hi), where those are
+        while (lo < hi) {
+          const uint32_t mid = (lo + hi) / 2;
+          if (off(mid) <= i0) lo = mid + 1;
+          else hi = mid;
+        }
+        r = lo - 1;
       }
-      uint32_t r = lo - 1;  // ~0u if none
       int64_t slot[PG_TOKENS];
       int32_t pos[PG_TOKENS], req[PG_TOKENS];
       uint32_t last_b = 0xFFFFFFFFu, last_r = 0xFFFFFFFFu;
@@ -250,7 +309,7 @@ __global__ __launch_bounds__(PG_BLOCK) void k_page_tables(TableArgs a) {
         if (r >= good) continue;
         const uint32_t s = start_of(r);
         if (s == PG_FAILED) continue;
-        const uint32_t c = uint32_t(a.ctx[r]), p = c + uint32_t(i - off(r)), b = page_of(a, p);
+        const uint32_t c = uint32_t(ctx_of(r)), p = c + uint32_t(i - off(r)), b = page_of(a, p);
         if (b != last_b || r != last_r) {
           const uint32_t old = pages_for(a, c);
           page = b < old ? a.table[r * a.table_stride + b] : a.free_pages[s + (b - old)];
@@ -278,10 +337,10 @@ __global__ __launch_bounds__(PG_BLOCK) void k_page_tables(TableArgs a) {
     } else {
       const uint64_t piece = (item - tiles) * (PG_BLOCK / 64) + (threadIdx.x >> 6);
       if (piece >= pieces) continue;
-      const uint32_t r = uint32_t(piece / per_row), lane = threadIdx.x & 63;
+      const uint32_t r = uint32_t(piece / per_row);
       const uint32_t from = uint32_t(piece - uint64_t(r) * per_row) * PG_PIECE, to = min(a.width, from + PG_PIECE);
       const uint32_t s = start_of(r);
-      const int32_t c = max(a.ctx[r], 0);
+      const int32_t c = max(ctx_of(r), 0);
       const uint32_t old = min(pages_for(a, uint32_t(c)), a.width);
       uint32_t end = old;  // a failed request, or one without new tokens, takes none
       if (s != PG_FAILED && off(r + 1) != off(r)) end = pages_for(a, uint32_t(c) + (off(r + 1) - off(r)));

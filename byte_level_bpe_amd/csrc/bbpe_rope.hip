@@ -25,6 +25,7 @@ namespace {
 
 constexpr uint32_t QK_GRID = 1024;      // workgroups of the backward pass at most
 constexpr uint32_t QK_MAX_BLOCK = 512;
+constexpr uint32_t QK_BATCH = 4;        // tokens of a batch of the backward pass at most
 constexpr uint64_t QK_MAX_TOKENS = 1u << 22;  // tokens of one forward launch
 
 struct Rows {
@@ -48,6 +49,7 @@ struct QkArgs {
   uint32_t hq, hk, dim, rot;
   uint32_t lanes;             // lanes of a row, a power of two >= dim / 16
   float eps;
+  uint32_t batch;             // backward: tokens of a batch
   float *part;                // backward: [workgroups][2][dim] sums of the weights' gradients
 };
 
@@ -185,13 +187,18 @@ __global__ __launch_bounds__(QK_MAX_BLOCK) void k_qk_norm_rope(QkArgs a) {
   }
 }
 
-// Backward.  Workgroup b takes tokens b, b + gridDim, ...; a lane's columns are
-// the same in all of its rows, so the weights' gradients add up in registers
-// (queries' and keys' apart), then over the workgroup's groups in LDS, and over
-// workgroups in k_qk_norm_weights: every order is fixed by the sizes.
-template <typename T, bool INTER>
+// Backward.  Workgroup b takes batches b, b + gridDim, ... of a.batch tokens,
+// whose turns are made at once, a barrier apart from their use and one batch
+// ahead.  A lane's columns are the same in all of its rows, so the weights'
+// gradients add up in registers (queries' and keys' apart), then over the
+// workgroup's groups in LDS, and over workgroups in k_qk_norm_weights: every
+// order is fixed by the sizes.  ONE: a token's rows fit the workgroup, so that
+// a lane keeps to one head, and its next token's rows are loaded before the
+// present one's are worked on.
+template <typename T, bool INTER, bool ONE>
 __global__ __launch_bounds__(QK_MAX_BLOCK) void k_qk_norm_rope_back(QkArgs a) {
-  __shared__ float2 cs[128];
+  typedef typename Vec8<T>::type V;
+  __shared__ float2 cs[2][QK_BATCH][128];
   extern __shared__ float sums[];  // [groups][dim]
   const uint32_t c = threadIdx.x & (a.lanes - 1), group = threadIdx.x / a.lanes, groups = blockDim.x / a.lanes;
   const bool in_row = 16 * c < a.dim;
@@ -199,54 +206,93 @@ __global__ __launch_bounds__(QK_MAX_BLOCK) void k_qk_norm_rope_back(QkArgs a) {
   uint32_t d0, d1;
   runs_of<INTER>(c, a.rot, d0, d1);
   f32x8 qa = 0.0f, qb = 0.0f, ka = 0.0f, kb = 0.0f;
-  for (uint64_t tok = blockIdx.x; tok < a.n_tok; tok += gridDim.x) {
-    if (a.rot) {
-      __syncthreads();  // the token before is done with the turns
-      for (uint32_t j = threadIdx.x; j < a.rot / 2; j += blockDim.x) cs[j] = turn_of(a.pos[tok], a.inv_freq[j]);
-      __syncthreads();
-    }
-    for (uint32_t r0 = 0; r0 < rows; r0 += groups) {
-      const uint32_t r = r0 + group;
-      const bool live = r < rows && in_row, is_q = r < a.hq;
+  struct Raw {
+    V xa, xb, ga, gb;
+  };
+  const auto load = [&](uint64_t tok, uint32_t r) {
+    Raw v{};
+    if (tok < a.n_tok && r < rows && in_row) {
+      const bool is_q = r < a.hq;
       const uint32_t h = is_q ? r : r - a.hq;
-      f32x8 xa = 0.0f, xb = 0.0f, ga = 0.0f, gb = 0.0f, wa = 1.0f, wb = 1.0f;
-      if (live) {
-        const Rows &src = is_q ? a.q : a.k, &up = is_q ? a.gq : a.gk;
-        const T *x = static_cast<const T *>(src.p) + int64_t(tok) * src.ts + int64_t(h) * src.hs;
-        const T *g = static_cast<const T *>(up.p) + int64_t(tok) * up.ts + int64_t(h) * up.hs;
-        xa = to_float<T>(load8_raw(x + d0, src.vec));
-        xb = to_float<T>(load8_raw(x + d1, src.vec));
-        ga = to_float<T>(load8_raw(g + d0, up.vec));
-        gb = to_float<T>(load8_raw(g + d1, up.vec));
-        const T *w = static_cast<const T *>(is_q ? a.wq : a.wk);
-        if (w) {
-          wa = to_float<T>(load8_raw(w + d0, true));
-          wb = to_float<T>(load8_raw(w + d1, true));
-        }
-      }
-      if (16 * c < a.rot) turn<INTER, true>(ga, gb, cs, c);
-      const f32x8 ha = ga * wa, hb = gb * wb;
-      const float ss = row_sum(sum_of(xa * xa) + sum_of(xb * xb), a.lanes);
-      const float rstd = 1.0f / sqrtf(ss / float(a.dim) + a.eps);
-      const f32x8 na = xa * rstd, nb = xb * rstd;
-      const float mean = row_sum(sum_of(ha * na) + sum_of(hb * nb), a.lanes) / float(a.dim);
-      if (live) {
-        const Rows &dst = is_q ? a.qo : a.ko;
-        T *o = static_cast<T *>(dst.p) + int64_t(tok) * dst.ts + int64_t(h) * dst.hs;
-        store8_raw(o + d0, from_float<T>((ha - na * mean) * rstd), dst.vec);
-        store8_raw(o + d1, from_float<T>((hb - nb * mean) * rstd), dst.vec);
-        if (is_q) {
-          qa += ga * na;
-          qb += gb * nb;
-        } else {
-          ka += ga * na;
-          kb += gb * nb;
+      const Rows &src = is_q ? a.q : a.k, &up = is_q ? a.gq : a.gk;
+      const T *x = static_cast<const T *>(src.p) + int64_t(tok) * src.ts + int64_t(h) * src.hs;
+      const T *g = static_cast<const T *>(up.p) + int64_t(tok) * up.ts + int64_t(h) * up.hs;
+      v.xa = load8_raw(x + d0, src.vec);
+      v.xb = load8_raw(x + d1, src.vec);
+      v.ga = load8_raw(g + d0, up.vec);
+      v.gb = load8_raw(g + d1, up.vec);
+    }
+    return v;
+  };
+  f32x8 wa = 1.0f, wb = 1.0f;
+  const auto weights = [&](uint32_t r) {
+    const T *w = static_cast<const T *>(r < a.hq ? a.wq : a.wk);
+    wa = wb = 1.0f;
+    if (w && in_row) {
+      wa = to_float<T>(load8_raw(w + d0, true));
+      wb = to_float<T>(load8_raw(w + d1, true));
+    }
+  };
+  const auto work = [&](const Raw &v, uint64_t tok, uint32_t r, const float2 *turns) {
+    const bool live = r < rows && in_row, is_q = r < a.hq;
+    f32x8 xa = to_float<T>(v.xa), xb = to_float<T>(v.xb), ga = to_float<T>(v.ga), gb = to_float<T>(v.gb);
+    if (16 * c < a.rot) turn<INTER, true>(ga, gb, turns, c);
+    const f32x8 ha = ga * wa, hb = gb * wb;
+    const float ss = row_sum(sum_of(xa * xa) + sum_of(xb * xb), a.lanes);
+    const float rstd = 1.0f / sqrtf(ss / float(a.dim) + a.eps);
+    const f32x8 na = xa * rstd, nb = xb * rstd;
+    const float mean = row_sum(sum_of(ha * na) + sum_of(hb * nb), a.lanes) / float(a.dim);
+    if (!live) return;
+    const uint32_t h = is_q ? r : r - a.hq;
+    const Rows &dst = is_q ? a.qo : a.ko;
+    T *o = static_cast<T *>(dst.p) + int64_t(tok) * dst.ts + int64_t(h) * dst.hs;
+    store8_raw(o + d0, from_float<T>((ha - na * mean) * rstd), dst.vec);
+    store8_raw(o + d1, from_float<T>((hb - nb * mean) * rstd), dst.vec);
+    if (ONE || is_q) {
+      qa += ga * na;
+      qb += gb * nb;
+    } else {
+      ka += ga * na;
+      kb += gb * nb;
+    }
+  };
+  const uint64_t batches = (a.n_tok + a.batch - 1) / a.batch;
+  const auto make = [&](uint64_t b, uint32_t buf) {
+    if (b >= batches) return;
+    for (uint32_t j = threadIdx.x; j < a.rot / 2 * a.batch; j += blockDim.x) {
+      const uint32_t t = j / (a.rot / 2), e = j - t * (a.rot / 2);
+      const uint64_t tok = b * a.batch + t;
+      if (tok < a.n_tok) cs[buf][t][e] = turn_of(a.pos[tok], a.inv_freq[e]);
+    }
+  };
+  uint32_t buf = 0;
+  Raw next{};
+  if (ONE) {
+    weights(group);
+    next = load(uint64_t(blockIdx.x) * a.batch, group);
+  }
+  make(blockIdx.x, 0);
+  for (uint64_t b = blockIdx.x; b < batches; b += gridDim.x, buf ^= 1) {
+    __syncthreads();  // this batch's turns are made, and the other buffer's are no longer read
+    make(b + gridDim.x, buf ^ 1);
+    for (uint32_t t = 0; t < a.batch; ++t) {
+      const uint64_t tok = b * a.batch + t;
+      if (tok >= a.n_tok) break;
+      if (ONE) {
+        const Raw v = next;
+        next = load(t + 1 < a.batch ? tok + 1 : (b + gridDim.x) * a.batch, group);
+        work(v, tok, group, cs[buf][t]);
+      } else {
+        for (uint32_t r0 = 0; r0 < rows; r0 += groups) {
+          weights(r0 + group);
+          work(load(tok, r0 + group), tok, r0 + group, cs[buf][t]);
         }
       }
     }
   }
   if (!a.part) return;
-  for (int which = 0; which < 2; ++which) {
+  // ONE: groups below hq hold queries' sums, those after them keys', in one round
+  for (int which = 0; which < (ONE ? 1 : 2); ++which) {
     __syncthreads();
     if (in_row) {
 #pragma unroll
@@ -256,30 +302,36 @@ __global__ __launch_bounds__(QK_MAX_BLOCK) void k_qk_norm_rope_back(QkArgs a) {
       }
     }
     __syncthreads();
-    for (uint32_t d = threadIdx.x; d < a.dim; d += blockDim.x) {
+    for (uint32_t e = threadIdx.x; e < (ONE ? 2 : 1) * a.dim; e += blockDim.x) {
+      const uint32_t keys = ONE ? e / a.dim : uint32_t(which), d = ONE ? e - keys * a.dim : e;
+      const uint32_t from = ONE && keys ? a.hq : 0, to = ONE ? (keys ? rows : a.hq) : groups;
       float s = 0.0f;
-      for (uint32_t g = 0; g < groups; ++g) s += sums[g * a.dim + d];
-      a.part[(uint64_t(blockIdx.x) * 2 + which) * a.dim + d] = s;
+      for (uint32_t g = from; g < to; ++g) s += sums[g * a.dim + d];
+      a.part[(uint64_t(blockIdx.x) * 2 + keys) * a.dim + d] = s;
     }
   }
 }
 
-// Sums the workgroups' parts: one workgroup for 16 columns of one weight, 16
-// threads a column.
-__global__ __launch_bounds__(256) void k_qk_norm_weights(const float *part, uint32_t n, uint32_t dim, float *dwq, float *dwk) {
-  __shared__ float sh[16][17];
-  const uint32_t d = blockIdx.x * 16 + (threadIdx.x & 15), g = threadIdx.x >> 4, which = blockIdx.y;
+// Sums the workgroups' parts: one workgroup for 16 columns of one weight, 64
+// threads a column, so that 1,024 parts are 16 loads under way at once.
+__global__ __launch_bounds__(1024) void k_qk_norm_weights(const float *part, uint32_t n, uint32_t dim, float *dwq, float *dwk) {
+  __shared__ float sh[64][17];
+  const uint32_t e = threadIdx.x & 15, d = blockIdx.x * 16 + e, g = threadIdx.x >> 4, which = blockIdx.y;
   float s = 0.0f;
-  if (d < dim)
-    for (uint32_t b = g; b < n; b += 16) s += part[(uint64_t(b) * 2 + which) * dim + d];
-  sh[g][threadIdx.x & 15] = s;
-  __syncthreads();
-  float *out = which ? dwk : dwq;
-  if (g == 0 && d < dim && out) {
-    float t = 0.0f;
-    for (int j = 0; j < 16; ++j) t += sh[j][threadIdx.x & 15];
-    out[d] = t;
+  if (d < dim) {
+    float v[QK_GRID / 64];
+#pragma unroll
+    for (uint32_t j = 0; j < QK_GRID / 64; ++j) v[j] = g + 64 * j < n ? part[(uint64_t(g + 64 * j) * 2 + which) * dim + d] : 0.0f;
+#pragma unroll
+    for (uint32_t j = 0; j < QK_GRID / 64; ++j) s += v[j];
   }
+  sh[g][e] = s;
+  for (uint32_t half = 32; half; half /= 2) {
+    __syncthreads();
+    if (g < half) sh[g][e] += sh[g + half][e];
+  }
+  float *out = which ? dwk : dwq;
+  if (g == 0 && d < dim && out) out[d] = sh[0][e];
 }
 
 uintptr_t addr(const void *p) { return reinterpret_cast<uintptr_t>(p); }
@@ -414,7 +466,9 @@ int bbpe_qk_norm_rope_backward(int dtype, uint64_t n_tokens, uint32_t n_q_heads,
   if (bad_rows(q, dtype) || bad_rows(k, dtype) || bad_rows(g_q, dtype) || bad_rows(g_k, dtype) || bad_rows(d_q, dtype) ||
       bad_rows(d_k, dtype) || (addr(d_wq) & 3) || (addr(d_wk) & 3))
     return BBPE_E_INVALID_ARG;
-  const uint32_t grid = uint32_t(std::min<uint64_t>(n_tokens, QK_GRID));
+  // few tokens: one a workgroup; more: up to four in a row
+  const uint32_t batch = uint32_t(std::min<uint64_t>(QK_BATCH, (n_tokens + QK_GRID - 1) / QK_GRID));
+  const uint32_t grid = batch ? uint32_t(std::min<uint64_t>((n_tokens + batch - 1) / batch, QK_GRID)) : 0;
   const bool weights = d_wq || d_wk;
   if (weights && grid &&
       (!d_workspace || (addr(d_workspace) & 255) || workspace_bytes < uint64_t(grid) * 2 * head_dim * sizeof(float)))
@@ -437,15 +491,18 @@ int bbpe_qk_norm_rope_backward(int dtype, uint64_t n_tokens, uint32_t n_q_heads,
   a.rot = rot_dim;
   a.eps = eps;
   a.part = weights ? static_cast<float *>(d_workspace) : nullptr;
+  a.batch = batch;
   uint32_t block;
   shape(a, a.hq + a.hk, block);
+  const bool one = (a.hq + a.hk) * a.lanes <= block;
   const hipStream_t st = static_cast<hipStream_t>(hip_stream);
   if (grid)
     with_type(dtype, interleaved, [&](auto t, auto inter) {
-      k_qk_norm_rope_back<decltype(t), decltype(inter)::value>
-          <<<grid, block, size_t(block / a.lanes) * a.dim * sizeof(float), st>>>(a);
+      const size_t lds = size_t(block / a.lanes) * a.dim * sizeof(float);
+      if (one) k_qk_norm_rope_back<decltype(t), decltype(inter)::value, true><<<grid, block, lds, st>>>(a);
+      else k_qk_norm_rope_back<decltype(t), decltype(inter)::value, false><<<grid, block, lds, st>>>(a);
     });
-  if (weights) k_qk_norm_weights<<<dim3((a.dim + 15) / 16, 2), 256, 0, st>>>(a.part, grid, a.dim, d_wq, d_wk);
+  if (weights) k_qk_norm_weights<<<dim3((a.dim + 15) / 16, 2), 1024, 0, st>>>(a.part, grid, a.dim, d_wq, d_wk);
   return hipGetLastError() == hipSuccess ? BBPE_OK : BBPE_E_HIP;
 }
 
