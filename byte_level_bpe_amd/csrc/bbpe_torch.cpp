@@ -78,6 +78,15 @@ struct Call {
   }
 };
 
+// A one-dimensional tensor of n elements, `at` bytes into the buffer's storage.
+Tensor part_of(const Tensor &buffer, int64_t at, int64_t n, at::ScalarType type) {
+  Tensor t = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(buffer.storage()), buffer.key_set(), c10::scalarTypeToTypeMeta(type));
+  t.unsafeGetTensorImpl()->set_storage_offset(at / int64_t(c10::elementSize(type)));
+  t.unsafeGetTensorImpl()->set_sizes_contiguous({n});
+  return t;
+}
+int64_t up16(int64_t n) { return (n + 15) / 16 * 16; }
+
 int dtype_of(at::ScalarType t) { return t == at::kBFloat16 ? BBPE_BF16 : t == at::kHalf ? BBPE_F16 : t == at::kFloat ? BBPE_F32 : -1; }
 
 PyObject *not_plain() { Py_RETURN_NOTIMPLEMENTED; }
@@ -99,8 +108,11 @@ PyObject *block_tables(PyObject *, PyObject *const *a, Py_ssize_t n_args) {
   const void *p_depth = c.flat(depth, at::kInt, n_tok);
   void *p_table = c.table(table, n), *stream;
   if (!c.ready(stream)) return not_plain();
-  Tensor slots = c.empty({n_tok}, at::kLong), pos = c.empty({n_tok}, at::kInt), req = c.empty({n_tok}, at::kInt), seq = c.empty({n}, at::kInt),
-         status = c.empty({4}, at::kLong);
+  // five small outputs that live and die together: one allocation
+  const int64_t at_slots = 32, at_pos = at_slots + up16(8 * n_tok), at_req = at_pos + up16(4 * n_tok), at_seq = at_req + up16(4 * n_tok);
+  const Tensor all = c.empty({at_seq + 4 * n}, at::kByte);
+  Tensor status = part_of(all, 0, 4, at::kLong), slots = part_of(all, at_slots, n_tok, at::kLong), pos = part_of(all, at_pos, n_tok, at::kInt),
+         req = part_of(all, at_req, n_tok, at::kInt), seq = part_of(all, at_seq, n, at::kInt);
   const int rc = f_tables(static_cast<const int64_t *>(p_off), static_cast<const int32_t *>(p_ctx), uint32_t(n),
                           static_cast<const int32_t *>(p_free), uint64_t(free_pages->size(0)), static_cast<int32_t *>(p_table),
                           uint64_t(table->stride(0)), uint32_t(table->size(1)), uint32_t(page), uint64_t(n_tok),
