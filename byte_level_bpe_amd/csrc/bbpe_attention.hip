@@ -42,6 +42,9 @@ constexpr uint32_t AT_TILE = 32;     // keys a wave takes at once
 constexpr uint32_t AT_KT_LOG = 7;    // log2 of a unit's keys (AT_WAVES tiles)
 constexpr uint32_t AT_RUNS = 512;    // workgroups of a launch, over all heads
 
+// Rows that a workgroup of k_attn_join takes.
+constexpr uint32_t join_rows(uint32_t m, uint32_t dim) { return m <= 32 ? 1 : 4 * (AT_BLOCK / (dim / 4)); }
+
 struct AttnArgs {
   const void *q;
   int64_t q_ts, q_hs;
@@ -541,8 +544,9 @@ __global__ __launch_bounds__(AT_BLOCK, (D * MT <= 128 ? 3 : D * MT <= 256 ? 2 : 
       left_open = true;
       if (threadIdx.x == 0) {
         meta[0] = uint32_t((u + n_units - 1) / per) - run + 1;  // parts
-        meta[1] = r;
-        meta[2] = sg.row0;
+        meta[1] = uint32_t(L.first);
+        meta[2] = L.n;
+        meta[3] = sg.row0;
       }
     }
     u += count;
@@ -904,8 +908,9 @@ __global__ __launch_bounds__(64 * W, 2) void k_attn_tiles(AttnArgs a) {
       left_open = true;
       if (threadIdx.x == 0) {
         meta[0] = uint32_t((u + sg.n_units - 1) / per) - run + 1;
-        meta[1] = sg.r;
-        meta[2] = sg.row0;
+        meta[1] = uint32_t(L.first);
+        meta[2] = L.n;
+        meta[3] = sg.row0;
       }
     }
     u += sg.count;
@@ -913,60 +918,103 @@ __global__ __launch_bounds__(64 * W, 2) void k_attn_tiles(AttnArgs a) {
   if (!left_open && threadIdx.x == 0) meta[0] = 0;
 }
 
-// Adds up the parts of the row tiles that were cut: a wave for each row of the
-// tile that begins in run blockIdx.y, a lane for every 64th of the row.
+// Adds up the parts of the row tiles that were cut, of the one that begins in
+// run blockIdx.y.  D / 4 threads have a row, four elements each.  Small tiles
+// are cut into many parts and are few: a workgroup takes one row, and its
+// threads' groups every SLOTS-th part; large ones come in two parts or three:
+// a group takes four rows, whose loads are under way together.
 template <typename T, uint32_t D, uint32_t M>
 __global__ __launch_bounds__(AT_BLOCK) void k_attn_join(AttnArgs a) {
-  constexpr uint32_t N = D / 64;
-  const uint32_t head = blockIdx.x, run = blockIdx.y, lane = threadIdx.x & 63;
-  const uint32_t row = blockIdx.z * AT_WAVES + (threadIdx.x >> 6);
-  const uint32_t *meta = a.meta + (uint64_t(head) * a.runs + run) * 4;
-  const uint32_t n = meta[0];
+  constexpr uint32_t TPR = D / 4, SLOTS = AT_BLOCK / TPR, R = join_rows(M, D) == 1 ? 1 : 4;
+  constexpr uint32_t U = R == 1 ? 4 : 2;  // parts whose loads are under way together
+  constexpr uint64_t SIZE = M * (D + 2);
+  __shared__ f32x4 s_o[R == 1 ? AT_BLOCK : 1];
+  __shared__ float s_top[SLOTS], s_sum[SLOTS];
+  const uint32_t head = blockIdx.x, run = blockIdx.y, slot = threadIdx.x / TPR, c = threadIdx.x % TPR;
+  const uint4 meta = *reinterpret_cast<const uint4 *>(a.meta + (uint64_t(head) * a.runs + run) * 4);
+  const uint32_t n = meta.x;
   if (n == 0) return;
   Segment sg;
-  sg.L = lengths_of(a, meta[1]);
-  sg.row0 = meta[2];
-  const Row own = row_of(a, sg, row);
-  if (!own.live) return;
+  sg.L.first = meta.y;
+  sg.L.n = meta.z;
+  sg.row0 = meta.w;
   // the first part is this run's second place, the others the first places of the runs after it
-  constexpr uint64_t SIZE = M * (D + 2);
   const float *base = a.part + (uint64_t(head) * a.runs + run) * 2 * SIZE;
   const auto at = [&](uint32_t p) { return base + (p == 0 ? SIZE : uint64_t(p) * 2 * SIZE); };
-  float top = -INFINITY;
-  for (uint32_t p = lane; p < n; p += 64) top = fmaxf(top, at(p)[M * D + row]);
-  for (int d = 32; d; d >>= 1) top = fmaxf(top, __shfl_xor(top, d, 64));
-  const float from = top == -INFINITY ? 0.0f : top;
-  float o[N], sum = 0.0f;
+  uint32_t row[R];
+  Row w[R];
+  float top[R], sum[R];
+  f32x4 o[R];
 #pragma unroll
-  for (uint32_t j = 0; j < N; ++j) o[j] = 0.0f;
-  for (uint32_t p0 = 0; p0 < n; p0 += 64) {
-    float f = 0.0f, l = 0.0f;
-    if (p0 + lane < n) {
-      f = __builtin_amdgcn_exp2f(at(p0 + lane)[M * D + row] - from);
-      l = at(p0 + lane)[M * D + M + row] * f;
-    }
-    for (int d = 32; d; d >>= 1) l += __shfl_xor(l, d, 64);
-    sum += l;
-    const uint32_t here = min(64u, n - p0);
-    for (uint32_t p = 0; p < here; p += 8) {  // eight loads in flight; lanes past the last part hold f = 0
-      float x[8][N];
+  for (uint32_t i = 0; i < R; ++i) {
+    row[i] = R == 1 ? blockIdx.z : (blockIdx.z * R + i) * SLOTS + slot;
+    w[i] = row_of(a, sg, row[i]);
+    top[i] = -INFINITY;
+    sum[i] = 0.0f;
+    o[i] = f32x4{};
+  }
+  if (R == 1 && !w[0].live) return;
+  for (uint32_t p0 = R == 1 ? slot : 0; p0 < n; p0 += R == 1 ? U * SLOTS : U) {
+    f32x4 x[R][U];
+    float m[R][U], l[R][U];
 #pragma unroll
-      for (uint32_t e = 0; e < 8; ++e) {
-        const float *src = at(p0 + min(p + e, here - 1)) + row * D + lane * N;
+    for (uint32_t i = 0; i < R; ++i)
 #pragma unroll
-        for (uint32_t j = 0; j < N; ++j) x[e][j] = src[j];
-      }
-#pragma unroll
-      for (uint32_t e = 0; e < 8; ++e) {
-        const float w = __shfl(f, int(p + e), 64);
-        if (p + e < here) {
-#pragma unroll
-          for (uint32_t j = 0; j < N; ++j) o[j] += x[e][j] * w;
+      for (uint32_t e = 0; e < U; ++e) {
+        const uint32_t p = p0 + e * (R == 1 ? SLOTS : 1);
+        m[i][e] = -INFINITY;
+        l[i][e] = 0.0f;
+        x[i][e] = f32x4{};
+        if (p < n && w[i].live) {
+          const float *src = at(p);
+          x[i][e] = *reinterpret_cast<const f32x4 *>(src + row[i] * D + 4 * c);
+          m[i][e] = src[M * D + row[i]];
+          l[i][e] = src[M * D + M + row[i]];
         }
       }
+#pragma unroll
+    for (uint32_t i = 0; i < R; ++i) {
+      float next = top[i];
+#pragma unroll
+      for (uint32_t e = 0; e < U; ++e) next = fmaxf(next, m[i][e]);
+      const float from = next == -INFINITY ? 0.0f : next;
+      const float f = __builtin_amdgcn_exp2f(top[i] - from);
+      sum[i] *= f;
+      o[i] *= f;
+#pragma unroll
+      for (uint32_t e = 0; e < U; ++e) {
+        const float g = __builtin_amdgcn_exp2f(m[i][e] - from);
+        sum[i] += l[i][e] * g;
+        o[i] += x[i][e] * g;
+      }
+      top[i] = next;
     }
   }
-  finish<T, N>(a, sg.L.first + own.token, head * a.grp + own.h, lane * N, o, top, sum, lane == 0);
+  if constexpr (R == 1) {
+    s_o[threadIdx.x] = o[0];
+    if (c == 0) {
+      s_top[slot] = top[0];
+      s_sum[slot] = sum[0];
+    }
+    __syncthreads();
+    if (slot) return;
+    const uint32_t used = min(n, SLOTS);
+    for (uint32_t e = 1; e < used; ++e) top[0] = fmaxf(top[0], s_top[e]);
+    const float from = top[0] == -INFINITY ? 0.0f : top[0];
+    sum[0] = 0.0f;
+    o[0] = f32x4{};
+    for (uint32_t e = 0; e < used; ++e) {
+      const float g = __builtin_amdgcn_exp2f(s_top[e] - from);
+      sum[0] += s_sum[e] * g;
+      o[0] += s_o[e * TPR + c] * g;
+    }
+  }
+#pragma unroll
+  for (uint32_t i = 0; i < R; ++i) {
+    if (!w[i].live) continue;
+    const float v[4] = {o[i][0], o[i][1], o[i][2], o[i][3]};
+    finish<T, 4>(a, sg.L.first + w[i].token, head * a.grp + w[i].h, 4 * c, v, top[i], sum[i], c == 0);
+  }
 }
 
 uintptr_t addr(const void *p) { return reinterpret_cast<uintptr_t>(p); }
@@ -1009,7 +1057,7 @@ void launch(const AttnArgs &a, hipStream_t st) {
   else if constexpr (D == 256 && M == 128) k_attn_tiles<T, D, 8, 1, 6><<<grid, 2 * AT_BLOCK, 0, st>>>(a);
   else if constexpr (M <= 128) k_attn_tiles<T, D, 4, M / 64, (D == 256 ? 5 : 6)><<<grid, AT_BLOCK, 0, st>>>(a);
   else k_attn_tiles<T, D, 8, M / 128, 6><<<grid, 2 * AT_BLOCK, 0, st>>>(a);
-  k_attn_join<T, D, M><<<dim3(a.hk, a.runs, M / AT_WAVES), AT_BLOCK, 0, st>>>(a);
+  k_attn_join<T, D, M><<<dim3(a.hk, a.runs, M / join_rows(M, D)), AT_BLOCK, 0, st>>>(a);
 }
 template <typename T, uint32_t D>
 void launch_rows(const AttnArgs &a, uint32_t rows, hipStream_t st) {
