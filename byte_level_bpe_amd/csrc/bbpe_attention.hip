@@ -40,10 +40,13 @@ constexpr uint32_t AT_BLOCK = 256, AT_WAVES = 4;
 constexpr uint32_t AT_REQ = 1024;    // requests of one launch (their units' sums lie in LDS)
 constexpr uint32_t AT_TILE = 32;     // keys a wave takes at once
 constexpr uint32_t AT_KT_LOG = 7;    // log2 of a unit's keys (AT_WAVES tiles)
+#ifndef AT_HEAD
+#define AT_HEAD 4u
+#endif
 constexpr uint32_t AT_RUNS = 512;    // workgroups of a launch, over all heads
 
 // Rows that a workgroup of k_attn_join takes.
-constexpr uint32_t join_rows(uint32_t m, uint32_t dim) { return m <= 32 ? 1 : 4 * (AT_BLOCK / (dim / 4)); }
+constexpr uint32_t join_rows(uint32_t m, uint32_t dim) { return m <= 32 ? 1 : 2 * (AT_BLOCK / (dim / 4)); }
 
 struct AttnArgs {
   const void *q;
@@ -100,26 +103,27 @@ __device__ __forceinline__ uint64_t ceil_sum(uint64_t n, uint32_t q) {
   return ((a * (a + 1) / 2) << q) + b * (a + 1);
 }
 
-// Units of a request's first t row tiles.  Masks: every row tile spans all
+// Units of a request's first t row tiles, HEAD of each standing for what a row
+// tile costs before and after its keys.  Masks: every row tile spans all
 // keys.  A chain: tile i ends at key ctx + (i + 1) * tokens, tokens = 2^tok_log.
-template <uint32_t KT_LOG>
+template <uint32_t KT_LOG, uint32_t HEAD>
 __device__ __forceinline__ uint64_t units_before(const AttnArgs &a, const Lengths &L, uint32_t t) {
   constexpr uint32_t KT = 1u << KT_LOG;
-  if (a.mask) return uint64_t(t) * ((L.klen + KT - 1) >> KT_LOG);
+  if (a.mask) return uint64_t(t) * (((L.klen + KT - 1) >> KT_LOG) + HEAD);
   const uint32_t base = min(L.ctx, a.cap), whole = base >> KT_LOG, rest = base & (KT - 1);
   if (a.tok_log <= KT_LOG) {
     const uint32_t s = (rest + (1u << a.tok_log) - 1) >> a.tok_log, q = KT_LOG - a.tok_log;
-    return uint64_t(t) * whole + ceil_sum(s + t, q) - ceil_sum(s, q);
+    return uint64_t(t) * (whole + HEAD) + ceil_sum(s + t, q) - ceil_sum(s, q);
   }
   const uint64_t steps = uint64_t(t) * (t + 1) / 2;
-  return uint64_t(t) * (whole + (rest ? 1 : 0)) + (steps << (a.tok_log - KT_LOG));
+  return uint64_t(t) * (whole + (rest ? 1 : 0) + HEAD) + (steps << (a.tok_log - KT_LOG));
 }
 __device__ __forceinline__ uint32_t row_tiles(const AttnArgs &a, uint32_t n) {
   return (n * a.grp + a.stride - 1) / a.stride;
 }
 
 // Sums of the requests' units up to and with each, into LDS; returns the total.
-template <uint32_t KT_LOG, uint32_t NT>
+template <uint32_t KT_LOG, uint32_t HEAD, uint32_t NT>
 __device__ __forceinline__ uint64_t scan_units(const AttnArgs &a, uint64_t *incl, uint64_t *sh) {
   constexpr uint32_t PER = AT_REQ / NT;
   const uint32_t k = (a.n_req + NT - 1) / NT, r0 = threadIdx.x * k;
@@ -129,7 +133,7 @@ __device__ __forceinline__ uint64_t scan_units(const AttnArgs &a, uint64_t *incl
     u[j] = 0;
     if (j < k && r0 + j < a.n_req) {
       const Lengths L = lengths_of(a, r0 + j);
-      u[j] = units_before<KT_LOG>(a, L, row_tiles(a, L.n));
+      u[j] = units_before<KT_LOG, HEAD>(a, L, row_tiles(a, L.n));
     }
     mine += u[j];
   }
@@ -151,7 +155,7 @@ struct Segment {
   uint32_t n_units, first, count;
   uint32_t klim, open;     // keys that any row of the tile sees, and those that all of them see
 };
-template <uint32_t KT_LOG>
+template <uint32_t KT_LOG, uint32_t HEAD>
 __device__ __forceinline__ Segment segment_at(const AttnArgs &a, const uint64_t *incl, uint64_t u, uint64_t u_end) {
   Segment s;
   uint32_t lo = 0, hi = a.n_req - 1;
@@ -166,11 +170,11 @@ __device__ __forceinline__ Segment segment_at(const AttnArgs &a, const uint64_t 
   uint32_t t = 0, t_hi = row_tiles(a, s.L.n) - 1;
   while (t < t_hi) {  // the last tile that begins at or before `local`
     const uint32_t mid = (t + t_hi + 1) / 2;
-    if (units_before<KT_LOG>(a, s.L, mid) <= local) t = mid;
+    if (units_before<KT_LOG, HEAD>(a, s.L, mid) <= local) t = mid;
     else t_hi = mid - 1;
   }
-  const uint64_t tile_u = units_before<KT_LOG>(a, s.L, t);
-  s.n_units = uint32_t(units_before<KT_LOG>(a, s.L, t + 1) - tile_u);
+  const uint64_t tile_u = units_before<KT_LOG, HEAD>(a, s.L, t);
+  s.n_units = uint32_t(units_before<KT_LOG, HEAD>(a, s.L, t + 1) - tile_u);
   s.first = uint32_t(local - tile_u);
   s.count = uint32_t(min(uint64_t(s.n_units - s.first), u_end - u));
   s.row0 = t * a.stride;
@@ -335,7 +339,7 @@ __global__ __launch_bounds__(AT_BLOCK, (D * MT <= 128 ? 3 : D * MT <= 256 ? 2 : 
 
   const uint32_t head = blockIdx.x, run = blockIdx.y;
   const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6, n16 = lane & 15, g = lane >> 4;
-  const uint64_t total = scan_units<AT_KT_LOG, AT_BLOCK>(a, s_incl, s_scan);
+  const uint64_t total = scan_units<AT_KT_LOG, 0, AT_BLOCK>(a, s_incl, s_scan);
   const uint64_t per = (total + a.runs - 1) / a.runs;
   const uint64_t u_end = min(total, (uint64_t(run) + 1) * per);
   uint64_t u = uint64_t(run) * per;
@@ -346,7 +350,7 @@ __global__ __launch_bounds__(AT_BLOCK, (D * MT <= 128 ? 3 : D * MT <= 256 ? 2 : 
   const char *vc = a.vc + int64_t(head) * a.head_stride * int64_t(sizeof(T));
 
   while (u < u_end) {
-    const Segment sg = segment_at<AT_KT_LOG>(a, s_incl, u, u_end);
+    const Segment sg = segment_at<AT_KT_LOG, 0>(a, s_incl, u, u_end);
     const Lengths &L = sg.L;
     const uint32_t r = sg.r, n_units = sg.n_units, first = sg.first, count = sg.count;
     const uint32_t klim = sg.klim, open = sg.open;
@@ -617,7 +621,7 @@ __global__ __launch_bounds__(64 * W, 2) void k_attn_tiles(AttnArgs a) {
 
   const uint32_t head = blockIdx.x, run = blockIdx.y;
   const uint32_t lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), n16 = lane & 15, g = lane >> 4;
-  const uint64_t total = scan_units<KT_LOG, 64 * W>(a, s_incl, s_scan);
+  const uint64_t total = scan_units<KT_LOG, AT_HEAD, 64 * W>(a, s_incl, s_scan);
   const uint64_t per = (total + a.runs - 1) / a.runs;
   const uint64_t u_end = min(total, (uint64_t(run) + 1) * per);
   uint64_t u = uint64_t(run) * per;
@@ -652,12 +656,14 @@ __global__ __launch_bounds__(64 * W, 2) void k_attn_tiles(AttnArgs a) {
   }
 
   while (u < u_end) {
-    const Segment sg = segment_at<KT_LOG>(a, s_incl, u, u_end);
+    const Segment sg = segment_at<KT_LOG, AT_HEAD>(a, s_incl, u, u_end);
     const Lengths &L = sg.L;
     // the table's row, read by scalar loads, whose counter the loads to LDS do not share
     const __attribute__((address_space(4))) int32_t *pages =
         (const __attribute__((address_space(4))) int32_t *)(a.table + uint64_t(sg.r) * a.table_stride);
-    const uint32_t unit_end = min(sg.first + sg.count, (sg.klim + KT - 1) >> KT_LOG);
+    // tiles of keys [unit0, unit_end): the segment's units without the row tile's first AT_HEAD
+    const uint32_t unit0 = max(sg.first, AT_HEAD) - AT_HEAD;
+    const uint32_t unit_end = min(max(sg.first + sg.count, AT_HEAD) - AT_HEAD, (sg.klim + KT - 1) >> KT_LOG);
 
     uint32_t page[GROUPS];  // of this wave's groups in the next tile to fetch
     const auto look = [&](uint32_t unit) {
@@ -692,9 +698,9 @@ __global__ __launch_bounds__(64 * W, 2) void k_attn_tiles(AttnArgs a) {
     };
     if (threadIdx.x == 0) s_odd = 0;
     __syncthreads();
-    if (sg.first < unit_end) {
-      look(sg.first);
-      fetch_all(sg.first, s_k0, s_v0, 0);
+    if (unit0 < unit_end) {
+      look(unit0);
+      fetch_all(unit0, s_k0, s_v0, 0);
     }
 
     T8 q[MT][NS];
@@ -861,14 +867,14 @@ __global__ __launch_bounds__(64 * W, 2) void k_attn_tiles(AttnArgs a) {
         __builtin_amdgcn_sched_barrier(0);
       }
     };
-    for (uint32_t unit = sg.first; unit < unit_end; unit += 2) {
+    for (uint32_t unit = unit0; unit < unit_end; unit += 2) {
       step(unit, 0, s_k0, s_v0, s_k1, s_v1);
       if (unit + 1 < unit_end) step(unit + 1, 1, s_k1, s_v1, s_k0, s_v0);
     }
     wait_loads();     // nothing is on its way to LDS any more,
     __syncthreads();  // s_odd is settled, and every stage is free for the next segment
     if (s_odd && any)
-      for (uint32_t unit = max(sg.first, sg.open >> KT_LOG); unit < unit_end; ++unit)
+      for (uint32_t unit = max(unit0, sg.open >> KT_LOG); unit < unit_end; ++unit)
         add_apart<T, MT>(a, sg, vc, unit << KT_LOG, min((unit + 1) << KT_LOG, sg.klim), token, [&](const T *v, uint32_t seen) {
 #pragma unroll
           for (uint32_t j = 0; j < ND; ++j)
@@ -922,11 +928,11 @@ __global__ __launch_bounds__(64 * W, 2) void k_attn_tiles(AttnArgs a) {
 // run blockIdx.y.  D / 4 threads have a row, four elements each.  Small tiles
 // are cut into many parts and are few: a workgroup takes one row, and its
 // threads' groups every SLOTS-th part; large ones come in two parts or three:
-// a group takes four rows, whose loads are under way together.
+// a group takes two rows, whose loads are under way together.
 template <typename T, uint32_t D, uint32_t M>
 __global__ __launch_bounds__(AT_BLOCK) void k_attn_join(AttnArgs a) {
-  constexpr uint32_t TPR = D / 4, SLOTS = AT_BLOCK / TPR, R = join_rows(M, D) == 1 ? 1 : 4;
-  constexpr uint32_t U = R == 1 ? 4 : 2;  // parts whose loads are under way together
+  constexpr uint32_t TPR = D / 4, SLOTS = AT_BLOCK / TPR, R = join_rows(M, D) == 1 ? 1 : 2;
+  constexpr uint32_t U = 4;  // parts whose loads are under way together
   constexpr uint64_t SIZE = M * (D + 2);
   __shared__ f32x4 s_o[R == 1 ? AT_BLOCK : 1];
   __shared__ float s_top[SLOTS], s_sum[SLOTS];
