@@ -40,9 +40,13 @@ constexpr uint32_t AT_BLOCK = 256, AT_WAVES = 4;
 constexpr uint32_t AT_REQ = 1024;    // requests of one launch (their units' sums lie in LDS)
 constexpr uint32_t AT_TILE = 32;     // keys a wave takes at once
 constexpr uint32_t AT_KT_LOG = 7;    // log2 of a unit's keys (AT_WAVES tiles)
-#ifndef AT_HEAD
-#define AT_HEAD 4u
-#endif
+// Units that stand for what a row tile costs k_attn_tiles besides its keys.
+// None: 765 us for a prompt of 8,192 tokens, as the runs of many short row
+// tiles end last; 2: 676, 4: 608, 8: 608.
+constexpr uint32_t AT_HEAD = 4;
+// Sums of 16 weights of a lane past which k_attn_tiles brings the maximum up to
+// date: no weight of float16 overflows below.
+constexpr float AT_GROWN = 16384.0f;
 constexpr uint32_t AT_RUNS = 512;    // workgroups of a launch, over all heads
 
 // Rows that a workgroup of k_attn_join takes.
@@ -720,6 +724,7 @@ __global__ __launch_bounds__(64 * W, 2) void k_attn_tiles(AttnArgs a) {
     any = __any(any);
     f32x4 acc[MT][ND];
     float m[MT], l[MT];
+    bool fresh = true;
 #pragma unroll
     for (uint32_t i = 0; i < MT; ++i) {
       m[i] = -INFINITY;
@@ -773,21 +778,6 @@ __global__ __launch_bounds__(64 * W, 2) void k_attn_tiles(AttnArgs a) {
 #pragma unroll
         for (uint32_t e = 0; e < NS; ++e) kf[k & 1][e] = *reinterpret_cast<const T8 *>(s_k + k_at[e] + 16 * k * D);
       };
-      f32x4 s[MT][KT / 16];
-      read_k(0);
-#pragma unroll
-      for (uint32_t k = 0; k < KT / 16; ++k) {
-        if (k + 1 < KT / 16) read_k(k + 1);
-        __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-        for (uint32_t i = 0; i < MT; ++i) s[i][k] = f32x4{};
-#pragma unroll
-        for (uint32_t e = 0; e < NS; ++e)
-#pragma unroll
-          for (uint32_t i = 0; i < MT; ++i) s[i][k] = Mma<T>::mul(kf[k & 1][e], q[i][e], s[i][k]);
-        __builtin_amdgcn_sched_barrier(0);
-      }
-      look(min(unit + 2, unit_end - 1));
       constexpr uint32_t VG = ND < 4 ? ND : 4, VN = ND / VG * (KT / 32);  // V's fragments of a group; groups
       T8 vf[2][VG];
       const auto read_v = [&](uint32_t n) {
@@ -798,52 +788,76 @@ __global__ __launch_bounds__(64 * W, 2) void k_attn_tiles(AttnArgs a) {
           vf[n & 1][e] = __builtin_bit_cast(T8, turned(p, p + 16 * D));
         }
       };
-      read_v(0);
-      __builtin_amdgcn_sched_barrier(0);
-      if (ends || hidden) {
-        uint64_t shown = ~uint64_t(0);
-        for (uint32_t e = 0; e < KT / 8; ++e)
-          if (hidden >> (8 * e) & 1) shown &= ~(uint64_t(0xFF) << (8 * e));
-#pragma unroll
-        for (uint32_t i = 0; i < MT; ++i) {
-          const uint64_t seen = (seen64(a, L, sg.klim, key0, token[i]) & shown) >> (4 * g);  // a lane's keys are 16 k + 4 g ..+3
-#pragma unroll
-          for (uint32_t k = 0; k < KT / 16; ++k)
-#pragma unroll
-            for (uint32_t e = 0; e < 4; ++e) s[i][k][e] = (seen >> (16 * k + e) & 1) ? s[i][k][e] : -INFINITY;
-        }
-      }
-      float top[MT];
-      bool more_top = false;
-#pragma unroll
-      for (uint32_t i = 0; i < MT; ++i) {
-        top[i] = -INFINITY;
-#pragma unroll
-        for (uint32_t k = 0; k < KT / 16; ++k) top[i] = max2(top[i], max2(max2(s[i][k][0], s[i][k][1]), max2(s[i][k][2], s[i][k][3])));
-        top[i] = max_quarters(top[i]);
-        more_top |= top[i] > m[i];
-      }
-      if (__any(more_top)) {
-#pragma unroll
-        for (uint32_t i = 0; i < MT; ++i) {
-          const float m_new = max2(m[i], top[i]);
-          const float f = m_new == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f((m[i] - m_new) * a.scale2);
-          m[i] = m_new;
-          l[i] *= f;
-#pragma unroll
-          for (uint32_t j = 0; j < ND; ++j) acc[i][j] *= f;
-        }
-      }
-#pragma unroll
-      for (uint32_t i = 0; i < MT; ++i) {
-        const float base = m[i] == -INFINITY ? 0.0f : m[i] * a.scale2;
+      f32x4 s[MT][KT / 16];
+      float add[MT];
+      // Weights are relative to m, which need not be the running maximum: it is
+      // brought up to it while a row has seen no key (`fresh`), and when weights
+      // grow past AT_GROWN; then the tile is done again.  Nearly every tile gets
+      // by without its maximum.
+      for (bool exact = fresh;; exact = true) {
+        read_k(0);
 #pragma unroll
         for (uint32_t k = 0; k < KT / 16; ++k) {
+          if (k + 1 < KT / 16) read_k(k + 1);
+          __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-          for (uint32_t e = 0; e < 4; ++e) s[i][k][e] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i][k][e], a.scale2, -base));
-          l[i] += (s[i][k][0] + s[i][k][1]) + (s[i][k][2] + s[i][k][3]);
+          for (uint32_t i = 0; i < MT; ++i) s[i][k] = f32x4{};
+#pragma unroll
+          for (uint32_t e = 0; e < NS; ++e)
+#pragma unroll
+            for (uint32_t i = 0; i < MT; ++i) s[i][k] = Mma<T>::mul(kf[k & 1][e], q[i][e], s[i][k]);
+          __builtin_amdgcn_sched_barrier(0);
         }
+        read_v(0);
+        __builtin_amdgcn_sched_barrier(0);
+        if (ends || hidden) {
+          uint64_t shown = ~uint64_t(0);
+          for (uint32_t e = 0; e < KT / 8; ++e)
+            if (hidden >> (8 * e) & 1) shown &= ~(uint64_t(0xFF) << (8 * e));
+#pragma unroll
+          for (uint32_t i = 0; i < MT; ++i) {
+            const uint64_t seen = (seen64(a, L, sg.klim, key0, token[i]) & shown) >> (4 * g);  // a lane's keys are 16 k + 4 g ..+3
+#pragma unroll
+            for (uint32_t k = 0; k < KT / 16; ++k)
+#pragma unroll
+              for (uint32_t e = 0; e < 4; ++e) s[i][k][e] = (seen >> (16 * k + e) & 1) ? s[i][k][e] : -INFINITY;
+          }
+        }
+        if (exact) {
+          bool none = false;
+#pragma unroll
+          for (uint32_t i = 0; i < MT; ++i) {
+            float top = m[i];
+#pragma unroll
+            for (uint32_t k = 0; k < KT / 16; ++k) top = max2(top, max2(max2(s[i][k][0], s[i][k][1]), max2(s[i][k][2], s[i][k][3])));
+            top = max_quarters(top);
+            const float f = top == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f((m[i] - top) * a.scale2);
+            m[i] = top;
+            none |= top == -INFINITY;
+            l[i] *= f;
+#pragma unroll
+            for (uint32_t j = 0; j < ND; ++j) acc[i][j] *= f;
+          }
+          fresh = __any(none);
+        }
+        bool grown = false;
+#pragma unroll
+        for (uint32_t i = 0; i < MT; ++i) {
+          const float base = m[i] == -INFINITY ? 0.0f : m[i] * a.scale2;
+          add[i] = 0.0f;
+#pragma unroll
+          for (uint32_t k = 0; k < KT / 16; ++k) {
+#pragma unroll
+            for (uint32_t e = 0; e < 4; ++e) s[i][k][e] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i][k][e], a.scale2, -base));
+            add[i] += (s[i][k][0] + s[i][k][1]) + (s[i][k][2] + s[i][k][3]);
+          }
+          grown |= add[i] > AT_GROWN;
+        }
+        if (exact || !__any(grown)) break;
       }
+      look(min(unit + 2, unit_end - 1));
+#pragma unroll
+      for (uint32_t i = 0; i < MT; ++i) l[i] += add[i];
       T8 pf[MT][KT / 32];
 #pragma unroll
       for (uint32_t k = 0; k < KT / 32; ++k)
