@@ -620,7 +620,7 @@ __global__ __launch_bounds__(64 * W, 2) void k_attn_tiles(AttnArgs a) {
   __shared__ __attribute__((aligned(1024))) T s_k0[KT * D], s_v0[KT * D], s_k1[KT * D], s_v1[KT * D];
   __shared__ uint64_t s_incl[AT_REQ];
   __shared__ uint64_t s_scan[2 * W + 1];
-  __shared__ uint8_t s_hidden[2][8];     // a tile's groups of eight keys whose page is not in the cache
+  __shared__ uint8_t s_hidden[4][8];  // a tile's groups of eight keys whose page is not in the cache
   __shared__ uint32_t s_odd;               // the segment has infinities or NaN in tiles with masked places
 
   const uint32_t head = blockIdx.x, run = blockIdx.y;
@@ -634,7 +634,7 @@ __global__ __launch_bounds__(64 * W, 2) void k_attn_tiles(AttnArgs a) {
   const char *kc = a.kc + int64_t(head) * a.head_stride * int64_t(sizeof(T));
   const char *vc = a.vc + int64_t(head) * a.head_stride * int64_t(sizeof(T));
   const uint32_t in_page = (1u << a.page_shift) - 1;
-  if (threadIdx.x < 16) (&s_hidden[0][0])[threadIdx.x] = 0;  // (a tile of 32 keys has four groups)
+  if (threadIdx.x < 32) (&s_hidden[0][0])[threadIdx.x] = 0;  // (a tile of 32 keys has four groups)
   // a lane's sources in its loads to LDS, from a group of eight rows' first on:
   // row i * RPI + lane / CH of the group, and the chunk whose place is lane % CH
   uint32_t k_from[GROUPS][LPG], v_from[LPG];
@@ -678,13 +678,13 @@ __global__ __launch_bounds__(64 * W, 2) void k_attn_tiles(AttnArgs a) {
     // this wave's rows of a tile, on their way to LDS: load n of LOADS, K's first.
     // (A page outside the cache reads page 0 and is masked.)
     int64_t from_at[GROUPS];
-    const auto aim = [&](uint32_t unit, uint32_t stage) {
+    const auto aim = [&](uint32_t unit) {
 #pragma unroll
       for (uint32_t gi = 0; gi < GROUPS; ++gi) {
         const uint32_t group = wave * GROUPS + gi, key = (unit << KT_LOG) + 8 * group;
         const bool ok = page[gi] < a.n_pages;
         from_at[gi] = (int64_t(ok ? page[gi] : 0) * a.page_stride + int64_t(key & in_page) * a.token_stride) * int64_t(sizeof(T));
-        if (lane == 0) s_hidden[stage][group] = !ok;
+        if (lane == 0) s_hidden[unit & 3][group] = !ok;
       }
     };
     const auto fetch = [&](uint32_t n, T *k_to, T *v_to) {
@@ -694,17 +694,15 @@ __global__ __launch_bounds__(64 * W, 2) void k_attn_tiles(AttnArgs a) {
       if (n < LOADS / 2) __builtin_amdgcn_global_load_lds((from)(kc + from_at[gi] + k_from[gi][i]), (to)(k_to + row * D), 16, 0, 0);
       else __builtin_amdgcn_global_load_lds((from)(vc + from_at[gi] + v_from[i]), (to)(v_to + row * D), 16, 0, 0);
     };
-    const auto fetch_all = [&](uint32_t unit, T *k_to, T *v_to, uint32_t stage) {
-      aim(min(unit, unit_end - 1), stage);
-#pragma unroll
-      for (uint32_t n = 0; n < LOADS; ++n) fetch(n, k_to, v_to);
-      look(min(unit + 1, unit_end - 1));
-    };
     if (threadIdx.x == 0) s_odd = 0;
     __syncthreads();
     if (unit0 < unit_end) {
       look(unit0);
-      fetch_all(unit0, s_k0, s_v0, 0);
+      aim(unit0);
+#pragma unroll
+      for (uint32_t n = 0; n < LOADS; ++n) fetch(n, s_k0, s_v0);
+      look(min(unit0 + 1, unit_end - 1));
+      aim(min(unit0 + 1, unit_end - 1));
     }
 
     T8 q[MT][NS];
@@ -755,21 +753,24 @@ __global__ __launch_bounds__(64 * W, 2) void k_attn_tiles(AttnArgs a) {
       if (all && __any(bad != 0)) s_odd = 1;  // (every wave that finds some writes the same)
     };
 
-    const auto step = [&](uint32_t unit, uint32_t stage, const T *s_k, T *s_v, T *k_free, T *v_free) {
+    const auto step = [&](uint32_t unit, const T *s_k, T *s_v, T *k_free, T *v_free) {
       wait_loads();  // this wave's rows of the tile are there
       const bool ends = ((unit + 1) << KT_LOG) > sg.open;  // some row does not see some key
-      uint64_t hidden = *reinterpret_cast<const uint64_t *>(s_hidden[stage]);  // (this wave's groups: its own writes)
+      uint64_t hidden = *reinterpret_cast<const uint64_t *>(s_hidden[unit & 3]);  // (this wave's groups: its own writes)
       if (ends || hidden) clean(s_v, ends, hidden);
       __syncthreads();  // everybody's are, and everybody is done with the tile before
-      // (past the segment's last tile, that one again: no branch cuts the products apart)
-      aim(min(unit + 1, unit_end - 1), stage ^ 1);
+      // The next tile's loads, aimed in the step before: what the waves do here
+      // they all do at once, with the matrix cores at rest.  (Past the segment's
+      // last tile they fetch that one again: no branch cuts the products apart.)
 #pragma unroll
       for (uint32_t n = 0; n < LOADS; ++n) fetch(n, k_free, v_free);
+      const uint32_t after = min(unit + 2, unit_end - 1);
       if (!any) {
-        look(min(unit + 2, unit_end - 1));
+        look(after);
+        aim(after);
         return;
       }
-      hidden = *reinterpret_cast<const uint64_t *>(s_hidden[stage]);
+      hidden = *reinterpret_cast<const uint64_t *>(s_hidden[unit & 3]);
       const uint32_t key0 = unit << KT_LOG;
       // Fragments are read a group ahead of the products that use them; left to
       // itself the compiler puts each read right before its use.
@@ -808,6 +809,7 @@ __global__ __launch_bounds__(64 * W, 2) void k_attn_tiles(AttnArgs a) {
             for (uint32_t i = 0; i < MT; ++i) s[i][k] = Mma<T>::mul(kf[k & 1][e], q[i][e], s[i][k]);
           __builtin_amdgcn_sched_barrier(0);
         }
+        look(after);
         read_v(0);
         __builtin_amdgcn_sched_barrier(0);
         if (ends || hidden) {
@@ -855,7 +857,7 @@ __global__ __launch_bounds__(64 * W, 2) void k_attn_tiles(AttnArgs a) {
         }
         if (exact || !__any(grown)) break;
       }
-      look(min(unit + 2, unit_end - 1));
+      aim(after);
 #pragma unroll
       for (uint32_t i = 0; i < MT; ++i) l[i] += add[i];
       T8 pf[MT][KT / 32];
@@ -882,8 +884,8 @@ __global__ __launch_bounds__(64 * W, 2) void k_attn_tiles(AttnArgs a) {
       }
     };
     for (uint32_t unit = unit0; unit < unit_end; unit += 2) {
-      step(unit, 0, s_k0, s_v0, s_k1, s_v1);
-      if (unit + 1 < unit_end) step(unit + 1, 1, s_k1, s_v1, s_k0, s_v0);
+      step(unit, s_k0, s_v0, s_k1, s_v1);
+      if (unit + 1 < unit_end) step(unit + 1, s_k1, s_v1, s_k0, s_v0);
     }
     wait_loads();     // nothing is on its way to LDS any more,
     __syncthreads();  // s_odd is settled, and every stage is free for the next segment
