@@ -126,9 +126,24 @@ __device__ __forceinline__ uint32_t row_tiles(const AttnArgs &a, uint32_t n) {
   return (n * a.grp + a.stride - 1) / a.stride;
 }
 
-// Sums of the requests' units up to and with each, into LDS; returns the total.
+// The requests in line: sums of their units up to and with each.  Up to 64,
+// every wave has them in its lanes, and their lengths too; more are in LDS.
+struct Line {
+  uint64_t total, incl;
+  Lengths L;
+};
 template <uint32_t KT_LOG, uint32_t HEAD, uint32_t NT>
-__device__ __forceinline__ uint64_t scan_units(const AttnArgs &a, uint64_t *incl, uint64_t *sh) {
+__device__ __forceinline__ Line line_up(const AttnArgs &a, uint64_t *incl, uint64_t *sh) {
+  const auto add = [](uint64_t x, uint64_t y) { return x + y; };
+  Line line;
+  if (a.n_req <= 64) {
+    const uint32_t lane = threadIdx.x & 63;
+    line.L = lengths_of(a, min(lane, a.n_req - 1));
+    line.incl = lane < a.n_req ? units_before<KT_LOG, HEAD>(a, line.L, row_tiles(a, line.L.n)) : 0;
+    line.incl = wave_incl_scan(line.incl, uint64_t(0), add);
+    line.total = lane63(line.incl);
+    return line;
+  }
   constexpr uint32_t PER = AT_REQ / NT;
   const uint32_t k = (a.n_req + NT - 1) / NT, r0 = threadIdx.x * k;
   uint64_t u[PER], mine = 0;
@@ -141,15 +156,28 @@ __device__ __forceinline__ uint64_t scan_units(const AttnArgs &a, uint64_t *incl
     }
     mine += u[j];
   }
-  uint64_t total;
-  uint64_t at = block_incl_scan<NT, uint64_t>(mine, 0, [](uint64_t x, uint64_t y) { return x + y; }, sh, total) - mine;
+  uint64_t at = block_incl_scan<NT, uint64_t>(mine, 0, add, sh, line.total) - mine;
 #pragma unroll
   for (uint32_t j = 0; j < PER; ++j) {
     at += u[j];
     if (j < k && r0 + j < a.n_req) incl[r0 + j] = at;
   }
   __syncthreads();
-  return total;
+  return line;
+}
+// Runs that a row tile of n units spans which begins at unit u, in run `run`.
+__device__ __forceinline__ uint32_t parts_of(uint64_t u, uint32_t n, uint64_t per, uint32_t run) {
+  const uint64_t x = u + n - 1;
+  return ((x | per) >> 32 ? uint32_t(x / per) : uint32_t(x) / uint32_t(per)) - run + 1;
+}
+// (a 64-bit division takes some hundred instructions)
+__device__ __forceinline__ uint64_t units_per_run(uint64_t total, uint32_t runs) {
+  const uint64_t x = total + runs - 1;
+  return x >> 32 ? x / runs : uint64_t(uint32_t(x) / runs);
+}
+__device__ __forceinline__ uint32_t lane_of(uint32_t v, uint32_t lane) { return uint32_t(__builtin_amdgcn_readlane(int(v), int(lane))); }
+__device__ __forceinline__ uint64_t lane_of(uint64_t v, uint32_t lane) {
+  return uint64_t(lane_of(uint32_t(v), lane)) | uint64_t(lane_of(uint32_t(v >> 32), lane)) << 32;
 }
 
 // The run's segments one after the other: which request, row tile and units.
@@ -160,17 +188,28 @@ struct Segment {
   uint32_t klim, open;     // keys that any row of the tile sees, and those that all of them see
 };
 template <uint32_t KT_LOG, uint32_t HEAD>
-__device__ __forceinline__ Segment segment_at(const AttnArgs &a, const uint64_t *incl, uint64_t u, uint64_t u_end) {
+__device__ __forceinline__ Segment segment_at(const AttnArgs &a, const Line &line, const uint64_t *incl, uint64_t u, uint64_t u_end) {
   Segment s;
-  uint32_t lo = 0, hi = a.n_req - 1;
-  while (lo < hi) {
-    const uint32_t mid = (lo + hi) / 2;
-    if (incl[mid] > u) hi = mid;
-    else lo = mid + 1;
+  uint64_t before;
+  if (a.n_req <= 64) {
+    s.r = uint32_t(__ffsll((unsigned long long)__ballot(line.incl > u)) - 1);
+    s.L.first = int64_t(lane_of(uint64_t(line.L.first), s.r));
+    s.L.n = lane_of(line.L.n, s.r);
+    s.L.ctx = lane_of(line.L.ctx, s.r);
+    s.L.klen = lane_of(line.L.klen, s.r);
+    before = s.r ? lane_of(line.incl, s.r - 1) : 0;
+  } else {
+    uint32_t lo = 0, hi = a.n_req - 1;
+    while (lo < hi) {
+      const uint32_t mid = (lo + hi) / 2;
+      if (incl[mid] > u) hi = mid;
+      else lo = mid + 1;
+    }
+    s.r = __builtin_amdgcn_readfirstlane(lo);
+    s.L = lengths_of(a, s.r);
+    before = s.r ? incl[s.r - 1] : 0;
   }
-  s.r = __builtin_amdgcn_readfirstlane(lo);
-  s.L = lengths_of(a, s.r);
-  const uint64_t local = u - (s.r ? incl[s.r - 1] : 0);
+  const uint64_t local = u - before;
   uint32_t t = 0, t_hi = row_tiles(a, s.L.n) - 1;
   while (t < t_hi) {  // the last tile that begins at or before `local`
     const uint32_t mid = (t + t_hi + 1) / 2;
@@ -343,8 +382,9 @@ __global__ __launch_bounds__(AT_BLOCK, (D * MT <= 128 ? 3 : D * MT <= 256 ? 2 : 
 
   const uint32_t head = blockIdx.x, run = blockIdx.y;
   const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6, n16 = lane & 15, g = lane >> 4;
-  const uint64_t total = scan_units<AT_KT_LOG, 0, AT_BLOCK>(a, s_incl, s_scan);
-  const uint64_t per = (total + a.runs - 1) / a.runs;
+  const Line line = line_up<AT_KT_LOG, 0, AT_BLOCK>(a, s_incl, s_scan);
+  const uint64_t total = line.total;
+  const uint64_t per = units_per_run(total, a.runs);
   const uint64_t u_end = min(total, (uint64_t(run) + 1) * per);
   uint64_t u = uint64_t(run) * per;
   uint32_t *meta = a.meta + (uint64_t(head) * a.runs + run) * 4;
@@ -354,7 +394,7 @@ __global__ __launch_bounds__(AT_BLOCK, (D * MT <= 128 ? 3 : D * MT <= 256 ? 2 : 
   const char *vc = a.vc + int64_t(head) * a.head_stride * int64_t(sizeof(T));
 
   while (u < u_end) {
-    const Segment sg = segment_at<AT_KT_LOG, 0>(a, s_incl, u, u_end);
+    const Segment sg = segment_at<AT_KT_LOG, 0>(a, line, s_incl, u, u_end);
     const Lengths &L = sg.L;
     const uint32_t r = sg.r, n_units = sg.n_units, first = sg.first, count = sg.count;
     const uint32_t klim = sg.klim, open = sg.open;
@@ -551,7 +591,7 @@ __global__ __launch_bounds__(AT_BLOCK, (D * MT <= 128 ? 3 : D * MT <= 256 ? 2 : 
     if (first == 0 && !whole) {
       left_open = true;
       if (threadIdx.x == 0) {
-        meta[0] = uint32_t((u + n_units - 1) / per) - run + 1;  // parts
+        meta[0] = parts_of(u, n_units, per, run);
         meta[1] = uint32_t(L.first);
         meta[2] = L.n;
         meta[3] = sg.row0;
@@ -625,8 +665,9 @@ __global__ __launch_bounds__(64 * W, 2) void k_attn_tiles(AttnArgs a) {
 
   const uint32_t head = blockIdx.x, run = blockIdx.y;
   const uint32_t lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), n16 = lane & 15, g = lane >> 4;
-  const uint64_t total = scan_units<KT_LOG, AT_HEAD, 64 * W>(a, s_incl, s_scan);
-  const uint64_t per = (total + a.runs - 1) / a.runs;
+  const Line line = line_up<KT_LOG, AT_HEAD, 64 * W>(a, s_incl, s_scan);
+  const uint64_t total = line.total;
+  const uint64_t per = units_per_run(total, a.runs);
   const uint64_t u_end = min(total, (uint64_t(run) + 1) * per);
   uint64_t u = uint64_t(run) * per;
   uint32_t *meta = a.meta + (uint64_t(head) * a.runs + run) * 4;
@@ -660,7 +701,7 @@ __global__ __launch_bounds__(64 * W, 2) void k_attn_tiles(AttnArgs a) {
   }
 
   while (u < u_end) {
-    const Segment sg = segment_at<KT_LOG, AT_HEAD>(a, s_incl, u, u_end);
+    const Segment sg = segment_at<KT_LOG, AT_HEAD>(a, line, s_incl, u, u_end);
     const Lengths &L = sg.L;
     // the table's row, read by scalar loads, whose counter the loads to LDS do not share
     const __attribute__((address_space(4))) int32_t *pages =
@@ -929,7 +970,7 @@ __global__ __launch_bounds__(64 * W, 2) void k_attn_tiles(AttnArgs a) {
     if (sg.first == 0 && !whole) {
       left_open = true;
       if (threadIdx.x == 0) {
-        meta[0] = uint32_t((u + sg.n_units - 1) / per) - run + 1;
+        meta[0] = parts_of(u, sg.n_units, per, run);
         meta[1] = uint32_t(L.first);
         meta[2] = L.n;
         meta[3] = sg.row0;

@@ -222,8 +222,11 @@ PyObject *qk_norm_rope_backward(PyObject *, PyObject *const *a, Py_ssize_t n_arg
   uint64_t bytes = 0;
   if (!c.ready(stream) || f_back_bytes(uint64_t(m.n), uint32_t(m.dim), &bytes)) return not_plain();
   Tensor dq = c.empty({m.n, m.hq, m.dim}, m.type), dk = c.empty({m.n, m.hk, m.dim}, m.type), dwq, dwk;
-  if (m.wq) dwq = c.empty({m.dim}, at::kFloat);
-  if (m.wk) dwk = c.empty({m.dim}, at::kFloat);
+  if (m.wq || m.wk) {
+    const Tensor both = c.empty({8 * m.dim}, at::kByte);
+    if (m.wq) dwq = part_of(both, 0, m.dim, at::kFloat);
+    if (m.wk) dwk = part_of(both, 4 * m.dim, m.dim, at::kFloat);
+  }
   const Tensor ws = c.empty({int64_t(bytes)}, at::kByte);
   const int rc = f_back(dtype_of(m.type), uint64_t(m.n), uint32_t(m.hq), uint32_t(m.hk), uint32_t(m.dim), uint32_t(2 * m.freq->size(0)), m.inter, m.eps,
                         p_gq, c.ts(gq), c.hs(gq), p_gk, c.ts(gk), c.hs(gk), m.p_q, c.ts(m.q), c.hs(m.q), m.p_k, c.ts(m.k), c.hs(m.k), m.p_wq, m.p_wk,
