@@ -44,6 +44,9 @@ constexpr uint32_t AT_KT_LOG = 7;    // log2 of a unit's keys (AT_WAVES tiles)
 // None: 765 us for a prompt of 8,192 tokens, as the runs of many short row
 // tiles end last; 2: 676, 4: 608, 8: 608.
 constexpr uint32_t AT_HEAD = 4;
+// Units of keys of the longest row tiles that are never cut, in k_attn_tiles and
+// k_attn_rows (60 requests of 95 to 120 tokens: SMALL).
+constexpr uint32_t AT_WHOLE = 5, AT_ROWS_WHOLE = 3;
 // Sums of 16 weights of a lane past which k_attn_tiles brings the maximum up to
 // date: no weight of float16 overflows below.
 constexpr float AT_GROWN = 16384.0f;
@@ -107,59 +110,86 @@ __device__ __forceinline__ uint64_t ceil_sum(uint64_t n, uint32_t q) {
   return ((a * (a + 1) / 2) << q) + b * (a + 1);
 }
 
-// Units of a request's first t row tiles, HEAD of each standing for what a row
-// tile costs before and after its keys.  Masks: every row tile spans all
+// Units of a request's first t row tiles.  Masks: every row tile spans all
 // keys.  A chain: tile i ends at key ctx + (i + 1) * tokens, tokens = 2^tok_log.
-template <uint32_t KT_LOG, uint32_t HEAD>
+template <uint32_t KT_LOG>
 __device__ __forceinline__ uint64_t units_before(const AttnArgs &a, const Lengths &L, uint32_t t) {
   constexpr uint32_t KT = 1u << KT_LOG;
-  if (a.mask) return uint64_t(t) * (((L.klen + KT - 1) >> KT_LOG) + HEAD);
-  const uint32_t base = min(L.ctx, a.cap), whole = base >> KT_LOG, rest = base & (KT - 1);
+  // (a request whose tokens pass the table's row: as with masks)
+  if (a.mask || uint64_t(L.ctx) + L.n > a.cap) return uint64_t(t) * ((L.klen + KT - 1) >> KT_LOG);
+  const uint32_t whole = L.ctx >> KT_LOG, rest = L.ctx & (KT - 1);
   if (a.tok_log <= KT_LOG) {
     const uint32_t s = (rest + (1u << a.tok_log) - 1) >> a.tok_log, q = KT_LOG - a.tok_log;
-    return uint64_t(t) * (whole + HEAD) + ceil_sum(s + t, q) - ceil_sum(s, q);
+    return uint64_t(t) * whole + ceil_sum(s + t, q) - ceil_sum(s, q);
   }
   const uint64_t steps = uint64_t(t) * (t + 1) / 2;
-  return uint64_t(t) * (whole + (rest ? 1 : 0) + HEAD) + (steps << (a.tok_log - KT_LOG));
+  return uint64_t(t) * (whole + (rest ? 1 : 0)) + (steps << (a.tok_log - KT_LOG));
 }
 __device__ __forceinline__ uint32_t row_tiles(const AttnArgs &a, uint32_t n) {
   return (n * a.grp + a.stride - 1) / a.stride;
 }
 
-// The requests in line: sums of their units up to and with each.  Up to 64,
-// every wave has them in its lanes, and their lengths too; more are in LDS.
+// The requests in line: sums of their units up to and with each, in a wave's
+// lanes, with their lengths, for up to 64 requests, else in LDS.
 struct Line {
   uint64_t total, incl;
+  uint64_t per;    // units of a run
+  uint32_t head;   // units of every row tile that stand for what it costs besides its keys
+  uint32_t whole;  // row tiles of up to so many units are not cut
   Lengths L;
 };
-template <uint32_t KT_LOG, uint32_t HEAD, uint32_t NT>
+// (a 64-bit division takes some hundred instructions)
+__device__ __forceinline__ uint64_t divide_up(uint64_t total, uint32_t runs) {
+  const uint64_t x = total + runs - 1;
+  return x >> 32 ? x / runs : uint64_t(uint32_t(x) / runs);
+}
+// HEAD counts where runs are long enough to be evened out by it: where they are
+// short it would be most of them.  Row tiles of up to WHOLE units besides it are
+// not cut: the second start and the join cost more than that saves.
+template <uint32_t HEAD, uint32_t WHOLE>
+__device__ __forceinline__ void set_runs(const AttnArgs &a, Line &line, uint64_t units, uint64_t tiles) {
+  line.head = HEAD && units >= uint64_t(2 * HEAD) * a.runs ? HEAD : 0;
+  line.total = units + line.head * tiles;
+  line.per = divide_up(line.total, a.runs);
+  line.whole = WHOLE + line.head;
+}
+template <uint32_t KT_LOG, uint32_t HEAD, uint32_t WHOLE, uint32_t NT>
 __device__ __forceinline__ Line line_up(const AttnArgs &a, uint64_t *incl, uint64_t *sh) {
   const auto add = [](uint64_t x, uint64_t y) { return x + y; };
   Line line;
   if (a.n_req <= 64) {
     const uint32_t lane = threadIdx.x & 63;
     line.L = lengths_of(a, min(lane, a.n_req - 1));
-    line.incl = lane < a.n_req ? units_before<KT_LOG, HEAD>(a, line.L, row_tiles(a, line.L.n)) : 0;
-    line.incl = wave_incl_scan(line.incl, uint64_t(0), add);
-    line.total = lane63(line.incl);
+    const uint32_t t = lane < a.n_req ? row_tiles(a, line.L.n) : 0;
+    const uint64_t units = wave_incl_scan(units_before<KT_LOG>(a, line.L, t), uint64_t(0), add);
+    const uint64_t tiles = HEAD ? wave_incl_scan(uint64_t(t), uint64_t(0), add) : 0;
+    set_runs<HEAD, WHOLE>(a, line, lane63(units), HEAD ? lane63(tiles) : 0);
+    line.incl = units + line.head * tiles;
     return line;
   }
   constexpr uint32_t PER = AT_REQ / NT;
   const uint32_t k = (a.n_req + NT - 1) / NT, r0 = threadIdx.x * k;
-  uint64_t u[PER], mine = 0;
+  uint64_t u[PER], units = 0, tiles = 0;
+  uint32_t t[PER];
 #pragma unroll
   for (uint32_t j = 0; j < PER; ++j) {
-    u[j] = 0;
+    u[j] = t[j] = 0;
     if (j < k && r0 + j < a.n_req) {
       const Lengths L = lengths_of(a, r0 + j);
-      u[j] = units_before<KT_LOG, HEAD>(a, L, row_tiles(a, L.n));
+      t[j] = row_tiles(a, L.n);
+      u[j] = units_before<KT_LOG>(a, L, t[j]);
     }
-    mine += u[j];
+    units += u[j];
+    tiles += t[j];
   }
-  uint64_t at = block_incl_scan<NT, uint64_t>(mine, 0, add, sh, line.total) - mine;
+  uint64_t all_units, all_tiles = 0;
+  uint64_t at = block_incl_scan<NT, uint64_t>(units, 0, add, sh, all_units) - units;
+  if (HEAD) tiles = block_incl_scan<NT, uint64_t>(tiles, 0, add, sh, all_tiles) - tiles;
+  set_runs<HEAD, WHOLE>(a, line, all_units, all_tiles);
+  at += line.head * tiles;
 #pragma unroll
   for (uint32_t j = 0; j < PER; ++j) {
-    at += u[j];
+    at += u[j] + line.head * t[j];
     if (j < k && r0 + j < a.n_req) incl[r0 + j] = at;
   }
   __syncthreads();
@@ -169,11 +199,6 @@ __device__ __forceinline__ Line line_up(const AttnArgs &a, uint64_t *incl, uint6
 __device__ __forceinline__ uint32_t parts_of(uint64_t u, uint32_t n, uint64_t per, uint32_t run) {
   const uint64_t x = u + n - 1;
   return ((x | per) >> 32 ? uint32_t(x / per) : uint32_t(x) / uint32_t(per)) - run + 1;
-}
-// (a 64-bit division takes some hundred instructions)
-__device__ __forceinline__ uint64_t units_per_run(uint64_t total, uint32_t runs) {
-  const uint64_t x = total + runs - 1;
-  return x >> 32 ? x / runs : uint64_t(uint32_t(x) / runs);
 }
 __device__ __forceinline__ uint32_t lane_of(uint32_t v, uint32_t lane) { return uint32_t(__builtin_amdgcn_readlane(int(v), int(lane))); }
 __device__ __forceinline__ uint64_t lane_of(uint64_t v, uint32_t lane) {
@@ -185,9 +210,10 @@ struct Segment {
   Lengths L;
   uint32_t r, row0;        // request, the row tile's first row in it (row: token * group + head)
   uint32_t n_units, first, count;
+  bool skip;               // another run's
   uint32_t klim, open;     // keys that any row of the tile sees, and those that all of them see
 };
-template <uint32_t KT_LOG, uint32_t HEAD>
+template <uint32_t KT_LOG>
 __device__ __forceinline__ Segment segment_at(const AttnArgs &a, const Line &line, const uint64_t *incl, uint64_t u, uint64_t u_end) {
   Segment s;
   uint64_t before;
@@ -213,13 +239,15 @@ __device__ __forceinline__ Segment segment_at(const AttnArgs &a, const Line &lin
   uint32_t t = 0, t_hi = row_tiles(a, s.L.n) - 1;
   while (t < t_hi) {  // the last tile that begins at or before `local`
     const uint32_t mid = (t + t_hi + 1) / 2;
-    if (units_before<KT_LOG, HEAD>(a, s.L, mid) <= local) t = mid;
+    if (units_before<KT_LOG>(a, s.L, mid) + line.head * uint64_t(mid) <= local) t = mid;
     else t_hi = mid - 1;
   }
-  const uint64_t tile_u = units_before<KT_LOG, HEAD>(a, s.L, t);
-  s.n_units = uint32_t(units_before<KT_LOG, HEAD>(a, s.L, t + 1) - tile_u);
-  s.first = uint32_t(local - tile_u);
-  s.count = uint32_t(min(uint64_t(s.n_units - s.first), u_end - u));
+  const uint64_t keys_u = units_before<KT_LOG>(a, s.L, t);
+  s.n_units = uint32_t(units_before<KT_LOG>(a, s.L, t + 1) - keys_u) + line.head;
+  s.first = uint32_t(local - keys_u - line.head * uint64_t(t));
+  // one that is not cut is the run's in which it begins
+  s.skip = s.n_units <= line.whole && s.first;
+  s.count = s.n_units <= line.whole ? s.n_units - s.first : uint32_t(min(uint64_t(s.n_units - s.first), u_end - u));
   s.row0 = t * a.stride;
   s.klim = a.mask ? s.L.klen : uint32_t(min(uint64_t(s.L.klen), uint64_t(s.L.ctx) + (uint64_t(t + 1) << a.tok_log)));
   // (a chain's rows all see the keys up to the tile's first token's)
@@ -382,9 +410,9 @@ __global__ __launch_bounds__(AT_BLOCK, (D * MT <= 128 ? 3 : D * MT <= 256 ? 2 : 
 
   const uint32_t head = blockIdx.x, run = blockIdx.y;
   const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6, n16 = lane & 15, g = lane >> 4;
-  const Line line = line_up<AT_KT_LOG, 0, AT_BLOCK>(a, s_incl, s_scan);
+  const Line line = line_up<AT_KT_LOG, 0, AT_ROWS_WHOLE, AT_BLOCK>(a, s_incl, s_scan);
   const uint64_t total = line.total;
-  const uint64_t per = units_per_run(total, a.runs);
+  const uint64_t per = line.per;
   const uint64_t u_end = min(total, (uint64_t(run) + 1) * per);
   uint64_t u = uint64_t(run) * per;
   uint32_t *meta = a.meta + (uint64_t(head) * a.runs + run) * 4;
@@ -394,7 +422,11 @@ __global__ __launch_bounds__(AT_BLOCK, (D * MT <= 128 ? 3 : D * MT <= 256 ? 2 : 
   const char *vc = a.vc + int64_t(head) * a.head_stride * int64_t(sizeof(T));
 
   while (u < u_end) {
-    const Segment sg = segment_at<AT_KT_LOG, 0>(a, line, s_incl, u, u_end);
+    const Segment sg = segment_at<AT_KT_LOG>(a, line, s_incl, u, u_end);
+    if (sg.skip) {
+      u += sg.count;
+      continue;
+    }
     const Lengths &L = sg.L;
     const uint32_t r = sg.r, n_units = sg.n_units, first = sg.first, count = sg.count;
     const uint32_t klim = sg.klim, open = sg.open;
@@ -665,9 +697,9 @@ __global__ __launch_bounds__(64 * W, 2) void k_attn_tiles(AttnArgs a) {
 
   const uint32_t head = blockIdx.x, run = blockIdx.y;
   const uint32_t lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), n16 = lane & 15, g = lane >> 4;
-  const Line line = line_up<KT_LOG, AT_HEAD, 64 * W>(a, s_incl, s_scan);
+  const Line line = line_up<KT_LOG, AT_HEAD, AT_WHOLE, 64 * W>(a, s_incl, s_scan);
   const uint64_t total = line.total;
-  const uint64_t per = units_per_run(total, a.runs);
+  const uint64_t per = line.per;
   const uint64_t u_end = min(total, (uint64_t(run) + 1) * per);
   uint64_t u = uint64_t(run) * per;
   uint32_t *meta = a.meta + (uint64_t(head) * a.runs + run) * 4;
@@ -701,14 +733,18 @@ __global__ __launch_bounds__(64 * W, 2) void k_attn_tiles(AttnArgs a) {
   }
 
   while (u < u_end) {
-    const Segment sg = segment_at<KT_LOG, AT_HEAD>(a, line, s_incl, u, u_end);
+    const Segment sg = segment_at<KT_LOG>(a, line, s_incl, u, u_end);
+    if (sg.skip) {
+      u += sg.count;
+      continue;
+    }
     const Lengths &L = sg.L;
     // the table's row, read by scalar loads, whose counter the loads to LDS do not share
     const __attribute__((address_space(4))) int32_t *pages =
         (const __attribute__((address_space(4))) int32_t *)(a.table + uint64_t(sg.r) * a.table_stride);
-    // tiles of keys [unit0, unit_end): the segment's units without the row tile's first AT_HEAD
-    const uint32_t unit0 = max(sg.first, AT_HEAD) - AT_HEAD;
-    const uint32_t unit_end = min(max(sg.first + sg.count, AT_HEAD) - AT_HEAD, (sg.klim + KT - 1) >> KT_LOG);
+    // tiles of keys [unit0, unit_end): the segment's units without the row tile's first line.head
+    const uint32_t unit0 = max(sg.first, line.head) - line.head;
+    const uint32_t unit_end = min(max(sg.first + sg.count, line.head) - line.head, (sg.klim + KT - 1) >> KT_LOG);
 
     uint32_t page[GROUPS];  // of this wave's groups in the next tile to fetch
     const auto look = [&](uint32_t unit) {
@@ -1120,6 +1156,10 @@ void launch(const AttnArgs &a, hipStream_t st) {
   else if constexpr (D == 256 && M == 128) k_attn_tiles<T, D, 8, 1, 6><<<grid, 2 * AT_BLOCK, 0, st>>>(a);
   else if constexpr (M <= 128) k_attn_tiles<T, D, 4, M / 64, (D == 256 ? 5 : 6)><<<grid, AT_BLOCK, 0, st>>>(a);
   else k_attn_tiles<T, D, 8, M / 128, 6><<<grid, 2 * AT_BLOCK, 0, st>>>(a);
+  // Nothing to join where no row tile can be long enough to be cut (a chain's
+  // last one counts keys up to its end, past the request's).
+  constexpr uint32_t whole = M <= 32 ? AT_ROWS_WHOLE << AT_KT_LOG : AT_WHOLE << (D == 256 && M == 64 ? 5 : 6);
+  if (uint64_t(a.cap) + (a.mask ? 0 : 1u << a.tok_log) <= whole) return;
   k_attn_join<T, D, M><<<dim3(a.hk, a.runs, M / join_rows(M, D)), AT_BLOCK, 0, st>>>(a);
 }
 template <typename T, uint32_t D>

@@ -539,6 +539,27 @@ def test_tree_attention_bad_pages_and_lengths():
     assert bool((out[4:] == 7).all()) and bool((out[:4] != 7).any())
 
 
+@pytest.mark.parametrize("dim,words", [(64, 0), (64, 1), (128, 0), (128, 1), (256, 0)])
+@pytest.mark.parametrize("hq", [1, 7, 16])
+def test_tree_attention_short_tables(dim, words, hq):
+    """Table rows about as long as the key counts at which row tiles are cut, or a join is needed at all: full to the
+    last key, and with tokens past the row's end."""
+    for keys in (32, 128, 160, 256, 320, 384, 400, 512):
+        for new in ([1, 1], [2, 60], [30, 33]):
+            if keys < 2 * max(new):
+                continue
+            page = 32 if keys % 128 else 128
+            s = attn_inputs(new, [keys - m for m in new], hq, 1, dim, page, BF, words=words, seed=keys)
+            s["table"] = s["table"][:, :keys // page].contiguous()
+            say("short table", dim, words, hq, keys, new)
+            attn_check(s)
+            s["ctx"] += torch.tensor([5, 300], dtype=torch.int32)  # the last tokens' own keys are past the row
+            out, lse = attn_run(s)
+            o, tol, l, lt = ref.attention(s["q"], s["k"], s["v"], s["table"], s["off"], s["ctx"], s["mask"])
+            near(out, o, tol, "out past the row")
+            near(lse, l, lt, "lse past the row")
+
+
 def test_tree_attention_many_requests():
     """More requests than one launch takes, of mixed lengths, most of them short."""
     r = np.random.default_rng(5)
