@@ -21,9 +21,17 @@
 // which is just how the second product, O^T = V^T P^T, reads P.  K's fragment
 // is 16 bytes of one key a lane.  V's needs eight keys of one element: a lane
 // loads D/16 elements of eight keys and turns that block over in registers
-// (one byte permute for two elements).  Keys and values go from HBM to
-// registers without a stop in LDS; the running maximum is one per lane and
-// wave, and the waves join at the end of a run.
+// (one byte permute for two elements).  In k_attn_rows, for few rows, keys and
+// values go from HBM to registers without a stop in LDS, and the waves join at
+// the end of a segment; in k_attn_tiles, for many, they are shared in LDS.
+//
+// Measured on an MI355X, bfloat16, 8 key/value heads of 128 (a copy of the card's
+// memory runs at 4.8 TB/s, a large matrix product at 1,140 to 1,380 TFLOP/s):
+// single tokens are bound by HBM: 128 requests of one on 64 to 32,768 keys, 480 us,
+// 5.8 TB/s read.  Many rows are bound by the matrix cores and the softmax's
+// arithmetic next to them: 32 trees of 64 drafts on 16,384 keys, 610 us, 900
+// TFLOP/s; a prompt of 8,192 tokens, 560 us, 980 TFLOP/s; heads of 64, where a
+// score costs as much softmax for half the product, 700.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -45,7 +53,8 @@ constexpr uint32_t AT_KT_LOG = 7;    // log2 of a unit's keys (AT_WAVES tiles)
 // tiles end last; 2: 676, 4: 608, 8: 608.
 constexpr uint32_t AT_HEAD = 4;
 // Units of keys of the longest row tiles that are never cut, in k_attn_tiles and
-// k_attn_rows (60 requests of 95 to 120 tokens: SMALL).
+// k_attn_rows (74 prompts of 95 to 120 tokens, most row tiles cut by a run's end:
+// 72 us, none cut: 55).
 constexpr uint32_t AT_WHOLE = 5, AT_ROWS_WHOLE = 3;
 // Sums of 16 weights of a lane past which k_attn_tiles brings the maximum up to
 // date: no weight of float16 overflows below.
@@ -1118,11 +1127,26 @@ __global__ __launch_bounds__(AT_BLOCK) void k_attn_join(AttnArgs a) {
 
 uintptr_t addr(const void *p) { return reinterpret_cast<uintptr_t>(p); }
 
-// Rows of a row tile, by the rows that a request has for one key/value head on
-// average: 16 or 32 of k_attn_rows, 64 or 128 of k_attn_tiles.
-uint32_t tile_rows(uint64_t n_tok, uint32_t n_req, uint32_t grp, uint32_t dim) {
+// Rows of a row tile: 16 or 32 (k_attn_rows), 64, 128 or 256 (k_attn_tiles), by
+// the rows that a request has for one key/value head on average.  us a call with
+// each, at 32 requests of 8,192 keys and 8 heads (4 of 256 elements):
+//   rows   heads of 64                 heads of 128                 heads of 256
+//     16   108, 114, 102, 104, 130     215, 213, 197, 198, 190      235, 242, 200, 203
+//     32   132, 120, 104, 107, 130     232, 220, 203, 203, 190      291, 252, 205, 210
+//     64   253, 157, 111, 114, 137     452, 225, 211, 215, 192      462, 320, 222, 221
+//     96   375, 307, 145, 119, 141     676, 593, 241, 226, 205      786, 624, 244, 232
+//    256   997, 589, 306, 212, 195     1788, 868, 511, 333, 294     1877, 922, 449, 363
+// Where row tiles are few they are cut into many parts, and the small tiles'
+// parts are joined sooner: one request of 4 rows and 4,000 keys takes 12, 17, 26,
+// 29, 21, and of 131,072 keys for a single head 38, 40, 114, 119, 86; 8 requests
+// of 1,000 keys take 16, 20, 15, 19, 20.
+uint32_t tile_rows(uint64_t n_tok, uint32_t n_req, uint32_t hk, uint32_t grp, uint32_t dim) {
   const uint64_t rows = std::max<uint64_t>(grp, n_tok * grp / std::max(1u, n_req));
-  return rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : rows <= 128 || dim == 256 ? 128 : 256;
+  if (rows <= 32 && uint64_t(n_req) * hk <= 64) return rows <= 16 ? 16 : 32;
+  if (rows <= 16) return 64;
+  if (dim == 128) return 256;
+  if (rows <= 64) return 64;
+  return rows <= 128 || dim == 256 ? 128 : 256;
 }
 
 struct Plan {
@@ -1131,7 +1155,7 @@ struct Plan {
 };
 Plan plan_of(uint64_t n_tok, uint32_t n_req, uint32_t hq, uint32_t hk, uint32_t dim) {
   Plan p;
-  p.rows = tile_rows(n_tok, n_req, hq / hk, dim);
+  p.rows = tile_rows(n_tok, n_req, hk, hq / hk, dim);
   p.runs = std::max(1u, (p.rows > 128 || (dim == 256 && p.rows == 128) ? AT_RUNS / 2 : AT_RUNS) / hk);
   p.meta_bytes = (uint64_t(hk) * p.runs * 16 + 255) / 256 * 256;
   p.bytes = p.meta_bytes + uint64_t(hk) * p.runs * 2 * p.rows * (dim + 2) * sizeof(float);
@@ -1164,11 +1188,12 @@ void launch(const AttnArgs &a, hipStream_t st) {
 }
 template <typename T, uint32_t D>
 void launch_rows(const AttnArgs &a, uint32_t rows, hipStream_t st) {
-  rows == 16    ? launch<T, D, 16>(a, st)
-  : rows == 32  ? launch<T, D, 32>(a, st)
-  : rows == 64  ? launch<T, D, 64>(a, st)
-  : rows == 128 || D == 256 ? launch<T, D, 128>(a, st)
-                : launch<T, D, (D == 256 ? 128 : 256)>(a, st);
+  if (rows == 16) return launch<T, D, 16>(a, st);
+  if (rows == 32) return launch<T, D, 32>(a, st);
+  if (rows == 64) return launch<T, D, 64>(a, st);
+  if constexpr (D != 128)
+    if (rows == 128) return launch<T, D, 128>(a, st);
+  if constexpr (D != 256) launch<T, D, 256>(a, st);
 }
 template <typename T>
 void launch_dim(const AttnArgs &a, uint32_t dim, uint32_t rows, hipStream_t st) {

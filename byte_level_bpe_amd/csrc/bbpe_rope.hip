@@ -11,8 +11,16 @@
 // one write) and the arithmetic is some ten operations an element.  A lane
 // holds 16 elements of a row as two runs of eight, chosen so that both
 // elements of a pair are in one lane: no exchange but the row's sum over its
-// D/16 lanes.  A workgroup takes one token, with its R/2 sines and cosines
-// made once, by R/2 lanes, for all of the token's heads.
+// D/16 lanes.  A workgroup takes a token, with its R/2 sines and cosines made
+// once, by R/2 lanes, for all of the token's heads.
+//
+// Measured on an MI355X, bfloat16, 32 + 8 heads of 128: forward into a cache,
+// 16,384 tokens, 93 us (403 MB, 4.3 TB/s; a copy reaches 4.8); one token a
+// workgroup and many workgroups hide the loads better than fewer that load
+// ahead (121 to 152 us with 512 to 1,024 workgroups).  Backward, 8,192 tokens,
+// 64 us and 4 for the weights' sums (252 MB, 3.9 TB/s): its sums of the weights'
+// gradients live in registers, which leaves room for two workgroups a compute
+// unit, so it loads ahead.  8 tokens forward: 4.6 us.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>

@@ -560,6 +560,38 @@ def test_tree_attention_short_tables(dim, words, hq):
             near(lse, l, lt, "lse past the row")
 
 
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("new, hq, hk, words", [
+    ([2, 1, 2], 4, 2, 0), ([5, 6], 8, 2, 1), ([1] * 39 + [3], 8, 2, 1), ([1] * 80, 2, 1, 0), ([12, 14], 4, 1, 1),
+    ([25, 30], 8, 2, 0), ([70, 50], 4, 1, 2),
+])
+def test_tree_attention_few_and_many_rows(new, hq, hk, words, dim, dtype):
+    """Requests of 4 to 240 rows each, for the row tiles of every size: right, and blind to what a row does not see."""
+    page = 32
+    ctx = [(77, 0, 45, 131)[r % 4] for r in range(len(new))]
+    say("rows", new[:3], hq, hk, words, dim, dtype)
+    s = attn_inputs(new, ctx, hq, hk, dim, page, dtype, seed=dim + len(new), words=words)
+    clean, lse = attn_check(s)
+    kc, vc, table = s["k"].clone(), s["v"].clone(), s["table"]
+    bad = [math.nan, math.inf, -math.inf, torch.finfo(dtype).max, torch.finfo(dtype).min]
+    for r, (c, m) in enumerate(zip(ctx, new)):
+        for j in range(c + m, -(-(c + m) // page) * page):
+            kc[table[r, j // page], :, j % page] = bad[j % 5]
+            vc[table[r, j // page], :, j % page] = bad[(j + 1) % 5]
+    out, l2 = attn_run(dict(s, k=kc, v=vc))
+    assert torch.equal(out, clean) and torch.equal(lse, l2)
+    n = new[0]
+    j = ctx[0] + n - 1  # the first request's last token
+    vc[table[0, j // page], hk - 1, j % page, 1] = math.inf
+    out, l2 = attn_run(dict(s, k=kc, v=vc))
+    see = torch.from_numpy(ref.visible(ctx[0], n, None if s["mask"] is None else s["mask"][:n].numpy())[:, j]).cuda()
+    want = clean.clone()
+    rows = want[:n, hq - hq // hk:, 1]
+    rows[see] = math.inf
+    assert torch.equal(out, want) and torch.equal(lse, l2)
+
+
 def test_tree_attention_many_requests():
     """More requests than one launch takes, of mixed lengths, most of them short."""
     r = np.random.default_rng(5)
@@ -678,3 +710,18 @@ def test_text_to_attention():
     plan = B.block_tables(off, ctx, free[taken:].contiguous(), table, page, sum(new), depth=depth)
     plan.wait()
     layer(ids[:sum(new)], off, plan, mask.cuda())
+
+
+def test_example():
+    """examples/serving_step.py: an accepted path is the same as a chain (two roundings of the output and of the
+    weights apart: values of order one, bfloat16), and gradients arrive."""
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "serving_step.py")
+    spec = importlib.util.spec_from_file_location("serving_step", path)
+    mod = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(mod)
+    off_by, tree, leaves = mod.main()
+    # each side: half a step of the output, and half a step of every weight on values below 8
+    assert off_by <= 2 * ref.half_step(BF) * (float(tree.float().abs().max()) + 8)
+    assert all(bool(torch.isfinite(t.grad).all()) and bool(t.grad.any()) for t in leaves)
