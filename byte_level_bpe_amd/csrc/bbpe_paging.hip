@@ -10,10 +10,10 @@
 // The work is stores (16 bytes a token, 4 a table entry) behind one scan over
 // the requests.  Up to PG_FOLD requests every workgroup makes that scan for
 // itself and one launch does everything; beyond, a one-workgroup scan goes
-// first.  Measured on an MI355X: 5.6 us for 8 requests of one token, nearly all
-// of it the launch and the chain of three dependent loads; 20.5 us for 4,096
+// first.  Measured on an MI355X: 5.5 us for 8 requests of one token, nearly all
+// of it the launch and the chain of three dependent loads; 18.6 us for 4,096
 // requests and 2.9 million tokens (46 MB, which a fill alone writes in 9 us),
-// of which the scan takes 8.
+// of which the scan, by instructions that every workgroup runs, takes 6.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -25,8 +25,8 @@ namespace bbpe {
 namespace {
 
 // Threads of a workgroup: many for many requests (a wave scans 64 at a time:
-// four rounds for 4,096 with 1,024 threads, 21 us for 700 tokens each, eight
-// with 512, 25 us), few for few (8 requests of 358,400 tokens: 15 us with 256,
+// four rounds for 4,096 with 1,024 threads, 18.6 us for 700 tokens each, eight
+// with 512, 26 us), few for few (8 requests of 358,400 tokens: 15 us with 256,
 // 17 with 512, 18 with 1,024).
 constexpr uint32_t PG_FEW = 256, PG_MANY = 1024, PG_FEW_REQ = 512;
 // Requests that every workgroup scans for itself.
@@ -62,7 +62,7 @@ __device__ __forceinline__ uint32_t pages_for(const TableArgs &a, uint32_t x) {
 
 // offsets that cannot be followed
 __device__ __forceinline__ bool off_broken(const TableArgs &a, int64_t lo, int64_t hi) {
-  return lo < 0 || hi < lo || uint64_t(hi) > a.n_tok;
+  return uint64_t(lo) > uint64_t(hi) || uint64_t(hi) > a.n_tok;  // (a negative one is a large one)
 }
 
 struct Request {
@@ -93,7 +93,7 @@ __device__ __forceinline__ uint32_t need_of(const TableArgs &a, const Request &q
 struct Tally {
   uint32_t first;  // first failed request (~0: none)
   int code;
-  uint64_t pages, tokens;
+  uint32_t pages, tokens;  // (pages handed out once, from fewer than 2^31; tokens up to n_tok)
 };
 __device__ __forceinline__ void settle(const TableArgs &a, const Request &q, uint32_t r, uint32_t need, int code,
                                        uint64_t start, bool write, uint32_t &kept, Tally &t) {
@@ -101,7 +101,7 @@ __device__ __forceinline__ void settle(const TableArgs &a, const Request &q, uin
   kept = code == BBPE_OK ? uint32_t(start < PG_FAILED ? start : PG_FAILED - 1) : PG_FAILED;
   if (code == BBPE_OK) {
     t.pages += need;
-    t.tokens += uint64_t(q.hi - q.lo);
+    t.tokens += uint32_t(q.hi - q.lo);
   } else if (r < t.first) {
     t.first = r;
     t.code = code;
@@ -179,19 +179,21 @@ template <bool FOLDED, uint32_t PG_BLOCK>
 __global__ __launch_bounds__(PG_BLOCK) void k_page_tables(TableArgs a) {
   constexpr uint32_t PG_TILE = PG_BLOCK * PG_TOKENS;  // a workgroup's tokens in one round
   constexpr uint32_t REQS = PG_BLOCK == PG_FEW ? PG_FEW_REQ : PG_FOLD;
-  __shared__ uint64_t sh[PG_BLOCK / 64], s_tally[PG_BLOCK / 64][3];
-  __shared__ uint32_t shm[PG_BLOCK / 64];
+  __shared__ uint64_t s_tally[PG_BLOCK / 64][3];
+  __shared__ uint32_t shm[2 * (PG_BLOCK / 64)];  // the waves' first broken requests, then their sums
   __shared__ uint32_t s_off[FOLDED ? REQS + 1 : 1], s_start[FOLDED ? REQS : 1];
   __shared__ int32_t s_ctx[FOLDED ? REQS : 1];
   const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   constexpr uint32_t WAVES = PG_BLOCK / 64;
   uint32_t good;
   if (FOLDED) {
-    // a wave scans 64 k requests one after the other, 64 at a time; rolled, since
-    // fetching straight-line code takes a small call longer than running it
+    // A wave scans 64 k requests one after the other, 64 at a time; rolled, since
+    // fetching straight-line code takes a small call longer than running it.
+    // Every workgroup does it, so instructions count: sums are 32 bits wide and
+    // stay at 2^32 - 1, past any free list, where they would pass it.
     const uint32_t k = (a.n_req + PG_BLOCK - 1) / PG_BLOCK;
-    uint32_t first = a.n_req;
-    uint64_t sum = 0;
+    const auto add = [](uint32_t u, uint32_t v) { return __builtin_elementwise_add_sat(u, v); };
+    uint32_t first = a.n_req, sum = 0;
     Request next{0, 0, 0};
     if (wave * k * 64 + lane < a.n_req) next = read_request(a, wave * k * 64 + lane);
 #pragma unroll 1
@@ -200,57 +202,67 @@ __global__ __launch_bounds__(PG_BLOCK) void k_page_tables(TableArgs a) {
       const Request q = next;
       if (j + 1 < k && r + 64 < a.n_req) next = read_request(a, r + 64);
       uint32_t need = 0;
+      int code = BBPE_E_INVALID_ARG;
       if (r < a.n_req) {
         const bool broken = off_broken(a, q.lo, q.hi);
         if (broken) first = min(first, r);
-        int code;
         need = need_of(a, q, broken, code);
         s_off[r] = uint32_t(q.lo);  // (read up to the first broken request's: within n_tok, so within 32 bits)
         if (r + 1 == a.n_req) s_off[r + 1] = uint32_t(q.hi);
         s_ctx[r] = q.ctx;
       }
-      const uint64_t incl = wave_incl_scan(uint64_t(need), uint64_t(0), [](uint64_t u, uint64_t v) { return u + v; });
-      const uint64_t at = sum + incl - need;
-      if (r < a.n_req) s_start[r] = at < PG_FAILED ? uint32_t(at) : PG_FAILED - 1;  // (past any free list)
-      sum += lane63(incl);
+      const uint32_t incl = add(sum, wave_incl_scan(need, 0u, add));
+      if (r < a.n_req) s_start[r] = code == BBPE_OK ? min(incl - need, PG_FAILED - 1) : PG_FAILED;
+      sum = lane63(incl);
     }
     first = wave_reduce(first, 0xFFFFFFFFu, [](uint32_t u, uint32_t v) { return min(u, v); });
     if (lane == 63) {
-      sh[wave] = sum;
       shm[wave] = first;
+      shm[WAVES + wave] = sum;
     }
     __syncthreads();
-    uint64_t base = 0;
+    uint32_t base = 0, total = 0;
     good = a.n_req;
 #pragma unroll
     for (uint32_t w = 0; w < WAVES; ++w) {
       good = min(good, shm[w]);
-      base += w < wave ? sh[w] : 0;
+      if (w == wave) base = total;
+      total = add(total, shm[WAVES + w]);
     }
-    // (requests from the first broken offset on fail: the others' sums do not depend on them)
-    Tally t{0xFFFFFFFFu, BBPE_OK, 0, 0};
+    if (blockIdx.x != 0 && total <= a.n_free) {
+      // the list is long enough for all: only what follows a broken offset still fails
 #pragma unroll 1
-    for (uint32_t j = 0; j < k; ++j) {
-      const uint32_t r = (wave * k + j) * 64 + lane;
-      if (r >= a.n_req) break;
-      Request q{0, 0, s_ctx[r]};
-      if (r < good) {
-        q.lo = s_off[r];
-        q.hi = s_off[r + 1];
+      for (uint32_t j = 0; j < k; ++j) {
+        const uint32_t r = (wave * k + j) * 64 + lane;
+        if (r >= a.n_req) break;
+        const uint32_t at = s_start[r];
+        s_start[r] = at == PG_FAILED || r >= good ? PG_FAILED : base + at;
       }
-      int code;
-      const uint32_t need = need_of(a, q, r >= good, code);
-      settle(a, q, r, need, code, base + s_start[r], blockIdx.x == 0, s_start[r], t);
-    }
-    if (blockIdx.x == 0) {
-      // the first failed request with its code in one word, and the sums
-      const auto add = [](uint64_t u, uint64_t v) { return u + v; };
-      const uint64_t key = wave_reduce(uint64_t(t.first) << 8 | uint8_t(-t.code), ~uint64_t(0), [](uint64_t u, uint64_t v) { return u < v ? u : v; });
-      const uint64_t pages = wave_reduce(t.pages, uint64_t(0), add), tokens = wave_reduce(t.tokens, uint64_t(0), add);
-      if (lane == 0) {
-        s_tally[wave][0] = key;
-        s_tally[wave][1] = pages;
-        s_tally[wave][2] = tokens;
+    } else {
+      // (requests from the first broken offset on fail: the others' sums do not depend on them)
+      Tally t{0xFFFFFFFFu, BBPE_OK, 0, 0};
+#pragma unroll 1
+      for (uint32_t j = 0; j < k; ++j) {
+        const uint32_t r = (wave * k + j) * 64 + lane;
+        if (r >= a.n_req) break;
+        Request q{0, 0, s_ctx[r]};
+        if (r < good) {
+          q.lo = s_off[r];
+          q.hi = s_off[r + 1];
+        }
+        int code;
+        const uint32_t need = need_of(a, q, r >= good, code);
+        settle(a, q, r, need, code, uint64_t(base) + s_start[r], blockIdx.x == 0, s_start[r], t);
+      }
+      if (blockIdx.x == 0) {
+        // the first failed request with its code in one word, and the sums
+        const uint64_t key = wave_reduce(uint64_t(t.first) << 8 | uint8_t(-t.code), ~uint64_t(0), [](uint64_t u, uint64_t v) { return u < v ? u : v; });
+        const uint32_t pages = wave_sum(t.pages), tokens = wave_sum(t.tokens);
+        if (lane == 0) {
+          s_tally[wave][0] = key;
+          s_tally[wave][1] = pages;
+          s_tally[wave][2] = tokens;
+        }
       }
     }
     __syncthreads();

@@ -136,6 +136,26 @@ def test_block_tables_failures(n):
     assert got.wait() == (n, n * 20)
 
 
+@pytest.mark.parametrize("n", [400, 3000, 4096])
+def test_block_tables_failures_among_many(n):
+    """The same over several workgroups that each scan all requests: with pages for all of them, and too few."""
+    r = np.random.default_rng(n)
+    new, ctx = r.integers(0, 40, n), r.integers(0, 50, n)
+    off = np.concatenate([[0], np.cumsum(new)])
+    total = int(off[-1])
+    for free in (None, n // 2):
+        say("many", n, free)
+        tables_case(new, ctx, 16, free=free)
+        c = ctx.copy()
+        c[n // 3], c[n // 2], c[n - 2] = -1, 1000, 5000
+        tables_case(new, c, 16, width=7, free=free)
+        for at, v in ((1, -1), (n // 2 + 1, 0), (n // 2 + 1, 2 ** 40), (n - 1, total + 1), (n, -2 ** 63)):
+            say("offset", at, v)
+            o = off.copy()
+            o[at] = v
+            tables_case(new, c, 16, width=7, free=free, q_off=o, n_tokens=total)
+
+
 def test_block_tables_graph_stream_and_outputs():
     """Captured into a graph and replayed with other lengths; on another stream; into given outputs."""
     dev = "cuda"
