@@ -1140,10 +1140,15 @@ uintptr_t addr(const void *p) { return reinterpret_cast<uintptr_t>(p); }
 // parts are joined sooner: one request of 4 rows and 4,000 keys takes 12, 17, 26,
 // 29, 21, and of 131,072 keys for a single head 38, 40, 114, 119, 86; 8 requests
 // of 1,000 keys take 16, 20, 15, 19, 20.
-uint32_t tile_rows(uint64_t n_tok, uint32_t n_req, uint32_t hk, uint32_t grp, uint32_t dim) {
+// Where table rows hold few keys a tile's start and end are most of its time,
+// and rows that a request does not fill are waste; 8 heads of 128 with tiles of
+// 64 and 256: 59 requests of 4 to 22 tokens by 4 query heads on up to 192 keys
+// 19 and 34, up to 900 37 and 55, up to 3,000 46 and 53; 64 of 20 to 60 tokens on
+// up to 1,000 50 and 63; but 64 prompts of 100 to 200 tokens 89 and 76.
+uint32_t tile_rows(uint64_t n_tok, uint32_t n_req, uint32_t hk, uint32_t grp, uint32_t dim, uint64_t keys) {
   const uint64_t rows = std::max<uint64_t>(grp, n_tok * grp / std::max(1u, n_req));
   if (rows <= 32 && uint64_t(n_req) * hk <= 64) return rows <= 16 ? 16 : 32;
-  if (rows <= 16) return 64;
+  if (rows <= 16 || (rows <= 256 && grp <= 64 && keys <= 4096)) return 64;
   if (dim == 128) return 256;
   if (rows <= 64) return 64;
   return rows <= 128 || dim == 256 ? 128 : 256;
@@ -1153,9 +1158,9 @@ struct Plan {
   uint32_t rows, runs;
   uint64_t meta_bytes, bytes;
 };
-Plan plan_of(uint64_t n_tok, uint32_t n_req, uint32_t hq, uint32_t hk, uint32_t dim) {
+Plan plan_of(uint64_t n_tok, uint32_t n_req, uint32_t hq, uint32_t hk, uint32_t dim, uint64_t keys) {
   Plan p;
-  p.rows = tile_rows(n_tok, n_req, hk, hq / hk, dim);
+  p.rows = tile_rows(n_tok, n_req, hk, hq / hk, dim, keys);
   p.runs = std::max(1u, (p.rows > 128 || (dim == 256 && p.rows == 128) ? AT_RUNS / 2 : AT_RUNS) / hk);
   p.meta_bytes = (uint64_t(hk) * p.runs * 16 + 255) / 256 * 256;
   p.bytes = p.meta_bytes + uint64_t(hk) * p.runs * 2 * p.rows * (dim + 2) * sizeof(float);
@@ -1210,7 +1215,9 @@ extern "C" {
 int bbpe_tree_attention_workspace_bytes(uint64_t n_tokens, uint32_t n_req, uint32_t n_q_heads,
                                         const bbpe_paged_cache *cache, uint64_t *out_bytes) {
   if (!out_bytes || !good_cache(cache) || !good_heads(n_q_heads, cache)) return BBPE_E_INVALID_ARG;
-  *out_bytes = plan_of(n_tokens, n_req, n_q_heads, cache->n_kv_heads, cache->head_dim).bytes;
+  // for tables of any width
+  *out_bytes = std::max(plan_of(n_tokens, n_req, n_q_heads, cache->n_kv_heads, cache->head_dim, 0).bytes,
+                        plan_of(n_tokens, n_req, n_q_heads, cache->n_kv_heads, cache->head_dim, ~uint64_t(0)).bytes);
   return BBPE_OK;
 }
 
@@ -1231,7 +1238,7 @@ int bbpe_tree_attention(const void *q, int64_t q_ts, int64_t q_hs, uint64_t n_to
   if ((addr(q) & 1) || (addr(out) & 1) || (addr(d_table) & 3) || (addr(d_q_off) & 7) || (addr(d_ctx_len) & 3) ||
       (addr(d_tree_mask) & 7) || (addr(d_lse) & 3))
     return BBPE_E_INVALID_ARG;
-  const Plan p = plan_of(n_tokens, n_req, n_q_heads, cache->n_kv_heads, cache->head_dim);
+  const Plan p = plan_of(n_tokens, n_req, n_q_heads, cache->n_kv_heads, cache->head_dim, uint64_t(table_width) * cache->page_size);
   if (!d_workspace || (addr(d_workspace) & 255) || workspace_bytes < p.bytes) return BBPE_E_WORKSPACE;
   AttnArgs a{};
   a.q = q;

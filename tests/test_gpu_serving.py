@@ -580,18 +580,21 @@ def test_tree_attention_short_tables(dim, words, hq):
             near(lse, l, lt, "lse past the row")
 
 
-@pytest.mark.parametrize("dtype", [BF, HF])
-@pytest.mark.parametrize("dim", [64, 128, 256])
-@pytest.mark.parametrize("new, hq, hk, words", [
+ROWS = [
     ([2, 1, 2], 4, 2, 0), ([5, 6], 8, 2, 1), ([1] * 39 + [3], 8, 2, 1), ([1] * 80, 2, 1, 0), ([12, 14], 4, 1, 1),
     ([25, 30], 8, 2, 0), ([70, 50], 4, 1, 2),
-])
-def test_tree_attention_few_and_many_rows(new, hq, hk, words, dim, dtype):
-    """Requests of 4 to 240 rows each, for the row tiles of every size: right, and blind to what a row does not see."""
+]
+
+
+def rows_check(new, hq, hk, words, dim, dtype, wide):
     page = 32
     ctx = [(77, 0, 45, 131)[r % 4] for r in range(len(new))]
-    say("rows", new[:3], hq, hk, words, dim, dtype)
+    say("rows", new[:3], hq, hk, words, dim, dtype, wide)
     s = attn_inputs(new, ctx, hq, hk, dim, page, dtype, seed=dim + len(new), words=words)
+    if wide:
+        table = torch.full((len(new), wide // page), -1, dtype=torch.int32)
+        table[:, :s["table"].shape[1]] = s["table"]
+        s["table"] = table
     clean, lse = attn_check(s)
     kc, vc, table = s["k"].clone(), s["v"].clone(), s["table"]
     bad = [math.nan, math.inf, -math.inf, torch.finfo(dtype).max, torch.finfo(dtype).min]
@@ -610,6 +613,22 @@ def test_tree_attention_few_and_many_rows(new, hq, hk, words, dim, dtype):
     rows = want[:n, hq - hq // hk:, 1]
     rows[see] = math.inf
     assert torch.equal(out, want) and torch.equal(lse, l2)
+
+
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("new, hq, hk, words", ROWS)
+def test_tree_attention_few_and_many_rows(new, hq, hk, words, dim, dtype):
+    """Requests of 4 to 240 rows each, for the row tiles of every size: right, and blind to what a row does not see."""
+    rows_check(new, hq, hk, words, dim, dtype, None)
+
+
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("new, hq, hk, words", ROWS)
+def test_tree_attention_few_and_many_rows_in_wide_tables(new, hq, hk, words, dim, dtype):
+    """The same where table rows could hold many keys."""
+    rows_check(new, hq, hk, words, dim, dtype, 5000 // 32 * 32)
 
 
 def test_tree_attention_many_requests():
