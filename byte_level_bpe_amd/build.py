@@ -1,8 +1,10 @@
 """Builds libbbpe.so (the C-ABI library) in this directory with hipcc for
-gfx950, and _serving.so, the binding's short way to it from torch.  Usage: python -m byte_level_bpe_amd.build"""
+gfx950, and, where torch is installed, _serving.so, the binding's short way to
+it from torch.  Usage: python -m byte_level_bpe_amd.build"""
 from __future__ import annotations
 
 import concurrent.futures as cf
+import importlib.util
 import os
 import subprocess
 import sys
@@ -45,7 +47,7 @@ def _serving() -> None:
     import torch
     from torch.utils.cpp_extension import include_paths, library_paths
     tmp = SERVING + ".tmp"
-    cmd = (["g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-w", "-D__HIP_PLATFORM_AMD__=1", "-DUSE_ROCM=1",
+    cmd = (["g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-Wall", "-D__HIP_PLATFORM_AMD__=1", "-DUSE_ROCM=1",
             "-D_GLIBCXX_USE_CXX11_ABI=%d" % torch._C._GLIBCXX_USE_CXX11_ABI, os.path.join(CSRC, "bbpe_torch.cpp"),
             "-I" + sysconfig.get_paths()["include"]] + ["-isystem" + p for p in include_paths(device_type="cuda")] +
            ["-L" + p for p in library_paths(device_type="cuda")] +
@@ -53,24 +55,30 @@ def _serving() -> None:
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError("compile failed: %s\n%s" % (" ".join(cmd), r.stderr))
+    if r.stderr.strip():
+        sys.stderr.write(r.stderr)
     os.replace(tmp, SERVING)
 
 
 def build(verbose: bool = False) -> str:
+    """The library first: it needs no torch, and no failure of the extension takes it away."""
     os.makedirs(BUILD, exist_ok=True)
     with cf.ThreadPoolExecutor(max_workers=min(8, len(SOURCES) + 1)) as ex:
-        serving = ex.submit(_serving)
+        serving = ex.submit(_serving) if importlib.util.find_spec("torch") else None
         objs = list(ex.map(_compile, SOURCES))
-        serving.result()
-    tmp = OUT + ".tmp"
-    # -z defs: a kernel declared but not defined fails the link here, not at load
-    cmd = [HIPCC, "--offload-arch=" + ARCH, "-shared", "-fPIC", "-Wl,-z,defs", "-o", tmp] + objs
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError("link failed: %s\n%s" % (" ".join(cmd), r.stderr))
-    os.replace(tmp, OUT)
-    if verbose:
-        print("built", OUT)
+        tmp = OUT + ".tmp"
+        # -z defs: a kernel declared but not defined fails the link here, not at load
+        cmd = [HIPCC, "--offload-arch=" + ARCH, "-shared", "-fPIC", "-Wl,-z,defs", "-o", tmp] + objs
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError("link failed: %s\n%s" % (" ".join(cmd), r.stderr))
+        os.replace(tmp, OUT)
+        if verbose:
+            print("built", OUT)
+        if serving is None:
+            sys.stderr.write("torch is not installed: _serving.so, for the operators on torch tensors, is not built\n")
+        else:
+            serving.result()
     return OUT
 
 
