@@ -264,9 +264,12 @@ def qk_norm_rope(q, k, q_weight, k_weight, positions, inv_freq, eps: float = 1e-
     by positions * inv_freq (bbpe_qk_norm_rope).  Returns (q_out, k_out).
 
     With a PagedCache, v and slots (block_tables'), keys and values go to their
-    slots, and k_out is None unless given.  Inputs may be strided over tokens
-    and heads; q_out may be q and k_out k.  A weight of None is ones."""
-    if q_out is None and k_out is None and stream is None and (cache is not None or slots is None):
+    slots, and k_out is None unless given; the three come together.  Inputs may
+    be strided over tokens and heads; q_out may be q and k_out k.  A weight of
+    None is ones."""
+    if not (cache is None) == (v is None) == (slots is None):
+        _bad("qk_norm_rope: cache, v and slots are given together or not at all")
+    if q_out is None and k_out is None and stream is None:
         got = (_short.qk_norm_rope(q, k, q_weight, k_weight, positions, inv_freq, eps, interleaved, None, None, None, None)
                if cache is None else
                _short.qk_norm_rope(q, k, q_weight, k_weight, positions, inv_freq, eps, interleaved, v, slots, cache.k,
@@ -276,11 +279,8 @@ def qk_norm_rope(q, k, q_weight, k_weight, positions, inv_freq, eps: float = 1e-
     dev, dt = q.device, q.dtype
     with _On(dev, stream, "qk_norm_rope") as on:
         n, hq, hk, dim, rot, ws, pos, freq = _norm_args("qk_norm_rope", q, k, q_weight, k_weight, positions, inv_freq)
-        if cache is not None:
-            if v is None or slots is None:
-                _bad("qk_norm_rope: a cache wants v and slots")
-            if cache.device != dev or cache.dtype is not dt:
-                _bad("qk_norm_rope: the cache is %s on %s, q %s on %s" % (cache.dtype, cache.device, dt, dev))
+        if cache is not None and (cache.device != dev or cache.dtype is not dt):
+            _bad("qk_norm_rope: the cache is %s on %s, q %s on %s" % (cache.dtype, cache.device, dt, dev))
         if q_out is None:
             q_out = torch.empty((n, hq, dim), dtype=dt, device=dev)
         if k_out is None and cache is None:
