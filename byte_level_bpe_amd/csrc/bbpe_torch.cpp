@@ -2,9 +2,10 @@
 // tensors as documented, on the current device and stream) are checked, their
 // outputs allocated and the library called here, in one step of a microsecond
 // or two where ctypes and tensor methods take fifteen.  Whatever is not plain
-// -- a stream, a mistake -- returns NotImplemented, and serving.py's own code,
-// which says what is wrong, takes it from the start.
+// -- a stream, gradients to be recorded, a mistake -- returns NotImplemented,
+// and serving.py's own code, which says what is wrong, takes it from the start.
 #include <ATen/ATen.h>
+#include <c10/core/GradMode.h>
 #include <c10/hip/HIPStream.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -26,7 +27,8 @@ using at::Tensor;
 struct Call {
   bool plain = true;
   int dev = -1;
-  const Tensor none;
+  // a call whose inputs require grad is not plain
+  bool recorded = c10::GradMode::is_enabled();
 
   // a tensor on the call's device; null where None is allowed and given
   const Tensor *tensor(PyObject *o, bool may_be_none = false) {
@@ -39,7 +41,7 @@ struct Call {
       return nullptr;
     }
     const Tensor &t = THPVariable_Unpack(o);
-    if (!t.is_cuda() || t.layout() != at::kStrided) plain = false;
+    if (!t.is_cuda() || t.layout() != at::kStrided || (recorded && t.requires_grad())) plain = false;
     else if (dev < 0) dev = t.get_device();
     else if (t.get_device() != dev) plain = false;
     return &t;
@@ -213,6 +215,7 @@ PyObject *qk_norm_rope_backward(PyObject *, PyObject *const *a, Py_ssize_t n_arg
   HANDLE_TH_ERRORS
   if (n_args != 10) return not_plain();
   Call c;
+  c.recorded = false;  // (a gradient's inputs may require grad; it is not differentiated again)
   Norm m;
   if (!m.read(c, a, a[6], a[7])) return not_plain();
   const Tensor *gq = c.tensor(a[8]), *gk = c.tensor(a[9]);

@@ -257,6 +257,29 @@ def _norm_args(what, q, k, q_weight, k_weight, positions, inv_freq):
             _dense("inv_freq", inv_freq, torch.float32, (None,), dev))
 
 
+def _wants_grad(*tensors):
+    return torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors)
+
+
+class _QkNormRope(torch.autograd.Function):
+    """qk_norm_rope where gradients are wanted (its forward runs without grad mode, so plainly)."""
+
+    @staticmethod
+    def forward(ctx, q, k, q_weight, k_weight, positions, inv_freq, eps, interleaved):
+        ctx.save_for_backward(q, k, q_weight, k_weight, positions, inv_freq)
+        ctx.how = (eps, interleaved)
+        return qk_norm_rope(q, k, q_weight, k_weight, positions, inv_freq, eps, interleaved)
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, grad_q, grad_k):
+        # (a sum's gradient, for one, is broadcast over the last dimension too)
+        grad_q, grad_k = (g if g.stride(2) == 1 else g.contiguous() for g in (grad_q, grad_k))
+        weights = ctx.saved_tensors[2:4]
+        dq, dk, *dw = qk_norm_rope_backward(grad_q, grad_k, *ctx.saved_tensors, *ctx.how)
+        return (dq, dk, *(d if w is None else d.to(w.dtype) for d, w in zip(dw, weights)), None, None, None, None)
+
+
 def qk_norm_rope(q, k, q_weight, k_weight, positions, inv_freq, eps: float = 1e-6, interleaved: bool = False,
                  q_out=None, k_out=None, v=None, cache=None, slots=None, stream=None):
     """RMS norm of every head's row of q [n, n_q_heads, dim] and k [n,
@@ -266,7 +289,12 @@ def qk_norm_rope(q, k, q_weight, k_weight, positions, inv_freq, eps: float = 1e-
     With a PagedCache, v and slots (block_tables'), keys and values go to their
     slots, and k_out is None unless given; the three come together.  Inputs may
     be strided over tokens and heads; q_out may be q and k_out k.  A weight of
-    None is ones."""
+    None is ones.
+
+    Where grad mode is on and an input requires grad, the outputs carry the
+    gradients of q, k and the weights (once; not those of positions and
+    inv_freq).  Into a cache or into given outputs there are none: such a call
+    is refused."""
     if not (cache is None) == (v is None) == (slots is None):
         _bad("qk_norm_rope: cache, v and slots are given together or not at all")
     if q_out is None and k_out is None and stream is None:
@@ -276,6 +304,13 @@ def qk_norm_rope(q, k, q_weight, k_weight, positions, inv_freq, eps: float = 1e-
                                    cache._p))
         if got is not NotImplemented:
             return got
+    if _wants_grad(q, k, q_weight, k_weight, inv_freq, v):
+        if cache is not None or q_out is not None or k_out is not None or inv_freq.requires_grad:
+            _bad("qk_norm_rope: no gradients into a cache or given outputs, nor of inv_freq; call it under torch.no_grad()")
+        with _On(q.device, stream, "qk_norm_rope") as on:
+            got = _QkNormRope.apply(q, k, q_weight, k_weight, positions, inv_freq, eps, interleaved)
+            on.keep(q, k, q_weight, k_weight, positions, inv_freq)
+        return got
     dev, dt = q.device, q.dtype
     with _On(dev, stream, "qk_norm_rope") as on:
         n, hq, hk, dim, rot, ws, pos, freq = _norm_args("qk_norm_rope", q, k, q_weight, k_weight, positions, inv_freq)
@@ -305,7 +340,8 @@ def qk_norm_rope_backward(grad_q, grad_k, q, k, q_weight, k_weight, positions, i
                           interleaved: bool = False, dq=None, dk=None, workspace=None, stream=None):
     """Gradients of qk_norm_rope's inputs from those of its outputs
     (bbpe_qk_norm_rope_backward): (dq, dk, dq_weight, dk_weight), the weights'
-    in float32, None where the weight is None.  dq may be grad_q, dk grad_k."""
+    in float32, None where the weight is None.  dq may be grad_q, dk grad_k.
+    They carry no gradients of their own."""
     if dq is None and dk is None and workspace is None and stream is None:
         got = _short.qk_norm_rope_backward(q, k, q_weight, k_weight, positions, inv_freq, eps, interleaved, grad_q, grad_k)
         if got is not NotImplemented:
@@ -353,12 +389,16 @@ def tree_attention(q, cache: PagedCache, table, q_off, ctx_len, tree_mask=None, 
     table, q_off, ctx_len: block_tables' arguments (ctx_len: before the new
     tokens); tree_mask: int64 [n_tokens, words], bit j of row i set where token i
     sees new token j of its request; without it, tokens see themselves and those
-    before; scale: dim ** -0.5 by default; lse: float32 [n_tokens, n_q_heads]."""
+    before; scale: dim ** -0.5 by default; lse: float32 [n_tokens, n_q_heads].
+    It has no gradient: where grad mode is on, inputs that require grad are
+    refused."""
     if out is None and lse is None and workspace is None and stream is None:
         got = _short.tree_attention(q, cache.k, cache._p, table, q_off, ctx_len, tree_mask,
                                     cache.head_dim ** -0.5 if scale is None else scale, return_lse)
         if got is not NotImplemented:
             return got if return_lse else got[0]
+    if _wants_grad(q, cache.k, cache.v):
+        _bad("tree_attention: it has no gradient, and an input requires grad; call it under torch.no_grad()")
     dev, dt = q.device, q.dtype
     with _On(dev, stream, "tree_attention") as on:
         if q.dim() != 3 or dt is not cache.dtype or dev != cache.device or q.shape[2] != cache.head_dim:

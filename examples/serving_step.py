@@ -44,21 +44,6 @@ class Layer:
         return B.tree_attention(q, cache, table, off, ctx, tree_mask=tree)
 
 
-class NormRotate(torch.autograd.Function):
-    """qk_norm_rope for training."""
-
-    @staticmethod
-    def forward(ctx, q, k, wq, wk, positions, inv_freq):
-        ctx.save_for_backward(q, k, wq, wk, positions, inv_freq)
-        return B.qk_norm_rope(q, k, wq, wk, positions, inv_freq)
-
-    @staticmethod
-    def backward(ctx, gq, gk):
-        q, k, wq, wk, positions, inv_freq = ctx.saved_tensors
-        dq, dk, dwq, dwk = B.qk_norm_rope_backward(gq.contiguous(), gk.contiguous(), q, k, wq, wk, positions, inv_freq)
-        return dq, dk, dwq.to(wq.dtype), dwk.to(wk.dtype), None, None
-
-
 def offsets(counts):
     out = torch.zeros(len(counts) + 1, dtype=torch.int64)
     out[1:] = torch.tensor(counts).cumsum(0)
@@ -121,7 +106,7 @@ def main():
     # training: gradients through the norm and the rotation
     q, k, _ = layer.qkv(chain_ids)
     leaves = [t.detach().clone().requires_grad_() for t in (q, k, layer.wq, layer.wk)]
-    out = NormRotate.apply(*leaves, plan.positions, layer.inv_freq)
+    out = B.qk_norm_rope(*leaves, plan.positions, layer.inv_freq)
     loss = sum((o.float() * torch.randn(o.shape, generator=g, device="cuda")).sum() for o in out)
     loss.backward()
     print("gradient norms: " + ", ".join("%.3g" % t.grad.float().norm().item() for t in leaves))

@@ -33,3 +33,20 @@ def test_norm_into_a_cache_wants_all_of_it():
         refuses(lambda: B.qk_norm_rope(*norm_args(), **kw), "given together")
     refuses(lambda: B.qk_norm_rope(*norm_args(), cache=c, v=v, slots=slots), "tensors on a GPU")
     refuses(lambda: B.qk_norm_rope(*norm_args()), "tensors on a GPU")
+
+
+@pytest.mark.parametrize("grad", ["q", "k", "wq", "wk"])
+def test_lost_gradients_are_refused(grad):
+    """Forms without a gradient refuse inputs that require one, unless grad mode is off."""
+    v, slots, c = torch.zeros(3, 2, 64, dtype=BF), torch.zeros(3, dtype=torch.int64), cache()
+    a = norm_args((grad,))
+    refuses(lambda: B.qk_norm_rope(*a, cache=c, v=v, slots=slots), "no_grad")
+    refuses(lambda: B.qk_norm_rope(*a, q_out=torch.zeros(3, 4, 64, dtype=BF)), "no_grad")
+    refuses(lambda: B.qk_norm_rope(*a, k_out=torch.zeros(3, 2, 64, dtype=BF)), "no_grad")
+    refuses(lambda: B.qk_norm_rope(*a[:5], a[5].clone().requires_grad_()), "no_grad")
+    table, off, ctx = torch.zeros(2, 4, dtype=torch.int32), torch.zeros(3, dtype=torch.int64), torch.zeros(2, dtype=torch.int32)
+    attend = lambda: B.tree_attention(a[0], c, table, off, ctx)  # noqa: E731
+    refuses(attend, "no_grad" if grad == "q" else "tensors on a GPU")
+    with torch.no_grad():
+        refuses(lambda: B.qk_norm_rope(*a, cache=c, v=v, slots=slots), "tensors on a GPU")
+        refuses(attend, "tensors on a GPU")
