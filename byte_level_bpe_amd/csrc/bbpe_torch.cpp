@@ -110,11 +110,12 @@ PyObject *block_tables(PyObject *, PyObject *const *a, Py_ssize_t n_args) {
   const void *p_depth = c.flat(depth, at::kInt, n_tok);
   void *p_table = c.table(table, n), *stream;
   if (!c.ready(stream)) return not_plain();
-  // five small outputs that live and die together: one allocation
-  const int64_t at_slots = 32, at_pos = at_slots + up16(8 * n_tok), at_req = at_pos + up16(4 * n_tok), at_seq = at_req + up16(4 * n_tok);
-  const Tensor all = c.empty({at_seq + 4 * n}, at::kByte);
-  Tensor status = part_of(all, 0, 4, at::kLong), slots = part_of(all, at_slots, n_tok, at::kLong), pos = part_of(all, at_pos, n_tok, at::kInt),
-         req = part_of(all, at_req, n_tok, at::kInt), seq = part_of(all, at_seq, n, at::kInt);
+  // the tokens' outputs, which live and die together, in one allocation; the
+  // requests' in another: a program keeps seq_len as its next context lengths
+  const int64_t at_pos = up16(8 * n_tok), at_req = at_pos + up16(4 * n_tok), at_seq = 32;
+  const Tensor tokens = c.empty({at_req + 4 * n_tok}, at::kByte), requests = c.empty({at_seq + 4 * n}, at::kByte);
+  Tensor slots = part_of(tokens, 0, n_tok, at::kLong), pos = part_of(tokens, at_pos, n_tok, at::kInt), req = part_of(tokens, at_req, n_tok, at::kInt),
+         status = part_of(requests, 0, 4, at::kLong), seq = part_of(requests, at_seq, n, at::kInt);
   const int rc = f_tables(static_cast<const int64_t *>(p_off), static_cast<const int32_t *>(p_ctx), uint32_t(n),
                           static_cast<const int32_t *>(p_free), uint64_t(free_pages->size(0)), static_cast<int32_t *>(p_table),
                           uint64_t(table->stride(0)), uint32_t(table->size(1)), uint32_t(page), uint64_t(n_tok),

@@ -193,11 +193,10 @@ def block_tables(q_off, ctx_len, free_pages, table, page_size: int, n_tokens: in
         if n_tokens < 0 or page_size <= 0:
             _bad("block_tables: n_tokens %d, page_size %d" % (n_tokens, page_size))
         if out is None:
-            slots = torch.empty(n_tokens, dtype=torch.int64, device=dev)
-            i32 = torch.empty(2 * ((n_tokens + 3) // 4 * 4) + n, dtype=torch.int32, device=dev)
             up = (n_tokens + 3) // 4 * 4
-            out = BlockTables(slots, i32[:n_tokens], i32[up:up + n_tokens], i32[2 * up:],
-                              torch.empty(4, dtype=torch.int64, device=dev))
+            i32 = torch.empty(up + n_tokens, dtype=torch.int32, device=dev)
+            out = BlockTables(torch.empty(n_tokens, dtype=torch.int64, device=dev), i32[:n_tokens], i32[up:],
+                              torch.empty(n, dtype=torch.int32, device=dev), torch.empty(4, dtype=torch.int64, device=dev))
         lib, need = _lib(), 0
         if n > 4096:
             size = C.c_uint64()
