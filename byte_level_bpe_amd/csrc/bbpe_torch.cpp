@@ -104,7 +104,7 @@ PyObject *block_tables(PyObject *, PyObject *const *a, Py_ssize_t n_args) {
     PyErr_Clear();
     return not_plain();
   }
-  if (!c.plain || ctx->dim() != 1 || ctx->size(0) > 4096 || page <= 0 || page > (1 << 30) || n_tok < 0) return not_plain();
+  if (!c.plain || ctx->dim() != 1 || ctx->size(0) > 4096 || page <= 0 || page > (1 << 30) || n_tok < 0 || n_tok > 0x7FFFFFFF) return not_plain();
   const int64_t n = ctx->size(0);
   const void *p_off = c.flat(q_off, at::kLong, n + 1), *p_ctx = c.flat(ctx, at::kInt, n), *p_free = c.flat(free_pages, at::kInt, -1);
   const void *p_depth = c.flat(depth, at::kInt, n_tok);

@@ -190,7 +190,7 @@ def block_tables(q_off, ctx_len, free_pages, table, page_size: int, n_tokens: in
             _bad("block_tables: table: an int32 tensor [%d, width] with contiguous rows on %s is wanted, got %s %s on %s" %
                  (n, dev, table.dtype, list(table.shape), table.device))
         n_tokens = int(n_tokens)
-        if n_tokens < 0 or page_size <= 0:
+        if not 0 <= n_tokens < 1 << 31 or not 0 < page_size <= 1 << 30:  # (before anything is allocated)
             _bad("block_tables: n_tokens %d, page_size %d" % (n_tokens, page_size))
         if out is None:
             up = (n_tokens + 3) // 4 * 4

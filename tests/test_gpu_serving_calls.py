@@ -33,3 +33,13 @@ def test_lengths_do_not_keep_the_tokens_outputs(on_a_stream):
     assert plan.seq_len.tolist() == [5000, 0] and plan.wait() == (313, 5000)
     assert max(t.untyped_storage().nbytes() for t in (plan.seq_len, plan.status)) < 1000
     assert all(t.data_ptr() % 16 == 0 for t in plan)
+
+
+@pytest.mark.parametrize("tokens,page", [(1 << 31, 16), (1 << 40, 16), (1 << 62, 16), (-1, 16), (5, 0), (5, -16), (5, (1 << 30) + 1), (5, 1 << 32)])
+def test_sizes_are_refused_before_memory_is_taken(tokens, page):
+    say("sizes", tokens, page)
+    args = tables_args(5)[:4]
+    for kw in ({}, dict(workspace=torch.empty(256, dtype=torch.uint8, device="cuda"))):
+        with pytest.raises(B.BBPEError) as e:
+            B.block_tables(*args, page, tokens, **kw)
+        assert e.value.status == B.E_INVALID_ARG
