@@ -226,7 +226,14 @@ class PagedCache:
     """A paged key/value cache over two tensors [n_pages, n_kv_heads,
     page_size, head_dim] of the same type (bfloat16 or float16), shape and
     strides, contiguous in the last dimension.  Views of one allocation will do,
-    as will another order of heads and tokens in memory."""
+    as will another order of heads and tokens in memory.  It is a handle to
+    their memory: other tensors want another PagedCache."""
+
+    def __setattr__(self, name, value):
+        # the kernels' description of the cache is made once, from these
+        if "_p" in self.__dict__:
+            raise AttributeError("PagedCache: %s is fixed; make another PagedCache" % name)
+        super().__setattr__(name, value)
 
     def __init__(self, k, v):
         if k.dim() != 4 or k.dtype not in (torch.bfloat16, torch.float16) or k.shape != v.shape or \

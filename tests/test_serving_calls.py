@@ -50,3 +50,13 @@ def test_lost_gradients_are_refused(grad):
     with torch.no_grad():
         refuses(lambda: B.qk_norm_rope(*a, cache=c, v=v, slots=slots), "tensors on a GPU")
         refuses(attend, "tensors on a GPU")
+
+
+def test_a_paged_cache_is_fixed():
+    """Its description for the kernels is made once: another tensor in its place would leave them at the old memory."""
+    c = cache()
+    p, k = c._p, c.k
+    for name in ("k", "v", "page_size", "n_pages", "dtype", "_s", "_p"):
+        with pytest.raises(AttributeError):
+            setattr(c, name, getattr(c, name))
+    assert c._p == p and c.k is k
