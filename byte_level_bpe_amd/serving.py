@@ -231,7 +231,7 @@ class PagedCache:
 
     def __setattr__(self, name, value):
         # the kernels' description of the cache is made once, from these
-        if "_p" in self.__dict__:
+        if "_p" in self.__dict__ and name in self.__dict__:
             raise AttributeError("PagedCache: %s is fixed; make another PagedCache" % name)
         super().__setattr__(name, value)
 

@@ -60,3 +60,5 @@ def test_a_paged_cache_is_fixed():
         with pytest.raises(AttributeError):
             setattr(c, name, getattr(c, name))
     assert c._p == p and c.k is k
+    c.layer = 3  # a program's own
+    assert c.layer == 3
