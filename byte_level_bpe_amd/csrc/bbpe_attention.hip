@@ -701,7 +701,7 @@ __global__ __launch_bounds__(64 * W, 2) void k_attn_tiles(AttnArgs a) {
   __shared__ __attribute__((aligned(1024))) T s_k0[KT * D], s_v0[KT * D], s_k1[KT * D], s_v1[KT * D];
   __shared__ uint64_t s_incl[AT_REQ];
   __shared__ uint64_t s_scan[2 * W + 1];
-  __shared__ uint8_t s_hidden[4][8];  // a tile's groups of eight keys whose page is not in the cache
+  __shared__ __attribute__((aligned(8))) uint8_t s_hidden[4][8];  // a tile's groups of eight keys whose page is not in the cache
   __shared__ uint32_t s_odd;               // the segment has infinities or NaN in tiles with masked places
 
   const uint32_t head = blockIdx.x, run = blockIdx.y;

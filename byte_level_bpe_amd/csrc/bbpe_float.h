@@ -18,13 +18,17 @@ template <typename T> struct Vec8;
 template <> struct Vec8<__bf16> { typedef bf16x8 type; };
 template <> struct Vec8<_Float16> { typedef f16x8 type; };
 template <> struct Vec8<float> { typedef f32x8 type; };
+// The same in memory, where 16 bytes are all that is asked for (a vector of
+// eight floats would have its accesses taken for 32-byte aligned ones).
+template <typename T> struct Mem8 { typedef typename Vec8<T>::type type __attribute__((aligned(16))); };
+static_assert(alignof(Mem8<float>::type) == 16 && alignof(Mem8<__bf16>::type) == 16, "");
 
 // Eight consecutive elements as they lie in memory.  VEC: p is 16-byte aligned.
 template <typename T>
 __device__ __forceinline__ typename Vec8<T>::type load8_raw(const T *p, bool vec) {
   typename Vec8<T>::type v;
   if (vec) {
-    v = *reinterpret_cast<const typename Vec8<T>::type *>(__builtin_assume_aligned(p, 16));
+    v = *reinterpret_cast<const typename Mem8<T>::type *>(p);
   } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = p[i];
@@ -34,7 +38,7 @@ __device__ __forceinline__ typename Vec8<T>::type load8_raw(const T *p, bool vec
 template <typename T>
 __device__ __forceinline__ void store8_raw(T *p, typename Vec8<T>::type v, bool vec) {
   if (vec) {
-    *reinterpret_cast<typename Vec8<T>::type *>(__builtin_assume_aligned(p, 16)) = v;
+    *reinterpret_cast<typename Mem8<T>::type *>(p) = v;
   } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i) p[i] = v[i];

@@ -5,7 +5,8 @@ torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
 
 import byte_level_bpe_amd as B  # noqa: E402
-from tests.test_gpu_serving import say  # noqa: E402
+from tests import serving_reference as ref  # noqa: E402
+from tests.test_gpu_serving import near, norm_inputs, say  # noqa: E402
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -43,3 +44,37 @@ def test_sizes_are_refused_before_memory_is_taken(tokens, page):
         with pytest.raises(B.BBPEError) as e:
             B.block_tables(*args, page, tokens, **kw)
         assert e.value.status == B.E_INVALID_ARG
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("inter", [False, True])
+def test_norm_rows_and_weights_16_bytes_off(dtype, inter):
+    """Rows, weights and outputs aligned to 16 bytes and to no more, which is all that is asked for."""
+    n, hq, hk, dim, eps = 5, 3, 2, 64, 1e-5
+    say("16 bytes off", dtype, inter)
+    step = 16 // torch.empty(0, dtype=dtype).element_size()
+    wide, dev, w, pos, freq, g = norm_inputs(n, hq, hk, dim, dim, dtype, 29)
+
+    def off(shape):  # 16 bytes into an allocation, rows 16 bytes apart besides their elements
+        *lead, last = shape
+        rows = 1
+        for m in lead:
+            rows *= m
+        store = torch.zeros(rows * (last + step) + step, dtype=dtype, device="cuda")[step:]
+        t = store[:rows * (last + step)].view(*lead, last + step)[..., :last]
+        assert t.data_ptr() % 32 == 16
+        return t
+    x, ws = off((n, hq + 2 * hk, dim)), [off((dim,)).copy_(t) for t in w]
+    x.copy_(dev)
+    q, k = B.qk_norm_rope(x[:, :hq], x[:, hq:hq + hk], *ws, pos.cuda(), freq.cuda(), eps=eps, interleaved=inter, q_out=off((n, hq, dim)),
+                          k_out=off((n, hk, dim)))
+    near(q, *ref.norm_rope(wide[:, :hq], w[0], pos, freq, eps, inter), "q")
+    near(k, *ref.norm_rope(wide[:, hq:hq + hk], w[1], pos, freq, eps, inter), "k")
+    gq, gk = torch.randn(n, hq, dim, generator=g).to(dtype), torch.randn(n, hk, dim, generator=g).to(dtype)
+    gqd, gkd = off((n, hq, dim)).copy_(gq), off((n, hk, dim)).copy_(gk)
+    dq, dk, dwq, dwk = B.qk_norm_rope_backward(gqd, gkd, x[:, :hq], x[:, hq:hq + hk], *ws, pos.cuda(), freq.cuda(), eps=eps, interleaved=inter,
+                                               dq=off((n, hq, dim)), dk=off((n, hk, dim)))
+    for dx, dw, up, xx, ww in ((dq, dwq, gq, wide[:, :hq], w[0]), (dk, dwk, gk, wide[:, hq:hq + hk], w[1])):
+        a, b = ref.norm_rope_grad(up, xx, ww, pos, freq, eps, inter)
+        near(dx, *a, "dx")
+        near(dw, *b, "dw")
