@@ -91,11 +91,14 @@ struct AttnArgs {
   uint32_t runs;           // workgroups of one head
   uint32_t q_vec, out_vec; // rows 16-byte aligned
   uint32_t *meta;          // [hk][runs][4]: the row tile that begins in a run and ends in a later one
+  const uint32_t *after;   // a launch behind others: not 0 where an earlier one met broken offsets
+  uint32_t *broken;        // a launch before others: what the next one reads there
   float *part;             // [hk][runs][2][M][D + 2]: its parts
 };
 
 // One request's lengths, as the kernels use them.
 struct Lengths {
+  bool ok;        // offsets that can be followed
   int64_t first;  // its first token
   uint32_t n;     // new tokens
   uint32_t ctx;   // context; past the table's row: the row's keys
@@ -104,9 +107,9 @@ struct Lengths {
 __device__ __forceinline__ Lengths lengths_of(const AttnArgs &a, uint32_t r) {
   Lengths L;
   const int64_t lo = a.q_off[r], hi = a.q_off[r + 1];
-  const bool ok = lo >= 0 && hi >= lo && uint64_t(hi) <= a.n_tok;
+  L.ok = lo >= 0 && hi >= lo && uint64_t(hi) <= a.n_tok;
   L.first = lo;
-  L.n = ok ? uint32_t(hi - lo) : 0;
+  L.n = L.ok ? uint32_t(hi - lo) : 0;
   const int32_t c = max(a.ctx[r], 0);
   L.ctx = uint32_t(c);
   L.klen = uint32_t(min(int64_t(c) + L.n, int64_t(a.cap)));
@@ -162,6 +165,13 @@ __device__ __forceinline__ void set_runs(const AttnArgs &a, Line &line, uint64_t
   line.per = divide_up(line.total, a.runs);
   line.whole = WHOLE + line.head;
 }
+// Requests from the first broken offset on have no row tiles, in this launch and
+// the ones after it: offsets that decrease would give a token to two requests.
+__device__ __forceinline__ uint32_t good_requests(const AttnArgs &a, uint32_t first) {
+  if (a.after && *a.after) first = 0;
+  if (a.broken && (blockIdx.x | blockIdx.y | threadIdx.x) == 0) *a.broken = first < a.n_req;
+  return first;
+}
 template <uint32_t KT_LOG, uint32_t HEAD, uint32_t WHOLE, uint32_t NT>
 __device__ __forceinline__ Line line_up(const AttnArgs &a, uint64_t *incl, uint64_t *sh) {
   const auto add = [](uint64_t x, uint64_t y) { return x + y; };
@@ -169,7 +179,9 @@ __device__ __forceinline__ Line line_up(const AttnArgs &a, uint64_t *incl, uint6
   if (a.n_req <= 64) {
     const uint32_t lane = threadIdx.x & 63;
     line.L = lengths_of(a, min(lane, a.n_req - 1));
-    const uint32_t t = lane < a.n_req ? row_tiles(a, line.L.n) : 0;
+    const uint64_t bad = __ballot(!line.L.ok);
+    const uint32_t good = good_requests(a, bad ? uint32_t(__ffsll((unsigned long long)bad)) - 1 : a.n_req);
+    const uint32_t t = lane < good ? row_tiles(a, line.L.n) : 0;
     const uint64_t units = wave_incl_scan(units_before<KT_LOG>(a, line.L, t), uint64_t(0), add);
     const uint64_t tiles = HEAD ? wave_incl_scan(uint64_t(t), uint64_t(0), add) : 0;
     set_runs<HEAD, WHOLE>(a, line, lane63(units), HEAD ? lane63(tiles) : 0);
@@ -179,7 +191,7 @@ __device__ __forceinline__ Line line_up(const AttnArgs &a, uint64_t *incl, uint6
   constexpr uint32_t PER = AT_REQ / NT;
   const uint32_t k = (a.n_req + NT - 1) / NT, r0 = threadIdx.x * k;
   uint64_t u[PER], units = 0, tiles = 0;
-  uint32_t t[PER];
+  uint32_t t[PER], good = a.n_req;
 #pragma unroll
   for (uint32_t j = 0; j < PER; ++j) {
     u[j] = t[j] = 0;
@@ -187,7 +199,18 @@ __device__ __forceinline__ Line line_up(const AttnArgs &a, uint64_t *incl, uint6
       const Lengths L = lengths_of(a, r0 + j);
       t[j] = row_tiles(a, L.n);
       u[j] = units_before<KT_LOG>(a, L, t[j]);
+      if (!L.ok) good = min(good, r0 + j);
     }
+  }
+  good = wave_reduce(good, ~0u, [](uint32_t x, uint32_t y) { return min(x, y); });
+  if ((threadIdx.x & 63) == 0) incl[threadIdx.x >> 6] = good;
+  __syncthreads();
+#pragma unroll
+  for (uint32_t w = 0; w < NT / 64; ++w) good = min(good, uint32_t(incl[w]));
+  good = good_requests(a, good);
+#pragma unroll
+  for (uint32_t j = 0; j < PER; ++j) {
+    if (r0 + j >= good) u[j] = t[j] = 0;
     units += u[j];
     tiles += t[j];
   }
@@ -1162,7 +1185,7 @@ Plan plan_of(uint64_t n_tok, uint32_t n_req, uint32_t hq, uint32_t hk, uint32_t 
   Plan p;
   p.rows = tile_rows(n_tok, n_req, hk, hq / hk, dim, keys);
   p.runs = std::max(1u, (p.rows > 128 || (dim == 256 && p.rows == 128) ? AT_RUNS / 2 : AT_RUNS) / hk);
-  p.meta_bytes = (uint64_t(hk) * p.runs * 16 + 255) / 256 * 256;
+  p.meta_bytes = (uint64_t(hk) * p.runs * 16 + 8 + 255) / 256 * 256;  // (and two words between launches)
   p.bytes = p.meta_bytes + uint64_t(hk) * p.runs * 2 * p.rows * (dim + 2) * sizeof(float);
   return p;
 }
@@ -1279,6 +1302,9 @@ int bbpe_tree_attention(const void *q, int64_t q_ts, int64_t q_hs, uint64_t n_to
     a.q_off = d_q_off + r0;
     a.ctx = d_ctx_len + r0;
     a.n_req = std::min(AT_REQ, n_req - r0);
+    uint32_t *const flags = a.meta + uint64_t(a.hk) * a.runs * 4;
+    a.after = r0 ? flags + (r0 / AT_REQ & 1) : nullptr;
+    a.broken = n_req - r0 > AT_REQ ? flags + (r0 / AT_REQ + 1 & 1) : nullptr;
     if (cache->dtype == BBPE_BF16) launch_dim<__bf16>(a, cache->head_dim, p.rows, st);
     else launch_dim<_Float16>(a, cache->head_dim, p.rows, st);
   }

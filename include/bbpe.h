@@ -501,7 +501,9 @@ int bbpe_qk_norm_rope_backward(int dtype, uint64_t n_tokens, uint32_t n_q_heads,
  * Table entries outside the cache, and positions past the row's end, are
  * masked.  Scores, statistics and sums are float; the softmax weights are
  * rounded to the cache's type for the product with the values.  Rows of out
- * and d_lse whose token is in no request are not written.
+ * and d_lse whose token is in no request are not written; a request whose
+ * offsets, or an earlier request's, are negative, decrease or pass n_tokens has
+ * no tokens (as in bbpe_block_tables).
  *
  * head_dim 64, 128 or 256; n_q_heads / n_kv_heads a whole number up to 128;
  * page_size a power of two from 8 to 65536; token_stride from 0 to 2^27 - 1;
