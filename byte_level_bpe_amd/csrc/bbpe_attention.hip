@@ -56,9 +56,6 @@ constexpr uint32_t AT_HEAD = 4;
 // k_attn_rows (74 prompts of 95 to 120 tokens, most row tiles cut by a run's end:
 // 72 us, none cut: 55).
 constexpr uint32_t AT_WHOLE = 5, AT_ROWS_WHOLE = 3;
-// Sums of 16 weights of a lane past which k_attn_tiles brings the maximum up to
-// date: no weight of float16 overflows below.
-constexpr float AT_GROWN = 16384.0f;
 constexpr uint32_t AT_RUNS = 512;    // workgroups of a launch, over all heads
 
 // Rows that a workgroup of k_attn_join takes.
@@ -304,13 +301,27 @@ template <> struct Mma<__bf16> {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(x, y, c, 0, 0, 0);
   }
   static constexpr uint32_t EXP = 0x7F80;  // exponent of infinities and NaN
+  // log2 of the weight of the maximum's key.  float16 has 24 powers of two below
+  // 1 and the least of them without bits to spare: with weights up to 2^7 a
+  // weight keeps its 11 bits down to 2^-21 of the largest, and is lost below
+  // 2^-32 (e^-22), where from 1 on those would be 2^-14 and 2^-25.
+  static constexpr float LIFT = 0.0f;
+  // Sums of 16 weights of a lane past which k_attn_tiles brings the maximum up to
+  // date; no weight of float16 overflows below.
+  static constexpr float GROWN = 16384.0f;
 };
 template <> struct Mma<_Float16> {
   static __device__ __forceinline__ f32x4 mul(f16x8 x, f16x8 y, f32x4 c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_f16(x, y, c, 0, 0, 0);
   }
   static constexpr uint32_t EXP = 0x7C00;
+  static constexpr float LIFT = 7.0f, GROWN = 32768.0f;
 };
+// What a row's weights are relative to, as an exponent of two, from its maximum.
+template <typename T>
+__device__ __forceinline__ float base_of(const AttnArgs &a, float m) {
+  return __builtin_fmaf(m, a.scale2, -Mma<T>::LIFT);
+}
 
 __device__ __forceinline__ float sum8(f32x8 a) {
   return ((a[0] + a[1]) + (a[2] + a[3])) + ((a[4] + a[5]) + (a[6] + a[7]));
@@ -364,8 +375,8 @@ __device__ __forceinline__ uint32_t seen8(const AttnArgs &a, const Lengths &L, u
   return within & (old | (uint32_t(w) & 0xFFu & ~old));
 }
 
-// N elements of one output row from d on, from the sums o relative to the
-// maximum `top` and the softmax sum.  A row that saw nothing: zeros, -inf.
+// N elements of one output row from d on, from the sums o relative to 2^top and
+// the softmax sum.  A row that saw nothing: zeros, -inf.
 template <typename T, uint32_t N>
 __device__ __forceinline__ void finish(const AttnArgs &a, int64_t token, uint32_t h, uint32_t d, const float *o, float top,
                                        float sum, bool with_lse) {
@@ -556,7 +567,7 @@ __global__ __launch_bounds__(AT_BLOCK, (D * MT <= 128 ? 3 : D * MT <= 256 ? 2 : 
 #pragma unroll
           for (uint32_t j = 0; j < VD; ++j) acc[i][j] *= f;
         }
-        const float base = m[i] == -INFINITY ? 0.0f : m[i] * a.scale2;
+        const float base = m[i] == -INFINITY ? 0.0f : base_of<T>(a, m[i]);
         f32x8 p;
 #pragma unroll
         for (uint32_t e = 0; e < 8; ++e) p[e] = __builtin_amdgcn_exp2f(__builtin_fmaf(x[e], a.scale2, -base));
@@ -606,7 +617,7 @@ __global__ __launch_bounds__(AT_BLOCK, (D * MT <= 128 ? 3 : D * MT <= 256 ? 2 : 
     for (uint32_t i = 0; i < MT; ++i) {
       l[i] = sum_quarters(l[i]);
       if (g == 0) {
-        s_m[wave][16 * i + n16] = m[i] == -INFINITY ? m[i] : m[i] * a.scale2;
+        s_m[wave][16 * i + n16] = base_of<T>(a, m[i]);
         s_l[wave][16 * i + n16] = l[i];
       }
     }
@@ -902,7 +913,7 @@ __global__ __launch_bounds__(64 * W, 2) void k_attn_tiles(AttnArgs a) {
       float add[MT];
       // Weights are relative to m, which need not be the running maximum: it is
       // brought up to it while a row has seen no key (`fresh`), and when weights
-      // grow past AT_GROWN; then the tile is done again.  Nearly every tile gets
+      // grow past GROWN; then the tile is done again.  Nearly every tile gets
       // by without its maximum.
       for (bool exact = fresh;; exact = true) {
         read_k(0);
@@ -954,7 +965,7 @@ __global__ __launch_bounds__(64 * W, 2) void k_attn_tiles(AttnArgs a) {
         bool grown = false;
 #pragma unroll
         for (uint32_t i = 0; i < MT; ++i) {
-          const float base = m[i] == -INFINITY ? 0.0f : m[i] * a.scale2;
+          const float base = m[i] == -INFINITY ? 0.0f : base_of<T>(a, m[i]);
           add[i] = 0.0f;
 #pragma unroll
           for (uint32_t k = 0; k < KT / 16; ++k) {
@@ -962,7 +973,7 @@ __global__ __launch_bounds__(64 * W, 2) void k_attn_tiles(AttnArgs a) {
             for (uint32_t e = 0; e < 4; ++e) s[i][k][e] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i][k][e], a.scale2, -base));
             add[i] += (s[i][k][0] + s[i][k][1]) + (s[i][k][2] + s[i][k][3]);
           }
-          grown |= add[i] > AT_GROWN;
+          grown |= add[i] > Mma<T>::GROWN;
         }
         if (exact || !__any(grown)) break;
       }
@@ -1016,7 +1027,7 @@ __global__ __launch_bounds__(64 * W, 2) void k_attn_tiles(AttnArgs a) {
     float *part = a.part + ((uint64_t(head) * a.runs + run) * 2 + (sg.first == 0 ? 1 : 0)) * (M * (D + 2));
 #pragma unroll
     for (uint32_t i = 0; i < MT; ++i) {
-      const float sum = sum_quarters(l[i]), top = m[i] == -INFINITY ? m[i] : m[i] * a.scale2;
+      const float sum = sum_quarters(l[i]), top = base_of<T>(a, m[i]);
       const uint32_t row = 16 * (wave * MT + i) + n16;
       const Row w = row_of(a, sg, row);
       if (!w.live) continue;

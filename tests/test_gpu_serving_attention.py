@@ -56,3 +56,20 @@ def test_requests_behind_a_broken_offset(n, at, value):
     near(out[:served], want, tol, "the requests before")
     near(lse[:served], want_lse, lse_tol, "the requests before")
     assert bool((out[served:] == 7).all()) and bool((lse[served:] == 7).all())
+
+
+@pytest.mark.parametrize("tokens,hq", [(1, 1), (20, 1), (40, 2), (70, 2), (300, 1)])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("below", [10, 14.5])
+def test_small_weights_in_float16(dim, tokens, hq, below):
+    """A first key that takes nearly all of the weight and has no values, in front of keys up to 17.45 below: their
+    weights, down to 2^-25 of the first's, are what the output is made of.  They are held to 2^-32 of it."""
+    say("small weights", dim, tokens, hq, below)
+    ctx = 290 if tokens < 300 else 20
+    s = attn_inputs([tokens], [ctx], hq, 1, dim, 16, HF, seed=dim + tokens)
+    g = torch.Generator().manual_seed(1)
+    s["q"].zero_()[..., 0] = 1
+    s["k"].zero_()[..., 0] = -below - (17.45 - below) * torch.rand(s["k"].shape[:3], generator=g)
+    s["v"].mul_(100)
+    s["k"][s["table"][0, 0], 0, 0], s["v"][s["table"][0, 0], 0, 0] = 0, 0
+    check(s, 1.0, flushed=2.0 ** -8)
