@@ -1174,15 +1174,35 @@ uintptr_t addr(const void *p) { return reinterpret_cast<uintptr_t>(p); }
 // parts are joined sooner: one request of 4 rows and 4,000 keys takes 12, 17, 26,
 // 29, 21, and of 131,072 keys for a single head 38, 40, 114, 119, 86; 8 requests
 // of 1,000 keys take 16, 20, 15, 19, 20.
-// Where table rows hold few keys a tile's start and end are most of its time,
-// and rows that a request does not fill are waste; 8 heads of 128 with tiles of
-// 64 and 256: 59 requests of 4 to 22 tokens by 4 query heads on up to 192 keys
-// 19 and 34, up to 900 37 and 55, up to 3,000 46 and 53; 64 of 20 to 60 tokens on
-// up to 1,000 50 and 63; but 64 prompts of 100 to 200 tokens 89 and 76.
+// Where a call is short a tile's start and end are most of its time, and rows that
+// a request does not fill are waste: tiles of 64 up to so many rows times keys of
+// a table row, over all requests and heads.  What a table row can hold is all
+// that the host knows of the keys.  us with tiles of 64 and of the size below,
+// trees by 4 query heads on contexts of a quarter to all of the row's keys (8
+// heads of 64 and 128, 4 of 256; of 64 with rows <= 128: 128, else 256):
+//   requests x rows, keys   heads of 64        heads of 128       heads of 256
+//     8 x 256, 1,000        22, 26             32, 37             39, 40
+//     8 x 256, 4,000        36, 35             52, 49             57, 54
+//     32 x 96, 500          23, 25             31, 34             36, 43
+//     32 x 96, 4,000        51, 46             93, 84             102, 84
+//     32 x 256, 1,000       46, 53             65, 71             73, 76
+//     32 x 256, 4,000       100, 91            190, 128           204, 148
+//     128 x 96, 1,000       73, 70             110, 111           118, 116
+//     128 x 96, 4,000       201, 157           414, 282           409, 284
+//     128 x 256, 250        89, 77             118, 104           111, 99
+//     128 x 256, 4,000      420, 304           918, 430           907, 579
+// The limits lie a little past where the two meet (at 2^26, and 2^25), since
+// contexts far shorter than the row gain more than full rows lose: 59 trees of 4
+// to 22 tokens on up to 192 keys take 19 and 34.  Heads of 256 on rows of 161 to
+// 320 keys are cut and joined only where tiles of 64 rows have units of 32 keys: 32
+// x 96 rows on 250 keys 30 and 23.
 uint32_t tile_rows(uint64_t n_tok, uint32_t n_req, uint32_t hk, uint32_t grp, uint32_t dim, uint64_t keys) {
   const uint64_t rows = std::max<uint64_t>(grp, n_tok * grp / std::max(1u, n_req));
   if (rows <= 32 && uint64_t(n_req) * hk <= 64) return rows <= 16 ? 16 : 32;
-  if (rows <= 16 || (rows <= 256 && grp <= 64 && keys <= 4096)) return 64;
+  const uint64_t all = std::max<uint64_t>(1, n_tok * grp * hk);
+  const bool brief = rows <= 256 && grp <= 64 && keys <= 4096 && keys <= (dim == 256 ? 1u << 26 : 1u << 27) / all &&
+                     !(dim == 256 && keys > AT_WHOLE * 32 && keys <= AT_WHOLE * 64);
+  if (rows <= 16 || brief) return 64;
   if (dim == 128) return 256;
   if (rows <= 64) return 64;
   return rows <= 128 || dim == 256 ? 128 : 256;

@@ -73,3 +73,25 @@ def test_small_weights_in_float16(dim, tokens, hq, below):
     s["v"].mul_(100)
     s["k"][s["table"][0, 0], 0, 0], s["v"][s["table"][0, 0], 0, 0] = 0, 0
     check(s, 1.0, flushed=2.0 ** -8)
+
+
+@pytest.mark.parametrize("dim,dtype", [(64, BF), (128, HF), (256, BF)])
+def test_the_same_requests_in_tables_of_any_width(dim, dtype):
+    """What a table row could hold decides over the row tiles, together with all rows: the same requests in rows just
+    long enough, and in longer ones, with a workspace of the size that is said to do for every width."""
+    new, ctx, hk, page = [50, 37, 64, 1, 0, 61] * 8, [70, 0, 129, 200, 5, 33] * 8, 32, 16
+    s = attn_inputs(new, ctx, hk, hk, dim, page, dtype, seed=dim)
+    want = dense.attention(s["q"], s["k"], s["v"], s["table"], s["off"], s["ctx"])
+    q, off, c, cache = s["q"].cuda(), s["off"].cuda(), s["ctx"].cuda(), B.PagedCache(on_gpu(s["k"]), on_gpu(s["v"]))
+    size = B.tree_attention_workspace_bytes(q.shape[0], len(new), hk, cache)
+    for keys in (s["table"].shape[1] * page, 320, 336, 512, 1024, 2048, 4096, 4112, 40000):
+        if keys < s["table"].shape[1] * page:
+            continue
+        say("table of", keys, dim, dtype)
+        table = torch.full((len(new), keys // page), -1, dtype=torch.int32)
+        table[:, :s["table"].shape[1]] = s["table"]
+        guard = torch.full((size + 4096,), 77, dtype=torch.uint8, device="cuda")
+        out, lse = B.tree_attention(q, cache, table.cuda(), off, c, return_lse=True, workspace=guard[:size])
+        near(out, want[0], want[1], "out")
+        near(lse, want[2], want[3], "lse")
+        assert bool((guard[size:] == 77).all())
