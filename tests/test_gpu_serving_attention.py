@@ -95,3 +95,106 @@ def test_the_same_requests_in_tables_of_any_width(dim, dtype):
         near(out, want[0], want[1], "out")
         near(lse, want[2], want[3], "lse")
         assert bool((guard[size:] == 77).all())
+
+
+# ---------------------------------------------------------------------------------------------------------------
+# row tiles and runs
+# ---------------------------------------------------------------------------------------------------------------
+def hard_case(new, ctx, hk, grp, dim, page, dtype, words, wide, seed):
+    """Requests among which every kind of tile is: pages outside the cache before and after the context's end, in the
+    first tiles, and everywhere; rows whose mask leaves nothing; scores that jump by some 25 nats for one row late in a
+    request; infinities and NaN in page 0 (which hidden keys are read from), in nobody's pages and past the last keys;
+    and in every third request in one new token's values, for the rows that see it."""
+    s = attn_inputs(new, ctx, hk * grp, hk, dim, page, dtype, seed=seed, words=words, spare=3)
+    r, table = np.random.default_rng(seed), s["table"]
+    # page 0 nobody's
+    spare = sorted(set(range(s["k"].shape[0])) - set(table[table >= 0].tolist()))[0]
+    table[table == 0] = spare
+    n_pages = s["k"].shape[0]
+    if wide:
+        t = torch.full((len(new), wide // page), -1, dtype=torch.int32)
+        t[:, :table.shape[1]] = table
+        s["table"] = table = t
+    bad = [math.nan, math.inf, -math.inf, torch.finfo(dtype).max, torch.finfo(dtype).min]
+    for p in set(range(n_pages)) - set(table[table > 0].tolist()):
+        for j in range(page):
+            s["k"][p, :, j], s["v"][p, :, j] = bad[j % 5], bad[(j + 2) % 5]
+    outside = [-1, n_pages, 2 ** 31 - 1, -2 ** 31]
+    first = 0
+    for i, (m, c) in enumerate(zip(new, ctx)):
+        held = -(-(c + m) // page)
+        place = lambda j: (int(table[i, j // page]), j % page)  # noqa: E731
+        for j in range(c + m, held * page) if i % 2 else ():  # leavings of one request, none of the next
+            p, o = place(j)
+            s["k"][p, :, o], s["v"][p, :, o] = bad[j % 5], bad[(j + 1) % 5]
+        if m and i % 3 == 0:
+            p, o = place(c + m // 2)
+            s["v"][p, 0, o, 1::4] = [math.inf, math.nan, -math.inf][i // 3 % 3]
+        elif m and c > 64:  # for one row, of one head, late
+            p, o = place(c - 3)
+            row = s["q"][first + m // 2, grp - 1].double()
+            s["k"][p, 0, o] = (row * (25 * dim ** 0.5 / row.square().sum())).to(dtype)
+        if i % 4 == 1:  # some pages
+            for b in r.choice(held, max(1, held // 3), replace=False):
+                table[i, b] = outside[int(b) % 4]
+        elif i % 8 == 2:  # the first tiles
+            table[i, :max(1, held * 2 // 3)] = outside[i % 4]
+        elif i % 8 == 6:  # all
+            table[i, :held] = outside[i % 4]
+        if words and m:
+            s["mask"][first + r.choice(m, max(1, m // 5), replace=False)] = 0
+        first += m
+    return s
+
+
+def check_hard(s, times=1):
+    """times: as often every head, which must give the same bits wherever its runs are."""
+    many = dict(s, q=s["q"].repeat(1, times, 1), k=s["k"].repeat(1, times, 1, 1), v=s["v"].repeat(1, times, 1, 1)) if times > 1 else s
+    out, lse = attn_run(many)
+    assert all(torch.equal(x.nan_to_num(0.0), y.nan_to_num(0.0)) for x, y in zip((out, lse), attn_run(many))), "the same bits again"
+    n, hq, dim = s["q"].shape
+    assert torch.equal(out.nan_to_num(0.0), out[:, :hq].nan_to_num(0.0).repeat(1, times, 1)) and torch.equal(lse, lse[:, :hq].repeat(1, times))
+    out, lse = out[:, :hq], lse[:, :hq]
+    o, tol, l, lt = dense.attention(s["q"], s["k"], s["v"], s["table"], s["off"], s["ctx"], s["mask"])
+    near(lse, l, lt, "lse")
+    assert torch.equal(out.isnan().cpu(), o.isnan()), "NaN where the definition has them"
+    near(out.nan_to_num(0.0, math.inf, -math.inf), o.nan_to_num(0.0, math.inf, -math.inf), tol, "out")
+
+
+FEW = ([40, 7, 33, 52, 61, 20, 48, 30], [0, 290, 300, 130, 77, 1000, 260, 64])
+# tokens a request for some 40, 100 and 240 rows by 4 query heads: tiles of 64, of 128 (heads of 128: 256), of 256 (heads of 256: 128)
+MANY = {40: [10, 3, 14, 9, 12, 8, 11, 13, 10], 100: [25, 9, 31, 22, 40, 0, 28, 33, 26], 240: [60, 21, 64, 70, 1, 64, 61, 90, 64]}
+MANY_CTX = [0, 300, 700, 333, 1025, 260, 512, 40, 500]
+
+
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("words", [0, 1])
+@pytest.mark.parametrize("wide", [0, 5120])
+def test_row_tiles_of_several_key_tiles(dim, dtype, words, wide):
+    """One key/value head: short row tiles whole, long ones cut into a unit a run; 4 and 1 query heads a group."""
+    for grp in (4, 1):
+        say("tiles", dim, dtype, words, wide, grp)
+        check_hard(hard_case(*FEW, 1, grp, dim, 32, dtype, words, wide, seed=dim + words + grp))
+
+
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("words", [0, 2])
+@pytest.mark.parametrize("rows", [40, 100, 240])
+@pytest.mark.parametrize("wide", [0, 5120])
+def test_long_runs(wide, rows, dim, dtype, words):
+    """Many key/value heads, so that a head has 4 to 8 runs, each over several requests: row tiles' own cost counted in
+    units, cut anywhere, and every workgroup's stages and flags used again from one segment to the next."""
+    say("runs", wide, rows, dim, dtype, words)
+    check_hard(hard_case(MANY[rows], MANY_CTX, 2, 4, dim, 32, dtype, words, wide, seed=rows + dim + words), times=32)
+
+
+@pytest.mark.parametrize("grp", [33, 64, 65, 100, 128])
+@pytest.mark.parametrize("dim,dtype", [(64, BF), (128, HF), (256, BF)])
+def test_large_groups(grp, dim, dtype):
+    """Up to 128 query heads on a key/value head."""
+    for new, ctx, words, wide in (([1, 1, 3, 1, 1], [0, 290, 70, 33, 600], 0, 0), ([5, 9, 2, 7], [40, 0, 300, 99], 1, 0),
+                                  ([12, 5, 7], [300, 64, 0], 0, 5120), ([12, 5, 7], [300, 64, 0], 1, 5120)):
+        say("groups", grp, dim, dtype, new, words, wide)
+        check_hard(hard_case(new, ctx, 2, grp, dim, 32, dtype, words, wide, seed=grp))

@@ -1,4 +1,6 @@
-"""What calls of the operators between ids and attention keep, and refuse, on the GPU."""
+"""What calls of the operators between ids and attention keep, and refuse, on the GPU, and sizes that
+tests/test_gpu_serving.py leaves out."""
+import numpy as np
 import pytest
 
 torch = pytest.importorskip("torch")
@@ -6,7 +8,7 @@ pytestmark = pytest.mark.gpu
 
 import byte_level_bpe_amd as B  # noqa: E402
 from tests import serving_reference as ref  # noqa: E402
-from tests.test_gpu_serving import near, norm_inputs, say  # noqa: E402
+from tests.test_gpu_serving import near, norm_inputs, say, tables_case  # noqa: E402
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -78,3 +80,52 @@ def test_norm_rows_and_weights_16_bytes_off(dtype, inter):
         a, b = ref.norm_rope_grad(up, xx, ww, pos, freq, eps, inter)
         near(dx, *a, "dx")
         near(dw, *b, "dw")
+
+
+@pytest.mark.parametrize("n", [1, 6, 700, 4500])
+@pytest.mark.parametrize("before", [1, 3, 300, 5000])
+def test_tokens_before_the_first_request(n, before):
+    """Offsets that begin above 0: tokens of no request in front, and behind."""
+    r = np.random.default_rng(n + before)
+    new, ctx = r.integers(0, 40, n), r.integers(0, 90, n)
+    say("before the first", n, before)
+    off = before + np.concatenate([[0], np.cumsum(new)])
+    got, _ = tables_case(new, ctx, 16, q_off=off, n_tokens=int(off[-1]) + 9, depth=bool(n & 1), seed=n)
+    assert got.slots[:before].eq(-1).all() and got.requests[:before].eq(-1).all() and got.positions[:before].eq(0).all()
+
+
+@pytest.mark.parametrize("n,hq,hk,dim,rot,dtype,inter", [(600, 64, 8, 128, 128, torch.bfloat16, False), (1301, 500, 40, 16, 16, torch.float16, True),
+                                                         (2100, 40, 40, 96, 32, torch.float32, False), (1030, 20, 20, 256, 128, torch.bfloat16, True)])
+def test_norm_of_more_rows_than_a_workgroup_has_at_once(n, hq, hk, dim, rot, dtype, inter):
+    """A token's rows in several rounds, forward and backward, with several tokens a batch in the backward pass."""
+    say("many heads", n, hq, hk, dim, rot, dtype, inter)
+    wide, dev, w, pos, freq, g = norm_inputs(n, hq, hk, dim, rot, dtype, 31)
+    args = (dev[:, :hq], dev[:, hq:hq + hk], w[0].cuda(), w[1].cuda(), pos.cuda(), freq.cuda())
+    q, k = B.qk_norm_rope(*args, interleaved=inter)
+    near(q, *ref.norm_rope(wide[:, :hq], w[0], pos, freq, 1e-6, inter), "q")
+    near(k, *ref.norm_rope(wide[:, hq:hq + hk], w[1], pos, freq, 1e-6, inter), "k")
+    gq, gk = torch.randn(n, hq, dim, generator=g).to(dtype), torch.randn(n, hk, dim, generator=g).to(dtype)
+    got = B.qk_norm_rope_backward(gq.cuda(), gk.cuda(), *args, interleaved=inter)
+    for dx, dw, up, x, ww in ((got[0], got[2], gq, wide[:, :hq], w[0]), (got[1], got[3], gk, wide[:, hq:hq + hk], w[1])):
+        a, b = ref.norm_rope_grad(up, x, ww, pos, freq, 1e-6, inter)
+        near(dx, *a, "dx")
+        near(dw, *b, "dw")
+    again = B.qk_norm_rope_backward(gq.cuda(), gk.cuda(), *args, interleaved=inter)
+    assert all(torch.equal(x, y) for x, y in zip(got, again))
+
+
+def test_norm_of_more_tokens_than_a_launch_takes():
+    """2^22 tokens and a few, one head of 16: rows on both sides of the launches' border, and everything else kept."""
+    n, dim, at = (1 << 22) + 70, 16, (1 << 22) - 50
+    say("many tokens", n)
+    g = torch.Generator(device="cuda").manual_seed(1)
+    x = torch.randn(n, 1, dim, generator=g, device="cuda").to(torch.bfloat16)
+    w = [torch.ones(dim, dtype=torch.bfloat16, device="cuda") * s for s in (1.5, 0.75)]
+    pos = torch.arange(n, dtype=torch.int32, device="cuda")
+    freq = torch.tensor([1.0, 0.5, 0.25, 0.125, 2e-2, 1e-2, 1e-3, 1e-4], device="cuda")
+    q, k = B.qk_norm_rope(x, x, *w, pos, freq)
+    for rows in (slice(0, 100), slice(at, n)):
+        for got, ww in ((q, w[0]), (k, w[1])):
+            near(got[rows], *ref.norm_rope(x[rows].cpu(), ww.cpu(), pos[rows].cpu(), freq.cpu(), 1e-6, False), "rows")
+    # the rotation keeps lengths: no row was left out
+    assert bool(((q.float().square().mean(-1) - 2.25).abs() < 0.1).all())
