@@ -84,3 +84,37 @@ def test_gradients_only_where_wanted():
         dw.sum().backward()
     say("the backward kernel by itself takes inputs that require grad")
     assert len(B.qk_norm_rope_backward(torch.ones(n, hq, dim, dtype=BF, device="cuda"), torch.ones(n, hk, dim, dtype=BF, device="cuda"), *a)) == 4
+
+
+def test_gradients_in_a_graph():
+    """Forward and backward captured together and replayed, with other inputs and eager passes between."""
+    say("graph")
+    n, hq, hk, dim = 700, 4, 2, 64
+    _, dev, w, pos, freq, g = norm_inputs(n, hq, hk, dim, dim, BF, 37)
+    x, ws = dev.clone().requires_grad_(), [t.cuda().requires_grad_() for t in w]
+    up = [torch.randn(n, h, dim, generator=g).to(BF).cuda() for h in (hq, hk)]
+    pos, freq = pos.cuda(), freq.cuda()
+
+    def step():
+        out = B.qk_norm_rope(x[:, :hq], x[:, hq:hq + hk], *ws, pos, freq)
+        grads = torch.autograd.grad(out, (x, *ws), up)
+        return [t.detach() for t in out] + list(grads)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        held = step()
+    for _ in range(4):
+        with torch.no_grad():
+            x.mul_(1.25)
+            up[0].add_(0.5)
+            ws[1].neg_()
+        want = step()
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(held, want))
