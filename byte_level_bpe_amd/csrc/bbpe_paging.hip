@@ -10,10 +10,13 @@
 // The work is stores (16 bytes a token, 4 a table entry) behind one scan over
 // the requests.  Up to PG_FOLD requests every workgroup makes that scan for
 // itself and one launch does everything; beyond, a one-workgroup scan goes
-// first.  Measured on an MI355X: 5.5 us for 8 requests of one token, nearly all
-// of it the launch and the chain of three dependent loads; 18.6 us for 4,096
-// requests and 2.9 million tokens (46 MB, which a fill alone writes in 9 us),
-// of which the scan, by instructions that every workgroup runs, takes 6.
+// first.  Measured on an MI355X, captured in a graph: 5.4 us for 8 requests of
+// one token (queued from Python 6.2), nearly all of it the launch and the chain of
+// three dependent loads; 18.2 us for 4,096 requests and 2.9 million tokens (46 MB,
+// which a fill alone writes in 9 us), of which the scan, by instructions that
+// every workgroup runs, takes 6; with the scan as a launch of its own 29.6.  8,192
+// requests of 350 tokens 40 us, 65,536 of 44 173: there the one workgroup's scan
+// is most of it (65,536 of one token 150).
 #include <hip/hip_runtime.h>
 
 #include <algorithm>

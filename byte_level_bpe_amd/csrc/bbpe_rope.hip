@@ -18,9 +18,13 @@
 // 16,384 tokens, 93 us (403 MB, 4.3 TB/s; a copy reaches 4.8); one token a
 // workgroup and many workgroups hide the loads better than fewer that load
 // ahead (121 to 152 us with 512 to 1,024 workgroups).  Backward, 8,192 tokens,
-// 64 us and 4 for the weights' sums (252 MB, 3.9 TB/s): its sums of the weights'
+// 65 us and 5 for the weights' sums (252 MB): its sums of the weights'
 // gradients live in registers, which leaves room for two workgroups a compute
-// unit, so it loads ahead.  8 tokens forward: 4.6 us.
+// unit, so it loads ahead.  8 tokens forward: 4.7 us in the kernel, 5.4 a call.
+// As many elements in other heads, calls queued, forward without a cache and
+// backward in TB/s: 32 + 8 of 128 4.5 and 3.6; 64 + 8 of 128, a workgroup's rows in
+// two rounds, 4.6 and 3.4; 40 + 40 of 128 4.0 and 3.8; 16 + 16 of 256 5.0 and
+// 4.5; 64 + 64 of 64 5.2 and 4.7.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>

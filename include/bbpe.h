@@ -498,6 +498,8 @@ int bbpe_qk_norm_rope_backward(int dtype, uint64_t n_tokens, uint32_t n_q_heads,
  * Every token sees the whole context of its request, the first d_ctx_len[r]
  * positions.  A token that sees nothing, or only scores of minus infinity,
  * gives zeros and -inf.  Masked places contribute nothing whatever they hold.
+ * (Infinite values that a token sees reach its output, as infinity, or as NaN
+ * where its weight has been rounded to zero.)
  * Table entries outside the cache, and positions past the row's end, are
  * masked.  Scores, statistics and sums are float; the softmax weights are
  * rounded to the cache's type for the product with the values.  Rows of out
