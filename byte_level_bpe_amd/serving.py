@@ -108,6 +108,14 @@ def _rows(name, t, dtype, shape, dev):
     return t.data_ptr(), t.stride(0), t.stride(1)
 
 
+def _written(name, t, dtype, shape, dev):
+    """_rows of a tensor to be written, whose rows must be places of their own."""
+    rows = _rows(name, t, dtype, shape, dev)
+    if any(t.stride(d) == 0 and shape[d] > 1 for d in (0, 1)):
+        _bad("%s: rows share memory: strides %s" % (name, t.stride()))
+    return rows
+
+
 _NONE = (None, 0, 0)
 
 
@@ -256,11 +264,11 @@ def _norm_args(what, q, k, q_weight, k_weight, positions, inv_freq):
         _bad("%s: q and k [tokens, heads, dim] of bfloat16, float16 or float32 are wanted, got %s %s, %s %s" %
              (what, q.dtype, list(q.shape), k.dtype, list(k.shape)))
     dev, (n, hq, dim), hk = q.device, q.shape, k.shape[1]
+    freq = _dense("inv_freq", inv_freq, torch.float32, (None,), dev)
     ws = [None if w is None else _dense(name, w, q.dtype, (dim,), dev)
           for name, w in (("q_weight", q_weight), ("k_weight", k_weight))]
     return (n, hq, hk, dim, 2 * inv_freq.shape[0], ws,
-            _dense("positions", positions, torch.int32, (n,), dev),
-            _dense("inv_freq", inv_freq, torch.float32, (None,), dev))
+            _dense("positions", positions, torch.int32, (n,), dev), freq)
 
 
 def _wants_grad(*tensors):
@@ -331,8 +339,8 @@ def qk_norm_rope(q, k, q_weight, k_weight, positions, inv_freq, eps: float = 1e-
             _DTYPES[dt], n, hq, hk, dim, rot, interleaved, eps,
             *_rows("q", q, dt, q.shape, dev), *_rows("k", k, dt, kshape, dev),
             *(_NONE if cache is None else _rows("v", v, dt, kshape, dev)), ws[0], ws[1], pos, freq,
-            *_rows("q_out", q_out, dt, q.shape, dev),
-            *(_NONE if k_out is None else _rows("k_out", k_out, dt, kshape, dev)),
+            *_written("q_out", q_out, dt, q.shape, dev),
+            *(_NONE if k_out is None else _written("k_out", k_out, dt, kshape, dev)),
             None if cache is None else cache._p,
             None if cache is None else _dense("slots", slots, torch.int64, (n,), dev), on.handle)
         _check(st, "qk_norm_rope")
@@ -370,7 +378,7 @@ def qk_norm_rope_backward(grad_q, grad_k, q, k, q_weight, k_weight, positions, i
             _DTYPES[dt], n, hq, hk, dim, rot, interleaved, eps,
             *_rows("grad_q", grad_q, dt, q.shape, dev), *_rows("grad_k", grad_k, dt, kshape, dev),
             *_rows("q", q, dt, q.shape, dev), *_rows("k", k, dt, kshape, dev), ws[0], ws[1], pos, freq,
-            *_rows("dq", dq, dt, q.shape, dev), *_rows("dk", dk, dt, kshape, dev),
+            *_written("dq", dq, dt, q.shape, dev), *_written("dk", dk, dt, kshape, dev),
             None if dws[0] is None else dws[0].data_ptr(), None if dws[1] is None else dws[1].data_ptr(),
             _dense("workspace", workspace, torch.uint8, (None,), dev), workspace.numel(), on.handle)
         _check(st, "qk_norm_rope_backward")
@@ -428,7 +436,7 @@ def tree_attention(q, cache: PagedCache, table, q_off, ctx_len, tree_mask=None, 
             _dense("ctx_len", ctx_len, torch.int32, (n_req,), dev), n_req,
             None if tree_mask is None else _dense("tree_mask", tree_mask, torch.int64, (n, None), dev),
             0 if tree_mask is None else tree_mask.shape[1], dim ** -0.5 if scale is None else scale,
-            *_rows("out", out, dt, q.shape, dev),
+            *_written("out", out, dt, q.shape, dev),
             None if lse is None else _dense("lse", lse, torch.float32, (n, hq), dev),
             _dense("workspace", workspace, torch.uint8, (None,), dev), workspace.numel(), on.handle)
         _check(st, "tree_attention")

@@ -129,3 +129,25 @@ def test_norm_of_more_tokens_than_a_launch_takes():
             near(got[rows], *ref.norm_rope(x[rows].cpu(), ww.cpu(), pos[rows].cpu(), freq.cpu(), 1e-6, False), "rows")
     # the rotation keeps lengths: no row was left out
     assert bool(((q.float().square().mean(-1) - 2.25).abs() < 0.1).all())
+
+
+def test_outputs_whose_rows_share_memory_are_refused():
+    """A broadcast tensor takes one row at last, whichever wrote it."""
+    say("shared rows")
+    n, hq, hk, dim, dt, dev = 3, 2, 2, 64, torch.bfloat16, "cuda"
+    x, one = torch.zeros(n, hq, dim, dtype=dt, device=dev), torch.zeros(1, 1, dim, dtype=dt, device=dev)
+    pos, freq = torch.zeros(n, dtype=torch.int32, device=dev), torch.zeros(dim // 2, device=dev)
+    cache = B.PagedCache(*(torch.zeros(2, hk, 16, dim, dtype=dt, device=dev) for _ in range(2)))
+    attn = (x, cache, torch.zeros(1, 2, dtype=torch.int32, device=dev), torch.tensor([0, n], device=dev), torch.zeros(1, dtype=torch.int32, device=dev))
+    for shared in (one.expand(n, hq, dim), torch.zeros(n, 1, dim, dtype=dt, device=dev).expand(n, hq, dim)):
+        for call in (lambda: B.qk_norm_rope(x, x, None, None, pos, freq, q_out=shared), lambda: B.qk_norm_rope(x, x, None, None, pos, freq, k_out=shared),
+                     lambda: B.qk_norm_rope_backward(x, x, x, x, None, None, pos, freq, dq=shared),
+                     lambda: B.qk_norm_rope_backward(x, x, x, x, None, None, pos, freq, dk=shared), lambda: B.tree_attention(*attn, out=shared)):
+            with pytest.raises(B.BBPEError) as e:
+                call()
+            assert e.value.status == B.E_INVALID_ARG and "share memory" in str(e.value)
+    # inputs may be broadcast, and a single row has no others
+    assert B.qk_norm_rope(one.expand(n, hq, dim), x, None, None, pos, freq)[0].shape == x.shape
+    B.qk_norm_rope(one, one, None, None, pos[:1], freq, q_out=one.clone().expand(1, 1, dim))
+    with pytest.raises(B.BBPEError):
+        B.qk_norm_rope(x, x, None, None, pos, torch.tensor(1.0, device=dev))
