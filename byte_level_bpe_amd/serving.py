@@ -2,8 +2,8 @@
 norm of queries and keys with their rotation, and attention of new tokens (a
 tree of drafts, a chain, one token) over a paged cache.
 
-Argument marshalling only, as in the package's encode calls: the work is in the
-HIP kernels behind include/bbpe.h.  Every call enqueues on the current stream
+Argument marshalling only, as in the package's encode calls, and the recording of
+qk_norm_rope's gradient: the work is in the HIP kernels behind include/bbpe.h.  Every call enqueues on the current stream
 (or the one given) and returns without synchronising; given buffers (`out=` and
 the like, and a workspace) it allocates nothing, so it can be captured into a
 HIP graph.
