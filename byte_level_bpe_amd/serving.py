@@ -2,11 +2,11 @@
 norm of queries and keys with their rotation, and attention of new tokens (a
 tree of drafts, a chain, one token) over a paged cache.
 
-Argument marshalling only, as in the package's encode calls, and the recording of
-qk_norm_rope's gradient: the work is in the HIP kernels behind include/bbpe.h.  Every call enqueues on the current stream
-(or the one given) and returns without synchronising; given buffers (`out=` and
-the like, and a workspace) it allocates nothing, so it can be captured into a
-HIP graph.
+Argument marshalling only, as in the package's encode calls, and the recording
+of qk_norm_rope's gradient: the work is in the HIP kernels behind
+include/bbpe.h.  Every call enqueues on the current stream (or the one given)
+and returns without synchronising; given buffers (`out=` and the like, and a
+workspace) it allocates nothing, so it can be captured into a HIP graph.
 
     ids, id_off, n = tok.encode_device(text, seg_off, allow, total)
     plan = block_tables(id_off, ctx_len, free_pages, table, 64, n)
