@@ -51,7 +51,9 @@ EXPORTS = ["bbpe_load_ranks", "bbpe_load_ranks_tiktoken_file", "bbpe_upload_tabl
            "bbpe_free", "bbpe_status_str",
            "bbpe_block_tables_workspace_bytes", "bbpe_block_tables", "bbpe_qk_norm_rope",
            "bbpe_qk_norm_rope_backward_workspace_bytes", "bbpe_qk_norm_rope_backward",
-           "bbpe_tree_attention_workspace_bytes", "bbpe_tree_attention"]
+           "bbpe_tree_attention_workspace_bytes", "bbpe_tree_attention",
+           "bbpe_token_logprobs", "bbpe_token_logprobs_backward", "bbpe_distill_loss",
+           "bbpe_distill_loss_backward"]
 
 _lib = None
 
@@ -603,15 +605,20 @@ def decode(tok: Tokenizer, ids) -> bytes:
 
 
 # The operators on what an encode call leaves on the device live in serving.py,
-# which needs torch at import; they load with their first use.
-_SERVING = ("BlockTables", "PagedCache", "block_tables", "qk_norm_rope", "qk_norm_rope_backward",
-            "tree_attention", "tree_attention_workspace_bytes")
+# those on a model's logits in scoring.py; both need torch at import and load
+# with their first use.
+_LATER = {"serving": ("BlockTables", "PagedCache", "block_tables", "qk_norm_rope", "qk_norm_rope_backward",
+                      "tree_attention", "tree_attention_workspace_bytes"),
+          "scoring": ("TokenLogprobs", "token_logprobs", "token_logprobs_backward", "DistillLoss", "distill_loss",
+                      "distill_loss_backward")}
 
 
 def __getattr__(name):
-    if name in _SERVING:
-        from . import serving
-        for n in _SERVING:
-            globals()[n] = getattr(serving, n)
-        return globals()[name]
+    for module, names in _LATER.items():
+        if name in names:
+            import importlib
+            found = importlib.import_module("." + module, __name__)
+            for n in names:
+                globals()[n] = getattr(found, n)
+            return globals()[name]
     raise AttributeError("module %r has no attribute %r" % (__name__, name))

@@ -1,0 +1,135 @@
+// Rows of logits: reading them in pieces of 16 bytes, and sums over them, for
+// the operators between a model's logits and ids.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <math.h>
+#include <stdint.h>
+
+#include <type_traits>
+
+#include "../../include/bbpe.h"
+
+namespace bbpe {
+
+constexpr uint32_t ROW_THREADS = 256;  // of a workgroup
+constexpr uint32_t ROW_WAVES = ROW_THREADS / 64;
+constexpr uint32_t ROW_UNROLL = 4;     // pieces of a thread's step
+constexpr uint32_t ROW_STEP = ROW_THREADS * ROW_UNROLL;  // pieces of a workgroup's step
+constexpr float LOG2E = 1.4426950408889634f;
+constexpr float LOWEST = -3.4028234663852886e38f;
+
+// Piece p of a row: elements [p * N, (p + 1) * N).  In memory a row may begin
+// at any element: vocabularies of odd sizes are common.
+template <typename T> struct Piece {
+  static constexpr uint32_t N = 16 / sizeof(T);
+  typedef T raw __attribute__((ext_vector_type(16 / sizeof(T))));
+  typedef T mem __attribute__((ext_vector_type(16 / sizeof(T)), aligned(sizeof(T))));
+  typedef float val __attribute__((ext_vector_type(16 / sizeof(T))));
+};
+
+// A piece of a row of `vocab` elements; past its end: minus infinity.
+template <typename T>
+__device__ __forceinline__ typename Piece<T>::raw load_piece(const T *x, uint32_t p, uint32_t vocab) {
+  constexpr uint32_t N = Piece<T>::N;
+  const uint32_t at = p * N;
+  typename Piece<T>::raw v;
+  if (at + N <= vocab) {
+    v = *reinterpret_cast<const typename Piece<T>::mem *>(x + at);
+  } else {
+#pragma unroll
+    for (uint32_t e = 0; e < N; ++e) v[e] = at + e < vocab ? x[at + e] : T(-INFINITY);
+  }
+  return v;
+}
+template <typename T>
+__device__ __forceinline__ void store_piece(T *x, uint32_t p, uint32_t vocab, typename Piece<T>::val f) {
+  constexpr uint32_t N = Piece<T>::N;
+  const uint32_t at = p * N;
+  const typename Piece<T>::raw v = __builtin_convertvector(f, typename Piece<T>::raw);  // to nearest even
+  if (at + N <= vocab) {
+    *reinterpret_cast<typename Piece<T>::mem *>(x + at) = v;
+  } else {
+#pragma unroll
+    for (uint32_t e = 0; e < N; ++e)
+      if (at + e < vocab) x[at + e] = v[e];
+  }
+}
+template <typename T>
+__device__ __forceinline__ typename Piece<T>::val values(typename Piece<T>::raw v) {
+  return __builtin_convertvector(v, typename Piece<T>::val);
+}
+
+__device__ __forceinline__ float wave_max(float v) {
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) v = fmaxf(v, __shfl_xor(v, d, 64));
+  return v;
+}
+template <typename V>
+__device__ __forceinline__ V wave_sum(V v) {
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) v += __shfl_xor(v, d, 64);
+  return v;
+}
+
+// Part of a row's softmax: the largest element so far, and relative to it the
+// sum of weights exp(scale * (x - max)) and of weights times (x - max).  No
+// element yet, or only minus infinity: max is that, the sums are 0.  A NaN or
+// plus infinity anywhere makes the sum of weights NaN.
+struct Partial {
+  float max, sum, mean;
+};
+__device__ __forceinline__ float finite_max(float m) { return m == -INFINITY ? 0.0f : m; }
+// p relative to `max`, which is p.max or above; c = scale * log2(e)
+__device__ __forceinline__ Partial relative(Partial p, float max, float c) {
+  const float d = p.max - finite_max(max);  // -inf where p has nothing
+  const float f = __builtin_amdgcn_exp2f(d * c);
+  return Partial{max, p.sum * f, f == 0.0f ? 0.0f : f * (p.mean + p.sum * d)};  // (0 times minus infinity is to be 0)
+}
+// The workgroup's, in every thread.  sh: ROW_WAVES of them.
+__device__ __forceinline__ Partial row_partial(Partial p, float c, Partial *sh) {
+  p = relative(p, wave_max(p.max), c);
+  p.sum = wave_sum(p.sum);
+  p.mean = wave_sum(p.mean);
+  if ((threadIdx.x & 63) == 0) sh[threadIdx.x >> 6] = p;
+  __syncthreads();
+  float m = sh[0].max;
+#pragma unroll
+  for (uint32_t w = 1; w < ROW_WAVES; ++w) m = fmaxf(m, sh[w].max);
+  Partial all{m, 0.0f, 0.0f};
+#pragma unroll
+  for (uint32_t w = 0; w < ROW_WAVES; ++w) {
+    const Partial q = relative(sh[w], m, c);
+    all.sum += q.sum;
+    all.mean += q.mean;
+  }
+  return all;
+}
+
+// What a gradient wants of a row's softmax: p_j = exp2(c * (x_j - max)) / sum,
+// max in the logits' own units and the natural logarithm of the sum.
+// A row with nothing in it has max -inf, one without probabilities (NaN or
+// plus infinity in it) a NaN logarithm.
+struct RowStats {
+  float max, log_sum;
+};
+
+// Calls f with a value of the element type.
+template <typename F>
+void with_element(int dtype, F f) {
+  if (dtype == BBPE_BF16) f((__bf16)0);
+  else if (dtype == BBPE_F16) f((_Float16)0);
+  else f(0.0f);
+}
+
+inline uintptr_t address(const void *p) { return reinterpret_cast<uintptr_t>(p); }
+
+// What the operators ask of a matrix of logits alike.  `grad`: one of gradients,
+// whose rows must not share memory.
+inline bool bad_logits(int dtype, const void *x, int64_t stride, uint64_t rows, uint32_t vocab, bool grad) {
+  if (dtype < BBPE_BF16 || dtype > BBPE_F32 || vocab == 0 || vocab > (1u << 30) || rows > 0x7FFFFFFFull) return true;
+  if (rows && (!x || (address(x) & (dtype == BBPE_F32 ? 3 : 1)))) return true;
+  return grad && rows > 1 && (stride < 0 ? -stride : stride) < int64_t(vocab);
+}
+
+}  // namespace bbpe

@@ -1,9 +1,9 @@
-// The short way from Python to the operators of serving.py: plain calls (all
+// The short way from Python to the operators of serving.py and scoring.py: plain calls (all
 // tensors as documented, on the current device and stream) are checked, their
 // outputs allocated and the library called here, in one step of a microsecond
 // or two where ctypes and tensor methods take fifteen.  Whatever is not plain
 // -- a stream, gradients to be recorded, a mistake -- returns NotImplemented,
-// and serving.py's own code, which says what is wrong, takes it from the start.
+// and the Python code, which says what is wrong, takes it from the start.
 #include <ATen/ATen.h>
 #include <c10/core/GradMode.h>
 #include <c10/hip/HIPStream.h>
@@ -21,6 +21,10 @@ decltype(&bbpe_qk_norm_rope_backward_workspace_bytes) f_back_bytes;
 decltype(&bbpe_qk_norm_rope_backward) f_back;
 decltype(&bbpe_tree_attention_workspace_bytes) f_attn_bytes;
 decltype(&bbpe_tree_attention) f_attn;
+decltype(&bbpe_token_logprobs) f_scores;
+decltype(&bbpe_token_logprobs_backward) f_scores_back;
+decltype(&bbpe_distill_loss) f_distill;
+decltype(&bbpe_distill_loss_backward) f_distill_back;
 
 using at::Tensor;
 
@@ -62,6 +66,12 @@ struct Call {
   }
   int64_t ts(const Tensor *t) const { return t && t->dim() == 3 ? t->stride(0) : 0; }
   int64_t hs(const Tensor *t) const { return t && t->dim() == 3 ? t->stride(1) : 0; }
+  // contiguous, of this type and [n, m]
+  void *dense(const Tensor *t, at::ScalarType type, int64_t n, int64_t m) {
+    if (!t) return nullptr;
+    if (t->scalar_type() != type || t->dim() != 2 || t->size(0) != n || t->size(1) != m || !t->is_contiguous()) plain = false;
+    return t->data_ptr();
+  }
   void *table(const Tensor *t, int64_t n) {
     if (!t) return nullptr;
     if (t->scalar_type() != at::kInt || t->dim() != 2 || t->size(0) != n || (t->size(1) > 1 && t->stride(1) != 1)) plain = false;
@@ -85,6 +95,11 @@ Tensor part_of(const Tensor &buffer, int64_t at, int64_t n, at::ScalarType type)
   Tensor t = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(buffer.storage()), buffer.key_set(), c10::scalarTypeToTypeMeta(type));
   t.unsafeGetTensorImpl()->set_storage_offset(at / int64_t(c10::elementSize(type)));
   t.unsafeGetTensorImpl()->set_sizes_contiguous({n});
+  return t;
+}
+Tensor part_of(const Tensor &buffer, int64_t at, int64_t n, int64_t m, at::ScalarType type) {
+  Tensor t = part_of(buffer, at, n * m, type);
+  t.unsafeGetTensorImpl()->set_sizes_contiguous({n, m});
   return t;
 }
 int64_t up16(int64_t n) { return (n + 15) / 16 * 16; }
@@ -296,14 +311,180 @@ PyObject *tree_attention(PyObject *, PyObject *const *a, Py_ssize_t n_args) {
   END_HANDLE_TH_ERRORS
 }
 
-// bind(addresses of the six functions above, in their order)
+// Rows of logits, or of their gradients.
+struct Logits {
+  const Tensor *t;
+  at::ScalarType type;
+  int64_t n, vocab;
+  void *p;
+
+  bool read(Call &c, PyObject *o) {
+    t = c.tensor(o);
+    if (!c.plain || t->dim() != 2 || (t->size(1) > 1 && t->stride(1) != 1) || t->size(1) > 0x7FFFFFFF) return false;
+    type = t->scalar_type();
+    n = t->size(0);
+    vocab = t->size(1);
+    p = t->data_ptr();
+    return dtype_of(type) >= 0;
+  }
+  bool like(Call &c, PyObject *o, const Logits &x) {
+    return read(c, o) && type == x.type && n == x.n && vocab == x.vocab && (n <= 1 || t->stride(0) >= vocab);
+  }
+};
+
+PyObject *tuple_of(std::initializer_list<Tensor> ts) {
+  PyObject *out = PyTuple_New(Py_ssize_t(ts.size()));
+  if (!out) return nullptr;
+  Py_ssize_t i = 0;
+  for (const Tensor &t : ts) PyTuple_SET_ITEM(out, i++, THPVariable_Wrap(t));
+  return out;
+}
+
+float *floats(void *p) { return static_cast<float *>(p); }
+int32_t *ints(void *p) { return static_cast<int32_t *>(p); }
+
+// logits, ids, top_k, scale -> (logprobs, entropy, lse, ranks, top_ids, top_logprobs, stats)
+PyObject *token_logprobs(PyObject *, PyObject *const *a, Py_ssize_t n_args) {
+  HANDLE_TH_ERRORS
+  if (n_args != 4) return not_plain();
+  Call c;
+  Logits x;
+  if (!x.read(c, a[0])) return not_plain();
+  const Tensor *ids = c.tensor(a[1]);
+  const int64_t k = PyLong_AsLongLong(a[2]), n = x.n;
+  const float scale = float(PyFloat_AsDouble(a[3]));
+  if (PyErr_Occurred()) {
+    PyErr_Clear();
+    return not_plain();
+  }
+  if (!c.plain || k < 0 || k > 256 || k > x.vocab) return not_plain();
+  void *p_ids = c.flat(ids, at::kInt, n), *stream;
+  if (!c.ready(stream)) return not_plain();
+  // what every row has, in one allocation; its alternatives in another
+  const int64_t step = up16(4 * n), at_stats = 4 * step, at_top = up16(4 * n * k);
+  const Tensor rows = c.empty({at_stats + 8 * n}, at::kByte), top = c.empty({2 * at_top}, at::kByte);
+  const Tensor lp = part_of(rows, 0, n, at::kFloat), entropy = part_of(rows, step, n, at::kFloat), lse = part_of(rows, 2 * step, n, at::kFloat),
+               ranks = part_of(rows, 3 * step, n, at::kInt), stats = part_of(rows, at_stats, n, 2, at::kFloat),
+               top_ids = part_of(top, 0, n, k, at::kInt), top_lp = part_of(top, at_top, n, k, at::kFloat);
+  const int rc = f_scores(dtype_of(x.type), x.p, x.t->stride(0), uint64_t(n), uint32_t(x.vocab), ints(p_ids), uint32_t(k), scale,
+                          floats(lp.data_ptr()), floats(entropy.data_ptr()), floats(lse.data_ptr()), ints(ranks.data_ptr()), ints(top_ids.data_ptr()),
+                          floats(top_lp.data_ptr()), floats(stats.data_ptr()), stream);
+  if (rc) return not_plain();
+  return tuple_of({lp, entropy, lse, ranks, top_ids, top_lp, stats});
+  END_HANDLE_TH_ERRORS
+}
+
+// logits, ids, entropy, top_ids, stats, grad_logprobs, grad_entropy, grad_lse, grad_top, scale -> dlogits
+PyObject *token_logprobs_backward(PyObject *, PyObject *const *a, Py_ssize_t n_args) {
+  HANDLE_TH_ERRORS
+  if (n_args != 10) return not_plain();
+  Call c;
+  c.recorded = false;  // (a gradient's inputs may require grad; it is not differentiated again)
+  Logits x;
+  if (!x.read(c, a[0])) return not_plain();
+  const Tensor *ids = c.tensor(a[1]), *entropy = c.tensor(a[2]), *top_ids = c.tensor(a[3]), *stats = c.tensor(a[4]);
+  const Tensor *g[4];
+  for (int i = 0; i < 4; ++i) g[i] = c.tensor(a[5 + i], true);
+  const float scale = float(PyFloat_AsDouble(a[9]));
+  if (PyErr_Occurred()) {
+    PyErr_Clear();
+    return not_plain();
+  }
+  if (!c.plain || top_ids->dim() != 2) return not_plain();
+  const int64_t n = x.n, k = top_ids->size(1);
+  void *p_ids = c.flat(ids, at::kInt, n), *p_entropy = c.flat(entropy, at::kFloat, n), *p_top = c.dense(top_ids, at::kInt, n, k),
+       *p_stats = c.dense(stats, at::kFloat, n, 2), *p_g[4], *stream;
+  for (int i = 0; i < 3; ++i) p_g[i] = c.flat(g[i], at::kFloat, n);
+  p_g[3] = c.dense(g[3], at::kFloat, n, k);
+  if (!c.ready(stream)) return not_plain();
+  Tensor dx = c.empty({n, x.vocab}, x.type);
+  const int rc = f_scores_back(dtype_of(x.type), x.p, x.t->stride(0), uint64_t(n), uint32_t(x.vocab), ints(p_ids), uint32_t(k), scale, floats(p_entropy),
+                               ints(p_top), floats(p_stats), floats(p_g[0]), floats(p_g[1]), floats(p_g[2]), floats(p_g[3]), dx.data_ptr(), x.vocab, stream);
+  if (rc) return not_plain();
+  return THPVariable_Wrap(std::move(dx));
+  END_HANDLE_TH_ERRORS
+}
+
+// The lists of a distillation: [n, k] ids and log probabilities.
+struct Lists {
+  int64_t k;
+  void *p_ids, *p_lp;
+
+  bool read(Call &c, PyObject *ids, PyObject *lp, int64_t n) {
+    const Tensor *t = c.tensor(ids), *l = c.tensor(lp);
+    if (!c.plain || t->dim() != 2) return false;
+    k = t->size(1);
+    p_ids = c.dense(t, at::kInt, n, k);
+    p_lp = c.dense(l, at::kFloat, n, k);
+    return c.plain && k <= 256;
+  }
+};
+
+// logits, top_ids, top_logprobs, tail, scale, weights, dlogits -> (loss, lse, stats)
+PyObject *distill_loss(PyObject *, PyObject *const *a, Py_ssize_t n_args) {
+  HANDLE_TH_ERRORS
+  if (n_args != 7) return not_plain();
+  Call c;
+  Logits x, d;
+  Lists l;
+  if (!x.read(c, a[0]) || !l.read(c, a[1], a[2], x.n)) return not_plain();
+  const int tail = PyObject_IsTrue(a[3]);
+  const float scale = float(PyFloat_AsDouble(a[4]));
+  if (PyErr_Occurred()) {
+    PyErr_Clear();
+    return not_plain();
+  }
+  const Tensor *weights = c.tensor(a[5], true);
+  if (!c.plain || (weights && !d.like(c, a[6], x))) return not_plain();
+  const int64_t n = x.n, step = up16(4 * n);
+  void *p_w = c.flat(weights, at::kFloat, n), *stream;
+  if (!c.ready(stream)) return not_plain();
+  const Tensor rows = c.empty({2 * step + 16 * n}, at::kByte);
+  const Tensor loss = part_of(rows, 0, n, at::kFloat), lse = part_of(rows, step, n, at::kFloat), stats = part_of(rows, 2 * step, n, 4, at::kFloat);
+  const int rc = f_distill(dtype_of(x.type), x.p, x.t->stride(0), uint64_t(n), uint32_t(x.vocab), ints(l.p_ids), floats(l.p_lp), uint32_t(l.k), tail, scale,
+                           floats(loss.data_ptr()), floats(lse.data_ptr()), floats(stats.data_ptr()), floats(p_w), weights ? d.p : nullptr,
+                           weights ? d.t->stride(0) : 0, stream);
+  if (rc) return not_plain();
+  return tuple_of({loss, lse, stats});
+  END_HANDLE_TH_ERRORS
+}
+
+// grad_loss, logits, top_ids, top_logprobs, stats, tail, scale -> dlogits
+PyObject *distill_loss_backward(PyObject *, PyObject *const *a, Py_ssize_t n_args) {
+  HANDLE_TH_ERRORS
+  if (n_args != 7) return not_plain();
+  Call c;
+  c.recorded = false;  // (a gradient's inputs may require grad; it is not differentiated again)
+  Logits x;
+  Lists l;
+  if (!x.read(c, a[1]) || !l.read(c, a[2], a[3], x.n)) return not_plain();
+  const Tensor *grad = c.tensor(a[0]), *stats = c.tensor(a[4]);
+  const int tail = PyObject_IsTrue(a[5]);
+  const float scale = float(PyFloat_AsDouble(a[6]));
+  if (PyErr_Occurred()) {
+    PyErr_Clear();
+    return not_plain();
+  }
+  if (!c.plain) return not_plain();
+  const int64_t n = x.n;
+  void *p_grad = c.flat(grad, at::kFloat, n), *p_stats = c.dense(stats, at::kFloat, n, 4), *stream;
+  if (!c.ready(stream)) return not_plain();
+  Tensor dx = c.empty({n, x.vocab}, x.type);
+  const int rc = f_distill_back(dtype_of(x.type), x.p, x.t->stride(0), uint64_t(n), uint32_t(x.vocab), ints(l.p_ids), floats(l.p_lp), uint32_t(l.k), tail,
+                                scale, floats(p_stats), floats(p_grad), dx.data_ptr(), x.vocab, stream);
+  if (rc) return not_plain();
+  return THPVariable_Wrap(std::move(dx));
+  END_HANDLE_TH_ERRORS
+}
+
+// bind(addresses of the ten functions above, in their order)
 PyObject *bind(PyObject *, PyObject *const *a, Py_ssize_t n_args) {
-  if (n_args != 6) {
-    PyErr_SetString(PyExc_TypeError, "bind: six addresses");
+  if (n_args != 10) {
+    PyErr_SetString(PyExc_TypeError, "bind: ten addresses");
     return nullptr;
   }
-  void *p[6];
-  for (int i = 0; i < 6; ++i) p[i] = PyLong_AsVoidPtr(a[i]);
+  void *p[10];
+  for (int i = 0; i < 10; ++i) p[i] = PyLong_AsVoidPtr(a[i]);
   if (PyErr_Occurred()) return nullptr;
   f_tables = reinterpret_cast<decltype(f_tables)>(p[0]);
   f_norm = reinterpret_cast<decltype(f_norm)>(p[1]);
@@ -311,16 +492,24 @@ PyObject *bind(PyObject *, PyObject *const *a, Py_ssize_t n_args) {
   f_back = reinterpret_cast<decltype(f_back)>(p[3]);
   f_attn_bytes = reinterpret_cast<decltype(f_attn_bytes)>(p[4]);
   f_attn = reinterpret_cast<decltype(f_attn)>(p[5]);
+  f_scores = reinterpret_cast<decltype(f_scores)>(p[6]);
+  f_scores_back = reinterpret_cast<decltype(f_scores_back)>(p[7]);
+  f_distill = reinterpret_cast<decltype(f_distill)>(p[8]);
+  f_distill_back = reinterpret_cast<decltype(f_distill_back)>(p[9]);
   Py_RETURN_NONE;
 }
 
-PyMethodDef methods[] = {
-    {"bind", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(bind)), METH_FASTCALL, nullptr},
-    {"block_tables", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(block_tables)), METH_FASTCALL, nullptr},
-    {"qk_norm_rope", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(qk_norm_rope)), METH_FASTCALL, nullptr},
-    {"qk_norm_rope_backward", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(qk_norm_rope_backward)), METH_FASTCALL, nullptr},
-    {"tree_attention", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(tree_attention)), METH_FASTCALL, nullptr},
-    {nullptr, nullptr, 0, nullptr}};
+#define METHOD(name) {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(name)), METH_FASTCALL, nullptr}
+PyMethodDef methods[] = {METHOD(bind),
+                         METHOD(block_tables),
+                         METHOD(qk_norm_rope),
+                         METHOD(qk_norm_rope_backward),
+                         METHOD(tree_attention),
+                         METHOD(token_logprobs),
+                         METHOD(token_logprobs_backward),
+                         METHOD(distill_loss),
+                         METHOD(distill_loss_backward),
+                         {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_serving", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace

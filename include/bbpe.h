@@ -520,6 +520,87 @@ int bbpe_tree_attention(const void *q, int64_t q_ts, int64_t q_hs, uint64_t n_to
                         int64_t out_hs, float *d_lse, void *d_workspace, uint64_t workspace_bytes,
                         void *hip_stream);
 
+/* --------------------------------------------------------------------------
+ * From logits to ids.  The operators below read a model's logits over the
+ * vocabulary, [n_rows][vocab] of dtype, rows row_stride elements apart and
+ * beginning at any element (16-byte aligned rows are not asked for).  What is
+ * said above of streams, graphs, checks and workspaces holds for them too.
+ * Arithmetic is in float, a row's few numbers in 64 bits; results do not depend
+ * on the order in which workgroups run.
+ *
+ * z = scale * logits, log p = z - log sum exp z.  scale (1 / temperature) is
+ * above 0.  Minus infinity is a token that cannot come; a row of nothing else
+ * has lse -inf, every log probability -inf, entropy 0 and no gradient.  A row
+ * with a NaN or plus infinity in it has no probabilities: its numbers are NaN.
+ * -------------------------------------------------------------------------- */
+
+/* Scores of given tokens.
+ *
+ *   d_ids[n_rows]:     the row's token.  Below 0: none (log probability 0, rank
+ *                      0, no gradient); vocab or above: NaN, rank 0;
+ *   top_k:             alternatives a row, 0 to 256, at most vocab;
+ *   d_logprobs[n_rows], d_entropy[n_rows], d_lse[n_rows] (natural logarithms);
+ *   d_ranks[n_rows]:   the token's place, from 1, in the order of logits, the
+ *                      largest first and the lowest id among equals (0 in a row
+ *                      without probabilities);
+ *   d_top_ids, d_top_logprobs [n_rows][top_k]: the first top_k in that order (a
+ *                      row without probabilities: -1 and NaN);
+ *   d_stats[n_rows][2]: for the gradient: the row's largest logit, and the
+ *                      logarithm of its sum of exp(scale * (logit - largest)). */
+int bbpe_token_logprobs(int dtype, const void *logits, int64_t row_stride, uint64_t n_rows,
+                        uint32_t vocab, const int32_t *d_ids, uint32_t top_k, float scale,
+                        float *d_logprobs, float *d_entropy, float *d_lse, int32_t *d_ranks,
+                        int32_t *d_top_ids, float *d_top_logprobs, float *d_stats,
+                        void *hip_stream);
+
+/* Its backward pass: from the gradients of d_logprobs, d_entropy, d_lse
+ * ([n_rows] float) and d_top_logprobs ([n_rows][top_k]; null: zeros) and what
+ * the forward call left, the gradient of the logits, of dtype, rounded once.
+ * d_logits may be logits (with the same stride).  A row whose given gradients
+ * are zeros gets zeros, whatever its logits hold. */
+int bbpe_token_logprobs_backward(int dtype, const void *logits, int64_t row_stride,
+                                 uint64_t n_rows, uint32_t vocab, const int32_t *d_ids,
+                                 uint32_t top_k, float scale, const float *d_entropy,
+                                 const int32_t *d_top_ids, const float *d_stats,
+                                 const float *g_logprobs, const float *g_entropy,
+                                 const float *g_lse, const float *g_top, void *d_logits,
+                                 int64_t dl_stride, void *hip_stream);
+
+/* Distillation from a teacher's top log probabilities (bbpe_token_logprobs').
+ *
+ *   d_top_ids, d_top_logprobs [n_rows][top_k]: top_k 1 to 256, at most vocab (with
+ *                      a tail below it).  Entries whose id is outside the
+ *                      vocabulary are not there: shorter lists end with -1.  A
+ *                      token named twice has both entries' probability;
+ *   tail 0:            the teacher is its list made to sum to 1:
+ *                      q_t = exp(a_t) / sum exp(a) (so any constant may be added
+ *                      to a row of it), and loss = sum_t q_t (log q_t - log p_t);
+ *   tail 1:            q_t = exp(a_t), and what they leave of 1, q_r (0 at
+ *                      least), is held against the student's sum p_r over all
+ *                      tokens that are not listed: + q_r (log q_r - log p_r);
+ *   d_loss[n_rows], d_lse[n_rows] (the student's), d_stats[n_rows][4] (for the
+ *                      gradient; 16-byte aligned);
+ *   d_weights[n_rows], d_logits: both or neither: the gradient of the weighted
+ *                      sum of the losses, in the same call (as the backward call
+ *                      makes it; d_logits may be logits).
+ *
+ * A row without a teacher (no entry; without a tail also none above minus
+ * infinity) has loss 0 and no gradient, whatever its logits hold.  A listed
+ * token that the student gives minus infinity makes the loss infinite. */
+int bbpe_distill_loss(int dtype, const void *logits, int64_t row_stride, uint64_t n_rows,
+                      uint32_t vocab, const int32_t *d_top_ids, const float *d_top_logprobs,
+                      uint32_t top_k, int tail, float scale, float *d_loss, float *d_lse,
+                      float *d_stats, const float *d_weights, void *d_logits, int64_t dl_stride,
+                      void *hip_stream);
+
+/* Its backward pass, d_grad[n_rows] the gradients of the losses (a row's of 0
+ * gives zeros, whatever its logits hold).  d_logits may be logits. */
+int bbpe_distill_loss_backward(int dtype, const void *logits, int64_t row_stride, uint64_t n_rows,
+                               uint32_t vocab, const int32_t *d_top_ids,
+                               const float *d_top_logprobs, uint32_t top_k, int tail, float scale,
+                               const float *d_stats, const float *d_grad, void *d_logits,
+                               int64_t dl_stride, void *hip_stream);
+
 /* A static English description of a status code. */
 const char *bbpe_status_str(int status);
 
