@@ -154,29 +154,30 @@ __global__ __launch_bounds__(ROW_THREADS) void k_distill(DistillArgs a) {
   __shared__ uint32_t bits[TAIL ? BIT_WORDS : 1];
   const uint64_t row = a.row0 + blockIdx.x;
   const T *x = static_cast<const T *>(a.x) + int64_t(row) * a.stride;
-  const uint32_t tid = threadIdx.x, pieces = (a.vocab + P::N - 1) / P::N;
+  const Row<const T> r(x, a.vocab);
+  const uint32_t tid = threadIdx.x;
   if (tid < a.k) {
     const int32_t id = a.ids[row * a.k + tid];
     ids[tid] = id >= 0 && uint32_t(id) < a.vocab ? id : -1;
   }
   Partial s{-INFINITY, 0.0f, 0.0f};
   float ref = 0.0f;
-  const uint32_t steps = (pieces + ROW_STEP - 1) / ROW_STEP;
+  const uint32_t steps = (r.pieces() + ROW_STEP - 1) / ROW_STEP;
   for (uint32_t i = 0; i < steps; ++i) {
     if (TAIL && i % STRETCH == 0) {
       const uint32_t from = i * ROW_STEP * P::N;
       __syncthreads();
       for (uint32_t w = tid; w < BIT_WORDS; w += ROW_THREADS) bits[w] = 0;
       __syncthreads();
-      if (tid < a.k && ids[tid] >= 0 && uint32_t(ids[tid]) - from < BIT_WORDS * 32)
-        atomicOr(&bits[(uint32_t(ids[tid]) - from) / 32], 1u << (uint32_t(ids[tid]) - from) % 32);
+      const uint32_t place = tid < a.k && ids[tid] >= 0 ? r.lead + uint32_t(ids[tid]) - from : ~0u;
+      if (place < BIT_WORDS * 32) atomicOr(&bits[place / 32], 1u << place % 32);
       __syncthreads();
     }
     typename P::val v[ROW_UNROLL];
     float m = -INFINITY;
     Raw raw[ROW_UNROLL];
 #pragma unroll
-    for (uint32_t u = 0; u < ROW_UNROLL; ++u) raw[u] = load_piece<T>(x, i * ROW_STEP + u * ROW_THREADS + tid, a.vocab);
+    for (uint32_t u = 0; u < ROW_UNROLL; ++u) raw[u] = r.load(i * ROW_STEP + u * ROW_THREADS + tid);
 #pragma unroll
     for (uint32_t u = 0; u < ROW_UNROLL; ++u) {
       v[u] = values<T>(raw[u]);
@@ -228,10 +229,11 @@ __global__ __launch_bounds__(ROW_THREADS) void k_distill_back(DistillBackArgs a)
   __shared__ float q[LIST_MAX];
   const uint32_t tid = threadIdx.x;
   const uint64_t block = a.block0 + blockIdx.x, row = block / a.parts;
-  const uint32_t pieces = (a.vocab + P::N - 1) / P::N;
-  const uint32_t from = uint32_t(block % a.parts) * a.part, to = min(pieces, from + a.part);
   const T *x = static_cast<const T *>(a.x) + int64_t(row) * a.stride;
   T *dx = static_cast<T *>(a.dx) + int64_t(row) * a.dx_stride;
+  const Row<T> r(dx, a.vocab);  // pieces as they are written
+  const uint32_t from = uint32_t(block % a.parts) * a.part, to = min(r.pieces(), from + a.part);
+  if (from >= to) return;  // (parts are counted for rows that begin anywhere)
   const float4 st = a.stats[row];
   const float g = a.grad[row] * a.scale;
   const bool zero = st.x == -INFINITY || g == 0.0f;
@@ -245,7 +247,7 @@ __global__ __launch_bounds__(ROW_THREADS) void k_distill_back(DistillBackArgs a)
     const bool there = id >= 0 && uint32_t(id) < a.vocab;
     ids[tid] = there ? id : -1;
     q[tid] = there ? __builtin_amdgcn_exp2f((lp - (a.tail ? 0.0f : st.w)) * LOG2E) : 0.0f;
-    mine = there && !zero && uint32_t(id) / P::N - from < to - from;
+    mine = there && !zero && (r.lead + uint32_t(id)) / P::N - from < to - from;
     if (mine) before = float(x[id]);
   }
   __syncthreads();
@@ -254,7 +256,7 @@ __global__ __launch_bounds__(ROW_THREADS) void k_distill_back(DistillBackArgs a)
     typename P::raw raw[ROW_UNROLL];
 #pragma unroll
     for (uint32_t u = 0; u < ROW_UNROLL; ++u)
-      if (p0 + u * ROW_THREADS < to && !zero) raw[u] = load_piece<T>(x, p0 + u * ROW_THREADS, a.vocab);
+      if (p0 + u * ROW_THREADS < to && !zero) raw[u] = r.load(x - r.lead, p0 + u * ROW_THREADS);
 #pragma unroll
     for (uint32_t u = 0; u < ROW_UNROLL; ++u) {
       if (p0 + u * ROW_THREADS >= to) break;
@@ -264,7 +266,7 @@ __global__ __launch_bounds__(ROW_THREADS) void k_distill_back(DistillBackArgs a)
 #pragma unroll
         for (uint32_t e = 0; e < P::N; ++e) v[e] = weight(v[e]) * all;
       }
-      store_piece<T>(dx, p0 + u * ROW_THREADS, a.vocab, v);
+      r.store(p0 + u * ROW_THREADS, v);
     }
   }
   __syncthreads();
@@ -315,9 +317,8 @@ int bbpe_distill_loss_backward(int dtype, const void *logits, int64_t row_stride
   a.lp = d_top_logprobs;
   a.stats = reinterpret_cast<const float4 *>(d_stats);
   a.grad = d_grad;
-  const uint32_t pieces = uint32_t((uint64_t(vocab) * (dtype == BBPE_F32 ? 4 : 2) + 15) / 16);
   a.part = 2 * ROW_STEP;
-  a.parts = (pieces + a.part - 1) / a.part;
+  a.parts = (most_pieces(dtype, vocab) + a.part - 1) / a.part;
   const hipStream_t st = static_cast<hipStream_t>(hip_stream);
   const uint64_t blocks = n_rows * a.parts;
   for (; a.block0 < blocks; a.block0 += MAX_GROUPS)

@@ -19,42 +19,54 @@ constexpr uint32_t ROW_STEP = ROW_THREADS * ROW_UNROLL;  // pieces of a workgrou
 constexpr float LOG2E = 1.4426950408889634f;
 constexpr float LOWEST = -3.4028234663852886e38f;
 
-// Piece p of a row: elements [p * N, (p + 1) * N).  In memory a row may begin
-// at any element: vocabularies of odd sizes are common.
 template <typename T> struct Piece {
   static constexpr uint32_t N = 16 / sizeof(T);
   typedef T raw __attribute__((ext_vector_type(16 / sizeof(T))));
-  typedef T mem __attribute__((ext_vector_type(16 / sizeof(T)), aligned(sizeof(T))));
+  typedef T mem __attribute__((ext_vector_type(16 / sizeof(T)), aligned(sizeof(T))));  // at any element
   typedef float val __attribute__((ext_vector_type(16 / sizeof(T))));
 };
 
-// A piece of a row of `vocab` elements; past its end: minus infinity.
-template <typename T>
-__device__ __forceinline__ typename Piece<T>::raw load_piece(const T *x, uint32_t p, uint32_t vocab) {
-  constexpr uint32_t N = Piece<T>::N;
-  const uint32_t at = p * N;
-  typename Piece<T>::raw v;
-  if (at + N <= vocab) {
-    v = *reinterpret_cast<const typename Piece<T>::mem *>(x + at);
-  } else {
-#pragma unroll
-    for (uint32_t e = 0; e < N; ++e) v[e] = at + e < vocab ? x[at + e] : T(-INFINITY);
+// A row in pieces of 16 aligned bytes, wherever it begins: vocabularies of odd
+// sizes are common, and loads across cache lines took an eighth more time.
+// Places count from the first piece's first element: [lead, end) are the row's.
+template <typename C> struct Row {
+  typedef typename std::remove_const<C>::type T;
+  static constexpr uint32_t N = Piece<T>::N;
+  C *at;  // place 0
+  uint32_t lead, end;
+
+  __device__ __forceinline__ Row(C *x, uint32_t vocab) {
+    lead = uint32_t(reinterpret_cast<uintptr_t>(x) & 15) / sizeof(T);
+    at = x - lead;
+    end = lead + vocab;
   }
-  return v;
-}
-template <typename T>
-__device__ __forceinline__ void store_piece(T *x, uint32_t p, uint32_t vocab, typename Piece<T>::val f) {
-  constexpr uint32_t N = Piece<T>::N;
-  const uint32_t at = p * N;
-  const typename Piece<T>::raw v = __builtin_convertvector(f, typename Piece<T>::raw);  // to nearest even
-  if (at + N <= vocab) {
-    *reinterpret_cast<typename Piece<T>::mem *>(x + at) = v;
-  } else {
+  __device__ __forceinline__ uint32_t pieces() const { return (end + N - 1) / N; }
+  __device__ __forceinline__ bool whole(uint32_t p) const { return p * N >= lead && p * N + N <= end; }
+  // Piece p, from `from` (place 0 of a row that may lie otherwise in memory);
+  // minus infinity where it is not the row's.
+  __device__ __forceinline__ typename Piece<T>::raw load(const T *from, uint32_t p) const {
+    typename Piece<T>::raw v;
+    if (whole(p)) {
+      v = *reinterpret_cast<const typename Piece<T>::mem *>(from + p * N);
+    } else {
 #pragma unroll
-    for (uint32_t e = 0; e < N; ++e)
-      if (at + e < vocab) x[at + e] = v[e];
+      for (uint32_t e = 0; e < N; ++e) v[e] = p * N + e >= lead && p * N + e < end ? from[p * N + e] : T(-INFINITY);
+    }
+    return v;
   }
-}
+  __device__ __forceinline__ typename Piece<T>::raw load(uint32_t p) const { return load(at, p); }
+  __device__ __forceinline__ void store(uint32_t p, typename Piece<T>::val f) const {
+    const typename Piece<T>::raw v = __builtin_convertvector(f, typename Piece<T>::raw);  // to nearest even
+    if (whole(p)) {
+      *reinterpret_cast<typename Piece<T>::raw *>(at + p * N) = v;
+    } else {
+#pragma unroll
+      for (uint32_t e = 0; e < N; ++e)
+        if (p * N + e >= lead && p * N + e < end) at[p * N + e] = v[e];
+    }
+  }
+};
+
 template <typename T>
 __device__ __forceinline__ typename Piece<T>::val values(typename Piece<T>::raw v) {
   return __builtin_convertvector(v, typename Piece<T>::val);
@@ -120,6 +132,12 @@ void with_element(int dtype, F f) {
   if (dtype == BBPE_BF16) f((__bf16)0);
   else if (dtype == BBPE_F16) f((_Float16)0);
   else f(0.0f);
+}
+
+// Pieces of a row that begins anywhere.
+inline uint32_t most_pieces(int dtype, uint32_t vocab) {
+  const uint32_t n = dtype == BBPE_F32 ? 4 : 8;
+  return (vocab + 2 * (n - 1)) / n;
 }
 
 inline uintptr_t address(const void *p) { return reinterpret_cast<uintptr_t>(p); }

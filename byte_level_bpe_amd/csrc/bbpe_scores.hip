@@ -121,11 +121,12 @@ __global__ __launch_bounds__(ROW_THREADS) void k_scores(ScoreArgs a) {
   __shared__ uint64_t reach;
   const uint64_t row = a.row0 + blockIdx.x;
   const T *x = static_cast<const T *>(a.x) + int64_t(row) * a.stride;
-  const uint32_t tid = threadIdx.x, pieces = (a.vocab + P::N - 1) / P::N, whole = a.vocab / P::N;
+  const Row<const T> r(x, a.vocab);
+  const uint32_t tid = threadIdx.x, pieces = r.pieces();
   const int32_t id = a.ids[row];
   const bool given = id >= 0 && uint32_t(id) < a.vocab;
   const float at_id = given ? float(x[id]) : INFINITY;  // nothing is above infinity
-  const uint32_t id_piece = given ? uint32_t(id) / P::N : 0;
+  const uint32_t id_piece = given ? (r.lead + uint32_t(id)) / P::N : 0;
   const float at_least = given ? next_below(at_id) : INFINITY;
 
   Partial s{-INFINITY, 0.0f, 0.0f};
@@ -169,18 +170,12 @@ __global__ __launch_bounds__(ROW_THREADS) void k_scores(ScoreArgs a) {
       }
     }
   };
-  const uint32_t steps = (pieces + ROW_STEP - 1) / ROW_STEP, full = whole / ROW_STEP;
-  Raw raw[ROW_UNROLL];
-  for (uint32_t i = 0; i < full; ++i) {
+  const uint32_t steps = (pieces + ROW_STEP - 1) / ROW_STEP;
+  for (uint32_t i = 0; i < steps; ++i) {
+    Raw raw[ROW_UNROLL];
 #pragma unroll
-    for (uint32_t u = 0; u < ROW_UNROLL; ++u)
-      raw[u] = *reinterpret_cast<const typename P::mem *>(x + uint64_t(i * ROW_STEP + u * ROW_THREADS + tid) * P::N);
+    for (uint32_t u = 0; u < ROW_UNROLL; ++u) raw[u] = r.load(i * ROW_STEP + u * ROW_THREADS + tid);
     work(raw, i);
-  }
-  if (full < steps) {
-#pragma unroll
-    for (uint32_t u = 0; u < ROW_UNROLL; ++u) raw[u] = load_piece<T>(x, full * ROW_STEP + u * ROW_THREADS + tid, a.vocab);
-    work(raw, full);
   }
   if ((tid & 63) == 0) sh_rank[tid >> 6] = above;
   if (TOP) {
@@ -199,7 +194,9 @@ __global__ __launch_bounds__(ROW_THREADS) void k_scores(ScoreArgs a) {
     int32_t rank = 0;
     if (given) {
       for (uint32_t w = 0; w < ROW_WAVES; ++w) rank += int32_t(sh_rank[w]);
-      for (uint32_t j = id_piece * P::N; j < uint32_t(id); ++j) rank += float(x[j]) == at_id;
+      for (uint32_t j = max(r.lead, id_piece * P::N); j < r.lead + uint32_t(id); ++j) rank += float(r.at[j]) == at_id;
+      // (places before the row have been taken for equal ones)
+      if (at_id == -INFINITY && id_piece > 0) rank -= int32_t(r.lead);
       rank = bad ? 0 : rank + 1;
       lp = bad ? nan : none ? -INFINITY : float((double(at_id) - s.max) * a.scale - log_sum);
     } else if (id >= 0) {
@@ -215,7 +212,7 @@ __global__ __launch_bounds__(ROW_THREADS) void k_scores(ScoreArgs a) {
 
   const auto put = [&](uint32_t rank, uint64_t key) {
     const float v = key_value<T>(key, a.index_bits);
-    a.top_ids[row * a.k + rank] = int32_t(key_place(key, a.index_bits));
+    a.top_ids[row * a.k + rank] = int32_t(key_place(key, a.index_bits) - r.lead);
     a.top_logprobs[row * a.k + rank] = none ? -INFINITY : float((double(v) - s.max) * a.scale - log_sum);
   };
   if (bad) {
@@ -226,8 +223,8 @@ __global__ __launch_bounds__(ROW_THREADS) void k_scores(ScoreArgs a) {
     return;
   }
   if (tid < 64) {
-    const uint64_t r = kth_key(keys, ROW_STEP, a.k);
-    if (tid == 0) reach = r;
+    const uint64_t bar = kth_key(keys, ROW_STEP, a.k);
+    if (tid == 0) reach = bar;
   }
   __syncthreads();
   for (uint32_t u = 0; u < ROW_UNROLL; ++u) {
@@ -243,11 +240,11 @@ __global__ __launch_bounds__(ROW_THREADS) void k_scores(ScoreArgs a) {
     for (uint32_t i = tid; i < n_pieces; i += ROW_THREADS) {
       const uint32_t p = (i % steps) * ROW_STEP + chosen[i / steps];
       if (p >= pieces) continue;
-      const typename P::val v = values<T>(load_piece<T>(x, p, a.vocab));
+      const typename P::val v = values<T>(r.load(p));
 #pragma unroll
       for (uint32_t e = 0; e < P::N; ++e) {
         const uint32_t j = p * P::N + e;
-        if (j >= a.vocab || order_key<T>(v[e], p * P::N, a.index_bits) < group_bar) continue;
+        if (j < r.lead || j >= r.end || order_key<T>(v[e], p * P::N, a.index_bits) < group_bar) continue;
         const uint64_t key = order_key<T>(v[e], j, a.index_bits);
         if (key >= low) take(key);
       }
@@ -320,10 +317,11 @@ __global__ __launch_bounds__(ROW_THREADS) void k_scores_back(ScoreBackArgs a) {
   __shared__ float sh_g[ROW_WAVES];
   const uint32_t tid = threadIdx.x;
   const uint64_t block = a.block0 + blockIdx.x, row = block / a.parts;
-  const uint32_t pieces = (a.vocab + P::N - 1) / P::N;
-  const uint32_t from = uint32_t(block % a.parts) * a.part, to = min(pieces, from + a.part);
   const T *x = static_cast<const T *>(a.x) + int64_t(row) * a.stride;
   T *dx = static_cast<T *>(a.dx) + int64_t(row) * a.dx_stride;
+  const Row<T> r(dx, a.vocab);  // pieces as they are written
+  const uint32_t from = uint32_t(block % a.parts) * a.part, to = min(r.pieces(), from + a.part);
+  if (from >= to) return;  // (parts are counted for rows that begin anywhere)
   // terms of single elements: the given token's, and the alternatives'
   const uint32_t n = 1 + (a.g_top ? a.k : 0);
   float mine = 0.0f;
@@ -359,14 +357,14 @@ __global__ __launch_bounds__(ROW_THREADS) void k_scores_back(ScoreBackArgs a) {
   float before[TERMS];
   for (uint32_t i = 0; i < TERMS; ++i) {
     const uint32_t t = tid + i * ROW_THREADS;
-    before[i] = t < n && own_id[t] >= 0 && uint32_t(own_id[t]) / P::N - from < to - from ? float(x[own_id[t]]) : 0.0f;
+    before[i] = t < n && own_id[t] >= 0 && (r.lead + uint32_t(own_id[t])) / P::N - from < to - from ? float(x[own_id[t]]) : 0.0f;
   }
   __syncthreads();
   for (uint32_t p0 = from + tid; p0 < to; p0 += ROW_STEP) {
     typename P::raw raw[ROW_UNROLL];
 #pragma unroll
     for (uint32_t u = 0; u < ROW_UNROLL; ++u)
-      if (p0 + u * ROW_THREADS < to && !zero) raw[u] = load_piece<T>(x, p0 + u * ROW_THREADS, a.vocab);
+      if (p0 + u * ROW_THREADS < to && !zero) raw[u] = r.load(x - r.lead, p0 + u * ROW_THREADS);
 #pragma unroll
     for (uint32_t u = 0; u < ROW_UNROLL; ++u) {
       if (p0 + u * ROW_THREADS >= to) break;
@@ -376,14 +374,14 @@ __global__ __launch_bounds__(ROW_THREADS) void k_scores_back(ScoreBackArgs a) {
 #pragma unroll
         for (uint32_t e = 0; e < P::N; ++e) v[e] = of(v[e]);
       }
-      store_piece<T>(dx, p0 + u * ROW_THREADS, a.vocab, v);
+      r.store(p0 + u * ROW_THREADS, v);
     }
   }
   __syncthreads();
   if (zero) return;
   for (uint32_t i = 0; i < TERMS; ++i) {
     const uint32_t t = tid + i * ROW_THREADS;
-    if (t >= n || own_id[t] < 0 || uint32_t(own_id[t]) / P::N - from >= to - from) continue;
+    if (t >= n || own_id[t] < 0 || (r.lead + uint32_t(own_id[t])) / P::N - from >= to - from) continue;
     float sum = 0.0f;
     for (uint32_t j = 0; j < n; ++j) sum += own_id[j] == own_id[t] ? own_g[j] : 0.0f;
     dx[own_id[t]] = T(of(before[i]) + a.scale * sum);
@@ -392,7 +390,7 @@ __global__ __launch_bounds__(ROW_THREADS) void k_scores_back(ScoreBackArgs a) {
 
 uint32_t bits_of(uint32_t vocab) {
   uint32_t b = 1;
-  while (b < 30 && (1u << b) < vocab) ++b;
+  while (b < 31 && (1u << b) < vocab) ++b;
   return b;
 }
 
@@ -426,7 +424,7 @@ int bbpe_token_logprobs(int dtype, const void *logits, int64_t row_stride, uint6
   a.k = top_k;
   a.scale = scale;
   a.c = scale * LOG2E;
-  a.index_bits = bits_of(vocab);
+  a.index_bits = bits_of(vocab + 8);  // places begin up to 7 before the row
   a.ids = d_ids;
   a.logprobs = d_logprobs;
   a.entropy = d_entropy;
@@ -475,9 +473,8 @@ int bbpe_token_logprobs_backward(int dtype, const void *logits, int64_t row_stri
   a.g_entropy = g_entropy;
   a.g_lse = g_lse;
   a.g_top = top_k ? g_top : nullptr;
-  const uint32_t pieces = uint32_t((uint64_t(vocab) * (dtype == BBPE_F32 ? 4 : 2) + 15) / 16);
   a.part = 2 * ROW_STEP;
-  a.parts = (pieces + a.part - 1) / a.part;
+  a.parts = (most_pieces(dtype, vocab) + a.part - 1) / a.part;
   const hipStream_t st = static_cast<hipStream_t>(hip_stream);
   const uint64_t blocks = n_rows * a.parts;
   for (; a.block0 < blocks; a.block0 += MAX_GROUPS)
