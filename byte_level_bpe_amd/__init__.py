@@ -52,8 +52,9 @@ EXPORTS = ["bbpe_load_ranks", "bbpe_load_ranks_tiktoken_file", "bbpe_upload_tabl
            "bbpe_block_tables_workspace_bytes", "bbpe_block_tables", "bbpe_qk_norm_rope",
            "bbpe_qk_norm_rope_backward_workspace_bytes", "bbpe_qk_norm_rope_backward",
            "bbpe_tree_attention_workspace_bytes", "bbpe_tree_attention",
-           "bbpe_token_logprobs", "bbpe_token_logprobs_backward", "bbpe_distill_loss",
-           "bbpe_distill_loss_backward"]
+           "bbpe_token_logprobs_workspace_bytes", "bbpe_token_logprobs",
+           "bbpe_token_logprobs_backward", "bbpe_distill_loss_workspace_bytes",
+           "bbpe_distill_loss", "bbpe_distill_loss_backward"]
 
 _lib = None
 

@@ -201,7 +201,7 @@ __global__ __launch_bounds__(ROW_THREADS) void k_distill(DistillArgs a) {
 #pragma unroll
       for (uint32_t e = 0; e < P::N; ++e) s.sum += __builtin_amdgcn_exp2f((v[u][e] - ref) * a.c);
   }
-  s = row_partial(s, a.c, sh);  // (with a barrier, for the list too)
+  s = row_partial<ROW_WAVES>(s, a.c, sh);  // (with a barrier, for the list too)
   if (tid < 64) end_row<T>(a, row, x, s, ids);
 }
 
@@ -328,10 +328,16 @@ int bbpe_distill_loss_backward(int dtype, const void *logits, int64_t row_stride
   return hipGetLastError() == hipSuccess ? BBPE_OK : BBPE_E_HIP;
 }
 
+int bbpe_distill_loss_workspace_bytes(int dtype, uint64_t n_rows, uint32_t vocab, uint64_t *out_bytes) {
+  if (!out_bytes || bad_sizes(dtype, n_rows, vocab)) return BBPE_E_INVALID_ARG;
+  *out_bytes = 0;
+  return BBPE_OK;
+}
+
 int bbpe_distill_loss(int dtype, const void *logits, int64_t row_stride, uint64_t n_rows, uint32_t vocab,
                       const int32_t *d_top_ids, const float *d_top_logprobs, uint32_t top_k, int tail, float scale,
                       float *d_loss, float *d_lse, float *d_stats, const float *d_weights, void *d_logits, int64_t dl_stride,
-                      void *hip_stream) {
+                      void *d_workspace, uint64_t workspace_bytes, void *hip_stream) {
   const int rc = check(dtype, logits, row_stride, n_rows, vocab, d_top_ids, d_top_logprobs, top_k, tail, scale);
   if (rc) return rc;
   if ((n_rows && (!d_loss || !d_lse || !d_stats)) || ((address(d_loss) | address(d_lse) | address(d_weights)) & 3) ||

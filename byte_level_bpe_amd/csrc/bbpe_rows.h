@@ -12,7 +12,7 @@
 
 namespace bbpe {
 
-constexpr uint32_t ROW_THREADS = 256;  // of a workgroup
+constexpr uint32_t ROW_THREADS = 256;  // of a workgroup, where it is not a template's
 constexpr uint32_t ROW_WAVES = ROW_THREADS / 64;
 constexpr uint32_t ROW_UNROLL = 4;     // pieces of a thread's step
 constexpr uint32_t ROW_STEP = ROW_THREADS * ROW_UNROLL;  // pieces of a workgroup's step
@@ -98,19 +98,24 @@ __device__ __forceinline__ Partial relative(Partial p, float max, float c) {
   const float f = __builtin_amdgcn_exp2f(d * c);
   return Partial{max, p.sum * f, f == 0.0f ? 0.0f : f * (p.mean + p.sum * d)};  // (0 times minus infinity is to be 0)
 }
-// The workgroup's, in every thread.  sh: ROW_WAVES of them.
-__device__ __forceinline__ Partial row_partial(Partial p, float c, Partial *sh) {
+// The wave's, and the workgroup's of WAVES waves (sh: room for them), in every thread.
+__device__ __forceinline__ Partial wave_partial(Partial p, float c) {
   p = relative(p, wave_max(p.max), c);
   p.sum = wave_sum(p.sum);
   p.mean = wave_sum(p.mean);
+  return p;
+}
+template <uint32_t WAVES>
+__device__ __forceinline__ Partial row_partial(Partial p, float c, Partial *sh) {
+  p = wave_partial(p, c);
   if ((threadIdx.x & 63) == 0) sh[threadIdx.x >> 6] = p;
   __syncthreads();
   float m = sh[0].max;
 #pragma unroll
-  for (uint32_t w = 1; w < ROW_WAVES; ++w) m = fmaxf(m, sh[w].max);
+  for (uint32_t w = 1; w < WAVES; ++w) m = fmaxf(m, sh[w].max);
   Partial all{m, 0.0f, 0.0f};
 #pragma unroll
-  for (uint32_t w = 0; w < ROW_WAVES; ++w) {
+  for (uint32_t w = 0; w < WAVES; ++w) {
     const Partial q = relative(sh[w], m, c);
     all.sum += q.sum;
     all.mean += q.mean;
@@ -142,11 +147,13 @@ inline uint32_t most_pieces(int dtype, uint32_t vocab) {
 
 inline uintptr_t address(const void *p) { return reinterpret_cast<uintptr_t>(p); }
 
+inline bool bad_sizes(int dtype, uint64_t rows, uint32_t vocab) {
+  return dtype < BBPE_BF16 || dtype > BBPE_F32 || vocab == 0 || vocab > (1u << 30) || rows > 0x7FFFFFFFull;
+}
 // What the operators ask of a matrix of logits alike.  `grad`: one of gradients,
 // whose rows must not share memory.
 inline bool bad_logits(int dtype, const void *x, int64_t stride, uint64_t rows, uint32_t vocab, bool grad) {
-  if (dtype < BBPE_BF16 || dtype > BBPE_F32 || vocab == 0 || vocab > (1u << 30) || rows > 0x7FFFFFFFull) return true;
-  if (rows && (!x || (address(x) & (dtype == BBPE_F32 ? 3 : 1)))) return true;
+  if (bad_sizes(dtype, rows, vocab) || (rows && (!x || (address(x) & (dtype == BBPE_F32 ? 3 : 1))))) return true;
   return grad && rows > 1 && (stride < 0 ? -stride : stride) < int64_t(vocab);
 }
 

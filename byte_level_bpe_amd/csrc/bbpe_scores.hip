@@ -19,15 +19,25 @@
 namespace bbpe {
 namespace {
 
-constexpr uint32_t TOP_MAX = 256;      // alternatives at most
-constexpr uint32_t TOP_ROOM = 2048;    // candidates for them at most
-static_assert(TOP_ROOM >= ROW_STEP && TOP_ROOM >= 8 * TOP_MAX, "");
+constexpr uint32_t TOP_MAX = 256;   // alternatives at most
+// What a bar may let through besides the first k: the halving ends some steps
+// earlier for it (64 alternatives of 200,064: 333 us exact, SLACKTIME with this).
+__host__ __device__ constexpr uint32_t with_slack(uint32_t k) { return k + k / 4 + 16; }
+constexpr uint32_t TOP_ROOM = with_slack(TOP_MAX);
+constexpr uint32_t KEPT_ROOM = (TOP_ROOM + 63) / 64 * 64;
+constexpr uint32_t PARTS_MAX = 64;  // parts of a row at most: a wave joins them
+constexpr uint32_t JOIN_KEYS = 4096;  // alternatives of all parts at most
+
+struct ScorePart {
+  Partial p;
+  uint32_t above;
+};
 
 struct ScoreArgs {
   const void *x;
   int64_t stride;
-  uint64_t row0;
-  uint32_t vocab, k;
+  uint64_t block0;
+  uint32_t vocab, k, parts, part;  // parts of a row, and pieces of one
   float scale, c;
   uint32_t index_bits;  // of a place in the row
   const int32_t *ids;
@@ -36,6 +46,8 @@ struct ScoreArgs {
   int32_t *top_ids;
   float *top_logprobs;
   float2 *stats;
+  ScorePart *parted;  // [rows][parts], and the parts' alternatives [rows][parts][k], 0 where there are fewer
+  uint64_t *parted_top;
 };
 
 // ---- order ----
@@ -62,18 +74,26 @@ __device__ __forceinline__ uint32_t key_place(uint64_t key, uint32_t bits) {
   return ((1u << bits) - 1) - (uint32_t(key) & ((1u << bits) - 1));
 }
 
-// A number that exactly k of the n keys in LDS reach, by one wave; 1 if there
-// are no more than k.  Keys differ from each other, but for absent ones, which are 0.
-__device__ uint64_t kth_key(const uint64_t *keys, uint32_t n, uint32_t k) {
-  const uint32_t lane = threadIdx.x & 63;
+// A number that k of the keys reach, and no more than `most`, by one wave; 1 if
+// there are no more than k.  get(i): the lane's i-th of N, or of n where N is 0.
+// Keys differ from each other, but for absent ones, which are 0.
+template <uint32_t N, typename G>
+__device__ __forceinline__ uint64_t top_bar(G get, uint32_t n, uint32_t k, uint32_t most) {
+  const auto each = [&](auto f) {
+    if constexpr (N > 0) {
+#pragma unroll
+      for (uint32_t i = 0; i < N; ++i) f(get(i));
+    } else {
+      for (uint32_t i = 0; i < n; ++i) f(get(i));
+    }
+  };
   uint64_t lo = ~uint64_t(0), hi = 0;
   uint32_t there = 0;
-  for (uint32_t i = 0; i < n; i += 64) {
-    const uint64_t v = i + lane < n ? keys[i + lane] : 0;
+  each([&](uint64_t v) {
     there += uint32_t(__popcll(__ballot(v != 0)));
     if (v > hi) hi = v;
     if (v && v < lo) lo = v;
-  }
+  });
   if (there <= k) return 1;
 #pragma unroll
   for (int d = 1; d < 64; d <<= 1) {
@@ -85,12 +105,62 @@ __device__ uint64_t kth_key(const uint64_t *keys, uint32_t n, uint32_t k) {
   while (lo < hi) {
     const uint64_t mid = lo + (hi - lo + 1) / 2;
     uint32_t reach = 0;
-    for (uint32_t i = 0; i < n; i += 64) reach += uint32_t(__popcll(__ballot(i + lane < n && keys[i + lane] >= mid)));
-    if (reach == k) return mid;
-    if (reach > k) lo = mid;
-    else hi = mid - 1;
+    each([&](uint64_t v) { reach += uint32_t(__popcll(__ballot(v >= mid))); });
+    if (reach < k) {
+      hi = mid - 1;
+    } else {
+      if (reach <= most) return mid;
+      lo = mid;
+    }
   }
   return lo;
+}
+
+// Puts n different keys in order, the first k of them: put(place, key).  keys:
+// ROOM of them in LDS, which the call uses up.  Sixty-four at a time are ranked
+// by counting; a key's place among the others is found by halving, in all of the
+// ordered sixty-fours at once (256 of 400 by counting alone: SLOWTIME a row).
+template <uint32_t WAVES, uint32_t ROOM, typename F>
+__device__ __forceinline__ void put_in_order(uint64_t *keys, uint32_t n, uint32_t k, F put) {
+  constexpr uint32_t Q = (ROOM / 64 + WAVES - 1) / WAVES;
+  const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6, blocks = (n + 63) / 64;
+  uint64_t mine[Q];
+  uint32_t place[Q];
+#pragma unroll
+  for (uint32_t q = 0; q < Q; ++q) {
+    const uint32_t b = wave + q * WAVES;
+    if (b >= blocks) break;
+    mine[q] = b * 64 + lane < n ? keys[b * 64 + lane] : 0;
+    const uint32_t there = min(64u, n - b * 64);
+    place[q] = 0;
+#pragma unroll 8
+    for (uint32_t j = 0; j < there; ++j) place[q] += keys[b * 64 + j] > mine[q];
+    if (lane >= there) place[q] = lane;
+  }
+  if (blocks > 1) {
+    __syncthreads();
+#pragma unroll
+    for (uint32_t q = 0; q < Q; ++q)
+      if (wave + q * WAVES < blocks) keys[(wave + q * WAVES) * 64 + place[q]] = mine[q];
+    __syncthreads();
+  }
+#pragma unroll
+  for (uint32_t q = 0; q < Q; ++q) {
+    const uint32_t b = wave + q * WAVES;
+    if (b >= blocks) break;
+    if (b * 64 + lane >= n) continue;
+    uint32_t at = place[q];
+#pragma unroll 4
+    for (uint32_t o = 0; o < blocks; ++o) {
+      const uint64_t *others = keys + o * 64;
+      uint32_t before = 0;
+#pragma unroll
+      for (uint32_t half = 32; half; half /= 2) before += others[before + half - 1] > mine[q] ? half : 0;
+      before += others[before] > mine[q];
+      at += o == b ? 0 : before;
+    }
+    if (at < k) put(at, mine[q]);
+  }
 }
 
 // The largest number below v in the order of floats; below minus infinity: NaN.
@@ -101,44 +171,112 @@ __device__ __forceinline__ float next_below(float v) {
   return __uint_as_float(v > 0.0f ? b - 1 : b + 1);
 }
 
-// One workgroup a row.
+// What a row's weights come to.
+struct RowEnd {
+  Partial p;
+  bool none, bad;  // nothing but minus infinity; a NaN or plus infinity
+  double log_sum;
+
+  __device__ __forceinline__ explicit RowEnd(Partial s) : p(s) {
+    none = s.max == -INFINITY && s.sum == 0.0f;
+    bad = !(s.sum == s.sum) || s.max == INFINITY;
+    log_sum = none ? -INFINITY : log(double(s.sum));
+  }
+  __device__ __forceinline__ float logprob(float v, float scale) const {
+    return bad ? __uint_as_float(0x7FC00000u) : none ? -INFINITY : float((double(v) - p.max) * scale - log_sum);
+  }
+};
+
+// The row's given token.
+template <typename T> struct Given {
+  bool there;
+  float value;      // infinity where there is none: nothing is above it
+  uint32_t place;
+  __device__ __forceinline__ Given(const ScoreArgs &a, const Row<const T> &r, int32_t id) {
+    there = id >= 0 && uint32_t(id) < a.vocab;
+    place = r.lead + (there ? uint32_t(id) : 0);
+    value = there ? float(r.at[place]) : INFINITY;
+  }
+  __device__ __forceinline__ uint32_t piece() const { return place / Piece<T>::N; }
+  // Elements before it in its piece that are equal to it.  Places before the row
+  // count as minus infinity in all pieces before its own, and are taken off.
+  __device__ __forceinline__ int32_t equal_before(const Row<const T> &r) const {
+    constexpr uint32_t N = Piece<T>::N;
+    const typename Piece<T>::val v = values<T>(r.load(piece()));
+    int32_t n = value == -INFINITY && piece() > 0 ? -int32_t(r.lead) : 0;
+#pragma unroll
+    for (uint32_t e = 0; e < N; ++e) n += piece() * N + e >= r.lead && piece() * N + e < place && v[e] == value;
+    return n;
+  }
+};
+
+// The row's numbers, by one thread.  above: elements before the given one in order.
+template <typename T>
+__device__ __forceinline__ void write_row(const ScoreArgs &a, uint64_t row, const RowEnd &end, int32_t id, const Given<T> &given, int32_t above) {
+  const float nan = __uint_as_float(0x7FC00000u);
+  a.logprobs[row] = given.there ? end.logprob(given.value, a.scale) : id < 0 ? 0.0f : nan;
+  a.ranks[row] = given.there && !end.bad ? above + 1 : 0;
+  a.entropy[row] = end.bad ? nan : end.none ? 0.0f : float(end.log_sum - double(end.p.mean) / end.p.sum * a.scale);
+  a.lse[row] = end.bad ? nan : end.none ? -INFINITY : float(double(end.p.max) * a.scale + end.log_sum);
+  a.stats[row] = end.bad ? make_float2(0.0f, nan) : make_float2(end.p.max, float(end.log_sum));
+}
+template <typename T>
+__device__ __forceinline__ void write_top(const ScoreArgs &a, uint64_t row, uint32_t lead, const RowEnd &end, uint32_t t, uint64_t key) {
+  a.top_ids[row * a.k + t] = end.bad ? -1 : int32_t(key_place(key, a.index_bits) - lead);
+  a.top_logprobs[row * a.k + t] = end.logprob(key_value<T>(key, a.index_bits), a.scale);
+}
+
+// One workgroup a row, or a part of one (SPLIT).
 //
 // Alternatives.  A thread's step takes ROW_UNROLL pieces; the pieces at one
-// place of all steps are a group, of which the thread keeps the largest element
-// and the first piece that has it.  An element among the row's first k lies in
-// one of the k groups whose largest come first: k groups without it would have
-// k elements before it.  Those groups are read once more, and what reaches the
-// k-th group's largest are the candidates, seldom many more than k.
-template <typename T, bool TOP>
-__global__ __launch_bounds__(ROW_THREADS) void k_scores(ScoreArgs a) {
+// place of all steps are a group, of which the thread keeps the largest element,
+// the first piece that has it, and the largest element of all other pieces.  A
+// bar that the largest of k groups or more reach keeps the first k elements: one
+// below it has k before it.  Of the groups that reach it the pieces with the
+// largest are read once more, and the others only where their largest reaches it
+// too: seldom.  What reaches it are the candidates, not many more than k.
+template <typename T, uint32_t WAVES, bool TOP, bool SPLIT>
+__global__ __launch_bounds__(64 * WAVES) void k_scores(ScoreArgs a) {
   typedef Piece<T> P;
-  typedef typename P::raw Raw;
-  __shared__ Partial sh[ROW_WAVES];
-  __shared__ uint32_t sh_rank[ROW_WAVES];
-  __shared__ uint64_t keys[TOP ? TOP_ROOM : 1];
-  __shared__ uint16_t chosen[TOP ? TOP_MAX : 1];
-  __shared__ uint32_t n_chosen, n_found;
+  constexpr uint32_t THREADS = 64 * WAVES, STEP = THREADS * ROW_UNROLL;
+  constexpr uint32_t ROOM = 2 * STEP;  // for candidates
+  static_assert(ROOM >= TOP_ROOM, "");
+  __shared__ Partial sh[WAVES];
+  __shared__ uint32_t sh_above[WAVES];
+  __shared__ uint64_t keys[TOP ? ROOM : 1];
+  __shared__ uint32_t chosen[TOP ? TOP_ROOM : 1];  // pieces
+  __shared__ uint16_t deep[TOP ? TOP_ROOM : 1];    // groups
+  __shared__ uint32_t n_chosen, n_deep, n_found;
   __shared__ uint64_t reach;
-  const uint64_t row = a.row0 + blockIdx.x;
+  const uint64_t block = a.block0 + blockIdx.x, row = SPLIT ? block / a.parts : block;
   const T *x = static_cast<const T *>(a.x) + int64_t(row) * a.stride;
   const Row<const T> r(x, a.vocab);
-  const uint32_t tid = threadIdx.x, pieces = r.pieces();
+  const uint32_t tid = threadIdx.x, first = SPLIT ? uint32_t(block % a.parts) * a.part : 0;
+  const uint32_t last = SPLIT ? min(r.pieces(), first + a.part) : r.pieces();
   const int32_t id = a.ids[row];
-  const bool given = id >= 0 && uint32_t(id) < a.vocab;
-  const float at_id = given ? float(x[id]) : INFINITY;  // nothing is above infinity
-  const uint32_t id_piece = given ? (r.lead + uint32_t(id)) / P::N : 0;
-  const float at_least = given ? next_below(at_id) : INFINITY;
+  const Given<T> given(a, r, id);
+  const uint32_t before_id = given.there ? min(last, given.piece()) : 0;  // pieces, where equal ones count too
+  const float at_least = given.there ? next_below(given.value) : INFINITY;
+  const int32_t beside = !SPLIT && given.there ? given.equal_before(r) : 0;
 
   Partial s{-INFINITY, 0.0f, 0.0f};
   float ref = 0.0f;
   uint32_t above = 0;  // the wave's
-  float best[ROW_UNROLL];
-  uint32_t step_of[ROW_UNROLL];
+  float best[ROW_UNROLL], second[ROW_UNROLL];
+  uint32_t best_at[ROW_UNROLL];
+#pragma unroll
   for (uint32_t u = 0; u < ROW_UNROLL; ++u) {
-    best[u] = -INFINITY;
-    step_of[u] = 0;
+    best[u] = second[u] = -INFINITY;
+    best_at[u] = first + u * THREADS + tid;
   }
-  const auto work = [&](const Raw (&raw)[ROW_UNROLL], uint32_t step) {
+  for (uint32_t p0 = first; p0 < last; p0 += STEP) {
+    typename P::raw raw[ROW_UNROLL];
+#pragma unroll
+    for (uint32_t u = 0; u < ROW_UNROLL; ++u) {
+      const uint32_t p = p0 + u * THREADS + tid;
+      if (!SPLIT || p < last) raw[u] = r.load(p);
+      else raw[u] = T(-INFINITY);
+    }
     typename P::val v[ROW_UNROLL];
     float m = -INFINITY;
 #pragma unroll
@@ -147,9 +285,12 @@ __global__ __launch_bounds__(ROW_THREADS) void k_scores(ScoreArgs a) {
       float pm = v[u][0];
 #pragma unroll
       for (uint32_t e = 1; e < P::N; ++e) pm = fmaxf(pm, v[u][e]);
-      if (TOP && pm > best[u]) {
-        best[u] = pm;
-        step_of[u] = step;
+      if (TOP) {
+        second[u] = fmaxf(second[u], fminf(best[u], pm));
+        if (pm > best[u]) {
+          best[u] = pm;
+          best_at[u] = p0 + u * THREADS + tid;
+        }
       }
       m = fmaxf(m, pm);
     }
@@ -159,8 +300,7 @@ __global__ __launch_bounds__(ROW_THREADS) void k_scores(ScoreArgs a) {
     }
 #pragma unroll
     for (uint32_t u = 0; u < ROW_UNROLL; ++u) {
-      const uint32_t p = step * ROW_STEP + u * ROW_THREADS + tid;
-      const float bar = p < id_piece ? at_least : at_id;
+      const float bar = p0 + u * THREADS + tid < before_id ? at_least : given.value;
 #pragma unroll
       for (uint32_t e = 0; e < P::N; ++e) {
         const float d = v[u][e] - ref, w = __builtin_amdgcn_exp2f(d * a.c);
@@ -169,77 +309,67 @@ __global__ __launch_bounds__(ROW_THREADS) void k_scores(ScoreArgs a) {
         above += uint32_t(__popcll(__ballot(!(v[u][e] <= bar))));
       }
     }
-  };
-  const uint32_t steps = (pieces + ROW_STEP - 1) / ROW_STEP;
-  for (uint32_t i = 0; i < steps; ++i) {
-    Raw raw[ROW_UNROLL];
-#pragma unroll
-    for (uint32_t u = 0; u < ROW_UNROLL; ++u) raw[u] = r.load(i * ROW_STEP + u * ROW_THREADS + tid);
-    work(raw, i);
   }
-  if ((tid & 63) == 0) sh_rank[tid >> 6] = above;
+  if ((tid & 63) == 0) sh_above[tid >> 6] = above;
   if (TOP) {
+#pragma unroll
     for (uint32_t u = 0; u < ROW_UNROLL; ++u) {
-      const uint32_t g = u * ROW_THREADS + tid;
-      keys[g] = g < pieces ? order_key<T>(best[u], (step_of[u] * ROW_STEP + g) * P::N, a.index_bits) : 0;
+      const uint32_t g = u * THREADS + tid;
+      keys[g] = first + g < last ? order_key<T>(best[u], best_at[u] * P::N, a.index_bits) : 0;
     }
-    if (tid == 0) n_chosen = n_found = 0;
+    if (tid == 0) n_chosen = n_deep = n_found = 0;
   }
-  s = row_partial(s, a.c, sh);  // (with a barrier)
-  const bool none = s.max == -INFINITY && s.sum == 0.0f, bad = !(s.sum == s.sum) || s.max == INFINITY;
-  const double log_sum = none ? -INFINITY : log(double(s.sum));
-  if (tid == 0) {
-    const float nan = __uint_as_float(0x7FC00000u);
-    float lp = 0.0f;
-    int32_t rank = 0;
-    if (given) {
-      for (uint32_t w = 0; w < ROW_WAVES; ++w) rank += int32_t(sh_rank[w]);
-      for (uint32_t j = max(r.lead, id_piece * P::N); j < r.lead + uint32_t(id); ++j) rank += float(r.at[j]) == at_id;
-      // (places before the row have been taken for equal ones)
-      if (at_id == -INFINITY && id_piece > 0) rank -= int32_t(r.lead);
-      rank = bad ? 0 : rank + 1;
-      lp = bad ? nan : none ? -INFINITY : float((double(at_id) - s.max) * a.scale - log_sum);
-    } else if (id >= 0) {
-      lp = nan;
-    }
-    a.logprobs[row] = lp;
-    a.ranks[row] = rank;
-    a.entropy[row] = bad ? nan : none ? 0.0f : float(log_sum - double(s.mean) / s.sum * a.scale);
-    a.lse[row] = bad ? nan : none ? -INFINITY : float(double(s.max) * a.scale + log_sum);
-    a.stats[row] = bad ? make_float2(0.0f, nan) : make_float2(s.max, float(log_sum));
+  const RowEnd end(row_partial<WAVES>(s, a.c, sh));  // (with a barrier)
+  if (tid == THREADS - 1) {  // (the first wave has the bar to find)
+    above = 0;
+    for (uint32_t w = 0; w < WAVES; ++w) above += sh_above[w];
+    if (SPLIT) a.parted[block] = ScorePart{end.p, above};
+    else write_row<T>(a, row, end, id, given, int32_t(above) + beside);
   }
   if (!TOP) return;
 
-  const auto put = [&](uint32_t rank, uint64_t key) {
-    const float v = key_value<T>(key, a.index_bits);
-    a.top_ids[row * a.k + rank] = int32_t(key_place(key, a.index_bits) - r.lead);
-    a.top_logprobs[row * a.k + rank] = none ? -INFINITY : float((double(v) - s.max) * a.scale - log_sum);
+  const auto put = [&](uint32_t t, uint64_t key) {
+    if (SPLIT) a.parted_top[block * a.k + t] = key;
+    else write_top<T>(a, row, r.lead, end, t, key);
   };
-  if (bad) {
-    for (uint32_t t = tid; t < a.k; t += ROW_THREADS) {
-      a.top_ids[row * a.k + t] = -1;
-      a.top_logprobs[row * a.k + t] = __uint_as_float(0x7FC00000u);
-    }
+  if (end.bad) {
+    for (uint32_t t = tid; t < a.k; t += THREADS) put(t, 0);
     return;
   }
   if (tid < 64) {
-    const uint64_t bar = kth_key(keys, ROW_STEP, a.k);
+    uint64_t mine[STEP / 64];
+#pragma unroll
+    for (uint32_t i = 0; i < STEP / 64; ++i) mine[i] = keys[i * 64 + tid];
+    const uint64_t bar = top_bar<STEP / 64>([&](uint32_t i) { return mine[i]; }, 0, a.k, with_slack(a.k));
     if (tid == 0) reach = bar;
   }
   __syncthreads();
+  const uint64_t group_bar = reach;
+#pragma unroll
   for (uint32_t u = 0; u < ROW_UNROLL; ++u) {
-    const uint32_t g = u * ROW_THREADS + tid;
-    if (keys[g] >= reach) chosen[atomicAdd(&n_chosen, 1u)] = uint16_t(g);  // (k at most; their order does not matter)
+    const uint32_t g = u * THREADS + tid;
+    if (keys[g] < group_bar) continue;
+    // (their order does not matter)
+    chosen[atomicAdd(&n_chosen, 1u)] = best_at[u];
+    if (order_key<T>(second[u], 0, a.index_bits) >= group_bar) deep[atomicAdd(&n_deep, 1u)] = uint16_t(g);
   }
   __syncthreads();
-  // Every element of the chosen groups that is no later in order than the k-th
-  // group's largest (as that key has it: by its piece's place) and reaches `low`.
-  const uint32_t n_pieces = n_chosen * steps;
-  const uint64_t group_bar = reach;
+  // Every element of the chosen groups that reaches the bar (by its piece's place,
+  // as groups do) and `low`.
+  const uint32_t n_pieces = n_chosen, deep_steps = (last - first + STEP - 1) / STEP, n_deep_pieces = n_deep * deep_steps;
   const auto each = [&](uint64_t low, auto take) {
-    for (uint32_t i = tid; i < n_pieces; i += ROW_THREADS) {
-      const uint32_t p = (i % steps) * ROW_STEP + chosen[i / steps];
-      if (p >= pieces) continue;
+    for (uint32_t i = tid; i < n_pieces + n_deep_pieces; i += THREADS) {
+      uint32_t p;
+      if (i < n_pieces) {
+        p = chosen[i];
+      } else {
+        const uint32_t g = deep[(i - n_pieces) / deep_steps];
+        p = first + (i - n_pieces) % deep_steps * STEP + g;
+        if (p >= last) continue;
+        bool done = false;  // its first piece is among the chosen ones
+        for (uint32_t j = 0; j < n_pieces; ++j) done |= chosen[j] == p;
+        if (done) continue;
+      }
       const typename P::val v = values<T>(r.load(p));
 #pragma unroll
       for (uint32_t e = 0; e < P::N; ++e) {
@@ -253,12 +383,12 @@ __global__ __launch_bounds__(ROW_THREADS) void k_scores(ScoreArgs a) {
   const auto collect = [&](uint64_t low) {
     each(low, [&](uint64_t key) {
       const uint32_t to = atomicAdd(&n_found, 1u);
-      if (to < TOP_ROOM) keys[to] = key;
+      if (to < ROOM) keys[to] = key;
     });
     __syncthreads();
   };
   collect(0);
-  if (n_found > TOP_ROOM) {
+  if (n_found > ROOM) {
     // Large elements crowd in a few groups: halve what is between until a bar
     // leaves k or more, and no more than there is room for.  (Keys differ, so
     // there is one that leaves k.)
@@ -275,7 +405,7 @@ __global__ __launch_bounds__(ROW_THREADS) void k_scores(ScoreArgs a) {
         hi = mid - 1;
       } else {
         lo = mid;
-        if (n <= TOP_ROOM) break;
+        if (n <= ROOM) break;
       }
     }
     __syncthreads();
@@ -284,12 +414,47 @@ __global__ __launch_bounds__(ROW_THREADS) void k_scores(ScoreArgs a) {
     collect(lo);
   }
   const uint32_t n = n_found;
-  for (uint32_t i = tid; i < n; i += ROW_THREADS) {
-    const uint64_t mine = keys[i];
-    uint32_t before = 0;
-    for (uint32_t j = 0; j < n; ++j) before += keys[j] > mine;
-    if (before < a.k) put(before, mine);
+  put_in_order<WAVES, ROOM>(keys, n, a.k, put);
+  if (SPLIT)
+    for (uint32_t t = n + tid; t < a.k; t += THREADS) put(t, 0);  // a part of fewer elements
+}
+
+// Joins a row's parts.
+template <typename T, bool TOP>
+__global__ __launch_bounds__(TOP ? ROW_THREADS : 64) void k_scores_join(ScoreArgs a) {
+  __shared__ uint64_t keys[TOP ? JOIN_KEYS : 1];
+  __shared__ uint64_t kept[TOP ? KEPT_ROOM : 1];
+  __shared__ uint32_t n_kept;
+  __shared__ uint64_t reach;
+  const uint64_t row = a.block0 + blockIdx.x;
+  const Row<const T> r(static_cast<const T *>(a.x) + int64_t(row) * a.stride, a.vocab);
+  const uint32_t tid = threadIdx.x, lane = tid & 63;
+  ScorePart part{Partial{-INFINITY, 0.0f, 0.0f}, 0};
+  if (lane < a.parts) part = a.parted[row * a.parts + lane];
+  const RowEnd end(wave_partial(part.p, a.c));
+  const uint32_t above = wave_sum(part.above);
+  const int32_t id = a.ids[row];
+  const Given<T> given(a, r, id);
+  if (tid == (TOP ? ROW_THREADS : 64) - 1)
+    write_row<T>(a, row, end, id, given, int32_t(above) + (given.there ? given.equal_before(r) : 0));
+  if (!TOP) return;
+  const uint32_t n = a.parts * a.k;
+  for (uint32_t i = tid; i < n; i += ROW_THREADS) keys[i] = a.parted_top[row * n + i];
+  if (tid == 0) n_kept = 0;
+  __syncthreads();
+  if (end.bad) {
+    for (uint32_t t = tid; t < a.k; t += ROW_THREADS) write_top<T>(a, row, r.lead, end, t, 0);
+    return;
   }
+  if (tid < 64) {
+    const uint64_t bar = top_bar<0>([&](uint32_t i) { return i * 64 + lane < n ? keys[i * 64 + lane] : 0; }, (n + 63) / 64, a.k, with_slack(a.k));
+    if (tid == 0) reach = bar;
+  }
+  __syncthreads();
+  for (uint32_t i = tid; i < n; i += ROW_THREADS)
+    if (keys[i] >= reach) kept[atomicAdd(&n_kept, 1u)] = keys[i];
+  __syncthreads();
+  put_in_order<ROW_WAVES, KEPT_ROOM>(kept, n_kept, a.k, [&](uint32_t t, uint64_t key) { write_top<T>(a, row, r.lead, end, t, key); });
 }
 
 struct ScoreBackArgs {
@@ -396,6 +561,34 @@ uint32_t bits_of(uint32_t vocab) {
 
 constexpr uint64_t MAX_GROUPS = 1u << 23;  // workgroups of a launch: fewer than 2^32 threads
 
+// How rows are cut: waves a workgroup, parts a row and pieces of a part.
+struct Cut {
+  uint32_t waves, parts, part;
+  uint64_t part_bytes, bytes;  // of the parts' numbers, and with their alternatives
+};
+Cut cut_of(int dtype, uint64_t n_rows, uint32_t vocab, uint32_t k) {
+  const uint32_t pieces = most_pieces(dtype, vocab);
+  Cut c{pieces <= 512 ? 1u : ROW_WAVES, 1, 0, 0, 0};
+  if (c.waves > 1 && n_rows) {
+    const uint64_t want = (2048 + n_rows - 1) / n_rows;
+    uint64_t most = std::min<uint64_t>(PARTS_MAX, (pieces + ROW_STEP - 1) / ROW_STEP);
+    if (k) most = std::min<uint64_t>(most, JOIN_KEYS / k);
+    c.parts = uint32_t(std::max<uint64_t>(1, std::min(want, most)));
+  }
+  c.part = ((pieces + c.parts - 1) / c.parts + 63) / 64 * 64;
+  if (c.parts > 1) {
+    c.part_bytes = (n_rows * c.parts * sizeof(ScorePart) + 255) / 256 * 256;
+    c.bytes = c.part_bytes + n_rows * c.parts * k * sizeof(uint64_t);
+  }
+  return c;
+}
+
+int check_scores(int dtype, const void *logits, int64_t stride, uint64_t n_rows, uint32_t vocab, uint32_t k, float scale) {
+  return bad_logits(dtype, logits, stride, n_rows, vocab, false) || k > TOP_MAX || k > vocab || !(scale > 0.0f) || !std::isfinite(scale)
+             ? BBPE_E_INVALID_ARG
+             : BBPE_OK;
+}
+
 }  // namespace
 }  // namespace bbpe
 
@@ -403,13 +596,18 @@ using namespace bbpe;
 
 extern "C" {
 
+int bbpe_token_logprobs_workspace_bytes(int dtype, uint64_t n_rows, uint32_t vocab, uint32_t top_k, uint64_t *out_bytes) {
+  if (!out_bytes || bad_sizes(dtype, n_rows, vocab) || top_k > TOP_MAX || top_k > vocab) return BBPE_E_INVALID_ARG;
+  *out_bytes = cut_of(dtype, n_rows, vocab, top_k).bytes;
+  return BBPE_OK;
+}
+
 int bbpe_token_logprobs(int dtype, const void *logits, int64_t row_stride, uint64_t n_rows, uint32_t vocab,
                         const int32_t *d_ids, uint32_t top_k, float scale, float *d_logprobs, float *d_entropy,
                         float *d_lse, int32_t *d_ranks, int32_t *d_top_ids, float *d_top_logprobs, float *d_stats,
-                        void *hip_stream) {
-  if (bad_logits(dtype, logits, row_stride, n_rows, vocab, false) || top_k > TOP_MAX || top_k > vocab || !(scale > 0.0f) ||
-      !std::isfinite(scale))
-    return BBPE_E_INVALID_ARG;
+                        void *d_workspace, uint64_t workspace_bytes, void *hip_stream) {
+  const int rc = check_scores(dtype, logits, row_stride, n_rows, vocab, top_k, scale);
+  if (rc) return rc;
   if (n_rows && (!d_ids || !d_logprobs || !d_entropy || !d_lse || !d_ranks || !d_stats ||
                  (top_k && (!d_top_ids || !d_top_logprobs))))
     return BBPE_E_INVALID_ARG;
@@ -417,11 +615,15 @@ int bbpe_token_logprobs(int dtype, const void *logits, int64_t row_stride, uint6
        address(d_top_logprobs)) & 3 || (address(d_stats) & 7))
     return BBPE_E_INVALID_ARG;
   if (n_rows == 0) return BBPE_OK;
+  const Cut cut = cut_of(dtype, n_rows, vocab, top_k);
+  if (cut.bytes && (!d_workspace || (address(d_workspace) & 255) || workspace_bytes < cut.bytes)) return BBPE_E_WORKSPACE;
   ScoreArgs a{};
   a.x = logits;
   a.stride = row_stride;
   a.vocab = vocab;
   a.k = top_k;
+  a.parts = cut.parts;
+  a.part = cut.part;
   a.scale = scale;
   a.c = scale * LOG2E;
   a.index_bits = bits_of(vocab + 8);  // places begin up to 7 before the row
@@ -433,13 +635,25 @@ int bbpe_token_logprobs(int dtype, const void *logits, int64_t row_stride, uint6
   a.top_ids = d_top_ids;
   a.top_logprobs = d_top_logprobs;
   a.stats = reinterpret_cast<float2 *>(d_stats);
+  a.parted = static_cast<ScorePart *>(d_workspace);
+  a.parted_top = reinterpret_cast<uint64_t *>(static_cast<char *>(d_workspace) + cut.part_bytes);
   const hipStream_t st = static_cast<hipStream_t>(hip_stream);
-  for (; a.row0 < n_rows; a.row0 += MAX_GROUPS)
-    with_element(dtype, [&](auto t) {
-      const uint32_t grid = uint32_t(std::min(n_rows - a.row0, MAX_GROUPS));
-      if (top_k) k_scores<decltype(t), true><<<grid, ROW_THREADS, 0, st>>>(a);
-      else k_scores<decltype(t), false><<<grid, ROW_THREADS, 0, st>>>(a);
-    });
+  const auto launch = [&](uint64_t blocks, auto kernel, uint32_t threads) {
+    for (a.block0 = 0; a.block0 < blocks; a.block0 += MAX_GROUPS)
+      kernel<<<uint32_t(std::min(blocks - a.block0, MAX_GROUPS)), threads, 0, st>>>(a);
+  };
+  with_element(dtype, [&](auto t) {
+    typedef decltype(t) T;
+    const uint64_t blocks = n_rows * cut.parts;
+    if (cut.parts > 1) {
+      launch(blocks, top_k ? k_scores<T, ROW_WAVES, true, true> : k_scores<T, ROW_WAVES, false, true>, ROW_THREADS);
+      launch(n_rows, top_k ? k_scores_join<T, true> : k_scores_join<T, false>, top_k ? ROW_THREADS : 64);
+    } else if (cut.waves > 1) {
+      launch(blocks, top_k ? k_scores<T, ROW_WAVES, true, false> : k_scores<T, ROW_WAVES, false, false>, ROW_THREADS);
+    } else {
+      launch(blocks, top_k ? k_scores<T, 1, true, false> : k_scores<T, 1, false, false>, 64);
+    }
+  });
   return hipGetLastError() == hipSuccess ? BBPE_OK : BBPE_E_HIP;
 }
 
@@ -448,9 +662,9 @@ int bbpe_token_logprobs_backward(int dtype, const void *logits, int64_t row_stri
                                  const int32_t *d_top_ids, const float *d_stats, const float *g_logprobs,
                                  const float *g_entropy, const float *g_lse, const float *g_top, void *d_logits,
                                  int64_t dl_stride, void *hip_stream) {
-  if (bad_logits(dtype, logits, row_stride, n_rows, vocab, false) || bad_logits(dtype, d_logits, dl_stride, n_rows, vocab, true) ||
-      top_k > TOP_MAX || top_k > vocab || !(scale > 0.0f) || !std::isfinite(scale))
-    return BBPE_E_INVALID_ARG;
+  const int rc = check_scores(dtype, logits, row_stride, n_rows, vocab, top_k, scale);
+  if (rc) return rc;
+  if (bad_logits(dtype, d_logits, dl_stride, n_rows, vocab, true)) return BBPE_E_INVALID_ARG;
   if (n_rows && (!d_ids || !d_entropy || !d_stats || (g_top && top_k && !d_top_ids))) return BBPE_E_INVALID_ARG;
   if ((address(d_ids) | address(d_entropy) | address(d_top_ids) | address(g_logprobs) | address(g_entropy) | address(g_lse) |
        address(g_top)) & 3 || (address(d_stats) & 7))

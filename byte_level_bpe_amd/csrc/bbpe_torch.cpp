@@ -21,8 +21,10 @@ decltype(&bbpe_qk_norm_rope_backward_workspace_bytes) f_back_bytes;
 decltype(&bbpe_qk_norm_rope_backward) f_back;
 decltype(&bbpe_tree_attention_workspace_bytes) f_attn_bytes;
 decltype(&bbpe_tree_attention) f_attn;
+decltype(&bbpe_token_logprobs_workspace_bytes) f_scores_bytes;
 decltype(&bbpe_token_logprobs) f_scores;
 decltype(&bbpe_token_logprobs_backward) f_scores_back;
+decltype(&bbpe_distill_loss_workspace_bytes) f_distill_bytes;
 decltype(&bbpe_distill_loss) f_distill;
 decltype(&bbpe_distill_loss_backward) f_distill_back;
 
@@ -360,6 +362,10 @@ PyObject *token_logprobs(PyObject *, PyObject *const *a, Py_ssize_t n_args) {
   if (!c.plain || k < 0 || k > 256 || k > x.vocab) return not_plain();
   void *p_ids = c.flat(ids, at::kInt, n), *stream;
   if (!c.ready(stream)) return not_plain();
+  uint64_t bytes = 0;
+  if (f_scores_bytes(dtype_of(x.type), uint64_t(n), uint32_t(x.vocab), uint32_t(k), &bytes)) return not_plain();
+  Tensor ws;
+  if (bytes) ws = c.empty({int64_t(bytes)}, at::kByte);
   // what every row has, in one allocation; its alternatives in another
   const int64_t step = up16(4 * n), at_stats = 4 * step, at_top = up16(4 * n * k);
   const Tensor rows = c.empty({at_stats + 8 * n}, at::kByte), top = c.empty({2 * at_top}, at::kByte);
@@ -368,7 +374,7 @@ PyObject *token_logprobs(PyObject *, PyObject *const *a, Py_ssize_t n_args) {
                top_ids = part_of(top, 0, n, k, at::kInt), top_lp = part_of(top, at_top, n, k, at::kFloat);
   const int rc = f_scores(dtype_of(x.type), x.p, x.t->stride(0), uint64_t(n), uint32_t(x.vocab), ints(p_ids), uint32_t(k), scale,
                           floats(lp.data_ptr()), floats(entropy.data_ptr()), floats(lse.data_ptr()), ints(ranks.data_ptr()), ints(top_ids.data_ptr()),
-                          floats(top_lp.data_ptr()), floats(stats.data_ptr()), stream);
+                          floats(top_lp.data_ptr()), floats(stats.data_ptr()), bytes ? ws.data_ptr() : nullptr, bytes, stream);
   if (rc) return not_plain();
   return tuple_of({lp, entropy, lse, ranks, top_ids, top_lp, stats});
   END_HANDLE_TH_ERRORS
@@ -438,12 +444,15 @@ PyObject *distill_loss(PyObject *, PyObject *const *a, Py_ssize_t n_args) {
   if (!c.plain || (weights && !d.like(c, a[6], x))) return not_plain();
   const int64_t n = x.n, step = up16(4 * n);
   void *p_w = c.flat(weights, at::kFloat, n), *stream;
-  if (!c.ready(stream)) return not_plain();
+  uint64_t bytes = 0;
+  if (!c.ready(stream) || f_distill_bytes(dtype_of(x.type), uint64_t(n), uint32_t(x.vocab), &bytes)) return not_plain();
+  Tensor ws;
+  if (bytes) ws = c.empty({int64_t(bytes)}, at::kByte);
   const Tensor rows = c.empty({2 * step + 16 * n}, at::kByte);
   const Tensor loss = part_of(rows, 0, n, at::kFloat), lse = part_of(rows, step, n, at::kFloat), stats = part_of(rows, 2 * step, n, 4, at::kFloat);
   const int rc = f_distill(dtype_of(x.type), x.p, x.t->stride(0), uint64_t(n), uint32_t(x.vocab), ints(l.p_ids), floats(l.p_lp), uint32_t(l.k), tail, scale,
                            floats(loss.data_ptr()), floats(lse.data_ptr()), floats(stats.data_ptr()), floats(p_w), weights ? d.p : nullptr,
-                           weights ? d.t->stride(0) : 0, stream);
+                           weights ? d.t->stride(0) : 0, bytes ? ws.data_ptr() : nullptr, bytes, stream);
   if (rc) return not_plain();
   return tuple_of({loss, lse, stats});
   END_HANDLE_TH_ERRORS
@@ -477,14 +486,15 @@ PyObject *distill_loss_backward(PyObject *, PyObject *const *a, Py_ssize_t n_arg
   END_HANDLE_TH_ERRORS
 }
 
-// bind(addresses of the ten functions above, in their order)
+// bind(addresses of the twelve functions above, in their order)
 PyObject *bind(PyObject *, PyObject *const *a, Py_ssize_t n_args) {
-  if (n_args != 10) {
-    PyErr_SetString(PyExc_TypeError, "bind: ten addresses");
+  constexpr int N = 12;
+  if (n_args != N) {
+    PyErr_SetString(PyExc_TypeError, "bind: twelve addresses");
     return nullptr;
   }
-  void *p[10];
-  for (int i = 0; i < 10; ++i) p[i] = PyLong_AsVoidPtr(a[i]);
+  void *p[N];
+  for (int i = 0; i < N; ++i) p[i] = PyLong_AsVoidPtr(a[i]);
   if (PyErr_Occurred()) return nullptr;
   f_tables = reinterpret_cast<decltype(f_tables)>(p[0]);
   f_norm = reinterpret_cast<decltype(f_norm)>(p[1]);
@@ -492,10 +502,12 @@ PyObject *bind(PyObject *, PyObject *const *a, Py_ssize_t n_args) {
   f_back = reinterpret_cast<decltype(f_back)>(p[3]);
   f_attn_bytes = reinterpret_cast<decltype(f_attn_bytes)>(p[4]);
   f_attn = reinterpret_cast<decltype(f_attn)>(p[5]);
-  f_scores = reinterpret_cast<decltype(f_scores)>(p[6]);
-  f_scores_back = reinterpret_cast<decltype(f_scores_back)>(p[7]);
-  f_distill = reinterpret_cast<decltype(f_distill)>(p[8]);
-  f_distill_back = reinterpret_cast<decltype(f_distill_back)>(p[9]);
+  f_scores_bytes = reinterpret_cast<decltype(f_scores_bytes)>(p[6]);
+  f_scores = reinterpret_cast<decltype(f_scores)>(p[7]);
+  f_scores_back = reinterpret_cast<decltype(f_scores_back)>(p[8]);
+  f_distill_bytes = reinterpret_cast<decltype(f_distill_bytes)>(p[9]);
+  f_distill = reinterpret_cast<decltype(f_distill)>(p[10]);
+  f_distill_back = reinterpret_cast<decltype(f_distill_back)>(p[11]);
   Py_RETURN_NONE;
 }
 

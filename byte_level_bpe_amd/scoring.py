@@ -32,9 +32,11 @@ def _lib():
         P, U32, U64, I64, I, F = (C.c_void_p, C.c_uint32, C.c_uint64, C.c_int64, C.c_int, C.c_float)
         X = [I, P, I64, U64, U32]  # dtype, logits, row stride, rows, vocabulary
         for name, args in {
-            "bbpe_token_logprobs": X + [P, U32, F] + 8 * [P],
+            "bbpe_token_logprobs_workspace_bytes": [I, U64, U32, U32, C.POINTER(U64)],
+            "bbpe_token_logprobs": X + [P, U32, F] + 8 * [P] + [U64, P],
             "bbpe_token_logprobs_backward": X + [P, U32, F] + 8 * [P] + [I64, P],
-            "bbpe_distill_loss": X + [P, P, U32, I, F] + 5 * [P] + [I64, P],
+            "bbpe_distill_loss_workspace_bytes": [I, U64, U32, C.POINTER(U64)],
+            "bbpe_distill_loss": X + [P, P, U32, I, F] + 5 * [P] + [I64, P, U64, P],
             "bbpe_distill_loss_backward": X + [P, P, U32, I, F] + 3 * [P] + [I64, P],
         }.items():
             fn = getattr(lib, name)
@@ -59,6 +61,17 @@ def _gradient(what, t, logits):
     if t.shape[0] > 1 and t.stride(0) < t.shape[1]:
         _bad("%s: dlogits: rows share memory: strides %s" % (what, t.stride()))
     return t.data_ptr(), t.stride(0)
+
+
+def _room(size_of, given, dev, what, *args):
+    """The workspace: (tensor or None, pointer, bytes).  size_of: the library's function that tells its size."""
+    if given is None:
+        size = C.c_uint64()
+        _check(size_of(*args, C.byref(size)), what)
+        if size.value == 0:
+            return None, None, 0
+        given = torch.empty(size.value, dtype=torch.uint8, device=dev)
+    return given, _dense("workspace", given, torch.uint8, (None,), dev), given.numel()
 
 
 def _or_none(name, t, shape, dev):
@@ -99,25 +112,26 @@ class _TokenLogprobs(torch.autograd.Function):
         return token_logprobs_backward(logits, ids, scored, *grads, scale=ctx.scale), None, None, None
 
 
-def token_logprobs(logits, ids, top_k: int = 0, scale: float = 1.0, out=None, stream=None) -> TokenLogprobs:
+def token_logprobs(logits, ids, top_k: int = 0, scale: float = 1.0, out=None, workspace=None, stream=None) -> TokenLogprobs:
     """Scores of the tokens ids [n] under softmax(scale * logits [n,
     vocabulary]) (bbpe_token_logprobs).
 
     logits: bfloat16, float16 or float32, contiguous rows at any stride; ids:
     int32, below 0 where a row has no token; top_k: alternatives a row, up to
     256, in the order of logits, the lower id first among equals; scale: 1 /
-    temperature; out: a TokenLogprobs to write into.
+    temperature; out: a TokenLogprobs to write into; workspace: uint8, for few
+    rows (bbpe_token_logprobs_workspace_bytes).
 
     Where grad mode is on and logits require grad, logprobs, entropy, lse and
     top_logprobs carry their gradients (once); into given outputs there are
     none, and such a call is refused."""
-    if out is None and stream is None:
+    if out is None and workspace is None and stream is None:
         got = _short.token_logprobs(logits, ids, top_k, scale)
         if got is not NotImplemented:
             return tuple.__new__(TokenLogprobs, got)
     if _wants_grad(logits):
-        if out is not None:
-            _bad("token_logprobs: no gradients into given outputs; call it under torch.no_grad()")
+        if out is not None or workspace is not None:
+            _bad("token_logprobs: no gradients into given outputs or workspaces; call it under torch.no_grad()")
         with _On(logits.device, stream, "token_logprobs") as on:
             got = TokenLogprobs(*_TokenLogprobs.apply(logits, ids, top_k, scale))
             on.keep(logits, ids)
@@ -131,13 +145,14 @@ def token_logprobs(logits, ids, top_k: int = 0, scale: float = 1.0, out=None, st
         if out is None:
             shapes = ((n,), f32), ((n,), f32), ((n,), f32), ((n,), i32), ((n, top_k), i32), ((n, top_k), f32), ((n, 2), f32)
             out = TokenLogprobs(*(torch.empty(s, dtype=t, device=dev) for s, t in shapes))
+        room, *space = _room(_lib().bbpe_token_logprobs_workspace_bytes, workspace, dev, "token_logprobs", x[0], n, x[4], top_k)
         st = _lib().bbpe_token_logprobs(
             *x, _dense("ids", ids, i32, (n,), dev), top_k, scale, *(
                 _dense(name, t, f32, (n,), dev) for name, t in (("logprobs", out.logprobs), ("entropy", out.entropy), ("lse", out.lse))),
             _dense("ranks", out.ranks, i32, (n,), dev), _dense("top_ids", out.top_ids, i32, (n, top_k), dev),
-            _dense("top_logprobs", out.top_logprobs, f32, (n, top_k), dev), _dense("stats", out.stats, f32, (n, 2), dev), on.handle)
+            _dense("top_logprobs", out.top_logprobs, f32, (n, top_k), dev), _dense("stats", out.stats, f32, (n, 2), dev), *space, on.handle)
         _check(st, "token_logprobs")
-        on.keep(logits, ids, *out)
+        on.keep(logits, ids, room, *out)
     return out
 
 
@@ -202,7 +217,7 @@ def _lists(what, top_ids, top_logprobs, n, dev):
 
 
 def distill_loss(logits, top_ids, top_logprobs, tail: bool = False, scale: float = 1.0, weights=None, dlogits=None, out=None,
-                 stream=None) -> DistillLoss:
+                 workspace=None, stream=None) -> DistillLoss:
     """Divergence of softmax(scale * logits [n, vocabulary]) from a teacher's
     listed tokens, top_ids (int32) and top_logprobs (float32) [n, k], k up to
     256 (bbpe_distill_loss).
@@ -213,19 +228,21 @@ def distill_loss(logits, top_ids, top_logprobs, tail: bool = False, scale: float
     against the student's sum over tokens not listed.  Ids below 0 end a list
     early; a row with none has loss 0 and no gradient.
 
+    workspace: uint8, for few rows (bbpe_distill_loss_workspace_bytes).
+
     With weights (float32 [n]) and dlogits (which may be logits) the call also
     writes the gradient of (weights * loss).sum(): one call of a training step
     that knows its weights.  Otherwise, where grad mode is on and logits
     require grad, loss carries its gradient (once; the teacher has none)."""
     if (weights is None) != (dlogits is None):
         _bad("distill_loss: weights and dlogits are given together or not at all")
-    if out is None and stream is None:
+    if out is None and workspace is None and stream is None:
         got = _short.distill_loss(logits, top_ids, top_logprobs, tail, scale, weights, dlogits)
         if got is not NotImplemented:
             return tuple.__new__(DistillLoss, got)
     if _wants_grad(logits, top_logprobs, weights):
-        if out is not None or dlogits is not None or top_logprobs.requires_grad:
-            _bad("distill_loss: no gradients into given outputs, nor of the teacher or the weights; call it under torch.no_grad()")
+        if out is not None or workspace is not None or dlogits is not None or top_logprobs.requires_grad:
+            _bad("distill_loss: no gradients into given outputs or workspaces, nor of the teacher or the weights; call it under torch.no_grad()")
         with _On(logits.device, stream, "distill_loss") as on:
             got = DistillLoss(*_DistillLoss.apply(logits, top_ids, top_logprobs, tail, scale))
             on.keep(logits, top_ids, top_logprobs)
@@ -237,12 +254,13 @@ def distill_loss(logits, top_ids, top_logprobs, tail: bool = False, scale: float
         ids, lp, k = _lists("distill_loss", top_ids, top_logprobs, n, dev)
         if out is None:
             out = DistillLoss(*(torch.empty(s, dtype=f32, device=dev) for s in ((n,), (n,), (n, 4))))
+        room, *space = _room(_lib().bbpe_distill_loss_workspace_bytes, workspace, dev, "distill_loss", x[0], n, x[4])
         st = _lib().bbpe_distill_loss(
             *x, ids, lp, k, tail, scale, _dense("loss", out.loss, f32, (n,), dev), _dense("lse", out.lse, f32, (n,), dev),
             _dense("stats", out.stats, f32, (n, 4), dev), _or_none("weights", weights, (n,), dev),
-            *((None, 0) if dlogits is None else _gradient("distill_loss", dlogits, logits)), on.handle)
+            *((None, 0) if dlogits is None else _gradient("distill_loss", dlogits, logits)), *space, on.handle)
         _check(st, "distill_loss")
-        on.keep(logits, top_ids, top_logprobs, weights, dlogits, *out)
+        on.keep(logits, top_ids, top_logprobs, weights, dlogits, room, *out)
     return out
 
 

@@ -74,8 +74,8 @@ def _short_way():
     lib = _lib()
     mod.bind(*(C.cast(getattr(lib, "bbpe_" + n), C.c_void_p).value for n in (
         "block_tables", "qk_norm_rope", "qk_norm_rope_backward_workspace_bytes", "qk_norm_rope_backward",
-        "tree_attention_workspace_bytes", "tree_attention", "token_logprobs", "token_logprobs_backward", "distill_loss",
-        "distill_loss_backward")))
+        "tree_attention_workspace_bytes", "tree_attention", "token_logprobs_workspace_bytes", "token_logprobs",
+        "token_logprobs_backward", "distill_loss_workspace_bytes", "distill_loss", "distill_loss_backward")))
     return mod
 
 

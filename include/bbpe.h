@@ -547,11 +547,13 @@ int bbpe_tree_attention(const void *q, int64_t q_ts, int64_t q_hs, uint64_t n_to
  *                      row without probabilities: -1 and NaN);
  *   d_stats[n_rows][2]: for the gradient: the row's largest logit, and the
  *                      logarithm of its sum of exp(scale * (logit - largest)). */
+int bbpe_token_logprobs_workspace_bytes(int dtype, uint64_t n_rows, uint32_t vocab,
+                                        uint32_t top_k, uint64_t *out_bytes);
 int bbpe_token_logprobs(int dtype, const void *logits, int64_t row_stride, uint64_t n_rows,
                         uint32_t vocab, const int32_t *d_ids, uint32_t top_k, float scale,
                         float *d_logprobs, float *d_entropy, float *d_lse, int32_t *d_ranks,
                         int32_t *d_top_ids, float *d_top_logprobs, float *d_stats,
-                        void *hip_stream);
+                        void *d_workspace, uint64_t workspace_bytes, void *hip_stream);
 
 /* Its backward pass: from the gradients of d_logprobs, d_entropy, d_lse
  * ([n_rows] float) and d_top_logprobs ([n_rows][top_k]; null: zeros) and what
@@ -587,11 +589,13 @@ int bbpe_token_logprobs_backward(int dtype, const void *logits, int64_t row_stri
  * A row without a teacher (no entry; without a tail also none above minus
  * infinity) has loss 0 and no gradient, whatever its logits hold.  A listed
  * token that the student gives minus infinity makes the loss infinite. */
+int bbpe_distill_loss_workspace_bytes(int dtype, uint64_t n_rows, uint32_t vocab,
+                                      uint64_t *out_bytes);
 int bbpe_distill_loss(int dtype, const void *logits, int64_t row_stride, uint64_t n_rows,
                       uint32_t vocab, const int32_t *d_top_ids, const float *d_top_logprobs,
                       uint32_t top_k, int tail, float scale, float *d_loss, float *d_lse,
                       float *d_stats, const float *d_weights, void *d_logits, int64_t dl_stride,
-                      void *hip_stream);
+                      void *d_workspace, uint64_t workspace_bytes, void *hip_stream);
 
 /* Its backward pass, d_grad[n_rows] the gradients of the losses (a row's of 0
  * gives zeros, whatever its logits hold).  d_logits may be logits. */

@@ -74,6 +74,34 @@ def test_scores(v, dtype):
         check_scores(x, ids, k, scale=[1.0, 0.7][k % 2], offset=k % 5, pad=[0, 3][k % 2])
 
 
+def many(t, n):
+    """Rows of t over and over, n of them."""
+    return t[torch.arange(n) % t.shape[0]]
+
+
+@pytest.mark.parametrize("dtype", [BF, HF, F])
+@pytest.mark.parametrize("v", [513, 1280, 5003, 33001])
+@pytest.mark.parametrize("n", [300, 1111, 2200])
+def test_scores_of_many_rows(n, v, dtype):
+    """Rows in parts and whole ones: each as its like in a small reference."""
+    x, g = logits(9, v, dtype, v)
+    x[3, 200:] = -INF
+    x[4] = -INF
+    x[5, 3] = NAN
+    x[6] = x[6].round()
+    ids = torch.randint(0, v, (9,), generator=g, dtype=torch.int32)
+    ids[1] = -1
+    for k in (0, 7, 256):
+        say("many rows", n, v, dtype, k)
+        dev = many(x, n).cuda()
+        got = B.token_logprobs(dev, many(ids, n).cuda(), top_k=k)
+        for name, (want, bound) in ref.scores(x, ids, k, 1.0).items():
+            if bound is None:
+                assert torch.equal(getattr(got, name).cpu().long(), many(want, n).long()), name
+            else:
+                near(getattr(got, name), many(want, n), many(bound, n), name)
+
+
 @pytest.mark.parametrize("dtype", [BF, HF, F])
 def test_rows_with_masks(dtype):
     """Minus infinity and the type's lowest value in masked places, rows with nothing, equal elements, zeros of both

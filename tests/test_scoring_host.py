@@ -1,5 +1,7 @@
 """The operators between logits and ids, on the CPU: the library refuses bad
 arguments before it touches a GPU, and so does the Python binding."""
+import ctypes as C
+
 import pytest
 
 torch = pytest.importorskip("torch")
@@ -15,7 +17,8 @@ WRITTEN = [dict(dx=None), dict(dx=X + 1), dict(dstride=99), dict(dstride=0)]
 
 
 def scores_call(**kw):
-    a = dict(dtype=0, x=X, stride=100, n=3, vocab=100, ids=X, k=5, scale=1.0, lp=X, entropy=X, lse=X, ranks=X, top=X, top_lp=X, stats=X, stream=None)
+    a = dict(dtype=0, x=X, stride=100, n=3, vocab=100, ids=X, k=5, scale=1.0, lp=X, entropy=X, lse=X, ranks=X, top=X, top_lp=X, stats=X, ws=X, ws_bytes=1 << 40,
+             stream=None)
     a.update(kw)
     return scoring._lib().bbpe_token_logprobs(*a.values())
 
@@ -25,6 +28,19 @@ def scores_call(**kw):
                                           dict(stats=X + 4), dict(top=X + 1), dict(lse=X + 2)])
 def test_scores_refuse(bad):
     assert scores_call(**bad) == B.E_INVALID_ARG
+
+
+def test_scores_workspace():
+    n = C.c_uint64()
+    size, big = scoring._lib().bbpe_token_logprobs_workspace_bytes, dict(n=3, vocab=100000, stride=100000)
+    assert size(0, 3, 100, 5, C.byref(n)) == 0 and n.value == 0 and size(0, 1 << 20, 100000, 5, C.byref(n)) == 0 and n.value == 0
+    assert size(0, 3, 100000, 5, C.byref(n)) == 0 and n.value > 0
+    assert scores_call(**big, ws=None) == B.E_WORKSPACE
+    assert scores_call(**big, ws_bytes=n.value - 1) == B.E_WORKSPACE
+    assert scores_call(**big, ws=X + 8) == B.E_WORKSPACE
+    for bad in ((3, 3, 100, 5), (0, 1 << 31, 100, 5), (0, 3, 0, 0), (0, 3, 100, 101), (0, 3, 1000, 257)):
+        assert size(*bad, C.byref(n)) == B.E_INVALID_ARG
+    assert size(0, 3, 100, 5, None) == B.E_INVALID_ARG
 
 
 def scores_back_call(**kw):
@@ -42,7 +58,7 @@ def test_scores_backward_refuses(bad):
 
 def distill_call(**kw):
     a = dict(dtype=0, x=X, stride=100, n=3, vocab=100, ids=X, lp=X, k=5, tail=0, scale=1.0, loss=X, lse=X, stats=X, w=X, dx=X, dstride=100,
-             stream=None)
+             ws=X, ws_bytes=1 << 40, stream=None)
     a.update(kw)
     return scoring._lib().bbpe_distill_loss(*a.values())
 
