@@ -176,8 +176,7 @@ __global__ __launch_bounds__(ROW_THREADS) void k_distill(DistillArgs a) {
     typename P::val v[ROW_UNROLL];
     float m = -INFINITY;
     Raw raw[ROW_UNROLL];
-#pragma unroll
-    for (uint32_t u = 0; u < ROW_UNROLL; ++u) raw[u] = r.load(i * ROW_STEP + u * ROW_THREADS + tid);
+    r.template load_step<ROW_THREADS>(raw, r.at, i * ROW_STEP + tid, r.pieces());
 #pragma unroll
     for (uint32_t u = 0; u < ROW_UNROLL; ++u) {
       v[u] = values<T>(raw[u]);
@@ -252,21 +251,20 @@ __global__ __launch_bounds__(ROW_THREADS) void k_distill_back(DistillBackArgs a)
   }
   __syncthreads();
   const float all = g * st.z * inv;
-  for (uint32_t p0 = from + tid; p0 < to; p0 += ROW_STEP) {
+  for (uint32_t p0 = from; p0 < to; p0 += ROW_STEP) {
     typename P::raw raw[ROW_UNROLL];
-#pragma unroll
-    for (uint32_t u = 0; u < ROW_UNROLL; ++u)
-      if (p0 + u * ROW_THREADS < to && !zero) raw[u] = r.load(x - r.lead, p0 + u * ROW_THREADS);
+    if (!zero) r.template load_step<ROW_THREADS>(raw, x - r.lead, p0 + tid, to);
 #pragma unroll
     for (uint32_t u = 0; u < ROW_UNROLL; ++u) {
-      if (p0 + u * ROW_THREADS >= to) break;
+      const uint32_t p = p0 + u * ROW_THREADS + tid;
+      if (p >= to) break;
       typename P::val v = 0.0f;
       if (!zero) {
         v = values<T>(raw[u]);
 #pragma unroll
         for (uint32_t e = 0; e < P::N; ++e) v[e] = weight(v[e]) * all;
       }
-      r.store(p0 + u * ROW_THREADS, v);
+      r.store(p, v);
     }
   }
   __syncthreads();

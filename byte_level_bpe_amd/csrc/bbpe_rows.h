@@ -21,7 +21,8 @@ constexpr float LOWEST = -3.4028234663852886e38f;
 
 template <typename T> struct Piece {
   static constexpr uint32_t N = 16 / sizeof(T);
-  typedef T raw __attribute__((ext_vector_type(16 / sizeof(T))));
+  typedef T vec __attribute__((ext_vector_type(16 / sizeof(T))));
+  typedef uint32_t raw __attribute__((ext_vector_type(4)));  // its bits: elements by themselves would be loaded one after another
   typedef T mem __attribute__((ext_vector_type(16 / sizeof(T)), aligned(sizeof(T))));  // at any element
   typedef float val __attribute__((ext_vector_type(16 / sizeof(T))));
 };
@@ -45,20 +46,33 @@ template <typename C> struct Row {
   // Piece p, from `from` (place 0 of a row that may lie otherwise in memory);
   // minus infinity where it is not the row's.
   __device__ __forceinline__ typename Piece<T>::raw load(const T *from, uint32_t p) const {
-    typename Piece<T>::raw v;
+    typename Piece<T>::vec t;
     if (whole(p)) {
-      v = *reinterpret_cast<const typename Piece<T>::mem *>(from + p * N);
-    } else {
-#pragma unroll
-      for (uint32_t e = 0; e < N; ++e) v[e] = p * N + e >= lead && p * N + e < end ? from[p * N + e] : T(-INFINITY);
+      t = *reinterpret_cast<const typename Piece<T>::mem *>(from + p * N);
+      return __builtin_bit_cast(typename Piece<T>::raw, t);
     }
-    return v;
+#pragma unroll
+    for (uint32_t e = 0; e < N; ++e) t[e] = p * N + e >= lead && p * N + e < end ? from[p * N + e] : T(-INFINITY);
+    return __builtin_bit_cast(typename Piece<T>::raw, t);
   }
   __device__ __forceinline__ typename Piece<T>::raw load(uint32_t p) const { return load(at, p); }
+  // A step's pieces p, p + STRIDE, ..., below `last`.
+  template <uint32_t STRIDE>
+  __device__ __forceinline__ void load_step(typename Piece<T>::raw (&v)[ROW_UNROLL], const T *from, uint32_t p, uint32_t last) const {
+#pragma unroll
+    for (uint32_t u = 0; u < ROW_UNROLL; ++u) {
+      if (p + u * STRIDE < last) {
+        v[u] = load(from, p + u * STRIDE);
+      } else {
+        const typename Piece<T>::vec t = T(-INFINITY);
+        v[u] = __builtin_bit_cast(typename Piece<T>::raw, t);
+      }
+    }
+  }
   __device__ __forceinline__ void store(uint32_t p, typename Piece<T>::val f) const {
-    const typename Piece<T>::raw v = __builtin_convertvector(f, typename Piece<T>::raw);  // to nearest even
+    const typename Piece<T>::vec v = __builtin_convertvector(f, typename Piece<T>::vec);  // to nearest even
     if (whole(p)) {
-      *reinterpret_cast<typename Piece<T>::raw *>(at + p * N) = v;
+      *reinterpret_cast<typename Piece<T>::raw *>(at + p * N) = __builtin_bit_cast(typename Piece<T>::raw, v);
     } else {
 #pragma unroll
       for (uint32_t e = 0; e < N; ++e)
@@ -69,7 +83,7 @@ template <typename C> struct Row {
 
 template <typename T>
 __device__ __forceinline__ typename Piece<T>::val values(typename Piece<T>::raw v) {
-  return __builtin_convertvector(v, typename Piece<T>::val);
+  return __builtin_convertvector(__builtin_bit_cast(typename Piece<T>::vec, v), typename Piece<T>::val);
 }
 
 __device__ __forceinline__ float wave_max(float v) {

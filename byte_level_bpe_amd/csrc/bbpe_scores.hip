@@ -24,6 +24,8 @@ constexpr uint32_t TOP_MAX = 256;   // alternatives at most
 // earlier for it (64 alternatives of 200,064: 333 us exact, SLACKTIME with this).
 __host__ __device__ constexpr uint32_t with_slack(uint32_t k) { return k + k / 4 + 16; }
 constexpr uint32_t TOP_ROOM = with_slack(TOP_MAX);
+constexpr uint32_t FEW = 32;            // alternatives up to which a group's second piece is not kept
+constexpr uint32_t SMALL_TOP = 64;      // alternatives up to which a wave may take a row
 constexpr uint32_t KEPT_ROOM = (TOP_ROOM + 63) / 64 * 64;
 constexpr uint32_t PARTS_MAX = 64;  // parts of a row at most: a wave joins them
 constexpr uint32_t JOIN_KEYS = 4096;  // alternatives of all parts at most
@@ -46,8 +48,8 @@ struct ScoreArgs {
   int32_t *top_ids;
   float *top_logprobs;
   float2 *stats;
-  ScorePart *parted;  // [rows][parts], and the parts' alternatives [rows][parts][k], 0 where there are fewer
-  uint64_t *parted_top;
+  ScorePart *parted;     // [rows][parts]
+  uint64_t *parted_top;  // [rows][parts][k], 0 where a part has fewer
 };
 
 // ---- order ----
@@ -116,50 +118,36 @@ __device__ __forceinline__ uint64_t top_bar(G get, uint32_t n, uint32_t k, uint3
   return lo;
 }
 
-// Puts n different keys in order, the first k of them: put(place, key).  keys:
-// ROOM of them in LDS, which the call uses up.  Sixty-four at a time are ranked
-// by counting; a key's place among the others is found by halving, in all of the
-// ordered sixty-fours at once (256 of 400 by counting alone: SLOWTIME a row).
-template <uint32_t WAVES, uint32_t ROOM, typename F>
-__device__ __forceinline__ void put_in_order(uint64_t *keys, uint32_t n, uint32_t k, F put) {
-  constexpr uint32_t Q = (ROOM / 64 + WAVES - 1) / WAVES;
+// Puts n different keys in order, the first k of them: put(place, key).  keys: in
+// LDS, with room for as many (in sixty-fours) from `half` on.  Sixty-four at a
+// time are ranked by counting and laid there in order; a key's place among the
+// others is found by halving, in several sixty-fours at once.
+template <uint32_t WAVES, typename F>
+__device__ __forceinline__ void put_in_order(uint64_t *keys, uint32_t half, uint32_t n, uint32_t k, F put) {
   const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6, blocks = (n + 63) / 64;
-  uint64_t mine[Q];
-  uint32_t place[Q];
-#pragma unroll
-  for (uint32_t q = 0; q < Q; ++q) {
-    const uint32_t b = wave + q * WAVES;
-    if (b >= blocks) break;
-    mine[q] = b * 64 + lane < n ? keys[b * 64 + lane] : 0;
+  for (uint32_t b = wave; b < blocks; b += WAVES) {
+    const uint64_t *own = keys + b * 64;
     const uint32_t there = min(64u, n - b * 64);
-    place[q] = 0;
+    const uint64_t mine = lane < there ? own[lane] : 0;
+    uint32_t place = 0;
 #pragma unroll 8
-    for (uint32_t j = 0; j < there; ++j) place[q] += keys[b * 64 + j] > mine[q];
-    if (lane >= there) place[q] = lane;
+    for (uint32_t j = 0; j < there; ++j) place += own[j] > mine;
+    keys[half + b * 64 + (lane < there ? place : lane)] = mine;
   }
-  if (blocks > 1) {
-    __syncthreads();
-#pragma unroll
-    for (uint32_t q = 0; q < Q; ++q)
-      if (wave + q * WAVES < blocks) keys[(wave + q * WAVES) * 64 + place[q]] = mine[q];
-    __syncthreads();
-  }
-#pragma unroll
-  for (uint32_t q = 0; q < Q; ++q) {
-    const uint32_t b = wave + q * WAVES;
-    if (b >= blocks) break;
-    if (b * 64 + lane >= n) continue;
-    uint32_t at = place[q];
+  __syncthreads();
+  for (uint32_t b = wave; b < blocks; b += WAVES) {
+    const uint64_t mine = keys[half + b * 64 + lane];
+    uint32_t at = lane;
 #pragma unroll 4
     for (uint32_t o = 0; o < blocks; ++o) {
-      const uint64_t *others = keys + o * 64;
+      const uint64_t *others = keys + half + o * 64;
       uint32_t before = 0;
 #pragma unroll
-      for (uint32_t half = 32; half; half /= 2) before += others[before + half - 1] > mine[q] ? half : 0;
-      before += others[before] > mine[q];
+      for (uint32_t step = 32; step; step /= 2) before += others[before + step - 1] > mine ? step : 0;
+      before += others[before] > mine;
       at += o == b ? 0 : before;
     }
-    if (at < k) put(at, mine[q]);
+    if (b * 64 + lane < n && at < k) put(at, mine);
   }
 }
 
@@ -180,7 +168,7 @@ struct RowEnd {
   __device__ __forceinline__ explicit RowEnd(Partial s) : p(s) {
     none = s.max == -INFINITY && s.sum == 0.0f;
     bad = !(s.sum == s.sum) || s.max == INFINITY;
-    log_sum = none ? -INFINITY : log(double(s.sum));
+    log_sum = none ? -INFINITY : double(logf(s.sum));
   }
   __device__ __forceinline__ float logprob(float v, float scale) const {
     return bad ? __uint_as_float(0x7FC00000u) : none ? -INFINITY : float((double(v) - p.max) * scale - log_sum);
@@ -226,7 +214,25 @@ __device__ __forceinline__ void write_top(const ScoreArgs &a, uint64_t row, uint
   a.top_logprobs[row * a.k + t] = end.logprob(key_value<T>(key, a.index_bits), a.scale);
 }
 
-// One workgroup a row, or a part of one (SPLIT).
+// KEEP: pieces of a group whose places a thread keeps; 0 without alternatives.
+template <uint32_t WAVES, uint32_t KEEP> struct ScoreShared {
+  static constexpr bool TOP = KEEP > 0;
+  static constexpr uint32_t GROUPS = 64 * WAVES * ROW_UNROLL;
+  // Candidates that can be put in order; twice as many can be held.  Where no more
+  // than k groups have pieces, all of their elements are.
+  static constexpr uint32_t ROOM = GROUPS > KEPT_ROOM ? GROUPS : KEPT_ROOM;
+  static_assert(2 * ROOM >= 8 * (WAVES == 1 ? SMALL_TOP : TOP_MAX), "");
+  Partial sums[WAVES];
+  uint32_t above[WAVES];
+  uint64_t keys[TOP ? 2 * ROOM : 1];
+  uint32_t chosen[TOP ? KEEP * TOP_ROOM : 1];  // pieces
+  uint32_t deep[TOP ? TOP_ROOM : 1][TOP ? 1 + KEEP : 1];  // a group, and its pieces among the chosen ones
+  uint32_t n_chosen, n_deep, n_found;
+  uint64_t reach;
+};
+
+// Pieces [first, last) of a row by a workgroup: the whole row, or a part of it
+// (`part`: where its numbers go).
 //
 // Alternatives.  A thread's step takes ROW_UNROLL pieces; the pieces at one
 // place of all steps are a group, of which the thread keeps the largest element,
@@ -234,49 +240,37 @@ __device__ __forceinline__ void write_top(const ScoreArgs &a, uint64_t row, uint
 // bar that the largest of k groups or more reach keeps the first k elements: one
 // below it has k before it.  Of the groups that reach it the pieces with the
 // largest are read once more, and the others only where their largest reaches it
-// too: seldom.  What reaches it are the candidates, not many more than k.
-template <typename T, uint32_t WAVES, bool TOP, bool SPLIT>
-__global__ __launch_bounds__(64 * WAVES) void k_scores(ScoreArgs a) {
+// too: seldom, of 1,024 groups, for 20 alternatives, but of one group in six for
+// 256.  There (KEEP 2) the thread keeps the second piece's place and the largest
+// of the third too.  What reaches the bar are the candidates, not many more than k.
+template <typename T, uint32_t WAVES, uint32_t KEEP, bool WHOLE>
+__device__ __forceinline__ void score_pieces(const ScoreArgs &a, uint64_t row, uint32_t first, uint32_t last, uint64_t part,
+                                             ScoreShared<WAVES, KEEP> &sh) {
   typedef Piece<T> P;
-  constexpr uint32_t THREADS = 64 * WAVES, STEP = THREADS * ROW_UNROLL;
-  constexpr uint32_t ROOM = 2 * STEP;  // for candidates
-  static_assert(ROOM >= TOP_ROOM, "");
-  __shared__ Partial sh[WAVES];
-  __shared__ uint32_t sh_above[WAVES];
-  __shared__ uint64_t keys[TOP ? ROOM : 1];
-  __shared__ uint32_t chosen[TOP ? TOP_ROOM : 1];  // pieces
-  __shared__ uint16_t deep[TOP ? TOP_ROOM : 1];    // groups
-  __shared__ uint32_t n_chosen, n_deep, n_found;
-  __shared__ uint64_t reach;
-  const uint64_t block = a.block0 + blockIdx.x, row = SPLIT ? block / a.parts : block;
-  const T *x = static_cast<const T *>(a.x) + int64_t(row) * a.stride;
-  const Row<const T> r(x, a.vocab);
-  const uint32_t tid = threadIdx.x, first = SPLIT ? uint32_t(block % a.parts) * a.part : 0;
-  const uint32_t last = SPLIT ? min(r.pieces(), first + a.part) : r.pieces();
+  constexpr bool TOP = KEEP > 0;
+  constexpr uint32_t THREADS = 64 * WAVES, STEP = THREADS * ROW_UNROLL, ROOM = ScoreShared<WAVES, KEEP>::ROOM;
+  const Row<const T> r(static_cast<const T *>(a.x) + int64_t(row) * a.stride, a.vocab);
+  const uint32_t tid = threadIdx.x;
+  last = min(last, r.pieces());
   const int32_t id = a.ids[row];
   const Given<T> given(a, r, id);
   const uint32_t before_id = given.there ? min(last, given.piece()) : 0;  // pieces, where equal ones count too
   const float at_least = given.there ? next_below(given.value) : INFINITY;
-  const int32_t beside = !SPLIT && given.there ? given.equal_before(r) : 0;
+  const int32_t beside = WHOLE && given.there ? given.equal_before(r) : 0;
 
   Partial s{-INFINITY, 0.0f, 0.0f};
   float ref = 0.0f;
   uint32_t above = 0;  // the wave's
-  float best[ROW_UNROLL], second[ROW_UNROLL];
-  uint32_t best_at[ROW_UNROLL];
+  float best[ROW_UNROLL], second[ROW_UNROLL], third[ROW_UNROLL];
+  uint32_t best_at[ROW_UNROLL], second_at[ROW_UNROLL];  // the piece's step
 #pragma unroll
   for (uint32_t u = 0; u < ROW_UNROLL; ++u) {
-    best[u] = second[u] = -INFINITY;
-    best_at[u] = first + u * THREADS + tid;
+    best[u] = second[u] = third[u] = -INFINITY;
+    best_at[u] = second_at[u] = ~0u;  // none
   }
   for (uint32_t p0 = first; p0 < last; p0 += STEP) {
     typename P::raw raw[ROW_UNROLL];
-#pragma unroll
-    for (uint32_t u = 0; u < ROW_UNROLL; ++u) {
-      const uint32_t p = p0 + u * THREADS + tid;
-      if (!SPLIT || p < last) raw[u] = r.load(p);
-      else raw[u] = T(-INFINITY);
-    }
+    r.template load_step<THREADS>(raw, r.at, p0 + tid, last);
     typename P::val v[ROW_UNROLL];
     float m = -INFINITY;
 #pragma unroll
@@ -286,11 +280,15 @@ __global__ __launch_bounds__(64 * WAVES) void k_scores(ScoreArgs a) {
 #pragma unroll
       for (uint32_t e = 1; e < P::N; ++e) pm = fmaxf(pm, v[u][e]);
       if (TOP) {
-        second[u] = fmaxf(second[u], fminf(best[u], pm));
-        if (pm > best[u]) {
-          best[u] = pm;
-          best_at[u] = p0 + u * THREADS + tid;
+        const bool more = pm > best[u];
+        if (KEEP > 1) {
+          // (a piece of nothing but minus infinity is no second one; third covers it)
+          third[u] = __builtin_amdgcn_fmed3f(third[u], second[u], pm);
+          second_at[u] = more ? best_at[u] : pm > second[u] ? p0 : second_at[u];
         }
+        second[u] = __builtin_amdgcn_fmed3f(second[u], best[u], pm);  // (they are in order)
+        best[u] = more ? pm : best[u];
+        best_at[u] = more ? p0 : best_at[u];
       }
       m = fmaxf(m, pm);
     }
@@ -310,27 +308,28 @@ __global__ __launch_bounds__(64 * WAVES) void k_scores(ScoreArgs a) {
       }
     }
   }
-  if ((tid & 63) == 0) sh_above[tid >> 6] = above;
+  if ((tid & 63) == 0) sh.above[tid >> 6] = above;
   if (TOP) {
 #pragma unroll
     for (uint32_t u = 0; u < ROW_UNROLL; ++u) {
       const uint32_t g = u * THREADS + tid;
-      keys[g] = first + g < last ? order_key<T>(best[u], best_at[u] * P::N, a.index_bits) : 0;
+      if (best_at[u] == ~0u) best_at[u] = first;  // nothing but minus infinity
+      sh.keys[g] = first + g < last ? order_key<T>(best[u], (best_at[u] + g) * P::N, a.index_bits) : 0;
     }
-    if (tid == 0) n_chosen = n_deep = n_found = 0;
+    if (tid == 0) sh.n_chosen = sh.n_deep = sh.n_found = 0;
   }
-  const RowEnd end(row_partial<WAVES>(s, a.c, sh));  // (with a barrier)
+  const RowEnd end(row_partial<WAVES>(s, a.c, sh.sums));  // (with a barrier)
   if (tid == THREADS - 1) {  // (the first wave has the bar to find)
     above = 0;
-    for (uint32_t w = 0; w < WAVES; ++w) above += sh_above[w];
-    if (SPLIT) a.parted[block] = ScorePart{end.p, above};
-    else write_row<T>(a, row, end, id, given, int32_t(above) + beside);
+    for (uint32_t w = 0; w < WAVES; ++w) above += sh.above[w];
+    if (WHOLE) write_row<T>(a, row, end, id, given, int32_t(above) + beside);
+    else a.parted[part] = ScorePart{end.p, above};
   }
   if (!TOP) return;
 
   const auto put = [&](uint32_t t, uint64_t key) {
-    if (SPLIT) a.parted_top[block * a.k + t] = key;
-    else write_top<T>(a, row, r.lead, end, t, key);
+    if (WHOLE) write_top<T>(a, row, r.lead, end, t, key);
+    else a.parted_top[part * a.k + t] = key;
   };
   if (end.bad) {
     for (uint32_t t = tid; t < a.k; t += THREADS) put(t, 0);
@@ -339,56 +338,67 @@ __global__ __launch_bounds__(64 * WAVES) void k_scores(ScoreArgs a) {
   if (tid < 64) {
     uint64_t mine[STEP / 64];
 #pragma unroll
-    for (uint32_t i = 0; i < STEP / 64; ++i) mine[i] = keys[i * 64 + tid];
+    for (uint32_t i = 0; i < STEP / 64; ++i) mine[i] = sh.keys[i * 64 + tid];
     const uint64_t bar = top_bar<STEP / 64>([&](uint32_t i) { return mine[i]; }, 0, a.k, with_slack(a.k));
-    if (tid == 0) reach = bar;
+    if (tid == 0) sh.reach = bar;
   }
   __syncthreads();
-  const uint64_t group_bar = reach;
+  const uint64_t group_bar = sh.reach;
 #pragma unroll
   for (uint32_t u = 0; u < ROW_UNROLL; ++u) {
     const uint32_t g = u * THREADS + tid;
-    if (keys[g] < group_bar) continue;
+    if (sh.keys[g] < group_bar) continue;
     // (their order does not matter)
-    chosen[atomicAdd(&n_chosen, 1u)] = best_at[u];
-    if (order_key<T>(second[u], 0, a.index_bits) >= group_bar) deep[atomicAdd(&n_deep, 1u)] = uint16_t(g);
+    sh.chosen[atomicAdd(&sh.n_chosen, 1u)] = best_at[u] + g;
+    float rest = second[u];
+    if (KEEP > 1) {
+      const bool two = second_at[u] != ~0u && order_key<T>(rest, (second_at[u] + g) * P::N, a.index_bits) >= group_bar;
+      if (two) {
+        sh.chosen[atomicAdd(&sh.n_chosen, 1u)] = second_at[u] + g;
+        rest = third[u];
+      } else {
+        second_at[u] = ~0u;
+      }
+    }
+    if (order_key<T>(rest, 0, a.index_bits) >= group_bar) {
+      uint32_t *to = sh.deep[atomicAdd(&sh.n_deep, 1u)];
+      to[0] = g;
+      to[1] = best_at[u] + g;
+      if (KEEP > 1) to[2] = second_at[u] == ~0u ? ~0u : second_at[u] + g;
+    }
   }
   __syncthreads();
   // Every element of the chosen groups that reaches the bar (by its piece's place,
   // as groups do) and `low`.
-  const uint32_t n_pieces = n_chosen, deep_steps = (last - first + STEP - 1) / STEP, n_deep_pieces = n_deep * deep_steps;
+  const uint32_t n_pieces = sh.n_chosen, deep_steps = (last - first + STEP - 1) / STEP, n_deep_pieces = sh.n_deep * deep_steps;
   const auto each = [&](uint64_t low, auto take) {
-    for (uint32_t i = tid; i < n_pieces + n_deep_pieces; i += THREADS) {
-      uint32_t p;
-      if (i < n_pieces) {
-        p = chosen[i];
+    for (uint32_t i = tid; i < (n_pieces + n_deep_pieces) * P::N; i += THREADS) {  // an element a thread
+      uint32_t p = i / P::N;
+      if (p < n_pieces) {
+        p = sh.chosen[p];
       } else {
-        const uint32_t g = deep[(i - n_pieces) / deep_steps];
-        p = first + (i - n_pieces) % deep_steps * STEP + g;
-        if (p >= last) continue;
-        bool done = false;  // its first piece is among the chosen ones
-        for (uint32_t j = 0; j < n_pieces; ++j) done |= chosen[j] == p;
-        if (done) continue;
+        p -= n_pieces;
+        const uint32_t *of = sh.deep[p / deep_steps];
+        p = first + p % deep_steps * STEP + of[0];
+        if (p >= last || p == of[1] || (KEEP > 1 && p == of[2])) continue;
       }
-      const typename P::val v = values<T>(r.load(p));
-#pragma unroll
-      for (uint32_t e = 0; e < P::N; ++e) {
-        const uint32_t j = p * P::N + e;
-        if (j < r.lead || j >= r.end || order_key<T>(v[e], p * P::N, a.index_bits) < group_bar) continue;
-        const uint64_t key = order_key<T>(v[e], j, a.index_bits);
-        if (key >= low) take(key);
-      }
+      const uint32_t j = p * P::N + i % P::N;
+      if (j < r.lead || j >= r.end) continue;
+      const float v = float(r.at[j]);
+      if (order_key<T>(v, p * P::N, a.index_bits) < group_bar) continue;
+      const uint64_t key = order_key<T>(v, j, a.index_bits);
+      if (key >= low) take(key);
     }
   };
   const auto collect = [&](uint64_t low) {
     each(low, [&](uint64_t key) {
-      const uint32_t to = atomicAdd(&n_found, 1u);
-      if (to < ROOM) keys[to] = key;
+      const uint32_t to = atomicAdd(&sh.n_found, 1u);
+      if (to < 2 * ROOM) sh.keys[to] = key;
     });
     __syncthreads();
   };
   collect(0);
-  if (n_found > ROOM) {
+  if (sh.n_found > 2 * ROOM) {
     // Large elements crowd in a few groups: halve what is between until a bar
     // leaves k or more, and no more than there is room for.  (Keys differ, so
     // there is one that leaves k.)
@@ -396,39 +406,66 @@ __global__ __launch_bounds__(64 * WAVES) void k_scores(ScoreArgs a) {
     for (;;) {
       const uint64_t mid = lo + (hi - lo + 1) / 2;
       __syncthreads();  // n_found has been read
-      if (tid == 0) n_found = 0;
+      if (tid == 0) sh.n_found = 0;
       __syncthreads();
-      each(mid, [&](uint64_t) { atomicAdd(&n_found, 1u); });
+      each(mid, [&](uint64_t) { atomicAdd(&sh.n_found, 1u); });
       __syncthreads();
-      const uint32_t n = n_found;
+      const uint32_t n = sh.n_found;
       if (n < a.k) {
         hi = mid - 1;
       } else {
         lo = mid;
-        if (n <= ROOM) break;
+        if (n <= 2 * ROOM) break;
       }
     }
     __syncthreads();
-    if (tid == 0) n_found = 0;
+    if (tid == 0) sh.n_found = 0;
     __syncthreads();
     collect(lo);
   }
-  const uint32_t n = n_found;
-  put_in_order<WAVES, ROOM>(keys, n, a.k, put);
-  if (SPLIT)
+  uint32_t n = sh.n_found;
+  if (n > ROOM) {
+    // more than can be put in order: those that reach a bar among them, moved to the front
+    if (tid < 64) {
+      const uint64_t bar = top_bar<0>([&](uint32_t i) { return i * 64 + tid < n ? sh.keys[i * 64 + tid] : 0; }, (n + 63) / 64, a.k, with_slack(a.k));
+      if (tid == 0) {
+        sh.reach = bar;
+        sh.n_found = 0;
+      }
+    }
+    __syncthreads();
+    for (uint32_t i = 0; i < n; i += THREADS) {
+      const uint64_t mine = i + tid < n ? sh.keys[i + tid] : 0;
+      __syncthreads();  // (no more are moved than have been read)
+      if (mine >= sh.reach) sh.keys[atomicAdd(&sh.n_found, 1u)] = mine;
+    }
+    __syncthreads();
+    n = sh.n_found;
+  }
+  put_in_order<WAVES>(sh.keys, ROOM, n, a.k, put);
+  if (!WHOLE)
     for (uint32_t t = n + tid; t < a.k; t += THREADS) put(t, 0);  // a part of fewer elements
+}
+
+// A workgroup a row or, SPLIT, a part of one.
+template <typename T, uint32_t WAVES, uint32_t KEEP, bool SPLIT>
+__global__ __launch_bounds__(64 * WAVES) void k_scores(ScoreArgs a) {
+  __shared__ ScoreShared<WAVES, KEEP> sh;
+  const uint64_t block = a.block0 + blockIdx.x, row = SPLIT ? block / a.parts : block;
+  const uint32_t first = SPLIT ? uint32_t(block % a.parts) * a.part : 0;
+  score_pieces<T, WAVES, KEEP, !SPLIT>(a, row, first, SPLIT ? first + a.part : ~0u, block, sh);
 }
 
 // Joins a row's parts.
 template <typename T, bool TOP>
 __global__ __launch_bounds__(TOP ? ROW_THREADS : 64) void k_scores_join(ScoreArgs a) {
   __shared__ uint64_t keys[TOP ? JOIN_KEYS : 1];
-  __shared__ uint64_t kept[TOP ? KEPT_ROOM : 1];
+  __shared__ uint64_t kept[TOP ? 2 * KEPT_ROOM : 1];
   __shared__ uint32_t n_kept;
   __shared__ uint64_t reach;
+  const uint32_t tid = threadIdx.x, lane = tid & 63;
   const uint64_t row = a.block0 + blockIdx.x;
   const Row<const T> r(static_cast<const T *>(a.x) + int64_t(row) * a.stride, a.vocab);
-  const uint32_t tid = threadIdx.x, lane = tid & 63;
   ScorePart part{Partial{-INFINITY, 0.0f, 0.0f}, 0};
   if (lane < a.parts) part = a.parted[row * a.parts + lane];
   const RowEnd end(wave_partial(part.p, a.c));
@@ -454,7 +491,7 @@ __global__ __launch_bounds__(TOP ? ROW_THREADS : 64) void k_scores_join(ScoreArg
   for (uint32_t i = tid; i < n; i += ROW_THREADS)
     if (keys[i] >= reach) kept[atomicAdd(&n_kept, 1u)] = keys[i];
   __syncthreads();
-  put_in_order<ROW_WAVES, KEPT_ROOM>(kept, n_kept, a.k, [&](uint32_t t, uint64_t key) { write_top<T>(a, row, r.lead, end, t, key); });
+  put_in_order<ROW_WAVES>(kept, KEPT_ROOM, n_kept, a.k, [&](uint32_t t, uint64_t key) { write_top<T>(a, row, r.lead, end, t, key); });
 }
 
 struct ScoreBackArgs {
@@ -525,21 +562,20 @@ __global__ __launch_bounds__(ROW_THREADS) void k_scores_back(ScoreBackArgs a) {
     before[i] = t < n && own_id[t] >= 0 && (r.lead + uint32_t(own_id[t])) / P::N - from < to - from ? float(x[own_id[t]]) : 0.0f;
   }
   __syncthreads();
-  for (uint32_t p0 = from + tid; p0 < to; p0 += ROW_STEP) {
+  for (uint32_t p0 = from; p0 < to; p0 += ROW_STEP) {
     typename P::raw raw[ROW_UNROLL];
-#pragma unroll
-    for (uint32_t u = 0; u < ROW_UNROLL; ++u)
-      if (p0 + u * ROW_THREADS < to && !zero) raw[u] = r.load(x - r.lead, p0 + u * ROW_THREADS);
+    if (!zero) r.template load_step<ROW_THREADS>(raw, x - r.lead, p0 + tid, to);
 #pragma unroll
     for (uint32_t u = 0; u < ROW_UNROLL; ++u) {
-      if (p0 + u * ROW_THREADS >= to) break;
+      const uint32_t p = p0 + u * ROW_THREADS + tid;
+      if (p >= to) break;
       typename P::val v = 0.0f;
       if (!zero) {
         v = values<T>(raw[u]);
 #pragma unroll
         for (uint32_t e = 0; e < P::N; ++e) v[e] = of(v[e]);
       }
-      r.store(p0 + u * ROW_THREADS, v);
+      r.store(p, v);
     }
   }
   __syncthreads();
@@ -564,11 +600,11 @@ constexpr uint64_t MAX_GROUPS = 1u << 23;  // workgroups of a launch: fewer than
 // How rows are cut: waves a workgroup, parts a row and pieces of a part.
 struct Cut {
   uint32_t waves, parts, part;
-  uint64_t part_bytes, bytes;  // of the parts' numbers, and with their alternatives
+  uint64_t parted_bytes, bytes;  // of the parts' numbers, and with their alternatives
 };
 Cut cut_of(int dtype, uint64_t n_rows, uint32_t vocab, uint32_t k) {
   const uint32_t pieces = most_pieces(dtype, vocab);
-  Cut c{pieces <= 512 ? 1u : ROW_WAVES, 1, 0, 0, 0};
+  Cut c{pieces <= 512 && k <= SMALL_TOP ? 1u : ROW_WAVES, 1, 0, 0, 0};
   if (c.waves > 1 && n_rows) {
     const uint64_t want = (2048 + n_rows - 1) / n_rows;
     uint64_t most = std::min<uint64_t>(PARTS_MAX, (pieces + ROW_STEP - 1) / ROW_STEP);
@@ -577,8 +613,8 @@ Cut cut_of(int dtype, uint64_t n_rows, uint32_t vocab, uint32_t k) {
   }
   c.part = ((pieces + c.parts - 1) / c.parts + 63) / 64 * 64;
   if (c.parts > 1) {
-    c.part_bytes = (n_rows * c.parts * sizeof(ScorePart) + 255) / 256 * 256;
-    c.bytes = c.part_bytes + n_rows * c.parts * k * sizeof(uint64_t);
+    c.parted_bytes = (n_rows * c.parts * sizeof(ScorePart) + 255) / 256 * 256;
+    c.bytes = c.parted_bytes + n_rows * c.parts * k * sizeof(uint64_t);
   }
   return c;
 }
@@ -636,7 +672,7 @@ int bbpe_token_logprobs(int dtype, const void *logits, int64_t row_stride, uint6
   a.top_logprobs = d_top_logprobs;
   a.stats = reinterpret_cast<float2 *>(d_stats);
   a.parted = static_cast<ScorePart *>(d_workspace);
-  a.parted_top = reinterpret_cast<uint64_t *>(static_cast<char *>(d_workspace) + cut.part_bytes);
+  a.parted_top = reinterpret_cast<uint64_t *>(static_cast<char *>(d_workspace) + cut.parted_bytes);
   const hipStream_t st = static_cast<hipStream_t>(hip_stream);
   const auto launch = [&](uint64_t blocks, auto kernel, uint32_t threads) {
     for (a.block0 = 0; a.block0 < blocks; a.block0 += MAX_GROUPS)
@@ -644,14 +680,16 @@ int bbpe_token_logprobs(int dtype, const void *logits, int64_t row_stride, uint6
   };
   with_element(dtype, [&](auto t) {
     typedef decltype(t) T;
-    const uint64_t blocks = n_rows * cut.parts;
+    // kernels by how many alternatives there are
+    const auto by_top = [&](auto none, auto few, auto many) { return top_k == 0 ? none : top_k <= FEW ? few : many; };
+    constexpr uint32_t W = ROW_WAVES;
     if (cut.parts > 1) {
-      launch(blocks, top_k ? k_scores<T, ROW_WAVES, true, true> : k_scores<T, ROW_WAVES, false, true>, ROW_THREADS);
+      launch(n_rows * cut.parts, by_top(k_scores<T, W, 0, true>, k_scores<T, W, 1, true>, k_scores<T, W, 2, true>), ROW_THREADS);
       launch(n_rows, top_k ? k_scores_join<T, true> : k_scores_join<T, false>, top_k ? ROW_THREADS : 64);
     } else if (cut.waves > 1) {
-      launch(blocks, top_k ? k_scores<T, ROW_WAVES, true, false> : k_scores<T, ROW_WAVES, false, false>, ROW_THREADS);
+      launch(n_rows, by_top(k_scores<T, W, 0, false>, k_scores<T, W, 1, false>, k_scores<T, W, 2, false>), ROW_THREADS);
     } else {
-      launch(blocks, top_k ? k_scores<T, 1, true, false> : k_scores<T, 1, false, false>, 64);
+      launch(n_rows, top_k ? k_scores<T, 1, 1, false> : k_scores<T, 1, 0, false>, 64);
     }
   });
   return hipGetLastError() == hipSuccess ? BBPE_OK : BBPE_E_HIP;
