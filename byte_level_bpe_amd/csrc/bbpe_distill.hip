@@ -22,19 +22,23 @@
 namespace bbpe {
 namespace {
 
-constexpr uint32_t LIST_MAX = 256;       // listed tokens at most
-constexpr uint32_t BIT_WORDS = 1u << 12; // words of 32 tokens in LDS: a stretch of 131,072 at a time
+constexpr uint32_t LIST_MAX = 256;  // listed tokens at most
+constexpr uint32_t STEP_WAVES = 8;  // of a workgroup that makes loss and gradient
 
 struct DistillArgs {
   const void *x;
   int64_t stride;
-  uint64_t row0;
-  uint32_t vocab, k, tail;
+  void *dx;  // where the gradient is wanted too
+  int64_t dx_stride;
+  uint64_t block0;
+  uint32_t vocab, k, tail, parts, part;  // parts of a row, and pieces of one
   float scale, c;
   const int32_t *ids;
   const float *lp;
   float *loss, *lse;
   float4 *stats;
+  const float *grad;
+  Partial *parted;  // [rows][parts]
 };
 
 __device__ __forceinline__ double wave_max(double v) {
@@ -51,7 +55,7 @@ __device__ __forceinline__ double wave_max(double v) {
 // of p_j in the gradient, of tokens that are not listed; with a tail the listed
 // ones' factor, without one the logarithm of the teacher's sum.
 template <typename T>
-__device__ void end_row(const DistillArgs &a, uint64_t row, const T *x, Partial p, const int32_t *ids) {
+__device__ __forceinline__ float4 end_row(const DistillArgs &a, uint64_t row, const T *x, Partial p, const int32_t *ids) {
   constexpr uint32_t E = LIST_MAX / 64;
   const uint32_t lane = threadIdx.x & 63;
   const float *lp = a.lp + row * a.k;
@@ -118,7 +122,6 @@ __device__ void end_row(const DistillArgs &a, uint64_t row, const T *x, Partial 
     loss += rest * (log(rest) + log1p(listed / others));
     ratio = others > 0.0 ? rest * (1.0 + listed / others) : 0.0;
   }
-  if (lane) return;
   const bool none = high == -INFINITY && sum == 0.0, bad = !(sum == sum) || high == INFINITY;
   const float nan = __uint_as_float(0x7FC00000u);
   float4 st = make_float4(high, float(log_sum), 0.0f, 0.0f);
@@ -139,50 +142,68 @@ __device__ void end_row(const DistillArgs &a, uint64_t row, const T *x, Partial 
     st.z = 1.0f;
     st.w = float(c);
   }
-  a.loss[row] = float(loss);
-  a.lse[row] = bad ? nan : none ? -INFINITY : float(double(high) * a.scale + log_sum);
-  a.stats[row] = st;
+  if (lane == 0) {
+    a.loss[row] = float(loss);
+    a.lse[row] = bad ? nan : none ? -INFINITY : float(double(high) * a.scale + log_sum);
+    a.stats[row] = st;
+  }
+  return st;
 }
 
-template <typename T, bool TAIL>
-__global__ __launch_bounds__(ROW_THREADS) void k_distill(DistillArgs a) {
-  typedef Piece<T> P;
-  typedef typename P::raw Raw;
-  constexpr uint32_t STRETCH = TAIL ? BIT_WORDS * 32 / P::N / ROW_STEP : 1;  // steps between two settings of the bits
-  __shared__ Partial sh[ROW_WAVES];
-  __shared__ int32_t ids[LIST_MAX];
-  __shared__ uint32_t bits[TAIL ? BIT_WORDS : 1];
-  const uint64_t row = a.row0 + blockIdx.x;
-  const T *x = static_cast<const T *>(a.x) + int64_t(row) * a.stride;
-  const Row<const T> r(x, a.vocab);
-  const uint32_t tid = threadIdx.x;
-  if (tid < a.k) {
-    const int32_t id = a.ids[row * a.k + tid];
-    ids[tid] = id >= 0 && uint32_t(id) < a.vocab ? id : -1;
+// Tokens by which bits of the list are set at a time, 16 or (float32) 32 steps.
+template <uint32_t WAVES> constexpr uint32_t BITS = 64 * WAVES * ROW_UNROLL * 8 * 16;
+
+template <uint32_t WAVES, bool TAIL> struct DistillShared {
+  Partial sums[WAVES];
+  int32_t ids[LIST_MAX];  // the row's list, -1 where an entry names no token
+  float q[LIST_MAX];
+  uint32_t bits[TAIL ? BITS<WAVES> / 32 : 1];
+  float4 stats;
+};
+
+// The list to LDS, without a barrier.
+template <uint32_t WAVES>
+__device__ __forceinline__ void load_list(const DistillArgs &a, uint64_t row, int32_t *ids) {
+  for (uint32_t t = threadIdx.x; t < a.k; t += 64 * WAVES) {
+    const int32_t id = a.ids[row * a.k + t];
+    ids[t] = id >= 0 && uint32_t(id) < a.vocab ? id : -1;
   }
+}
+
+// The weights of pieces [first, last) of a row; with a tail, of tokens that are
+// not listed.
+template <typename T, uint32_t WAVES, bool TAIL>
+__device__ __forceinline__ Partial sum_pieces(const DistillArgs &a, const Row<const T> &r, uint32_t first, uint32_t last,
+                                              DistillShared<WAVES, TAIL> &sh) {
+  typedef Piece<T> P;
+  constexpr uint32_t THREADS = 64 * WAVES, STEP = THREADS * ROW_UNROLL;
+  constexpr uint32_t STRETCH = BITS<WAVES> / P::N;  // pieces between two settings of the bits
+  const uint32_t tid = threadIdx.x;
+  last = min(last, r.pieces());
   Partial s{-INFINITY, 0.0f, 0.0f};
   float ref = 0.0f;
-  const uint32_t steps = (r.pieces() + ROW_STEP - 1) / ROW_STEP;
-  for (uint32_t i = 0; i < steps; ++i) {
-    if (TAIL && i % STRETCH == 0) {
-      const uint32_t from = i * ROW_STEP * P::N;
+  for (uint32_t p0 = first; p0 < last; p0 += STEP) {
+    if (TAIL && (p0 - first) % STRETCH == 0) {
+      const uint32_t from = p0 * P::N, words = (min(last - p0, STRETCH) * P::N + 31) / 32;
       __syncthreads();
-      for (uint32_t w = tid; w < BIT_WORDS; w += ROW_THREADS) bits[w] = 0;
+      for (uint32_t w = tid; w < words; w += THREADS) sh.bits[w] = 0;
       __syncthreads();
-      const uint32_t place = tid < a.k && ids[tid] >= 0 ? r.lead + uint32_t(ids[tid]) - from : ~0u;
-      if (place < BIT_WORDS * 32) atomicOr(&bits[place / 32], 1u << place % 32);
+      for (uint32_t t = tid; t < a.k; t += THREADS) {
+        const uint32_t place = sh.ids[t] >= 0 ? r.lead + uint32_t(sh.ids[t]) - from : ~0u;
+        if (place < words * 32) atomicOr(&sh.bits[place / 32], 1u << place % 32);
+      }
       __syncthreads();
     }
+    typename P::raw raw[ROW_UNROLL];
+    r.template load_step<THREADS>(raw, r.at, p0 + tid, last);
     typename P::val v[ROW_UNROLL];
     float m = -INFINITY;
-    Raw raw[ROW_UNROLL];
-    r.template load_step<ROW_THREADS>(raw, r.at, i * ROW_STEP + tid, r.pieces());
 #pragma unroll
     for (uint32_t u = 0; u < ROW_UNROLL; ++u) {
       v[u] = values<T>(raw[u]);
       if (TAIL) {
-        const uint32_t place = (i % STRETCH * ROW_STEP + u * ROW_THREADS + tid) * P::N;
-        const uint32_t mask = bits[place / 32] >> place % 32 & ((1u << P::N) - 1);
+        const uint32_t place = ((p0 - first) % STRETCH + u * THREADS + tid) * P::N;  // (past `last`: of old bits, and nothing to mask)
+        const uint32_t mask = sh.bits[place / 32] >> place % 32 & ((1u << P::N) - 1);
         if (__any(mask)) {
 #pragma unroll
           for (uint32_t e = 0; e < P::N; ++e) v[u][e] = mask >> e & 1 ? -INFINITY : v[u][e];
@@ -200,63 +221,43 @@ __global__ __launch_bounds__(ROW_THREADS) void k_distill(DistillArgs a) {
 #pragma unroll
       for (uint32_t e = 0; e < P::N; ++e) s.sum += __builtin_amdgcn_exp2f((v[u][e] - ref) * a.c);
   }
-  s = row_partial<ROW_WAVES>(s, a.c, sh);  // (with a barrier, for the list too)
-  if (tid < 64) end_row<T>(a, row, x, s, ids);
+  return row_partial<WAVES>(s, a.c, sh.sums);  // (with a barrier, for the list too)
 }
 
-struct DistillBackArgs {
-  const void *x;
-  int64_t stride;
-  void *dx;
-  int64_t dx_stride;
-  uint64_t block0;
-  uint32_t vocab, k, tail, parts, part;  // parts of a row, and pieces of one
-  float scale, c;
-  const int32_t *ids;
-  const float *lp;
-  const float4 *stats;
-  const float *grad;
-};
-
-// One workgroup a part of a row.  The listed tokens are written once more when
-// the part is done, from what was there before (dx may be x): each by one
-// thread, or by several with the same value.
-template <typename T>
-__global__ __launch_bounds__(ROW_THREADS) void k_distill_back(DistillBackArgs a) {
+// The gradient of pieces [from, to) of a row as they are written, from its stats
+// and list in LDS.  The listed tokens are written once more when the part is
+// done, from what was there before (dx may be x): each by one thread, or by
+// several with the same value.
+template <typename T, uint32_t WAVES>
+__device__ __forceinline__ void grad_pieces(const DistillArgs &a, uint64_t row, const T *x, const Row<T> &r, uint32_t from, uint32_t to, float4 st,
+                                            const int32_t *ids, float *q) {
   typedef Piece<T> P;
-  __shared__ int32_t ids[LIST_MAX];
-  __shared__ float q[LIST_MAX];
+  constexpr uint32_t THREADS = 64 * WAVES, STEP = THREADS * ROW_UNROLL, TERMS = (LIST_MAX + THREADS - 1) / THREADS;
   const uint32_t tid = threadIdx.x;
-  const uint64_t block = a.block0 + blockIdx.x, row = block / a.parts;
-  const T *x = static_cast<const T *>(a.x) + int64_t(row) * a.stride;
-  T *dx = static_cast<T *>(a.dx) + int64_t(row) * a.dx_stride;
-  const Row<T> r(dx, a.vocab);  // pieces as they are written
-  const uint32_t from = uint32_t(block % a.parts) * a.part, to = min(r.pieces(), from + a.part);
-  if (from >= to) return;  // (parts are counted for rows that begin anywhere)
-  const float4 st = a.stats[row];
   const float g = a.grad[row] * a.scale;
   const bool zero = st.x == -INFINITY || g == 0.0f;
   const float inv = __builtin_amdgcn_exp2f(-st.y * LOG2E);
   const auto weight = [&](float v) { return __builtin_amdgcn_exp2f((v - st.x) * a.c); };
-  float before = 0.0f;
-  bool mine = false;
-  if (tid < a.k) {
-    const int32_t id = a.ids[row * a.k + tid];
-    const float lp = a.lp[row * a.k + tid];
-    const bool there = id >= 0 && uint32_t(id) < a.vocab;
-    ids[tid] = there ? id : -1;
-    q[tid] = there ? __builtin_amdgcn_exp2f((lp - (a.tail ? 0.0f : st.w)) * LOG2E) : 0.0f;
-    mine = there && !zero && (r.lead + uint32_t(id)) / P::N - from < to - from;
-    if (mine) before = float(x[id]);
+  float before[TERMS];
+  bool mine[TERMS];
+#pragma unroll
+  for (uint32_t i = 0; i < TERMS; ++i) {
+    const uint32_t t = tid + i * THREADS;
+    mine[i] = false;
+    if (t >= a.k) continue;
+    const int32_t id = ids[t];
+    q[t] = id >= 0 ? __builtin_amdgcn_exp2f((a.lp[row * a.k + t] - (a.tail ? 0.0f : st.w)) * LOG2E) : 0.0f;
+    mine[i] = id >= 0 && !zero && (r.lead + uint32_t(id)) / P::N - from < to - from;
+    if (mine[i]) before[i] = float(x[id]);
   }
   __syncthreads();
   const float all = g * st.z * inv;
-  for (uint32_t p0 = from; p0 < to; p0 += ROW_STEP) {
+  for (uint32_t p0 = from; p0 < to; p0 += STEP) {
     typename P::raw raw[ROW_UNROLL];
-    if (!zero) r.template load_step<ROW_THREADS>(raw, x - r.lead, p0 + tid, to);
+    if (!zero) r.template load_step<THREADS>(raw, x - r.lead, p0 + tid, to);
 #pragma unroll
     for (uint32_t u = 0; u < ROW_UNROLL; ++u) {
-      const uint32_t p = p0 + u * ROW_THREADS + tid;
+      const uint32_t p = p0 + u * THREADS + tid;
       if (p >= to) break;
       typename P::val v = 0.0f;
       if (!zero) {
@@ -268,13 +269,67 @@ __global__ __launch_bounds__(ROW_THREADS) void k_distill_back(DistillBackArgs a)
     }
   }
   __syncthreads();
-  if (!mine) return;
-  float sum = 0.0f;
-  for (uint32_t t = 0; t < a.k; ++t) sum += ids[t] == ids[tid] ? q[t] : 0.0f;
-  dx[ids[tid]] = T(g * ((a.tail ? st.w : st.z) * inv * weight(before) - sum));
+#pragma unroll
+  for (uint32_t i = 0; i < TERMS; ++i) {
+    if (!mine[i]) continue;
+    const int32_t id = ids[tid + i * THREADS];
+    float sum = 0.0f;
+    for (uint32_t t = 0; t < a.k; ++t) sum += ids[t] == id ? q[t] : 0.0f;
+    r.at[r.lead + uint32_t(id)] = T(g * ((a.tail ? st.w : st.z) * inv * weight(before[i]) - sum));
+  }
 }
 
-constexpr uint64_t MAX_GROUPS = 1u << 23;  // workgroups of a launch: fewer than 2^32 threads
+// A workgroup a row or, SPLIT, a part of one.  GRAD: the gradient too, the row
+// read again while it is near.
+template <typename T, uint32_t WAVES, bool TAIL, bool SPLIT, bool GRAD>
+__global__ __launch_bounds__(64 * WAVES) void k_distill(DistillArgs a) {
+  __shared__ DistillShared<WAVES, TAIL> sh;
+  const uint64_t block = a.block0 + blockIdx.x, row = SPLIT ? block / a.parts : block;
+  const uint32_t first = SPLIT ? uint32_t(block % a.parts) * a.part : 0;
+  const T *x = static_cast<const T *>(a.x) + int64_t(row) * a.stride;
+  if (TAIL || !SPLIT) load_list<WAVES>(a, row, sh.ids);
+  const Partial s = sum_pieces<T, WAVES, TAIL>(a, Row<const T>(x, a.vocab), first, SPLIT ? first + a.part : ~0u, sh);
+  if (SPLIT) {
+    if (threadIdx.x == 0) a.parted[block] = s;
+    return;
+  }
+  if (threadIdx.x < 64) {
+    const float4 st = end_row<T>(a, row, x, s, sh.ids);
+    if (GRAD && threadIdx.x == 0) sh.stats = st;
+  }
+  if (!GRAD) return;
+  __syncthreads();
+  const Row<T> r(static_cast<T *>(a.dx) + int64_t(row) * a.dx_stride, a.vocab);
+  grad_pieces<T, WAVES>(a, row, x, r, 0, r.pieces(), sh.stats, sh.ids, sh.q);
+}
+
+// Joins a row's parts.
+template <typename T>
+__global__ __launch_bounds__(64) void k_distill_join(DistillArgs a) {
+  __shared__ int32_t ids[LIST_MAX];
+  const uint64_t row = a.block0 + blockIdx.x;
+  const T *x = static_cast<const T *>(a.x) + int64_t(row) * a.stride;
+  load_list<1>(a, row, ids);
+  Partial p{-INFINITY, 0.0f, 0.0f};
+  if (threadIdx.x < a.parts) p = a.parted[row * a.parts + threadIdx.x];
+  p = wave_partial(p, a.c);
+  __syncthreads();
+  end_row<T>(a, row, x, p, ids);
+}
+
+// The gradient by itself: a workgroup a part of a row.
+template <typename T, uint32_t WAVES>
+__global__ __launch_bounds__(64 * WAVES) void k_distill_back(DistillArgs a) {
+  __shared__ int32_t ids[LIST_MAX];
+  __shared__ float q[LIST_MAX];
+  const uint64_t block = a.block0 + blockIdx.x, row = block / a.parts;
+  const Row<T> r(static_cast<T *>(a.dx) + int64_t(row) * a.dx_stride, a.vocab);
+  const uint32_t from = uint32_t(block % a.parts) * a.part, to = min(r.pieces(), from + a.part);
+  if (from >= to) return;  // (parts are counted for rows that begin anywhere)
+  load_list<WAVES>(a, row, ids);
+  // (every thread reads back the entries that it has written itself, until the barrier)
+  grad_pieces<T, WAVES>(a, row, static_cast<const T *>(a.x) + int64_t(row) * a.stride, r, from, to, a.stats[row], ids, q);
+}
 
 int check(int dtype, const void *logits, int64_t row_stride, uint64_t n_rows, uint32_t vocab, const int32_t *ids, const float *lp,
           uint32_t k, int tail, float scale) {
@@ -285,12 +340,50 @@ int check(int dtype, const void *logits, int64_t row_stride, uint64_t n_rows, ui
   return BBPE_OK;
 }
 
+DistillArgs args_of(const void *logits, int64_t row_stride, uint32_t vocab, const int32_t *ids, const float *lp, uint32_t k, int tail, float scale) {
+  DistillArgs a{};
+  a.x = logits;
+  a.stride = row_stride;
+  a.vocab = vocab;
+  a.k = k;
+  a.tail = uint32_t(tail);
+  a.scale = scale;
+  a.c = scale * LOG2E;
+  a.ids = ids;
+  a.lp = lp;
+  return a;
+}
+
+uint64_t parted_bytes(const Cut &cut, uint64_t n_rows) { return cut.parts > 1 ? n_rows * cut.parts * sizeof(Partial) : 0; }
+
+// The gradient from rows' stats.
+void launch_back(DistillArgs a, int dtype, uint64_t n_rows, hipStream_t st) {
+  const uint32_t pieces = most_pieces(dtype, a.vocab);
+  const bool small = pieces <= 512;
+  a.part = small ? pieces : 2 * ROW_STEP;
+  a.parts = (pieces + a.part - 1) / a.part;
+  const uint64_t blocks = n_rows * a.parts;
+  with_element(dtype, [&](auto t) {
+    for (a.block0 = 0; a.block0 < blocks; a.block0 += MAX_GROUPS) {
+      const uint32_t grid = uint32_t(std::min(blocks - a.block0, MAX_GROUPS));
+      if (small) k_distill_back<decltype(t), 1><<<grid, 64, 0, st>>>(a);
+      else k_distill_back<decltype(t), ROW_WAVES><<<grid, ROW_THREADS, 0, st>>>(a);
+    }
+  });
+}
+
 }  // namespace
 }  // namespace bbpe
 
 using namespace bbpe;
 
 extern "C" {
+
+int bbpe_distill_loss_workspace_bytes(int dtype, uint64_t n_rows, uint32_t vocab, uint64_t *out_bytes) {
+  if (!out_bytes || bad_sizes(dtype, n_rows, vocab)) return BBPE_E_INVALID_ARG;
+  *out_bytes = parted_bytes(cut_rows(dtype, n_rows, vocab, true, PARTS_MAX), n_rows);
+  return BBPE_OK;
+}
 
 int bbpe_distill_loss_backward(int dtype, const void *logits, int64_t row_stride, uint64_t n_rows, uint32_t vocab,
                                const int32_t *d_top_ids, const float *d_top_logprobs, uint32_t top_k, int tail, float scale,
@@ -301,35 +394,13 @@ int bbpe_distill_loss_backward(int dtype, const void *logits, int64_t row_stride
       (address(d_stats) & 15) || (address(d_grad) & 3))
     return BBPE_E_INVALID_ARG;
   if (n_rows == 0) return BBPE_OK;
-  DistillBackArgs a{};
-  a.x = logits;
-  a.stride = row_stride;
+  DistillArgs a = args_of(logits, row_stride, vocab, d_top_ids, d_top_logprobs, top_k, tail, scale);
   a.dx = d_logits;
   a.dx_stride = dl_stride;
-  a.vocab = vocab;
-  a.k = top_k;
-  a.tail = uint32_t(tail);
-  a.scale = scale;
-  a.c = scale * LOG2E;
-  a.ids = d_top_ids;
-  a.lp = d_top_logprobs;
-  a.stats = reinterpret_cast<const float4 *>(d_stats);
+  a.stats = reinterpret_cast<float4 *>(const_cast<float *>(d_stats));
   a.grad = d_grad;
-  a.part = 2 * ROW_STEP;
-  a.parts = (most_pieces(dtype, vocab) + a.part - 1) / a.part;
-  const hipStream_t st = static_cast<hipStream_t>(hip_stream);
-  const uint64_t blocks = n_rows * a.parts;
-  for (; a.block0 < blocks; a.block0 += MAX_GROUPS)
-    with_element(dtype, [&](auto t) {
-      k_distill_back<decltype(t)><<<uint32_t(std::min(blocks - a.block0, MAX_GROUPS)), ROW_THREADS, 0, st>>>(a);
-    });
+  launch_back(a, dtype, n_rows, static_cast<hipStream_t>(hip_stream));
   return hipGetLastError() == hipSuccess ? BBPE_OK : BBPE_E_HIP;
-}
-
-int bbpe_distill_loss_workspace_bytes(int dtype, uint64_t n_rows, uint32_t vocab, uint64_t *out_bytes) {
-  if (!out_bytes || bad_sizes(dtype, n_rows, vocab)) return BBPE_E_INVALID_ARG;
-  *out_bytes = 0;
-  return BBPE_OK;
 }
 
 int bbpe_distill_loss(int dtype, const void *logits, int64_t row_stride, uint64_t n_rows, uint32_t vocab,
@@ -343,30 +414,43 @@ int bbpe_distill_loss(int dtype, const void *logits, int64_t row_stride, uint64_
       (d_logits && bad_logits(dtype, d_logits, dl_stride, n_rows, vocab, true)))
     return BBPE_E_INVALID_ARG;
   if (n_rows == 0) return BBPE_OK;
-  DistillArgs a{};
-  a.x = logits;
-  a.stride = row_stride;
-  a.vocab = vocab;
-  a.k = top_k;
-  a.tail = uint32_t(tail);
-  a.scale = scale;
-  a.c = scale * LOG2E;
-  a.ids = d_top_ids;
-  a.lp = d_top_logprobs;
+  const Cut cut = cut_rows(dtype, n_rows, vocab, true, PARTS_MAX);
+  const uint64_t need = parted_bytes(cut, n_rows);
+  if (need && (!d_workspace || (address(d_workspace) & 255) || workspace_bytes < need)) return BBPE_E_WORKSPACE;
+  DistillArgs a = args_of(logits, row_stride, vocab, d_top_ids, d_top_logprobs, top_k, tail, scale);
+  a.dx = d_logits;
+  a.dx_stride = dl_stride;
+  a.parts = cut.parts;
+  a.part = cut.part;
   a.loss = d_loss;
   a.lse = d_lse;
   a.stats = reinterpret_cast<float4 *>(d_stats);
+  a.grad = d_weights;
+  a.parted = static_cast<Partial *>(d_workspace);
   const hipStream_t st = static_cast<hipStream_t>(hip_stream);
-  for (; a.row0 < n_rows; a.row0 += MAX_GROUPS)
-    with_element(dtype, [&](auto t) {
-      const uint32_t grid = uint32_t(std::min(n_rows - a.row0, MAX_GROUPS));
-      if (tail) k_distill<decltype(t), true><<<grid, ROW_THREADS, 0, st>>>(a);
-      else k_distill<decltype(t), false><<<grid, ROW_THREADS, 0, st>>>(a);
-    });
+  const auto launch = [&](uint64_t blocks, auto kernel, uint32_t threads) {
+    for (a.block0 = 0; a.block0 < blocks; a.block0 += MAX_GROUPS)
+      kernel<<<uint32_t(std::min(blocks - a.block0, MAX_GROUPS)), threads, 0, st>>>(a);
+  };
+  const bool grad = d_logits != nullptr;
+  with_element(dtype, [&](auto t) {
+    typedef decltype(t) T;
+    constexpr uint32_t W = ROW_WAVES;
+    if (cut.parts > 1) {
+      launch(n_rows * cut.parts, tail ? k_distill<T, W, true, true, false> : k_distill<T, W, false, true, false>, ROW_THREADS);
+      launch(n_rows, k_distill_join<T>, 64);
+    } else if (cut.waves == 1) {
+      if (grad) launch(n_rows, tail ? k_distill<T, 1, true, false, true> : k_distill<T, 1, false, false, true>, 64);
+      else launch(n_rows, tail ? k_distill<T, 1, true, false, false> : k_distill<T, 1, false, false, false>, 64);
+    } else if (grad) {
+      launch(n_rows, tail ? k_distill<T, STEP_WAVES, true, false, true> : k_distill<T, STEP_WAVES, false, false, true>, 64 * STEP_WAVES);
+    } else {
+      launch(n_rows, tail ? k_distill<T, W, true, false, false> : k_distill<T, W, false, false, false>, ROW_THREADS);
+    }
+  });
   if (hipGetLastError() != hipSuccess) return BBPE_E_HIP;
-  return d_logits ? bbpe_distill_loss_backward(dtype, logits, row_stride, n_rows, vocab, d_top_ids, d_top_logprobs, top_k, tail,
-                                               scale, d_stats, d_weights, d_logits, dl_stride, hip_stream)
-                  : BBPE_OK;
+  if (grad && cut.parts > 1) launch_back(a, dtype, n_rows, st);
+  return hipGetLastError() == hipSuccess ? BBPE_OK : BBPE_E_HIP;
 }
 
 }  // extern "C"

@@ -159,6 +159,30 @@ inline uint32_t most_pieces(int dtype, uint32_t vocab) {
   return (vocab + 2 * (n - 1)) / n;
 }
 
+constexpr uint32_t PARTS_MAX = 64;         // parts of a row at most: a wave joins them
+constexpr uint64_t MAX_GROUPS = 1u << 22;  // workgroups of a launch: fewer than 2^32 threads
+
+// How rows are cut: waves a workgroup, parts a row and pieces of a part.  Rows of
+// up to 512 pieces go to a wave each (where `small` allows it); longer ones to a
+// workgroup each, and where they are fewer than 1,024, to several, a step each at
+// least (WHY).
+struct Cut {
+  uint32_t waves, parts, part;
+};
+inline Cut cut_rows(int dtype, uint64_t n_rows, uint32_t vocab, bool small, uint32_t most_parts) {
+  const uint32_t pieces = most_pieces(dtype, vocab);
+  Cut c{small && pieces <= 512 ? 1u : ROW_WAVES, 1, 0};
+  if (c.waves > 1 && n_rows) {
+    const uint64_t want = (1024 + n_rows - 1) / n_rows;
+    uint64_t most = (pieces + ROW_STEP - 1) / ROW_STEP;
+    most = most < PARTS_MAX ? most : PARTS_MAX;
+    most = most < most_parts ? most : most_parts;
+    c.parts = uint32_t(want < most ? want : most);
+  }
+  c.part = ((pieces + c.parts - 1) / c.parts + 63) / 64 * 64;
+  return c;
+}
+
 inline uintptr_t address(const void *p) { return reinterpret_cast<uintptr_t>(p); }
 
 inline bool bad_sizes(int dtype, uint64_t rows, uint32_t vocab) {

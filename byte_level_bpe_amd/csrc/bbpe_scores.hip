@@ -24,10 +24,8 @@ constexpr uint32_t TOP_MAX = 256;   // alternatives at most
 // earlier for it (64 alternatives of 200,064: 333 us exact, SLACKTIME with this).
 __host__ __device__ constexpr uint32_t with_slack(uint32_t k) { return k + k / 4 + 16; }
 constexpr uint32_t TOP_ROOM = with_slack(TOP_MAX);
-constexpr uint32_t FEW = 32;            // alternatives up to which a group's second piece is not kept
 constexpr uint32_t SMALL_TOP = 64;      // alternatives up to which a wave may take a row
 constexpr uint32_t KEPT_ROOM = (TOP_ROOM + 63) / 64 * 64;
-constexpr uint32_t PARTS_MAX = 64;  // parts of a row at most: a wave joins them
 constexpr uint32_t JOIN_KEYS = 4096;  // alternatives of all parts at most
 
 struct ScorePart {
@@ -220,13 +218,14 @@ template <uint32_t WAVES, uint32_t KEEP> struct ScoreShared {
   static constexpr uint32_t GROUPS = 64 * WAVES * ROW_UNROLL;
   // Candidates that can be put in order; twice as many can be held.  Where no more
   // than k groups have pieces, all of their elements are.
-  static constexpr uint32_t ROOM = GROUPS > KEPT_ROOM ? GROUPS : KEPT_ROOM;
-  static_assert(2 * ROOM >= 8 * (WAVES == 1 ? SMALL_TOP : TOP_MAX), "");
+  static constexpr uint32_t LIST = with_slack(KEEP < 2 ? SMALL_TOP : TOP_MAX);  // groups that reach the bar
+  static constexpr uint32_t ROOM = GROUPS;
+  static_assert(ROOM >= LIST && 2 * ROOM >= 8 * (WAVES == 1 ? SMALL_TOP : TOP_MAX), "");
   Partial sums[WAVES];
   uint32_t above[WAVES];
   uint64_t keys[TOP ? 2 * ROOM : 1];
-  uint32_t chosen[TOP ? KEEP * TOP_ROOM : 1];  // pieces
-  uint32_t deep[TOP ? TOP_ROOM : 1][TOP ? 1 + KEEP : 1];  // a group, and its pieces among the chosen ones
+  uint32_t chosen[TOP ? KEEP * LIST : 1];  // pieces
+  uint32_t deep[TOP ? LIST : 1][TOP ? 1 + KEEP : 1];  // a group, and its pieces among the chosen ones
   uint32_t n_chosen, n_deep, n_found;
   uint64_t reach;
 };
@@ -595,23 +594,11 @@ uint32_t bits_of(uint32_t vocab) {
   return b;
 }
 
-constexpr uint64_t MAX_GROUPS = 1u << 23;  // workgroups of a launch: fewer than 2^32 threads
-
-// How rows are cut: waves a workgroup, parts a row and pieces of a part.
-struct Cut {
-  uint32_t waves, parts, part;
+struct ScoreCut : Cut {
   uint64_t parted_bytes, bytes;  // of the parts' numbers, and with their alternatives
 };
-Cut cut_of(int dtype, uint64_t n_rows, uint32_t vocab, uint32_t k) {
-  const uint32_t pieces = most_pieces(dtype, vocab);
-  Cut c{pieces <= 512 && k <= SMALL_TOP ? 1u : ROW_WAVES, 1, 0, 0, 0};
-  if (c.waves > 1 && n_rows) {
-    const uint64_t want = (2048 + n_rows - 1) / n_rows;
-    uint64_t most = std::min<uint64_t>(PARTS_MAX, (pieces + ROW_STEP - 1) / ROW_STEP);
-    if (k) most = std::min<uint64_t>(most, JOIN_KEYS / k);
-    c.parts = uint32_t(std::max<uint64_t>(1, std::min(want, most)));
-  }
-  c.part = ((pieces + c.parts - 1) / c.parts + 63) / 64 * 64;
+ScoreCut cut_of(int dtype, uint64_t n_rows, uint32_t vocab, uint32_t k) {
+  ScoreCut c{cut_rows(dtype, n_rows, vocab, k <= SMALL_TOP, k ? JOIN_KEYS / k : PARTS_MAX), 0, 0};
   if (c.parts > 1) {
     c.parted_bytes = (n_rows * c.parts * sizeof(ScorePart) + 255) / 256 * 256;
     c.bytes = c.parted_bytes + n_rows * c.parts * k * sizeof(uint64_t);
@@ -651,7 +638,7 @@ int bbpe_token_logprobs(int dtype, const void *logits, int64_t row_stride, uint6
        address(d_top_logprobs)) & 3 || (address(d_stats) & 7))
     return BBPE_E_INVALID_ARG;
   if (n_rows == 0) return BBPE_OK;
-  const Cut cut = cut_of(dtype, n_rows, vocab, top_k);
+  const ScoreCut cut = cut_of(dtype, n_rows, vocab, top_k);
   if (cut.bytes && (!d_workspace || (address(d_workspace) & 255) || workspace_bytes < cut.bytes)) return BBPE_E_WORKSPACE;
   ScoreArgs a{};
   a.x = logits;
@@ -680,14 +667,12 @@ int bbpe_token_logprobs(int dtype, const void *logits, int64_t row_stride, uint6
   };
   with_element(dtype, [&](auto t) {
     typedef decltype(t) T;
-    // kernels by how many alternatives there are
-    const auto by_top = [&](auto none, auto few, auto many) { return top_k == 0 ? none : top_k <= FEW ? few : many; };
     constexpr uint32_t W = ROW_WAVES;
     if (cut.parts > 1) {
-      launch(n_rows * cut.parts, by_top(k_scores<T, W, 0, true>, k_scores<T, W, 1, true>, k_scores<T, W, 2, true>), ROW_THREADS);
+      launch(n_rows * cut.parts, top_k ? k_scores<T, W, 2, true> : k_scores<T, W, 0, true>, ROW_THREADS);
       launch(n_rows, top_k ? k_scores_join<T, true> : k_scores_join<T, false>, top_k ? ROW_THREADS : 64);
     } else if (cut.waves > 1) {
-      launch(n_rows, by_top(k_scores<T, W, 0, false>, k_scores<T, W, 1, false>, k_scores<T, W, 2, false>), ROW_THREADS);
+      launch(n_rows, top_k ? k_scores<T, W, 2, false> : k_scores<T, W, 0, false>, ROW_THREADS);
     } else {
       launch(n_rows, top_k ? k_scores<T, 1, 1, false> : k_scores<T, 1, 0, false>, 64);
     }

@@ -262,6 +262,31 @@ def test_distill(v, k, dtype):
         check_distill(x, ids, lp, tail, scale, w, offset=int(tail), pad=3)
 
 
+@pytest.mark.parametrize("dtype", [BF, HF, F])
+@pytest.mark.parametrize("v,k", [(513, 5), (1280, 16), (5003, 64), (33001, 256)])
+@pytest.mark.parametrize("n", [300, 1111])
+def test_distill_of_many_rows(n, v, k, dtype):
+    """Rows in parts and whole ones, loss and gradient apart and in one call: each as its like in a small reference."""
+    x, g = logits(7, v, dtype, v)
+    w = torch.randn(7, generator=g)
+    w[2] = 0.0
+    for tail in (False, True):
+        say("many rows", n, v, k, dtype, tail)
+        ids, lp = teacher(x, k, g, tail, 1.0)
+        ids[1] = -1
+        y = x.clone()
+        y[3] = -INF
+        y[4, 5] = NAN
+        loss, dx, _ = ref.distill(y, ids, lp, tail, 1.0, w)
+        dev, a, up = many(y, n).cuda(), (many(ids, n).cuda(), many(lp, n).cuda()), many(w, n).cuda()
+        got = B.distill_loss(dev, *a, tail=tail)
+        near(got.loss, many(loss[0], n), many(loss[1], n), "loss")
+        near(B.distill_loss_backward(up, dev, *a, got, tail=tail), many(dx[0], n), many(dx[1], n), "dx")
+        both = B.distill_loss(dev, *a, tail=tail, weights=up, dlogits=dev)
+        near(both.loss, many(loss[0], n), many(loss[1], n), "loss, in one call")
+        near(dev, many(dx[0], n), many(dx[1], n), "dx, in one call")
+
+
 @pytest.mark.parametrize("tail", [False, True])
 def test_distill_odd_rows(tail):
     """No teacher, tokens named twice, ids out of range, teachers and students with no probability for a token,

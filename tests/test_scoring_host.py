@@ -70,6 +70,19 @@ def test_distill_refuses(bad):
     assert distill_call(**bad) == B.E_INVALID_ARG
 
 
+def test_distill_workspace():
+    n = C.c_uint64()
+    size, big = scoring._lib().bbpe_distill_loss_workspace_bytes, dict(n=3, vocab=100000, stride=100000, dstride=100000)
+    assert size(0, 3, 100, C.byref(n)) == 0 and n.value == 0 and size(0, 1 << 20, 100000, C.byref(n)) == 0 and n.value == 0
+    assert size(0, 3, 100000, C.byref(n)) == 0 and n.value > 0
+    assert distill_call(**big, ws=None) == B.E_WORKSPACE
+    assert distill_call(**big, ws_bytes=n.value - 1) == B.E_WORKSPACE
+    assert distill_call(**big, ws=X + 8) == B.E_WORKSPACE
+    for bad in ((3, 3, 100), (0, 1 << 31, 100), (0, 3, 0)):
+        assert size(*bad, C.byref(n)) == B.E_INVALID_ARG
+    assert size(0, 3, 100, None) == B.E_INVALID_ARG
+
+
 def distill_back_call(**kw):
     a = dict(dtype=0, x=X, stride=100, n=3, vocab=100, ids=X, lp=X, k=5, tail=0, scale=1.0, stats=X, g=X, dx=X, dstride=100, stream=None)
     a.update(kw)
