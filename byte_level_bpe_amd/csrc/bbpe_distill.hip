@@ -23,7 +23,9 @@ namespace bbpe {
 namespace {
 
 constexpr uint32_t LIST_MAX = 256;  // listed tokens at most
-constexpr uint32_t STEP_WAVES = 8;  // of a workgroup that makes loss and gradient
+constexpr uint32_t HELD = 16;       // pieces that a thread holds from the loss to the gradient
+constexpr uint64_t STEP_ROWS = 256;
+constexpr uint32_t STEP_MOST = 1u << 15;
 
 struct DistillArgs {
   const void *x;
@@ -47,75 +49,111 @@ __device__ __forceinline__ double wave_max(double v) {
   return v;
 }
 
-// The end of a row, by one wave: p holds the weights of the whole row (with a
-// tail: of the tokens that are not listed).  ids: the row's list in LDS, -1
-// where an entry names no token.
+// What the teacher lists for a row, and what comes of it before the row is read.
+// By one wave, four entries a lane.
+template <uint32_t LIST> struct ListShared {
+  double q[LIST], log_q[LIST];
+  int32_t ids[LIST];  // -1 where an entry names no token
+  float own[LIST];    // the student's element; minus infinity where it is not there
+  bool first[LIST];   // with a tail: the first entry that names this token
+  double mass, rest, log_norm;
+  int some;
+};
+template <uint32_t LIST> struct ListLoads {
+  int32_t id[LIST / 64];
+  float lp[LIST / 64];
+};
+template <uint32_t LIST>
+__device__ __forceinline__ ListLoads<LIST> load_list(const DistillArgs &a, uint64_t row) {
+  ListLoads<LIST> l;
+#pragma unroll
+  for (uint32_t i = 0; i < LIST / 64; ++i) {
+    const uint32_t t = (threadIdx.x & 63) + 64 * i;
+    const int32_t id = t < a.k ? a.ids[row * a.k + t] : -1;
+    l.id[i] = id >= 0 && uint32_t(id) < a.vocab ? id : -1;
+    l.lp[i] = l.id[i] >= 0 ? a.lp[row * a.k + t] : -INFINITY;
+  }
+  return l;
+}
+template <uint32_t LIST>
+__device__ __forceinline__ void keep_ids(const ListLoads<LIST> &l, ListShared<LIST> &sh) {
+#pragma unroll
+  for (uint32_t i = 0; i < LIST / 64; ++i) sh.ids[(threadIdx.x & 63) + 64 * i] = l.id[i];
+  __builtin_amdgcn_wave_barrier();  // the wave reads them below
+}
+// (sh.ids are there)
+template <typename T, uint32_t LIST>
+__device__ __forceinline__ void read_list(const DistillArgs &a, const T *x, const ListLoads<LIST> &l, ListShared<LIST> &sh) {
+  constexpr uint32_t LIST_EACH = LIST / 64;
+  const uint32_t lane = threadIdx.x & 63;
+  float own[LIST_EACH];
+  double top = -INFINITY;
+  bool some = false;
+#pragma unroll
+  for (uint32_t i = 0; i < LIST_EACH; ++i) {
+    own[i] = l.id[i] >= 0 ? float(x[l.id[i]]) : -INFINITY;
+    some |= l.id[i] >= 0 && (a.tail || l.lp[i] != -INFINITY);
+    top = fmax(top, double(l.lp[i]));
+  }
+  some = __any(some);
+  double c = 0.0, mass = 0.0, rest = 0.0;
+  if (!a.tail) c = wave_max(top);
+#pragma unroll
+  for (uint32_t i = 0; i < LIST_EACH; ++i)
+    if (64 * i < a.k) mass += l.lp[i] == -INFINITY ? 0.0 : exp(double(l.lp[i]) - c);
+  mass = wave_sum(mass);
+  if (a.tail) rest = mass < 1.0 ? 1.0 - mass : mass == mass ? 0.0 : mass;
+  else c += log(mass);
+#pragma unroll
+  for (uint32_t i = 0; i < LIST_EACH; ++i) {
+    if (64 * i >= a.k) continue;
+    const uint32_t t = lane + 64 * i;
+    bool first = l.id[i] >= 0;
+    if (a.tail)
+      for (uint32_t s = 0; s < min(t, a.k); ++s) first &= sh.ids[s] != l.id[i];
+    const double log_q = l.lp[i] == -INFINITY ? -INFINITY : double(l.lp[i]) - c;
+    sh.first[t] = first;
+    sh.log_q[t] = log_q;
+    sh.q[t] = exp(log_q);
+    sh.own[t] = own[i];
+  }
+  if (lane == 0) {
+    sh.mass = mass;
+    sh.rest = rest;
+    sh.log_norm = c;
+    sh.some = some;
+  }
+}
+
+// The end of a row, by the wave that has read the list: p holds the weights of the
+// whole row (with a tail: of the tokens that are not listed).
 //
 // stats: the row's maximum and the logarithm of its sum of weights; the factor
 // of p_j in the gradient, of tokens that are not listed; with a tail the listed
 // ones' factor, without one the logarithm of the teacher's sum.
-template <typename T>
-__device__ __forceinline__ float4 end_row(const DistillArgs &a, uint64_t row, const T *x, Partial p, const int32_t *ids) {
-  constexpr uint32_t E = LIST_MAX / 64;
+template <uint32_t LIST>
+__device__ __forceinline__ float4 end_row(const DistillArgs &a, uint64_t row, Partial p, const ListShared<LIST> &sh) {
   const uint32_t lane = threadIdx.x & 63;
-  const float *lp = a.lp + row * a.k;
-  double teach[E];
-  float own[E];
-  bool first[E];  // of the entries that name this token
-  double top = -INFINITY;
   float high = p.max;
-  bool some = false;
-#pragma unroll
-  for (uint32_t i = 0; i < E; ++i) {
-    teach[i] = -INFINITY;
-    own[i] = -INFINITY;
-    first[i] = false;
-    if (64 * i >= a.k) continue;
-    const uint32_t t = lane + 64 * i;
-    const int32_t id = t < a.k ? ids[t] : -1;
-    if (id >= 0) {
-      own[i] = float(x[id]);
-      teach[i] = double(lp[t]);
-    }
-    some |= id >= 0 && (a.tail || teach[i] != -INFINITY);
-    top = fmax(top, teach[i]);
-    if (a.tail) {
-      high = fmaxf(high, own[i]);
-      first[i] = id >= 0;
-      for (uint32_t s = 0; s < t && s < a.k; ++s) first[i] &= ids[s] != id;
-    }
+  if (a.tail) {
+    for (uint32_t t = lane; t < a.k; t += 64) high = fmaxf(high, sh.own[t]);
+    high = wave_max(high);
   }
-  some = __any(some);
-  // the teacher
-  double c = 0.0, mass = 0.0, rest = 0.0;
-  if (!a.tail) c = top = wave_max(top);
-#pragma unroll
-  for (uint32_t i = 0; i < E; ++i)
-    if (64 * i < a.k) mass += teach[i] == -INFINITY ? 0.0 : exp(teach[i] - c);
-  mass = wave_sum(mass);
-  if (a.tail) rest = mass < 1.0 ? 1.0 - mass : mass == mass ? 0.0 : mass;
-  else c += log(mass);
-  // the student
-  if (a.tail) high = wave_max(high);
   const float ref = finite_max(high);
   double others = double(p.sum), listed = 0.0;
   if (a.tail) {
     if (p.max != -INFINITY) others *= exp((double(p.max) - ref) * a.scale);
-#pragma unroll
-    for (uint32_t i = 0; i < E; ++i)
-      if (64 * i < a.k && first[i]) listed += exp((double(own[i]) - ref) * a.scale);
+    for (uint32_t t = lane; t < a.k; t += 64) listed += sh.first[t] ? exp((double(sh.own[t]) - ref) * a.scale) : 0.0;
     listed = wave_sum(listed);
   }
   const double sum = others + listed, log_sum = log(sum);
   double loss = 0.0;
-#pragma unroll
-  for (uint32_t i = 0; i < E; ++i) {
-    if (64 * i >= a.k || teach[i] == -INFINITY) continue;
-    const double log_q = teach[i] - c, q = exp(log_q);
-    const double log_p = own[i] == -INFINITY ? -INFINITY : (double(own[i]) - ref) * a.scale - log_sum;
-    if (q != 0.0) loss += q * (log_q - log_p);
+  for (uint32_t t = lane; t < a.k; t += 64) {
+    const double log_q = sh.log_q[t], log_p = sh.own[t] == -INFINITY ? -INFINITY : (double(sh.own[t]) - ref) * a.scale - log_sum;
+    if (sh.q[t] != 0.0) loss += sh.q[t] * (log_q - log_p);
   }
   loss = wave_sum(loss);
+  const double rest = sh.rest, mass = sh.mass;
   double ratio = 0.0;
   if (rest > 0.0) {
     // log p_r = -log(1 + listed / others): of the ratio, not of two logarithms
@@ -125,7 +163,7 @@ __device__ __forceinline__ float4 end_row(const DistillArgs &a, uint64_t row, co
   const bool none = high == -INFINITY && sum == 0.0, bad = !(sum == sum) || high == INFINITY;
   const float nan = __uint_as_float(0x7FC00000u);
   float4 st = make_float4(high, float(log_sum), 0.0f, 0.0f);
-  if (!some) {  // no teacher: no loss and no gradient, whatever the row holds
+  if (!sh.some) {  // no teacher: no loss and no gradient, whatever the row holds
     loss = 0.0;
     st.x = -INFINITY;
   } else if (bad) {
@@ -140,7 +178,7 @@ __device__ __forceinline__ float4 end_row(const DistillArgs &a, uint64_t row, co
     st.w = float(mass + rest);
   } else {
     st.z = 1.0f;
-    st.w = float(c);
+    st.w = float(sh.log_norm);
   }
   if (lane == 0) {
     a.loss[row] = float(loss);
@@ -153,182 +191,234 @@ __device__ __forceinline__ float4 end_row(const DistillArgs &a, uint64_t row, co
 // Tokens by which bits of the list are set at a time, 16 or (float32) 32 steps.
 template <uint32_t WAVES> constexpr uint32_t BITS = 64 * WAVES * ROW_UNROLL * 8 * 16;
 
-template <uint32_t WAVES, bool TAIL> struct DistillShared {
+template <uint32_t WAVES, bool TAIL, uint32_t LIST> struct DistillShared {
   Partial sums[WAVES];
-  int32_t ids[LIST_MAX];  // the row's list, -1 where an entry names no token
-  float q[LIST_MAX];
+  ListShared<LIST> list;
   uint32_t bits[TAIL ? BITS<WAVES> / 32 : 1];
   float4 stats;
 };
 
-// The list to LDS, without a barrier.
-template <uint32_t WAVES>
-__device__ __forceinline__ void load_list(const DistillArgs &a, uint64_t row, int32_t *ids) {
-  for (uint32_t t = threadIdx.x; t < a.k; t += 64 * WAVES) {
-    const int32_t id = a.ids[row * a.k + t];
-    ids[t] = id >= 0 && uint32_t(id) < a.vocab ? id : -1;
+// Sets the bits of listed tokens among `pieces` pieces from `first` on.
+template <typename T, uint32_t WAVES, bool TAIL, uint32_t LIST>
+__device__ __forceinline__ void set_bits(const DistillArgs &a, const Row<const T> &r, uint32_t first, uint32_t pieces,
+                                         DistillShared<WAVES, TAIL, LIST> &sh) {
+  constexpr uint32_t THREADS = 64 * WAVES;
+  const uint32_t tid = threadIdx.x, from = first * Piece<T>::N, words = (pieces * Piece<T>::N + 31) / 32;
+  __syncthreads();
+  for (uint32_t w = tid; w < words; w += THREADS) sh.bits[w] = 0;
+  __syncthreads();
+  for (uint32_t t = tid; t < a.k; t += THREADS) {
+    const uint32_t place = sh.list.ids[t] >= 0 ? r.lead + uint32_t(sh.list.ids[t]) - from : ~0u;
+    if (place < words * 32) atomicOr(&sh.bits[place / 32], 1u << place % 32);
   }
+  __syncthreads();
 }
 
-// The weights of pieces [first, last) of a row; with a tail, of tokens that are
-// not listed.
-template <typename T, uint32_t WAVES, bool TAIL>
-__device__ __forceinline__ Partial sum_pieces(const DistillArgs &a, const Row<const T> &r, uint32_t first, uint32_t last,
-                                              DistillShared<WAVES, TAIL> &sh) {
+// Adds a step's pieces to s; with a tail, their tokens that are not listed.  at:
+// the thread's first piece, counted from where the bits begin.
+template <typename T, uint32_t WAVES, bool TAIL, uint32_t LIST>
+__device__ __forceinline__ void add_step(const DistillArgs &a, const typename Piece<T>::raw *raw, uint32_t at, DistillShared<WAVES, TAIL, LIST> &sh,
+                                         Partial &s) {
   typedef Piece<T> P;
+  typename P::val v[ROW_UNROLL];
+  float m = -INFINITY;
+#pragma unroll
+  for (uint32_t u = 0; u < ROW_UNROLL; ++u) {
+    v[u] = values<T>(raw[u]);
+    if (TAIL) {
+      const uint32_t place = (at + u * 64 * WAVES) * P::N;  // (past the row: of old bits, and nothing to mask)
+      const uint32_t mask = sh.bits[place / 32] >> place % 32 & ((1u << P::N) - 1);
+      if (__any(mask)) {
+#pragma unroll
+        for (uint32_t e = 0; e < P::N; ++e) v[u][e] = mask >> e & 1 ? -INFINITY : v[u][e];
+      }
+    }
+#pragma unroll
+    for (uint32_t e = 0; e < P::N; ++e) m = fmaxf(m, v[u][e]);
+  }
+  if (m > s.max) {
+    s.sum = s.max == -INFINITY ? s.sum : relative(s, m, a.c).sum;
+    s.max = m;
+  }
+  const float ref = finite_max(s.max);
+#pragma unroll
+  for (uint32_t u = 0; u < ROW_UNROLL; ++u)
+#pragma unroll
+    for (uint32_t e = 0; e < P::N; ++e) s.sum += __builtin_amdgcn_exp2f((v[u][e] - ref) * a.c);
+}
+
+// Adds pieces [first, last) of a row to s; with a tail, their tokens that are not
+// listed.
+template <typename T, uint32_t WAVES, bool TAIL, uint32_t LIST>
+__device__ __forceinline__ void add_pieces(const DistillArgs &a, const Row<const T> &r, uint32_t first, uint32_t last,
+                                           DistillShared<WAVES, TAIL, LIST> &sh, Partial &s) {
   constexpr uint32_t THREADS = 64 * WAVES, STEP = THREADS * ROW_UNROLL;
-  constexpr uint32_t STRETCH = BITS<WAVES> / P::N;  // pieces between two settings of the bits
-  const uint32_t tid = threadIdx.x;
-  last = min(last, r.pieces());
-  Partial s{-INFINITY, 0.0f, 0.0f};
-  float ref = 0.0f;
+  constexpr uint32_t STRETCH = BITS<WAVES> / Piece<T>::N;  // pieces between two settings of the bits
   for (uint32_t p0 = first; p0 < last; p0 += STEP) {
-    if (TAIL && (p0 - first) % STRETCH == 0) {
-      const uint32_t from = p0 * P::N, words = (min(last - p0, STRETCH) * P::N + 31) / 32;
-      __syncthreads();
-      for (uint32_t w = tid; w < words; w += THREADS) sh.bits[w] = 0;
-      __syncthreads();
-      for (uint32_t t = tid; t < a.k; t += THREADS) {
-        const uint32_t place = sh.ids[t] >= 0 ? r.lead + uint32_t(sh.ids[t]) - from : ~0u;
-        if (place < words * 32) atomicOr(&sh.bits[place / 32], 1u << place % 32);
-      }
-      __syncthreads();
-    }
-    typename P::raw raw[ROW_UNROLL];
-    r.template load_step<THREADS>(raw, r.at, p0 + tid, last);
-    typename P::val v[ROW_UNROLL];
-    float m = -INFINITY;
-#pragma unroll
-    for (uint32_t u = 0; u < ROW_UNROLL; ++u) {
-      v[u] = values<T>(raw[u]);
-      if (TAIL) {
-        const uint32_t place = ((p0 - first) % STRETCH + u * THREADS + tid) * P::N;  // (past `last`: of old bits, and nothing to mask)
-        const uint32_t mask = sh.bits[place / 32] >> place % 32 & ((1u << P::N) - 1);
-        if (__any(mask)) {
-#pragma unroll
-          for (uint32_t e = 0; e < P::N; ++e) v[u][e] = mask >> e & 1 ? -INFINITY : v[u][e];
-        }
-      }
-#pragma unroll
-      for (uint32_t e = 0; e < P::N; ++e) m = fmaxf(m, v[u][e]);
-    }
-    if (m > s.max) {
-      s.sum = s.max == -INFINITY ? s.sum : relative(s, m, a.c).sum;
-      ref = s.max = m;
-    }
-#pragma unroll
-    for (uint32_t u = 0; u < ROW_UNROLL; ++u)
-#pragma unroll
-      for (uint32_t e = 0; e < P::N; ++e) s.sum += __builtin_amdgcn_exp2f((v[u][e] - ref) * a.c);
-  }
-  return row_partial<WAVES>(s, a.c, sh.sums);  // (with a barrier, for the list too)
-}
-
-// The gradient of pieces [from, to) of a row as they are written, from its stats
-// and list in LDS.  The listed tokens are written once more when the part is
-// done, from what was there before (dx may be x): each by one thread, or by
-// several with the same value.
-template <typename T, uint32_t WAVES>
-__device__ __forceinline__ void grad_pieces(const DistillArgs &a, uint64_t row, const T *x, const Row<T> &r, uint32_t from, uint32_t to, float4 st,
-                                            const int32_t *ids, float *q) {
-  typedef Piece<T> P;
-  constexpr uint32_t THREADS = 64 * WAVES, STEP = THREADS * ROW_UNROLL, TERMS = (LIST_MAX + THREADS - 1) / THREADS;
-  const uint32_t tid = threadIdx.x;
-  const float g = a.grad[row] * a.scale;
-  const bool zero = st.x == -INFINITY || g == 0.0f;
-  const float inv = __builtin_amdgcn_exp2f(-st.y * LOG2E);
-  const auto weight = [&](float v) { return __builtin_amdgcn_exp2f((v - st.x) * a.c); };
-  float before[TERMS];
-  bool mine[TERMS];
-#pragma unroll
-  for (uint32_t i = 0; i < TERMS; ++i) {
-    const uint32_t t = tid + i * THREADS;
-    mine[i] = false;
-    if (t >= a.k) continue;
-    const int32_t id = ids[t];
-    q[t] = id >= 0 ? __builtin_amdgcn_exp2f((a.lp[row * a.k + t] - (a.tail ? 0.0f : st.w)) * LOG2E) : 0.0f;
-    mine[i] = id >= 0 && !zero && (r.lead + uint32_t(id)) / P::N - from < to - from;
-    if (mine[i]) before[i] = float(x[id]);
-  }
-  __syncthreads();
-  const float all = g * st.z * inv;
-  for (uint32_t p0 = from; p0 < to; p0 += STEP) {
-    typename P::raw raw[ROW_UNROLL];
-    if (!zero) r.template load_step<THREADS>(raw, x - r.lead, p0 + tid, to);
-#pragma unroll
-    for (uint32_t u = 0; u < ROW_UNROLL; ++u) {
-      const uint32_t p = p0 + u * THREADS + tid;
-      if (p >= to) break;
-      typename P::val v = 0.0f;
-      if (!zero) {
-        v = values<T>(raw[u]);
-#pragma unroll
-        for (uint32_t e = 0; e < P::N; ++e) v[e] = weight(v[e]) * all;
-      }
-      r.store(p, v);
-    }
-  }
-  __syncthreads();
-#pragma unroll
-  for (uint32_t i = 0; i < TERMS; ++i) {
-    if (!mine[i]) continue;
-    const int32_t id = ids[tid + i * THREADS];
-    float sum = 0.0f;
-    for (uint32_t t = 0; t < a.k; ++t) sum += ids[t] == id ? q[t] : 0.0f;
-    r.at[r.lead + uint32_t(id)] = T(g * ((a.tail ? st.w : st.z) * inv * weight(before[i]) - sum));
+    if (TAIL && (p0 - first) % STRETCH == 0) set_bits<T>(a, r, p0, min(last - p0, STRETCH), sh);
+    typename Piece<T>::raw raw[ROW_UNROLL];
+    r.template load_step<THREADS>(raw, r.at, p0 + threadIdx.x, last);
+    add_step<T>(a, raw, (p0 - first) % STRETCH + threadIdx.x, sh, s);
   }
 }
 
-// A workgroup a row or, SPLIT, a part of one.  GRAD: the gradient too, the row
-// read again while it is near.
-template <typename T, uint32_t WAVES, bool TAIL, bool SPLIT, bool GRAD>
+// The gradient of a row from its stats.
+template <typename T, uint32_t WAVES> struct Gradient {
+  static constexpr uint32_t THREADS = 64 * WAVES;
+  float4 st;
+  float g, inv, c;
+  bool zero;
+
+  __device__ __forceinline__ Gradient(const DistillArgs &a, float4 stats, float grad) : st(stats), g(grad * a.scale), c(a.c) {
+    zero = st.x == -INFINITY || g == 0.0f;
+    inv = __builtin_amdgcn_exp2f(-st.y * LOG2E);
+  }
+  __device__ __forceinline__ float weight(float v) const { return __builtin_amdgcn_exp2f((v - st.x) * c); }
+  __device__ __forceinline__ typename Piece<T>::val of(typename Piece<T>::raw raw) const {
+    typename Piece<T>::val v = 0.0f;
+    if (zero) return v;
+    const float all = g * st.z * inv;
+    v = values<T>(raw);
+#pragma unroll
+    for (uint32_t e = 0; e < Piece<T>::N; ++e) v[e] = weight(v[e]) * all;
+    return v;
+  }
+  // Pieces [from, to), as out has them.
+  __device__ __forceinline__ void pieces(const T *x, const Row<T> &out, uint32_t from, uint32_t to) const {
+    for (uint32_t p0 = from; p0 < to; p0 += THREADS * ROW_UNROLL) {
+      typename Piece<T>::raw raw[ROW_UNROLL];
+      if (!zero) out.template load_step<THREADS>(raw, x - out.lead, p0 + threadIdx.x, to);
+#pragma unroll
+      for (uint32_t u = 0; u < ROW_UNROLL; ++u) {
+        const uint32_t p = p0 + u * THREADS + threadIdx.x;
+        if (p < to) out.store(p, of(raw[u]));
+      }
+    }
+  }
+  // The listed tokens among pieces [from, to), written once more when those are (a
+  // barrier apart) from what was there before (dx may be x): each by one thread,
+  // or by several with the same value.
+  template <typename Q>
+  __device__ __forceinline__ void listed(const DistillArgs &a, const Row<T> &out, uint32_t from, uint32_t to, const int32_t *ids, const float *own,
+                                         const Q *q) const {
+    if (zero) return;
+    for (uint32_t t = threadIdx.x; t < a.k; t += THREADS) {
+      const int32_t id = ids[t];
+      const uint32_t place = out.lead + uint32_t(id);
+      if (id < 0 || place / Piece<T>::N - from >= to - from) continue;
+      float sum = 0.0f;
+      for (uint32_t i = 0; i < a.k; ++i) sum += ids[i] == id ? float(q[i]) : 0.0f;
+      out.at[place] = T(g * ((a.tail ? st.w : st.z) * inv * weight(own[t]) - sum));
+    }
+  }
+};
+
+// The loss: a workgroup a row or, SPLIT, a part of one.
+template <typename T, uint32_t WAVES, bool TAIL, bool SPLIT, uint32_t LIST>
 __global__ __launch_bounds__(64 * WAVES) void k_distill(DistillArgs a) {
-  __shared__ DistillShared<WAVES, TAIL> sh;
+  __shared__ DistillShared<WAVES, TAIL, LIST> sh;
   const uint64_t block = a.block0 + blockIdx.x, row = SPLIT ? block / a.parts : block;
-  const uint32_t first = SPLIT ? uint32_t(block % a.parts) * a.part : 0;
   const T *x = static_cast<const T *>(a.x) + int64_t(row) * a.stride;
-  if (TAIL || !SPLIT) load_list<WAVES>(a, row, sh.ids);
-  const Partial s = sum_pieces<T, WAVES, TAIL>(a, Row<const T>(x, a.vocab), first, SPLIT ? first + a.part : ~0u, sh);
+  const Row<const T> r(x, a.vocab);
+  const uint32_t first = SPLIT ? uint32_t(block % a.parts) * a.part : 0;
+  if ((TAIL || !SPLIT) && threadIdx.x < 64) {
+    const ListLoads<LIST> l = load_list<LIST>(a, row);
+    keep_ids(l, sh.list);
+    if (!SPLIT) read_list(a, x, l, sh.list);
+  }
+  Partial s{-INFINITY, 0.0f, 0.0f};
+  add_pieces<T>(a, r, first, SPLIT ? min(r.pieces(), first + a.part) : r.pieces(), sh, s);
+  s = row_partial<WAVES>(s, a.c, sh.sums);  // (with a barrier, for the list too)
   if (SPLIT) {
     if (threadIdx.x == 0) a.parted[block] = s;
-    return;
+  } else if (threadIdx.x < 64) {
+    end_row(a, row, s, sh.list);
   }
-  if (threadIdx.x < 64) {
-    const float4 st = end_row<T>(a, row, x, s, sh.ids);
-    if (GRAD && threadIdx.x == 0) sh.stats = st;
+}
+
+// Loss and gradient of a row by a workgroup.  A thread's first HELD pieces stay in
+// its registers between the two; what a row has besides is read again.
+template <typename T, uint32_t WAVES, bool TAIL, uint32_t LIST>
+__global__ __launch_bounds__(64 * WAVES, 4) void k_distill_step(DistillArgs a) {
+  constexpr uint32_t THREADS = 64 * WAVES, STEP = THREADS * ROW_UNROLL;
+  static_assert(HELD % ROW_UNROLL == 0 && THREADS * HELD * Piece<T>::N <= BITS<WAVES>, "");
+  __shared__ DistillShared<WAVES, TAIL, LIST> sh;
+  const uint64_t row = a.block0 + blockIdx.x;
+  const T *x = static_cast<const T *>(a.x) + int64_t(row) * a.stride;
+  T *dx = static_cast<T *>(a.dx) + int64_t(row) * a.dx_stride;
+  const Row<const T> r(x, a.vocab);
+  const uint32_t tid = threadIdx.x, pieces = r.pieces(), held = min(pieces, THREADS * HELD);
+  const float weight = a.grad[row];
+  ListLoads<LIST> l;
+  if (tid < 64) l = load_list<LIST>(a, row);
+  typename Piece<T>::raw raw[HELD / ROW_UNROLL][ROW_UNROLL];
+#pragma unroll
+  for (uint32_t i = 0; i < HELD / ROW_UNROLL; ++i) r.template load_step<THREADS>(raw[i], r.at, i * STEP + tid, held);
+  if (tid < 64) keep_ids(l, sh.list);
+  if (TAIL) set_bits<T>(a, r, 0, held, sh);
+  if (tid < 64) read_list(a, x, l, sh.list);
+  Partial s{-INFINITY, 0.0f, 0.0f};
+#pragma unroll
+  for (uint32_t i = 0; i < HELD / ROW_UNROLL; ++i)
+    if (i * STEP < held) add_step<T>(a, raw[i], i * STEP + tid, sh, s);
+  add_pieces<T>(a, r, held, pieces, sh, s);
+  s = row_partial<WAVES>(s, a.c, sh.sums);
+  if (tid < 64) {
+    const float4 st = end_row(a, row, s, sh.list);
+    if (tid == 0) sh.stats = st;
   }
-  if (!GRAD) return;
   __syncthreads();
-  const Row<T> r(static_cast<T *>(a.dx) + int64_t(row) * a.dx_stride, a.vocab);
-  grad_pieces<T, WAVES>(a, row, x, r, 0, r.pieces(), sh.stats, sh.ids, sh.q);
+  const Gradient<T, WAVES> grad(a, sh.stats, weight);
+  const Row<T> out = r.over(dx);
+#pragma unroll
+  for (uint32_t i = 0; i < HELD; ++i) {
+    const uint32_t p = i * THREADS + tid;
+    if (p < held) out.store(p, grad.of(raw[i / ROW_UNROLL][i % ROW_UNROLL]));
+  }
+  grad.pieces(x, out, held, pieces);
+  __syncthreads();
+  grad.listed(a, out, 0, pieces, sh.list.ids, sh.list.own, sh.list.q);
 }
 
 // Joins a row's parts.
 template <typename T>
 __global__ __launch_bounds__(64) void k_distill_join(DistillArgs a) {
-  __shared__ int32_t ids[LIST_MAX];
+  __shared__ ListShared<LIST_MAX> sh;
   const uint64_t row = a.block0 + blockIdx.x;
-  const T *x = static_cast<const T *>(a.x) + int64_t(row) * a.stride;
-  load_list<1>(a, row, ids);
   Partial p{-INFINITY, 0.0f, 0.0f};
   if (threadIdx.x < a.parts) p = a.parted[row * a.parts + threadIdx.x];
+  const ListLoads<LIST_MAX> l = load_list<LIST_MAX>(a, row);
+  keep_ids(l, sh);
+  __syncthreads();
+  read_list(a, static_cast<const T *>(a.x) + int64_t(row) * a.stride, l, sh);
   p = wave_partial(p, a.c);
   __syncthreads();
-  end_row<T>(a, row, x, p, ids);
+  end_row(a, row, p, sh);
 }
 
 // The gradient by itself: a workgroup a part of a row.
 template <typename T, uint32_t WAVES>
 __global__ __launch_bounds__(64 * WAVES) void k_distill_back(DistillArgs a) {
+  constexpr uint32_t THREADS = 64 * WAVES;
   __shared__ int32_t ids[LIST_MAX];
-  __shared__ float q[LIST_MAX];
+  __shared__ float own[LIST_MAX], q[LIST_MAX];
   const uint64_t block = a.block0 + blockIdx.x, row = block / a.parts;
+  const T *x = static_cast<const T *>(a.x) + int64_t(row) * a.stride;
   const Row<T> r(static_cast<T *>(a.dx) + int64_t(row) * a.dx_stride, a.vocab);
   const uint32_t from = uint32_t(block % a.parts) * a.part, to = min(r.pieces(), from + a.part);
   if (from >= to) return;  // (parts are counted for rows that begin anywhere)
-  load_list<WAVES>(a, row, ids);
-  // (every thread reads back the entries that it has written itself, until the barrier)
-  grad_pieces<T, WAVES>(a, row, static_cast<const T *>(a.x) + int64_t(row) * a.stride, r, from, to, a.stats[row], ids, q);
+  const Gradient<T, WAVES> grad(a, a.stats[row], a.grad[row]);
+  for (uint32_t t = threadIdx.x; t < a.k; t += THREADS) {
+    const int32_t id = a.ids[row * a.k + t];
+    const bool there = id >= 0 && uint32_t(id) < a.vocab;
+    ids[t] = there ? id : -1;
+    q[t] = there ? __builtin_amdgcn_exp2f((a.lp[row * a.k + t] - (a.tail ? 0.0f : grad.st.w)) * LOG2E) : 0.0f;
+    own[t] = there && (r.lead + uint32_t(id)) / Piece<T>::N - from < to - from ? float(x[id]) : 0.0f;
+  }
+  __syncthreads();
+  grad.pieces(x, r, from, to);
+  __syncthreads();
+  grad.listed(a, r, from, to, ids, own, q);
 }
 
 int check(int dtype, const void *logits, int64_t row_stride, uint64_t n_rows, uint32_t vocab, const int32_t *ids, const float *lp,
@@ -381,7 +471,8 @@ extern "C" {
 
 int bbpe_distill_loss_workspace_bytes(int dtype, uint64_t n_rows, uint32_t vocab, uint64_t *out_bytes) {
   if (!out_bytes || bad_sizes(dtype, n_rows, vocab)) return BBPE_E_INVALID_ARG;
-  *out_bytes = parted_bytes(cut_rows(dtype, n_rows, vocab, true, PARTS_MAX), n_rows);
+  // (a list's length decides whether short rows go to waves: the larger of both)
+  *out_bytes = parted_bytes(cut_rows(dtype, n_rows, vocab, false, PARTS_MAX), n_rows);
   return BBPE_OK;
 }
 
@@ -414,7 +505,7 @@ int bbpe_distill_loss(int dtype, const void *logits, int64_t row_stride, uint64_
       (d_logits && bad_logits(dtype, d_logits, dl_stride, n_rows, vocab, true)))
     return BBPE_E_INVALID_ARG;
   if (n_rows == 0) return BBPE_OK;
-  const Cut cut = cut_rows(dtype, n_rows, vocab, true, PARTS_MAX);
+  const Cut cut = cut_rows(dtype, n_rows, vocab, top_k <= 64, PARTS_MAX);
   const uint64_t need = parted_bytes(cut, n_rows);
   if (need && (!d_workspace || (address(d_workspace) & 255) || workspace_bytes < need)) return BBPE_E_WORKSPACE;
   DistillArgs a = args_of(logits, row_stride, vocab, d_top_ids, d_top_logprobs, top_k, tail, scale);
@@ -432,24 +523,28 @@ int bbpe_distill_loss(int dtype, const void *logits, int64_t row_stride, uint64_
     for (a.block0 = 0; a.block0 < blocks; a.block0 += MAX_GROUPS)
       kernel<<<uint32_t(std::min(blocks - a.block0, MAX_GROUPS)), threads, 0, st>>>(a);
   };
-  const bool grad = d_logits != nullptr;
+  const uint32_t pieces = most_pieces(dtype, vocab);
+  const bool whole = d_logits && (n_rows >= STEP_ROWS || cut.parts == 1);  // loss and gradient of a row by one workgroup
   with_element(dtype, [&](auto t) {
     typedef decltype(t) T;
-    constexpr uint32_t W = ROW_WAVES;
-    if (cut.parts > 1) {
-      launch(n_rows * cut.parts, tail ? k_distill<T, W, true, true, false> : k_distill<T, W, false, true, false>, ROW_THREADS);
+    const auto by_tail = [&](uint64_t blocks, uint32_t threads, auto without, auto with) { launch(blocks, tail ? with : without, threads); };
+    constexpr uint32_t W = ROW_WAVES, L = LIST_MAX;
+    if (whole) {
+      if (pieces <= 64 * HELD && top_k <= 64) by_tail(n_rows, 64, k_distill_step<T, 1, false, 64>, k_distill_step<T, 1, true, 64>);
+      else if (pieces <= 256 * HELD) by_tail(n_rows, 256, k_distill_step<T, 4, false, L>, k_distill_step<T, 4, true, L>);
+      else if (pieces <= STEP_MOST) by_tail(n_rows, 512, k_distill_step<T, 8, false, L>, k_distill_step<T, 8, true, L>);
+      else by_tail(n_rows, 1024, k_distill_step<T, 16, false, L>, k_distill_step<T, 16, true, L>);
+    } else if (cut.parts > 1) {
+      by_tail(n_rows * cut.parts, ROW_THREADS, k_distill<T, W, false, true, L>, k_distill<T, W, true, true, L>);
       launch(n_rows, k_distill_join<T>, 64);
     } else if (cut.waves == 1) {
-      if (grad) launch(n_rows, tail ? k_distill<T, 1, true, false, true> : k_distill<T, 1, false, false, true>, 64);
-      else launch(n_rows, tail ? k_distill<T, 1, true, false, false> : k_distill<T, 1, false, false, false>, 64);
-    } else if (grad) {
-      launch(n_rows, tail ? k_distill<T, STEP_WAVES, true, false, true> : k_distill<T, STEP_WAVES, false, false, true>, 64 * STEP_WAVES);
+      by_tail(n_rows, 64, k_distill<T, 1, false, false, 64>, k_distill<T, 1, true, false, 64>);
     } else {
-      launch(n_rows, tail ? k_distill<T, W, true, false, false> : k_distill<T, W, false, false, false>, ROW_THREADS);
+      by_tail(n_rows, ROW_THREADS, k_distill<T, W, false, false, L>, k_distill<T, W, true, false, L>);
     }
   });
   if (hipGetLastError() != hipSuccess) return BBPE_E_HIP;
-  if (grad && cut.parts > 1) launch_back(a, dtype, n_rows, st);
+  if (d_logits && !whole) launch_back(a, dtype, n_rows, st);
   return hipGetLastError() == hipSuccess ? BBPE_OK : BBPE_E_HIP;
 }
 

@@ -41,6 +41,14 @@ template <typename C> struct Row {
     at = x - lead;
     end = lead + vocab;
   }
+  // The same pieces in another matrix, where they may begin at any element.
+  template <typename D> __device__ __forceinline__ Row<D> over(D *y) const {
+    Row<D> o(y, 0);
+    o.at = y - lead;
+    o.lead = lead;
+    o.end = end;
+    return o;
+  }
   __device__ __forceinline__ uint32_t pieces() const { return (end + N - 1) / N; }
   __device__ __forceinline__ bool whole(uint32_t p) const { return p * N >= lead && p * N + N <= end; }
   // Piece p, from `from` (place 0 of a row that may lie otherwise in memory);
@@ -72,7 +80,7 @@ template <typename C> struct Row {
   __device__ __forceinline__ void store(uint32_t p, typename Piece<T>::val f) const {
     const typename Piece<T>::vec v = __builtin_convertvector(f, typename Piece<T>::vec);  // to nearest even
     if (whole(p)) {
-      *reinterpret_cast<typename Piece<T>::raw *>(at + p * N) = __builtin_bit_cast(typename Piece<T>::raw, v);
+      *reinterpret_cast<typename Piece<T>::mem *>(at + p * N) = v;
     } else {
 #pragma unroll
       for (uint32_t e = 0; e < N; ++e)
