@@ -34,7 +34,8 @@ struct DistillArgs {
   int64_t dx_stride;
   uint64_t block0;
   uint32_t vocab, k, tail, parts, part;  // parts of a row, and pieces of one
-  float scale, c;
+  float scale;
+  Exponent x2;
   const int32_t *ids;
   const float *lp;
   float *loss, *lse;
@@ -140,7 +141,7 @@ __device__ __forceinline__ float4 end_row(const DistillArgs &a, uint64_t row, Pa
     high = wave_max(high);
   }
   const float ref = finite_max(high);
-  double others = double(p.sum), listed = 0.0;
+  double others = p.sum, listed = 0.0;
   if (a.tail) {
     if (p.max != -INFINITY) others *= exp((double(p.max) - ref) * a.scale);
     for (uint32_t t = lane; t < a.k; t += 64) listed += sh.first[t] ? exp((double(sh.own[t]) - ref) * a.scale) : 0.0;
@@ -237,14 +238,16 @@ __device__ __forceinline__ void add_step(const DistillArgs &a, const typename Pi
     for (uint32_t e = 0; e < P::N; ++e) m = fmaxf(m, v[u][e]);
   }
   if (m > s.max) {
-    s.sum = s.max == -INFINITY ? s.sum : relative(s, m, a.c).sum;
+    if (s.max != -INFINITY) s.sum *= double(weight_of(s.max - m, a.x2));
     s.max = m;
   }
   const float ref = finite_max(s.max);
+  float sum = 0.0f;
 #pragma unroll
   for (uint32_t u = 0; u < ROW_UNROLL; ++u)
 #pragma unroll
-    for (uint32_t e = 0; e < P::N; ++e) s.sum += __builtin_amdgcn_exp2f((v[u][e] - ref) * a.c);
+    for (uint32_t e = 0; e < P::N; ++e) sum += weight_of(v[u][e] - ref, a.x2);
+  s.sum += double(sum);
 }
 
 // Adds pieces [first, last) of a row to s; with a tail, their tokens that are not
@@ -266,14 +269,15 @@ __device__ __forceinline__ void add_pieces(const DistillArgs &a, const Row<const
 template <typename T, uint32_t WAVES> struct Gradient {
   static constexpr uint32_t THREADS = 64 * WAVES;
   float4 st;
-  float g, inv, c;
+  float g, inv;
+  Exponent x2;
   bool zero;
 
-  __device__ __forceinline__ Gradient(const DistillArgs &a, float4 stats, float grad) : st(stats), g(grad * a.scale), c(a.c) {
+  __device__ __forceinline__ Gradient(const DistillArgs &a, float4 stats, float grad) : st(stats), g(grad * a.scale), x2(a.x2) {
     zero = st.x == -INFINITY || g == 0.0f;
     inv = __builtin_amdgcn_exp2f(-st.y * LOG2E);
   }
-  __device__ __forceinline__ float weight(float v) const { return __builtin_amdgcn_exp2f((v - st.x) * c); }
+  __device__ __forceinline__ float weight(float v) const { return weight_of(v - st.x, x2); }
   __device__ __forceinline__ typename Piece<T>::val of(typename Piece<T>::raw raw) const {
     typename Piece<T>::val v = 0.0f;
     if (zero) return v;
@@ -326,9 +330,9 @@ __global__ __launch_bounds__(64 * WAVES) void k_distill(DistillArgs a) {
     keep_ids(l, sh.list);
     if (!SPLIT) read_list(a, x, l, sh.list);
   }
-  Partial s{-INFINITY, 0.0f, 0.0f};
+  Partial s{0.0, -INFINITY, 0.0f};
   add_pieces<T>(a, r, first, SPLIT ? min(r.pieces(), first + a.part) : r.pieces(), sh, s);
-  s = row_partial<WAVES>(s, a.c, sh.sums);  // (with a barrier, for the list too)
+  s = row_partial<WAVES>(s, a.x2, sh.sums);  // (with a barrier, for the list too)
   if (SPLIT) {
     if (threadIdx.x == 0) a.parted[block] = s;
   } else if (threadIdx.x < 64) {
@@ -357,12 +361,12 @@ __global__ __launch_bounds__(64 * WAVES, 4) void k_distill_step(DistillArgs a) {
   if (tid < 64) keep_ids(l, sh.list);
   if (TAIL) set_bits<T>(a, r, 0, held, sh);
   if (tid < 64) read_list(a, x, l, sh.list);
-  Partial s{-INFINITY, 0.0f, 0.0f};
+  Partial s{0.0, -INFINITY, 0.0f};
 #pragma unroll
   for (uint32_t i = 0; i < HELD / ROW_UNROLL; ++i)
     if (i * STEP < held) add_step<T>(a, raw[i], i * STEP + tid, sh, s);
   add_pieces<T>(a, r, held, pieces, sh, s);
-  s = row_partial<WAVES>(s, a.c, sh.sums);
+  s = row_partial<WAVES>(s, a.x2, sh.sums);
   if (tid < 64) {
     const float4 st = end_row(a, row, s, sh.list);
     if (tid == 0) sh.stats = st;
@@ -385,13 +389,13 @@ template <typename T>
 __global__ __launch_bounds__(64) void k_distill_join(DistillArgs a) {
   __shared__ ListShared<LIST_MAX> sh;
   const uint64_t row = a.block0 + blockIdx.x;
-  Partial p{-INFINITY, 0.0f, 0.0f};
+  Partial p{0.0, -INFINITY, 0.0f};
   if (threadIdx.x < a.parts) p = a.parted[row * a.parts + threadIdx.x];
   const ListLoads<LIST_MAX> l = load_list<LIST_MAX>(a, row);
   keep_ids(l, sh);
   __syncthreads();
   read_list(a, static_cast<const T *>(a.x) + int64_t(row) * a.stride, l, sh);
-  p = wave_partial(p, a.c);
+  p = wave_partial(p, a.x2);
   __syncthreads();
   end_row(a, row, p, sh);
 }
@@ -438,7 +442,7 @@ DistillArgs args_of(const void *logits, int64_t row_stride, uint32_t vocab, cons
   a.k = k;
   a.tail = uint32_t(tail);
   a.scale = scale;
-  a.c = scale * LOG2E;
+  a.x2 = exponent_of(scale);
   a.ids = ids;
   a.lp = lp;
   return a;

@@ -17,6 +17,7 @@ constexpr uint32_t ROW_WAVES = ROW_THREADS / 64;
 constexpr uint32_t ROW_UNROLL = 4;     // pieces of a thread's step
 constexpr uint32_t ROW_STEP = ROW_THREADS * ROW_UNROLL;  // pieces of a workgroup's step
 constexpr float LOG2E = 1.4426950408889634f;
+constexpr double LN2 = 0.69314718055994530942;
 constexpr float LOWEST = -3.4028234663852886e38f;
 
 template <typename T> struct Piece {
@@ -106,39 +107,59 @@ __device__ __forceinline__ V wave_sum(V v) {
   return v;
 }
 
+// scale * log2(e) as two floats, the first rounded down: with one, weights of
+// elements ten units below the largest would be off by a millionth, all the same way.
+struct Exponent {
+  float c, low;  // low > 0, so that minus infinity stays that
+};
+inline Exponent exponent_of(float scale) {
+  const double e = double(scale) * 1.4426950408889634074;
+  Exponent x{float(e), 0.0f};
+  if (double(x.c) > e) x.c = nextafterf(x.c, 0.0f);
+  x.low = fmaxf(float(e - double(x.c)), 1.17549435e-38f);
+  return x;
+}
+// exp(scale * d), d up to 0
+__device__ __forceinline__ float weight_of(float d, Exponent x) { return __builtin_amdgcn_exp2f(__builtin_fmaf(d, x.low, d * x.c)); }
+
 // Part of a row's softmax: the largest element so far, and relative to it the
 // sum of weights exp(scale * (x - max)) and of weights times (x - max).  No
 // element yet, or only minus infinity: max is that, the sums are 0.  A NaN or
-// plus infinity anywhere makes the sum of weights NaN.
+// plus infinity anywhere makes the sum of weights NaN.  Threads add a step's 32
+// weights in 32 bits and the steps in 64: sums of 100,000 in 32 bits are off by
+// as much as a loss near 0 is worth.
 struct Partial {
-  float max, sum, mean;
+  double sum;
+  float max, mean;
 };
 __device__ __forceinline__ float finite_max(float m) { return m == -INFINITY ? 0.0f : m; }
-// p relative to `max`, which is p.max or above; c = scale * log2(e)
-__device__ __forceinline__ Partial relative(Partial p, float max, float c) {
+// p relative to `max`, which is p.max or above, by the factor f = weight of the distance
+__device__ __forceinline__ Partial scaled(Partial p, float max, float d, float f) {
+  return Partial{p.sum * double(f), max, f == 0.0f ? 0.0f : f * (p.mean + float(p.sum) * d)};  // (0 times minus infinity is to be 0)
+}
+__device__ __forceinline__ Partial relative(Partial p, float max, Exponent x) {
   const float d = p.max - finite_max(max);  // -inf where p has nothing
-  const float f = __builtin_amdgcn_exp2f(d * c);
-  return Partial{max, p.sum * f, f == 0.0f ? 0.0f : f * (p.mean + p.sum * d)};  // (0 times minus infinity is to be 0)
+  return scaled(p, max, d, weight_of(d, x));
 }
 // The wave's, and the workgroup's of WAVES waves (sh: room for them), in every thread.
-__device__ __forceinline__ Partial wave_partial(Partial p, float c) {
-  p = relative(p, wave_max(p.max), c);
+__device__ __forceinline__ Partial wave_partial(Partial p, Exponent x) {
+  p = relative(p, wave_max(p.max), x);
   p.sum = wave_sum(p.sum);
   p.mean = wave_sum(p.mean);
   return p;
 }
 template <uint32_t WAVES>
-__device__ __forceinline__ Partial row_partial(Partial p, float c, Partial *sh) {
-  p = wave_partial(p, c);
+__device__ __forceinline__ Partial row_partial(Partial p, Exponent x, Partial *sh) {
+  p = wave_partial(p, x);
   if ((threadIdx.x & 63) == 0) sh[threadIdx.x >> 6] = p;
   __syncthreads();
   float m = sh[0].max;
 #pragma unroll
   for (uint32_t w = 1; w < WAVES; ++w) m = fmaxf(m, sh[w].max);
-  Partial all{m, 0.0f, 0.0f};
+  Partial all{0.0, m, 0.0f};
 #pragma unroll
   for (uint32_t w = 0; w < WAVES; ++w) {
-    const Partial q = relative(sh[w], m, c);
+    const Partial q = relative(sh[w], m, x);
     all.sum += q.sum;
     all.mean += q.mean;
   }

@@ -38,7 +38,8 @@ struct ScoreArgs {
   int64_t stride;
   uint64_t block0;
   uint32_t vocab, k, parts, part;  // parts of a row, and pieces of one
-  float scale, c;
+  float scale;
+  Exponent x2;
   uint32_t index_bits;  // of a place in the row
   const int32_t *ids;
   float *logprobs, *entropy, *lse;
@@ -164,9 +165,9 @@ struct RowEnd {
   double log_sum;
 
   __device__ __forceinline__ explicit RowEnd(Partial s) : p(s) {
-    none = s.max == -INFINITY && s.sum == 0.0f;
+    none = s.max == -INFINITY && s.sum == 0.0;
     bad = !(s.sum == s.sum) || s.max == INFINITY;
-    log_sum = none ? -INFINITY : double(logf(s.sum));
+    log_sum = none ? -INFINITY : log(s.sum);
   }
   __device__ __forceinline__ float logprob(float v, float scale) const {
     return bad ? __uint_as_float(0x7FC00000u) : none ? -INFINITY : float((double(v) - p.max) * scale - log_sum);
@@ -257,7 +258,7 @@ __device__ __forceinline__ void score_pieces(const ScoreArgs &a, uint64_t row, u
   const float at_least = given.there ? next_below(given.value) : INFINITY;
   const int32_t beside = WHOLE && given.there ? given.equal_before(r) : 0;
 
-  Partial s{-INFINITY, 0.0f, 0.0f};
+  Partial s{0.0, -INFINITY, 0.0f};
   float ref = 0.0f;
   uint32_t above = 0;  // the wave's
   float best[ROW_UNROLL], second[ROW_UNROLL], third[ROW_UNROLL];
@@ -292,21 +293,26 @@ __device__ __forceinline__ void score_pieces(const ScoreArgs &a, uint64_t row, u
       m = fmaxf(m, pm);
     }
     if (m > s.max) {
-      s = s.max == -INFINITY ? Partial{m, s.sum, 0.0f} : relative(s, m, a.c);
+      const float d = s.max - m;
+      s = s.max == -INFINITY ? Partial{s.sum, m, 0.0f} : scaled(s, m, d, __builtin_amdgcn_exp2f(d * a.x2.c));
       ref = m;
     }
+    float sum = 0.0f;
 #pragma unroll
     for (uint32_t u = 0; u < ROW_UNROLL; ++u) {
       const float bar = p0 + u * THREADS + tid < before_id ? at_least : given.value;
 #pragma unroll
       for (uint32_t e = 0; e < P::N; ++e) {
-        const float d = v[u][e] - ref, w = __builtin_amdgcn_exp2f(d * a.c);
-        s.sum += w;
+        const float d = v[u][e] - ref, w = __builtin_amdgcn_exp2f(d * a.x2.c);
+        sum += w;
         s.mean += w * fmaxf(d, LOWEST);  // (0 times minus infinity is to be 0)
         above += uint32_t(__popcll(__ballot(!(v[u][e] <= bar))));
       }
     }
+    s.sum += double(sum);
   }
+  // (the exponent's second part, to first order: each weight times LN2 * low * (x - max))
+  s.sum += LN2 * double(a.x2.low) * double(s.mean);
   if ((tid & 63) == 0) sh.above[tid >> 6] = above;
   if (TOP) {
 #pragma unroll
@@ -317,7 +323,7 @@ __device__ __forceinline__ void score_pieces(const ScoreArgs &a, uint64_t row, u
     }
     if (tid == 0) sh.n_chosen = sh.n_deep = sh.n_found = 0;
   }
-  const RowEnd end(row_partial<WAVES>(s, a.c, sh.sums));  // (with a barrier)
+  const RowEnd end(row_partial<WAVES>(s, a.x2, sh.sums));  // (with a barrier)
   if (tid == THREADS - 1) {  // (the first wave has the bar to find)
     above = 0;
     for (uint32_t w = 0; w < WAVES; ++w) above += sh.above[w];
@@ -465,9 +471,9 @@ __global__ __launch_bounds__(TOP ? ROW_THREADS : 64) void k_scores_join(ScoreArg
   const uint32_t tid = threadIdx.x, lane = tid & 63;
   const uint64_t row = a.block0 + blockIdx.x;
   const Row<const T> r(static_cast<const T *>(a.x) + int64_t(row) * a.stride, a.vocab);
-  ScorePart part{Partial{-INFINITY, 0.0f, 0.0f}, 0};
+  ScorePart part{Partial{0.0, -INFINITY, 0.0f}, 0};
   if (lane < a.parts) part = a.parted[row * a.parts + lane];
-  const RowEnd end(wave_partial(part.p, a.c));
+  const RowEnd end(wave_partial(part.p, a.x2));
   const uint32_t above = wave_sum(part.above);
   const int32_t id = a.ids[row];
   const Given<T> given(a, r, id);
@@ -500,7 +506,8 @@ struct ScoreBackArgs {
   int64_t dx_stride;
   uint64_t block0;
   uint32_t vocab, k, parts, part;  // parts of a row, and pieces of one
-  float scale, c;
+  float scale;
+  Exponent x2;
   const int32_t *ids, *top_ids;
   const float *entropy;
   const float2 *stats;
@@ -546,13 +553,14 @@ __global__ __launch_bounds__(ROW_THREADS) void k_scores_back(ScoreBackArgs a) {
   if (a.g_lse) g -= a.g_lse[row];
   const float gh = a.g_entropy ? a.g_entropy[row] : 0.0f;
   const float2 st = a.stats[row];
-  // p (g + gh (log p + entropy)) = w (alpha + beta d), d = x - max, w = exp2(c d)
+  // p (g + gh (log p + entropy)) = w (alpha + beta t), t = scale log2(e) (x - max), w = exp2(t);
+  // t is bounded where w is 0, so that their product is 0
   const bool zero = st.x == -INFINITY || (g == 0.0f && gh == 0.0f && !any);
   const float inv = a.scale * __builtin_amdgcn_exp2f(-st.y * LOG2E);
-  const float alpha = -inv * (g + gh * (a.entropy[row] - st.y)), beta = -inv * gh * a.scale;
+  const float alpha = -inv * (g + gh * (a.entropy[row] - st.y)), beta = -inv * gh * float(LN2);
   const auto of = [&](float v) {
-    const float d = fmaxf(v - st.x, LOWEST);
-    return __builtin_amdgcn_exp2f(d * a.c) * (alpha + beta * d);
+    const float d = v - st.x, t = fmaxf(__builtin_fmaf(d, a.x2.low, d * a.x2.c), -16384.0f);
+    return __builtin_amdgcn_exp2f(t) * (alpha + beta * t);
   };
   constexpr uint32_t TERMS = (TOP_MAX + ROW_THREADS) / ROW_THREADS;
   float before[TERMS];
@@ -648,7 +656,7 @@ int bbpe_token_logprobs(int dtype, const void *logits, int64_t row_stride, uint6
   a.parts = cut.parts;
   a.part = cut.part;
   a.scale = scale;
-  a.c = scale * LOG2E;
+  a.x2 = exponent_of(scale);
   a.index_bits = bits_of(vocab + 8);  // places begin up to 7 before the row
   a.ids = d_ids;
   a.logprobs = d_logprobs;
@@ -701,7 +709,7 @@ int bbpe_token_logprobs_backward(int dtype, const void *logits, int64_t row_stri
   a.vocab = vocab;
   a.k = top_k;
   a.scale = scale;
-  a.c = scale * LOG2E;
+  a.x2 = exponent_of(scale);
   a.ids = d_ids;
   a.top_ids = d_top_ids;
   a.entropy = d_entropy;

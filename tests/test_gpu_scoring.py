@@ -220,6 +220,22 @@ def test_gradients_of_odd_rows():
     assert not dx[3].any() and dx[2].isnan().all()
 
 
+@pytest.mark.parametrize("dtype", [BF, F])
+def test_large_gradients_beside_masked_places(dtype):
+    """Given gradients of thousands (a loss scale) where tokens are minus infinity or the type's lowest value."""
+    v, k = 1003, 3
+    x, g = logits(3, v, dtype, 13)
+    x[0, 5:900] = -INF
+    x[1, 5:900] = torch.finfo(dtype).min
+    ids = torch.tensor([1, 2, 1000], dtype=torch.int32)
+    up = {a: None if t is None else t * 4096 for a, t in grads(3, k, g, "ghlt").items()}
+    say("large gradients", dtype)
+    dev, got = check_scores(x, ids, k, 0.7)
+    dx = B.token_logprobs_backward(dev, ids.cuda(), got, **back_args(up), scale=0.7)
+    near(dx, *ref.scores_grad(x, ids, k, 0.7, **up), "dx")
+    assert not dx[:2, 5:900].any()
+
+
 def teacher(x, k, g, tail, scale, noise=0.5):
     """Lists of a teacher that differs a little: ids, log probabilities."""
     n, v = x.shape
