@@ -428,7 +428,7 @@ __global__ __launch_bounds__(64 * WAVES) void k_distill_back(DistillArgs a) {
 int check(int dtype, const void *logits, int64_t row_stride, uint64_t n_rows, uint32_t vocab, const int32_t *ids, const float *lp,
           uint32_t k, int tail, float scale) {
   if (bad_logits(dtype, logits, row_stride, n_rows, vocab, false) || k == 0 || k > LIST_MAX || tail < 0 || tail > 1 ||
-      k > vocab || (tail && k >= vocab) || !(scale > 0.0f) || !std::isfinite(scale))
+      k > vocab || (tail && k >= vocab) || bad_scale(scale))
     return BBPE_E_INVALID_ARG;
   if ((n_rows && (!ids || !lp)) || ((address(ids) | address(lp)) & 3)) return BBPE_E_INVALID_ARG;
   return BBPE_OK;

@@ -189,7 +189,7 @@ inline uint32_t most_pieces(int dtype, uint32_t vocab) {
 }
 
 constexpr uint32_t PARTS_MAX = 64;         // parts of a row at most: a wave joins them
-constexpr uint64_t MAX_GROUPS = 1u << 22;  // workgroups of a launch: fewer than 2^32 threads
+constexpr uint64_t MAX_GROUPS = 1u << 21;  // workgroups (of up to 1,024) a launch: fewer than 2^32 threads
 
 // How rows are cut: waves a workgroup, parts a row and pieces of a part.  Rows of
 // up to 512 pieces go to a wave each (where `small` allows it); longer ones to a
@@ -217,6 +217,8 @@ inline uintptr_t address(const void *p) { return reinterpret_cast<uintptr_t>(p);
 inline bool bad_sizes(int dtype, uint64_t rows, uint32_t vocab) {
   return dtype < BBPE_BF16 || dtype > BBPE_F32 || vocab == 0 || vocab > (1u << 30) || rows > 0x7FFFFFFFull;
 }
+// Scales whose two parts are ordinary floats.
+inline bool bad_scale(float scale) { return !(scale >= 1e-30f && scale <= 1e30f); }
 // What the operators ask of a matrix of logits alike.  `grad`: one of gradients,
 // whose rows must not share memory.
 inline bool bad_logits(int dtype, const void *x, int64_t stride, uint64_t rows, uint32_t vocab, bool grad) {

@@ -615,7 +615,7 @@ ScoreCut cut_of(int dtype, uint64_t n_rows, uint32_t vocab, uint32_t k) {
 }
 
 int check_scores(int dtype, const void *logits, int64_t stride, uint64_t n_rows, uint32_t vocab, uint32_t k, float scale) {
-  return bad_logits(dtype, logits, stride, n_rows, vocab, false) || k > TOP_MAX || k > vocab || !(scale > 0.0f) || !std::isfinite(scale)
+  return bad_logits(dtype, logits, stride, n_rows, vocab, false) || k > TOP_MAX || k > vocab || bad_scale(scale)
              ? BBPE_E_INVALID_ARG
              : BBPE_OK;
 }

@@ -525,11 +525,12 @@ int bbpe_tree_attention(const void *q, int64_t q_ts, int64_t q_hs, uint64_t n_to
  * vocabulary, [n_rows][vocab] of dtype, rows row_stride elements apart and
  * beginning at any element (16-byte aligned rows are not asked for).  What is
  * said above of streams, graphs, checks and workspaces holds for them too.
- * Arithmetic is in float, a row's few numbers in 64 bits; results do not depend
- * on the order in which workgroups run.
+ * Arithmetic is in float, long sums and a row's few numbers in 64 bits.  Results
+ * do not depend on the order in which workgroups run; in their last digits they
+ * may on how many rows a call has and where in 16 bytes a row begins.
  *
  * z = scale * logits, log p = z - log sum exp z.  scale (1 / temperature) is
- * above 0.  Minus infinity is a token that cannot come; a row of nothing else
+ * from 1e-30 to 1e30.  Minus infinity is a token that cannot come; a row of nothing else
  * has lse -inf, every log probability -inf, entropy 0 and no gradient.  A row
  * with a NaN or plus infinity in it has no probabilities: its numbers are NaN.
  * -------------------------------------------------------------------------- */

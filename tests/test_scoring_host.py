@@ -12,7 +12,7 @@ from byte_level_bpe_amd import scoring  # noqa: E402
 X = 1 << 20  # an aligned address that nothing reads
 NAN, INF = float("nan"), float("inf")
 MATRIX = [dict(dtype=3), dict(dtype=-1), dict(x=None), dict(x=X + 1), dict(vocab=0), dict(vocab=(1 << 30) + 1), dict(n=1 << 31),
-          dict(scale=0.0), dict(scale=-1.0), dict(scale=NAN), dict(scale=INF)]
+          dict(scale=0.0), dict(scale=-1.0), dict(scale=NAN), dict(scale=INF), dict(scale=1e-31), dict(scale=1e31)]
 WRITTEN = [dict(dx=None), dict(dx=X + 1), dict(dstride=99), dict(dstride=0)]
 
 
