@@ -24,8 +24,8 @@ namespace {
 
 constexpr uint32_t LIST_MAX = 256;  // listed tokens at most
 constexpr uint32_t HELD = 16;       // pieces that a thread holds from the loss to the gradient
-constexpr uint64_t STEP_ROWS = 256;
-constexpr uint32_t STEP_MOST = 1u << 15;
+constexpr uint64_t STEP_ROWS = 160;
+constexpr uint32_t STEP_MOST = 1u << 14;
 
 struct DistillArgs {
   const void *x;
@@ -54,9 +54,9 @@ __device__ __forceinline__ double wave_max(double v) {
 // By one wave, four entries a lane.
 template <uint32_t LIST> struct ListShared {
   double q[LIST], log_q[LIST];
-  int32_t ids[LIST];  // -1 where an entry names no token
-  float own[LIST];    // the student's element; minus infinity where it is not there
-  bool first[LIST];   // with a tail: the first entry that names this token
+  alignas(16) int32_t ids[LIST];  // -1 where an entry names no token
+  float own[LIST];                // the student's element; minus infinity where it is not there
+  bool first[LIST], alone[LIST];  // the first entry that names this token, the only one
   double mass, rest, log_norm;
   int some;
 };
@@ -82,6 +82,27 @@ __device__ __forceinline__ void keep_ids(const ListLoads<LIST> &l, ListShared<LI
   for (uint32_t i = 0; i < LIST / 64; ++i) sh.ids[(threadIdx.x & 63) + 64 * i] = l.id[i];
   __builtin_amdgcn_wave_barrier();  // the wave reads them below
 }
+// How a list names entry t's token: first, and nowhere else.  ids: 16-byte aligned
+// in LDS, -1 from k on.
+struct Named {
+  bool first, alone;
+};
+__device__ __forceinline__ Named named(const int32_t *ids, uint32_t k, uint32_t t) {
+  typedef int32_t i32x4 __attribute__((ext_vector_type(4)));
+  const int32_t id = ids[t];
+  Named n{true, true};
+#pragma unroll 4
+  for (uint32_t s = 0; s < k; s += 4) {
+    const i32x4 v = *reinterpret_cast<const i32x4 *>(ids + s);
+#pragma unroll
+    for (uint32_t e = 0; e < 4; ++e) {
+      n.alone &= v[e] != id || s + e == t;
+      n.first &= v[e] != id || s + e >= t;
+    }
+  }
+  return n;
+}
+
 // (sh.ids are there)
 template <typename T, uint32_t LIST>
 __device__ __forceinline__ void read_list(const DistillArgs &a, const T *x, const ListLoads<LIST> &l, ListShared<LIST> &sh) {
@@ -109,11 +130,10 @@ __device__ __forceinline__ void read_list(const DistillArgs &a, const T *x, cons
   for (uint32_t i = 0; i < LIST_EACH; ++i) {
     if (64 * i >= a.k) continue;
     const uint32_t t = lane + 64 * i;
-    bool first = l.id[i] >= 0;
-    if (a.tail)
-      for (uint32_t s = 0; s < min(t, a.k); ++s) first &= sh.ids[s] != l.id[i];
+    const Named n = named(sh.ids, a.k, t);
     const double log_q = l.lp[i] == -INFINITY ? -INFINITY : double(l.lp[i]) - c;
-    sh.first[t] = first;
+    sh.first[t] = l.id[i] >= 0 && n.first;
+    sh.alone[t] = n.alone;
     sh.log_q[t] = log_q;
     sh.q[t] = exp(log_q);
     sh.own[t] = own[i];
@@ -303,15 +323,18 @@ template <typename T, uint32_t WAVES> struct Gradient {
   // barrier apart) from what was there before (dx may be x): each by one thread,
   // or by several with the same value.
   template <typename Q>
-  __device__ __forceinline__ void listed(const DistillArgs &a, const Row<T> &out, uint32_t from, uint32_t to, const int32_t *ids, const float *own,
-                                         const Q *q) const {
+  __device__ __forceinline__ void listed(const DistillArgs &a, const Row<T> &out, uint32_t from, uint32_t to, const int32_t *ids, const bool *alone,
+                                         const float *own, const Q *q) const {
     if (zero) return;
     for (uint32_t t = threadIdx.x; t < a.k; t += THREADS) {
       const int32_t id = ids[t];
       const uint32_t place = out.lead + uint32_t(id);
       if (id < 0 || place / Piece<T>::N - from >= to - from) continue;
-      float sum = 0.0f;
-      for (uint32_t i = 0; i < a.k; ++i) sum += ids[i] == id ? float(q[i]) : 0.0f;
+      float sum = float(q[t]);
+      if (!alone[t]) {
+        sum = 0.0f;
+        for (uint32_t i = 0; i < a.k; ++i) sum += ids[i] == id ? float(q[i]) : 0.0f;
+      }
       out.at[place] = T(g * ((a.tail ? st.w : st.z) * inv * weight(own[t]) - sum));
     }
   }
@@ -341,17 +364,20 @@ __global__ __launch_bounds__(64 * WAVES) void k_distill(DistillArgs a) {
 }
 
 // Loss and gradient of a row by a workgroup.  A thread's first HELD pieces stay in
-// its registers between the two; what a row has besides is read again.
-template <typename T, uint32_t WAVES, bool TAIL, uint32_t LIST>
+// its registers between the two and, KEEP, some more in LDS, as much as leaves
+// room for 16 waves a compute unit; what a row has besides is read again.
+template <typename T, uint32_t WAVES, bool TAIL, uint32_t LIST, bool KEEP>
 __global__ __launch_bounds__(64 * WAVES, 4) void k_distill_step(DistillArgs a) {
   constexpr uint32_t THREADS = 64 * WAVES, STEP = THREADS * ROW_UNROLL;
-  static_assert(HELD % ROW_UNROLL == 0 && THREADS * HELD * Piece<T>::N <= BITS<WAVES>, "");
+  constexpr uint32_t KEPT = !KEEP ? 0 : TAIL ? 4 : 8;
+  static_assert(HELD % ROW_UNROLL == 0 && KEPT % ROW_UNROLL == 0 && THREADS * (HELD + KEPT) * Piece<T>::N <= BITS<WAVES>, "");
   __shared__ DistillShared<WAVES, TAIL, LIST> sh;
+  __shared__ typename Piece<T>::raw kept[KEPT ? KEPT * THREADS : 1];
   const uint64_t row = a.block0 + blockIdx.x;
   const T *x = static_cast<const T *>(a.x) + int64_t(row) * a.stride;
   T *dx = static_cast<T *>(a.dx) + int64_t(row) * a.dx_stride;
   const Row<const T> r(x, a.vocab);
-  const uint32_t tid = threadIdx.x, pieces = r.pieces(), held = min(pieces, THREADS * HELD);
+  const uint32_t tid = threadIdx.x, pieces = r.pieces(), held = min(pieces, THREADS * HELD), near = min(pieces, THREADS * (HELD + KEPT));
   const float weight = a.grad[row];
   ListLoads<LIST> l;
   if (tid < 64) l = load_list<LIST>(a, row);
@@ -359,13 +385,23 @@ __global__ __launch_bounds__(64 * WAVES, 4) void k_distill_step(DistillArgs a) {
 #pragma unroll
   for (uint32_t i = 0; i < HELD / ROW_UNROLL; ++i) r.template load_step<THREADS>(raw[i], r.at, i * STEP + tid, held);
   if (tid < 64) keep_ids(l, sh.list);
-  if (TAIL) set_bits<T>(a, r, 0, held, sh);
+  if (TAIL) set_bits<T>(a, r, 0, near, sh);
   if (tid < 64) read_list(a, x, l, sh.list);
   Partial s{0.0, -INFINITY, 0.0f};
 #pragma unroll
   for (uint32_t i = 0; i < HELD / ROW_UNROLL; ++i)
     if (i * STEP < held) add_step<T>(a, raw[i], i * STEP + tid, sh, s);
-  add_pieces<T>(a, r, held, pieces, sh, s);
+#pragma unroll
+  for (uint32_t i = 0; i < KEPT / ROW_UNROLL; ++i) {
+    const uint32_t p = THREADS * HELD + i * STEP + tid;
+    if (p - tid >= near) break;
+    typename Piece<T>::raw more[ROW_UNROLL];
+    r.template load_step<THREADS>(more, r.at, p, near);
+#pragma unroll
+    for (uint32_t u = 0; u < ROW_UNROLL; ++u) kept[i * STEP + u * THREADS + tid] = more[u];
+    add_step<T>(a, more, p, sh, s);
+  }
+  add_pieces<T>(a, r, near, pieces, sh, s);
   s = row_partial<WAVES>(s, a.x2, sh.sums);
   if (tid < 64) {
     const float4 st = end_row(a, row, s, sh.list);
@@ -379,9 +415,14 @@ __global__ __launch_bounds__(64 * WAVES, 4) void k_distill_step(DistillArgs a) {
     const uint32_t p = i * THREADS + tid;
     if (p < held) out.store(p, grad.of(raw[i / ROW_UNROLL][i % ROW_UNROLL]));
   }
-  grad.pieces(x, out, held, pieces);
+#pragma unroll
+  for (uint32_t i = 0; i < KEPT; ++i) {
+    const uint32_t p = (HELD + i) * THREADS + tid;
+    if (p < near) out.store(p, grad.of(kept[i * THREADS + tid]));
+  }
+  grad.pieces(x, out, near, pieces);
   __syncthreads();
-  grad.listed(a, out, 0, pieces, sh.list.ids, sh.list.own, sh.list.q);
+  grad.listed(a, out, 0, pieces, sh.list.ids, sh.list.alone, sh.list.own, sh.list.q);
 }
 
 // Joins a row's parts.
@@ -404,25 +445,30 @@ __global__ __launch_bounds__(64) void k_distill_join(DistillArgs a) {
 template <typename T, uint32_t WAVES>
 __global__ __launch_bounds__(64 * WAVES) void k_distill_back(DistillArgs a) {
   constexpr uint32_t THREADS = 64 * WAVES;
-  __shared__ int32_t ids[LIST_MAX];
+  __shared__ alignas(16) int32_t ids[LIST_MAX];
   __shared__ float own[LIST_MAX], q[LIST_MAX];
+  __shared__ bool alone[LIST_MAX];
   const uint64_t block = a.block0 + blockIdx.x, row = block / a.parts;
   const T *x = static_cast<const T *>(a.x) + int64_t(row) * a.stride;
   const Row<T> r(static_cast<T *>(a.dx) + int64_t(row) * a.dx_stride, a.vocab);
   const uint32_t from = uint32_t(block % a.parts) * a.part, to = min(r.pieces(), from + a.part);
   if (from >= to) return;  // (parts are counted for rows that begin anywhere)
   const Gradient<T, WAVES> grad(a, a.stats[row], a.grad[row]);
-  for (uint32_t t = threadIdx.x; t < a.k; t += THREADS) {
-    const int32_t id = a.ids[row * a.k + t];
+  for (uint32_t t = threadIdx.x; t < LIST_MAX; t += THREADS) {
+    const int32_t id = t < a.k ? a.ids[row * a.k + t] : -1;
     const bool there = id >= 0 && uint32_t(id) < a.vocab;
     ids[t] = there ? id : -1;
+    if (t >= a.k) continue;
     q[t] = there ? __builtin_amdgcn_exp2f((a.lp[row * a.k + t] - (a.tail ? 0.0f : grad.st.w)) * LOG2E) : 0.0f;
     own[t] = there && (r.lead + uint32_t(id)) / Piece<T>::N - from < to - from ? float(x[id]) : 0.0f;
   }
   __syncthreads();
+  // (of the entries that this part has: listed() looks at no others)
+  for (uint32_t t = threadIdx.x; t < a.k; t += THREADS)
+    if (ids[t] >= 0 && (r.lead + uint32_t(ids[t])) / Piece<T>::N - from < to - from) alone[t] = named(ids, a.k, t).alone;
   grad.pieces(x, r, from, to);
   __syncthreads();
-  grad.listed(a, r, from, to, ids, own, q);
+  grad.listed(a, r, from, to, ids, alone, own, q);
 }
 
 int check(int dtype, const void *logits, int64_t row_stride, uint64_t n_rows, uint32_t vocab, const int32_t *ids, const float *lp,
@@ -527,17 +573,19 @@ int bbpe_distill_loss(int dtype, const void *logits, int64_t row_stride, uint64_
     for (a.block0 = 0; a.block0 < blocks; a.block0 += MAX_GROUPS)
       kernel<<<uint32_t(std::min(blocks - a.block0, MAX_GROUPS)), threads, 0, st>>>(a);
   };
-  const uint32_t pieces = most_pieces(dtype, vocab);
-  const bool whole = d_logits && (n_rows >= STEP_ROWS || cut.parts == 1);  // loss and gradient of a row by one workgroup
+  // loss and gradient of a row by one workgroup
+  const uint32_t per = dtype == BBPE_F32 ? 4 : 8, pieces = (vocab + per - 1) / per;
+  const bool whole = d_logits && (n_rows >= STEP_ROWS || pieces <= 256 * HELD);
   with_element(dtype, [&](auto t) {
     typedef decltype(t) T;
     const auto by_tail = [&](uint64_t blocks, uint32_t threads, auto without, auto with) { launch(blocks, tail ? with : without, threads); };
     constexpr uint32_t W = ROW_WAVES, L = LIST_MAX;
     if (whole) {
-      if (pieces <= 64 * HELD && top_k <= 64) by_tail(n_rows, 64, k_distill_step<T, 1, false, 64>, k_distill_step<T, 1, true, 64>);
-      else if (pieces <= 256 * HELD) by_tail(n_rows, 256, k_distill_step<T, 4, false, L>, k_distill_step<T, 4, true, L>);
-      else if (pieces <= STEP_MOST) by_tail(n_rows, 512, k_distill_step<T, 8, false, L>, k_distill_step<T, 8, true, L>);
-      else by_tail(n_rows, 1024, k_distill_step<T, 16, false, L>, k_distill_step<T, 16, true, L>);
+      if (pieces <= 64 * HELD && top_k <= 64) by_tail(n_rows, 64, k_distill_step<T, 1, false, 64, false>, k_distill_step<T, 1, true, 64, false>);
+      else if (pieces <= 256 * HELD) by_tail(n_rows, 256, k_distill_step<T, 4, false, L, false>, k_distill_step<T, 4, true, L, false>);
+      else if (pieces <= 512 * HELD) by_tail(n_rows, 512, k_distill_step<T, 8, false, L, false>, k_distill_step<T, 8, true, L, false>);
+      else if (sizeof(T) == 2 || pieces <= STEP_MOST) by_tail(n_rows, 512, k_distill_step<T, 8, false, L, true>, k_distill_step<T, 8, true, L, true>);
+      else by_tail(n_rows, 1024, k_distill_step<T, 16, false, L, true>, k_distill_step<T, 16, true, L, true>);
     } else if (cut.parts > 1) {
       by_tail(n_rows * cut.parts, ROW_THREADS, k_distill<T, W, false, true, L>, k_distill<T, W, true, true, L>);
       launch(n_rows, k_distill_join<T>, 64);
