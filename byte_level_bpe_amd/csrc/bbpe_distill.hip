@@ -103,7 +103,17 @@ __device__ __forceinline__ Named named(const int32_t *ids, uint32_t k, uint32_t 
   return n;
 }
 
-// (sh.ids are there)
+// Of all entries, by the threads from `from` on.  (sh.ids are there)
+template <uint32_t WAVES, uint32_t LIST>
+__device__ __forceinline__ void read_names(const DistillArgs &a, uint32_t from, ListShared<LIST> &sh) {
+  for (uint32_t t = threadIdx.x - from; t < a.k; t += 64 * WAVES - from) {
+    const Named n = named(sh.ids, a.k, t);
+    sh.first[t] = sh.ids[t] >= 0 && n.first;
+    sh.alone[t] = n.alone;
+  }
+}
+
+// What the row has for the list, and the teacher's sums, by one wave.
 template <typename T, uint32_t LIST>
 __device__ __forceinline__ void read_list(const DistillArgs &a, const T *x, const ListLoads<LIST> &l, ListShared<LIST> &sh) {
   constexpr uint32_t LIST_EACH = LIST / 64;
@@ -130,10 +140,7 @@ __device__ __forceinline__ void read_list(const DistillArgs &a, const T *x, cons
   for (uint32_t i = 0; i < LIST_EACH; ++i) {
     if (64 * i >= a.k) continue;
     const uint32_t t = lane + 64 * i;
-    const Named n = named(sh.ids, a.k, t);
     const double log_q = l.lp[i] == -INFINITY ? -INFINITY : double(l.lp[i]) - c;
-    sh.first[t] = l.id[i] >= 0 && n.first;
-    sh.alone[t] = n.alone;
     sh.log_q[t] = log_q;
     sh.q[t] = exp(log_q);
     sh.own[t] = own[i];
@@ -353,6 +360,10 @@ __global__ __launch_bounds__(64 * WAVES) void k_distill(DistillArgs a) {
     keep_ids(l, sh.list);
     if (!SPLIT) read_list(a, x, l, sh.list);
   }
+  if (TAIL && !SPLIT) {
+    __syncthreads();
+    if (WAVES == 1 || threadIdx.x >= 64) read_names<WAVES>(a, WAVES == 1 ? 0 : 64, sh.list);
+  }
   Partial s{0.0, -INFINITY, 0.0f};
   add_pieces<T>(a, r, first, SPLIT ? min(r.pieces(), first + a.part) : r.pieces(), sh, s);
   s = row_partial<WAVES>(s, a.x2, sh.sums);  // (with a barrier, for the list too)
@@ -386,7 +397,9 @@ __global__ __launch_bounds__(64 * WAVES, 4) void k_distill_step(DistillArgs a) {
   for (uint32_t i = 0; i < HELD / ROW_UNROLL; ++i) r.template load_step<THREADS>(raw[i], r.at, i * STEP + tid, held);
   if (tid < 64) keep_ids(l, sh.list);
   if (TAIL) set_bits<T>(a, r, 0, near, sh);
+  else __syncthreads();
   if (tid < 64) read_list(a, x, l, sh.list);
+  if (WAVES == 1 || tid >= 64) read_names<WAVES>(a, WAVES == 1 ? 0 : 64, sh.list);
   Partial s{0.0, -INFINITY, 0.0f};
 #pragma unroll
   for (uint32_t i = 0; i < HELD / ROW_UNROLL; ++i)
@@ -436,6 +449,7 @@ __global__ __launch_bounds__(64) void k_distill_join(DistillArgs a) {
   keep_ids(l, sh);
   __syncthreads();
   read_list(a, static_cast<const T *>(a.x) + int64_t(row) * a.stride, l, sh);
+  if (a.tail) read_names<1>(a, 0, sh);
   p = wave_partial(p, a.x2);
   __syncthreads();
   end_row(a, row, p, sh);
