@@ -25,7 +25,6 @@ namespace {
 constexpr uint32_t LIST_MAX = 256;  // listed tokens at most
 constexpr uint32_t HELD = 16;       // pieces that a thread holds from the loss to the gradient
 constexpr uint64_t STEP_ROWS = 160;
-constexpr uint32_t STEP_MOST = 1u << 14;
 
 struct DistillArgs {
   const void *x;
@@ -375,12 +374,12 @@ __global__ __launch_bounds__(64 * WAVES) void k_distill(DistillArgs a) {
 }
 
 // Loss and gradient of a row by a workgroup.  A thread's first HELD pieces stay in
-// its registers between the two and, KEEP, some more in LDS, as much as leaves
-// room for 16 waves a compute unit; what a row has besides is read again.
-template <typename T, uint32_t WAVES, bool TAIL, uint32_t LIST, bool KEEP>
+// its registers between the two and, of 16 waves, some more in LDS; what a row has
+// besides is read again.
+template <typename T, uint32_t WAVES, bool TAIL, uint32_t LIST>
 __global__ __launch_bounds__(64 * WAVES, 4) void k_distill_step(DistillArgs a) {
   constexpr uint32_t THREADS = 64 * WAVES, STEP = THREADS * ROW_UNROLL;
-  constexpr uint32_t KEPT = !KEEP ? 0 : TAIL ? 4 : 8;
+  constexpr uint32_t KEPT = WAVES < 16 ? 0 : TAIL ? 4 : 8;
   static_assert(HELD % ROW_UNROLL == 0 && KEPT % ROW_UNROLL == 0 && THREADS * (HELD + KEPT) * Piece<T>::N <= BITS<WAVES>, "");
   __shared__ DistillShared<WAVES, TAIL, LIST> sh;
   __shared__ typename Piece<T>::raw kept[KEPT ? KEPT * THREADS : 1];
@@ -595,11 +594,10 @@ int bbpe_distill_loss(int dtype, const void *logits, int64_t row_stride, uint64_
     const auto by_tail = [&](uint64_t blocks, uint32_t threads, auto without, auto with) { launch(blocks, tail ? with : without, threads); };
     constexpr uint32_t W = ROW_WAVES, L = LIST_MAX;
     if (whole) {
-      if (pieces <= 64 * HELD && top_k <= 64) by_tail(n_rows, 64, k_distill_step<T, 1, false, 64, false>, k_distill_step<T, 1, true, 64, false>);
-      else if (pieces <= 256 * HELD) by_tail(n_rows, 256, k_distill_step<T, 4, false, L, false>, k_distill_step<T, 4, true, L, false>);
-      else if (pieces <= 512 * HELD) by_tail(n_rows, 512, k_distill_step<T, 8, false, L, false>, k_distill_step<T, 8, true, L, false>);
-      else if (sizeof(T) == 2 || pieces <= STEP_MOST) by_tail(n_rows, 512, k_distill_step<T, 8, false, L, true>, k_distill_step<T, 8, true, L, true>);
-      else by_tail(n_rows, 1024, k_distill_step<T, 16, false, L, true>, k_distill_step<T, 16, true, L, true>);
+      if (pieces <= 64 * HELD && top_k <= 64) by_tail(n_rows, 64, k_distill_step<T, 1, false, 64>, k_distill_step<T, 1, true, 64>);
+      else if (pieces <= 256 * HELD) by_tail(n_rows, 256, k_distill_step<T, 4, false, L>, k_distill_step<T, 4, true, L>);
+      else if (pieces <= 512 * HELD || sizeof(T) == 2) by_tail(n_rows, 512, k_distill_step<T, 8, false, L>, k_distill_step<T, 8, true, L>);
+      else by_tail(n_rows, 1024, k_distill_step<T, 16, false, L>, k_distill_step<T, 16, true, L>);
     } else if (cut.parts > 1) {
       by_tail(n_rows * cut.parts, ROW_THREADS, k_distill<T, W, false, true, L>, k_distill<T, W, true, true, L>);
       launch(n_rows, k_distill_join<T>, 64);
