@@ -517,12 +517,13 @@ struct ScoreBackArgs {
 // One workgroup a part of a row.  Elements that have a term of their own are
 // written once more when the part is done, from what was there before (dx may
 // be x): each by one thread, or by several with the same value.
-template <typename T>
-__global__ __launch_bounds__(ROW_THREADS) void k_scores_back(ScoreBackArgs a) {
+template <typename T, uint32_t WAVES>
+__global__ __launch_bounds__(64 * WAVES) void k_scores_back(ScoreBackArgs a) {
+  constexpr uint32_t THREADS = 64 * WAVES, STEP = THREADS * ROW_UNROLL;
   typedef Piece<T> P;
   __shared__ int32_t own_id[TOP_MAX + 1];
   __shared__ float own_g[TOP_MAX + 1];
-  __shared__ float sh_g[ROW_WAVES];
+  __shared__ float sh_g[WAVES];
   const uint32_t tid = threadIdx.x;
   const uint64_t block = a.block0 + blockIdx.x, row = block / a.parts;
   const T *x = static_cast<const T *>(a.x) + int64_t(row) * a.stride;
@@ -533,7 +534,7 @@ __global__ __launch_bounds__(ROW_THREADS) void k_scores_back(ScoreBackArgs a) {
   // terms of single elements: the given token's, and the alternatives'
   const uint32_t n = 1 + (a.g_top ? a.k : 0);
   float mine = 0.0f;
-  for (uint32_t t = tid; t < n; t += ROW_THREADS) {
+  for (uint32_t t = tid; t < n; t += THREADS) {
     int32_t id = t ? a.top_ids[row * a.k + t - 1] : a.ids[row];
     if (id < 0 || uint32_t(id) >= a.vocab) id = -1;
     const float *g = t ? a.g_top : a.g_logprobs;
@@ -546,9 +547,9 @@ __global__ __launch_bounds__(ROW_THREADS) void k_scores_back(ScoreBackArgs a) {
   if ((tid & 63) == 0) sh_g[tid >> 6] = mine;
   __syncthreads();
   float g = 0.0f;
-  for (uint32_t w = 0; w < ROW_WAVES; ++w) g += sh_g[w];
+  for (uint32_t w = 0; w < WAVES; ++w) g += sh_g[w];
   bool any = false;
-  for (uint32_t t = tid; t < n; t += ROW_THREADS) any |= own_g[t] != 0.0f;
+  for (uint32_t t = tid; t < n; t += THREADS) any |= own_g[t] != 0.0f;
   any = __syncthreads_or(any);
   if (a.g_lse) g -= a.g_lse[row];
   const float gh = a.g_entropy ? a.g_entropy[row] : 0.0f;
@@ -562,19 +563,19 @@ __global__ __launch_bounds__(ROW_THREADS) void k_scores_back(ScoreBackArgs a) {
     const float d = v - st.x, t = fmaxf(__builtin_fmaf(d, a.x2.low, d * a.x2.c), -16384.0f);
     return __builtin_amdgcn_exp2f(t) * (alpha + beta * t);
   };
-  constexpr uint32_t TERMS = (TOP_MAX + ROW_THREADS) / ROW_THREADS;
+  constexpr uint32_t TERMS = (TOP_MAX + THREADS) / THREADS;
   float before[TERMS];
   for (uint32_t i = 0; i < TERMS; ++i) {
-    const uint32_t t = tid + i * ROW_THREADS;
+    const uint32_t t = tid + i * THREADS;
     before[i] = t < n && own_id[t] >= 0 && (r.lead + uint32_t(own_id[t])) / P::N - from < to - from ? float(x[own_id[t]]) : 0.0f;
   }
   __syncthreads();
-  for (uint32_t p0 = from; p0 < to; p0 += ROW_STEP) {
+  for (uint32_t p0 = from; p0 < to; p0 += STEP) {
     typename P::raw raw[ROW_UNROLL];
-    if (!zero) r.template load_step<ROW_THREADS>(raw, x - r.lead, p0 + tid, to);
+    if (!zero) r.template load_step<THREADS>(raw, x - r.lead, p0 + tid, to);
 #pragma unroll
     for (uint32_t u = 0; u < ROW_UNROLL; ++u) {
-      const uint32_t p = p0 + u * ROW_THREADS + tid;
+      const uint32_t p = p0 + u * THREADS + tid;
       if (p >= to) break;
       typename P::val v = 0.0f;
       if (!zero) {
@@ -588,7 +589,7 @@ __global__ __launch_bounds__(ROW_THREADS) void k_scores_back(ScoreBackArgs a) {
   __syncthreads();
   if (zero) return;
   for (uint32_t i = 0; i < TERMS; ++i) {
-    const uint32_t t = tid + i * ROW_THREADS;
+    const uint32_t t = tid + i * THREADS;
     if (t >= n || own_id[t] < 0 || (r.lead + uint32_t(own_id[t])) / P::N - from >= to - from) continue;
     float sum = 0.0f;
     for (uint32_t j = 0; j < n; ++j) sum += own_id[j] == own_id[t] ? own_g[j] : 0.0f;
@@ -718,13 +719,17 @@ int bbpe_token_logprobs_backward(int dtype, const void *logits, int64_t row_stri
   a.g_entropy = g_entropy;
   a.g_lse = g_lse;
   a.g_top = top_k ? g_top : nullptr;
-  a.part = 2 * ROW_STEP;
-  a.parts = (most_pieces(dtype, vocab) + a.part - 1) / a.part;
+  const uint32_t pieces = most_pieces(dtype, vocab);
+  const bool small = pieces <= 512;
+  a.part = small ? pieces : 2 * ROW_STEP;
+  a.parts = (pieces + a.part - 1) / a.part;
   const hipStream_t st = static_cast<hipStream_t>(hip_stream);
   const uint64_t blocks = n_rows * a.parts;
   for (; a.block0 < blocks; a.block0 += MAX_GROUPS)
     with_element(dtype, [&](auto t) {
-      k_scores_back<decltype(t)><<<uint32_t(std::min(blocks - a.block0, MAX_GROUPS)), ROW_THREADS, 0, st>>>(a);
+      const uint32_t grid = uint32_t(std::min(blocks - a.block0, MAX_GROUPS));
+      if (small) k_scores_back<decltype(t), 1><<<grid, 64, 0, st>>>(a);
+      else k_scores_back<decltype(t), ROW_WAVES><<<grid, ROW_THREADS, 0, st>>>(a);
     });
   return hipGetLastError() == hipSuccess ? BBPE_OK : BBPE_E_HIP;
 }
