@@ -314,15 +314,6 @@ __device__ __forceinline__ void score_pieces(const ScoreArgs &a, uint64_t row, u
   // (the exponent's second part, to first order: each weight times LN2 * low * (x - max))
   s.sum += LN2 * double(a.x2.low) * double(s.mean);
   if ((tid & 63) == 0) sh.above[tid >> 6] = above;
-  if (TOP) {
-#pragma unroll
-    for (uint32_t u = 0; u < ROW_UNROLL; ++u) {
-      const uint32_t g = u * THREADS + tid;
-      if (best_at[u] == ~0u) best_at[u] = first;  // nothing but minus infinity
-      sh.keys[g] = first + g < last ? order_key<T>(best[u], (best_at[u] + g) * P::N, a.index_bits) : 0;
-    }
-    if (tid == 0) sh.n_chosen = sh.n_deep = sh.n_found = 0;
-  }
   const RowEnd end(row_partial<WAVES>(s, a.x2, sh.sums));  // (with a barrier)
   if (tid == THREADS - 1) {  // (the first wave has the bar to find)
     above = 0;
@@ -340,42 +331,11 @@ __device__ __forceinline__ void score_pieces(const ScoreArgs &a, uint64_t row, u
     for (uint32_t t = tid; t < a.k; t += THREADS) put(t, 0);
     return;
   }
-  if (tid < 64) {
-    uint64_t mine[STEP / 64];
-#pragma unroll
-    for (uint32_t i = 0; i < STEP / 64; ++i) mine[i] = sh.keys[i * 64 + tid];
-    const uint64_t bar = top_bar<STEP / 64>([&](uint32_t i) { return mine[i]; }, 0, a.k, with_slack(a.k));
-    if (tid == 0) sh.reach = bar;
-  }
-  __syncthreads();
-  const uint64_t group_bar = sh.reach;
-#pragma unroll
-  for (uint32_t u = 0; u < ROW_UNROLL; ++u) {
-    const uint32_t g = u * THREADS + tid;
-    if (sh.keys[g] < group_bar) continue;
-    // (their order does not matter)
-    sh.chosen[atomicAdd(&sh.n_chosen, 1u)] = best_at[u] + g;
-    float rest = second[u];
-    if (KEEP > 1) {
-      const bool two = second_at[u] != ~0u && order_key<T>(rest, (second_at[u] + g) * P::N, a.index_bits) >= group_bar;
-      if (two) {
-        sh.chosen[atomicAdd(&sh.n_chosen, 1u)] = second_at[u] + g;
-        rest = third[u];
-      } else {
-        second_at[u] = ~0u;
-      }
-    }
-    if (order_key<T>(rest, 0, a.index_bits) >= group_bar) {
-      uint32_t *to = sh.deep[atomicAdd(&sh.n_deep, 1u)];
-      to[0] = g;
-      to[1] = best_at[u] + g;
-      if (KEEP > 1) to[2] = second_at[u] == ~0u ? ~0u : second_at[u] + g;
-    }
-  }
-  __syncthreads();
   // Every element of the chosen groups that reaches the bar (by its piece's place,
   // as groups do) and `low`.
-  const uint32_t n_pieces = sh.n_chosen, deep_steps = (last - first + STEP - 1) / STEP, n_deep_pieces = sh.n_deep * deep_steps;
+  const uint32_t deep_steps = (last - first + STEP - 1) / STEP;
+  uint32_t n_pieces, n_deep_pieces;
+  uint64_t group_bar;
   const auto each = [&](uint64_t low, auto take) {
     for (uint32_t i = tid; i < (n_pieces + n_deep_pieces) * P::N; i += THREADS) {  // an element a thread
       uint32_t p = i / P::N;
@@ -402,7 +362,60 @@ __device__ __forceinline__ void score_pieces(const ScoreArgs &a, uint64_t row, u
     });
     __syncthreads();
   };
-  collect(0);
+  for (uint32_t most = with_slack(a.k);; most = a.k) {
+#pragma unroll
+    for (uint32_t u = 0; u < ROW_UNROLL; ++u) {
+      const uint32_t g = u * THREADS + tid;
+      if (best_at[u] == ~0u) best_at[u] = first;  // nothing but minus infinity
+      sh.keys[g] = first + g < last ? order_key<T>(best[u], (best_at[u] + g) * P::N, a.index_bits) : 0;
+    }
+    if (tid == 0) sh.n_chosen = sh.n_deep = sh.n_found = 0;
+    __syncthreads();
+    if (tid < 64) {
+      uint64_t mine[STEP / 64];
+#pragma unroll
+      for (uint32_t i = 0; i < STEP / 64; ++i) mine[i] = sh.keys[i * 64 + tid];
+      const uint64_t bar = top_bar<STEP / 64>([&](uint32_t i) { return mine[i]; }, 0, a.k, most);
+      if (tid == 0) sh.reach = bar;
+    }
+    __syncthreads();
+    group_bar = sh.reach;
+#pragma unroll
+    for (uint32_t u = 0; u < ROW_UNROLL; ++u) {
+      const uint32_t g = u * THREADS + tid;
+      if (sh.keys[g] < group_bar) continue;
+      // (their order does not matter)
+      sh.chosen[atomicAdd(&sh.n_chosen, 1u)] = best_at[u] + g;
+      float rest = second[u];
+      if (KEEP > 1) {
+        const bool two = second_at[u] != ~0u && order_key<T>(rest, (second_at[u] + g) * P::N, a.index_bits) >= group_bar;
+        if (two) {
+          sh.chosen[atomicAdd(&sh.n_chosen, 1u)] = second_at[u] + g;
+          rest = third[u];
+        } else {
+          second_at[u] = ~0u;
+        }
+      }
+      // the others' key is no larger than that of their largest at the first of them
+      uint32_t other = first;
+      if (other == best_at[u]) other += STEP;
+      if (KEEP > 1 && other == second_at[u]) other += other + STEP == best_at[u] ? 2 * STEP : STEP;
+      if (other + g < last && order_key<T>(rest, (other + g) * P::N, a.index_bits) >= group_bar) {
+        uint32_t *to = sh.deep[atomicAdd(&sh.n_deep, 1u)];
+        to[0] = g;
+        to[1] = best_at[u] + g;
+        if (KEEP > 1) to[2] = second_at[u] == ~0u ? ~0u : second_at[u] + g;
+      }
+    }
+    __syncthreads();
+    n_pieces = sh.n_chosen;
+    n_deep_pieces = sh.n_deep * deep_steps;
+    collect(0);
+    // Among equal elements a bar lets through whole pieces: with the smallest bar
+    // that is 8 k elements, with some slack it may be more than there is room for.
+    if (sh.n_found <= 2 * ROOM || most == a.k) break;
+    __syncthreads();  // the lists have been read
+  }
   if (sh.n_found > 2 * ROOM) {
     // Large elements crowd in a few groups: halve what is between until a bar
     // leaves k or more, and no more than there is room for.  (Keys differ, so
@@ -429,6 +442,7 @@ __device__ __forceinline__ void score_pieces(const ScoreArgs &a, uint64_t row, u
     collect(lo);
   }
   uint32_t n = sh.n_found;
+  __syncthreads();  // n_found has been read
   if (n > ROOM) {
     // more than can be put in order: those that reach a bar among them, moved to the front
     if (tid < 64) {

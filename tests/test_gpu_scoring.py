@@ -152,6 +152,28 @@ def test_alternatives_that_crowd(dtype):
         check_scores(x, ids, k)
 
 
+@pytest.mark.parametrize("dtype", [BF, F])
+@pytest.mark.parametrize("v", [1280, 5003, 33001])
+def test_alternatives_among_equal_elements(v, dtype):
+    """Fewer tokens allowed than alternatives asked for, rows of one value, of two, and of whole numbers: candidates that
+    are eight times as many as are wanted, and more."""
+    x, g = logits(6, v, dtype, 17)
+    x[0, torch.rand(v, generator=g) > 0.005] = -INF
+    x[1] = 2.5
+    x[2] = (torch.rand(v, generator=g) > 0.5).to(dtype)
+    x[3] = x[3].round().clamp(-2, 2)
+    x[4, : v // 2] = -INF
+    x[4, v // 2:] = 1.0
+    x[5] = torch.finfo(dtype).min
+    ids = torch.randint(0, v, (6,), generator=g, dtype=torch.int32)
+    for k in (1, 16, 64, 65, 200, 256):
+        say("equal", v, dtype, k)
+        check_scores(x, ids, k)
+        n = 1100  # a workgroup or a wave a row
+        got = B.token_logprobs(many(x, n).cuda(), many(ids, n).cuda(), top_k=k)
+        assert torch.equal(got.top_ids.cpu().long(), many(ref.scores(x, ids, k, 1.0)["top_ids"][0], n))
+
+
 @pytest.mark.parametrize("dtype,scale", [(BF, 1.0), (HF, 2.0), (F, 0.25), (F, 100.0)])
 def test_far_values(dtype, scale):
     """Elements of thousands, and peaks a few units apart."""
