@@ -367,6 +367,8 @@ __device__ __forceinline__ void score_pieces(const ScoreArgs &a, uint64_t row, u
     for (uint32_t u = 0; u < ROW_UNROLL; ++u) {
       const uint32_t g = u * THREADS + tid;
       if (best_at[u] == ~0u) best_at[u] = first;  // nothing but minus infinity
+      // (keys made ahead of the loop take 18 registers: 4 waves a SIMD, not 5, and 4% of the time)
+      asm("" : "+v"(best[u]), "+v"(second[u]), "+v"(third[u]));
       sh.keys[g] = first + g < last ? order_key<T>(best[u], (best_at[u] + g) * P::N, a.index_bits) : 0;
     }
     if (tid == 0) sh.n_chosen = sh.n_deep = sh.n_found = 0;
