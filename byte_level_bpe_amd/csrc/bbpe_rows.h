@@ -166,14 +166,6 @@ __device__ __forceinline__ Partial row_partial(Partial p, Exponent x, Partial *s
   return all;
 }
 
-// What a gradient wants of a row's softmax: p_j = exp2(c * (x_j - max)) / sum,
-// max in the logits' own units and the natural logarithm of the sum.
-// A row with nothing in it has max -inf, one without probabilities (NaN or
-// plus infinity in it) a NaN logarithm.
-struct RowStats {
-  float max, log_sum;
-};
-
 // Calls f with a value of the element type.
 template <typename F>
 void with_element(int dtype, F f) {
@@ -191,17 +183,28 @@ inline uint32_t most_pieces(int dtype, uint32_t vocab) {
 constexpr uint32_t PARTS_MAX = 64;         // parts of a row at most: a wave joins them
 constexpr uint64_t MAX_GROUPS = 1u << 21;  // workgroups (of up to 1,024) a launch: fewer than 2^32 threads
 
-// How rows are cut: waves a workgroup, parts a row and pieces of a part.  Rows of
-// up to 512 pieces go to a wave each (where `small` allows it); longer ones to a
-// workgroup each, and where they are fewer than 1,024, to several, a step each at
-// least (WHY).
+// How rows are cut: waves a workgroup, parts a row and pieces of a part.
+//
+// Short rows go to a wave each (where `small` allows it), which has no barrier to
+// wait at: up to 512 pieces always (8,192 rows of 2,048 in bfloat16: log
+// probabilities 12.2 us, by workgroups 29; with 20 alternatives 26 and 76), up to
+// 1,024 where there are more than 512 rows (8,192 rows of 8,192: 30.6 and 34.4,
+// with alternatives 47 and 86; but 512 rows of 5,000: 7.7 and 6.1).
+//
+// Longer rows go to a workgroup each.  Up to 512 of them would not fill 256 CUs,
+// and go to several, about 1,024 in all, a step each at least, which a second
+// kernel joins (1 row of 100,256: 8.8 us and, by one workgroup, 16; 400 rows: 25 us,
+// with 800 workgroups 26.7, with 2,048 26.7); from 513 rows on the second kernel
+// costs more (1,000 rows: by one each 43 us, by two 49, with 20 alternatives 51
+// and 63).
 struct Cut {
   uint32_t waves, parts, part;
 };
 inline Cut cut_rows(int dtype, uint64_t n_rows, uint32_t vocab, bool small, uint32_t most_parts) {
-  const uint32_t pieces = most_pieces(dtype, vocab);
-  Cut c{small && pieces <= 512 ? 1u : ROW_WAVES, 1, 0};
-  if (c.waves > 1 && n_rows) {
+  const uint32_t per = dtype == BBPE_F32 ? 4 : 8, pieces = most_pieces(dtype, vocab);
+  const bool few = n_rows <= 512, step = (vocab + per - 1) / per <= ROW_STEP;  // (a row within one, but for where it begins)
+  Cut c{small && (pieces <= 512 || (step && !few)) ? 1u : ROW_WAVES, 1, 0};
+  if (c.waves > 1 && n_rows && few && !step) {
     const uint64_t want = (1024 + n_rows - 1) / n_rows;
     uint64_t most = (pieces + ROW_STEP - 1) / ROW_STEP;
     most = most < PARTS_MAX ? most : PARTS_MAX;
