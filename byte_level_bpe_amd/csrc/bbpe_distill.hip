@@ -23,7 +23,13 @@ namespace bbpe {
 namespace {
 
 constexpr uint32_t LIST_MAX = 256;  // listed tokens at most
-constexpr uint32_t HELD = 16;       // pieces that a thread holds from the loss to the gradient
+// Pieces that a thread holds from the loss to the gradient: 64 of the 128 registers
+// that four waves a SIMD leave it.
+constexpr uint32_t HELD = 16;
+// Rows from which on loss and gradient of a long row are by one workgroup.  Fewer do
+// not fill the card, and go to the kernels that cut rows (of 100,277 tokens in
+// bfloat16, 128 rows: 29.4 us cut, 28.3 whole; 64: 24.2 and 26.2; 160: 34.7 and 29.7;
+// 256: 43.9 and 33.4).
 constexpr uint64_t STEP_ROWS = 160;
 
 struct DistillArgs {
@@ -347,6 +353,10 @@ template <typename T, uint32_t WAVES> struct Gradient {
 };
 
 // The loss: a workgroup a row or, SPLIT, a part of one.
+//
+// Bound by the one read of the row: 4,096 rows of 100,277 in bfloat16 with a tail,
+// 157 us (5.2 TB/s).  The listed tokens' bits cost a word of LDS a piece, and a
+// branch that one piece in hundreds takes.
 template <typename T, uint32_t WAVES, bool TAIL, bool SPLIT, uint32_t LIST>
 __global__ __launch_bounds__(64 * WAVES) void k_distill(DistillArgs a) {
   __shared__ DistillShared<WAVES, TAIL, LIST> sh;
@@ -376,6 +386,14 @@ __global__ __launch_bounds__(64 * WAVES) void k_distill(DistillArgs a) {
 // Loss and gradient of a row by a workgroup.  A thread's first HELD pieces stay in
 // its registers between the two and, of 16 waves, some more in LDS; what a row has
 // besides is read again.
+//
+// Bound by the read and the write of a row where it is held (4,096 rows of 100,277
+// in bfloat16: 375 us, 4.4 TB/s; the two kernels apart 480), and by what is read
+// again where it is not (2,048 rows of 200,005 in float32, 256 listed: 805 us, 4.1
+// TB/s in two moves; of a row of 800 KB 384 are held or kept).  All of a workgroup loads
+// before any of it stores, so a CU needs workgroups besides: that is why waves are
+// no more than a row needs.  Loading the next row's pieces ahead spilled (936 us for
+// 403).
 template <typename T, uint32_t WAVES, bool TAIL, uint32_t LIST>
 __global__ __launch_bounds__(64 * WAVES, 4) void k_distill_step(DistillArgs a) {
   constexpr uint32_t THREADS = 64 * WAVES, STEP = THREADS * ROW_UNROLL;
@@ -586,7 +604,14 @@ int bbpe_distill_loss(int dtype, const void *logits, int64_t row_stride, uint64_
     for (a.block0 = 0; a.block0 < blocks; a.block0 += MAX_GROUPS)
       kernel<<<uint32_t(std::min(blocks - a.block0, MAX_GROUPS)), threads, 0, st>>>(a);
   };
-  // loss and gradient of a row by one workgroup
+  // Loss and gradient of a row by one workgroup, of as few waves as hold it:
+  //   one, up to 1,024 pieces (8,192 rows of 8,192 in bfloat16: 61.5 us, four 81.7;
+  //   of 16,384, more than it holds: 157 and 113);
+  //   four, up to 3,584 (4,096 rows of 28,000: 104 us, eight 106; of 32,000, 119 and 113);
+  //   eight, up to 8,192, and for 16-bit rows of any length (2,048 of 65,536: 115 us,
+  //   four 146; of 100,277: 206, sixteen 230);
+  //   sixteen for longer ones of float32 (2,048 of 100,277: 339 us, eight 359; of
+  //   200,005: 771 and 817).
   const uint32_t per = dtype == BBPE_F32 ? 4 : 8, pieces = (vocab + per - 1) / per;
   const bool whole = d_logits && (n_rows >= STEP_ROWS || pieces <= 256 * HELD);
   with_element(dtype, [&](auto t) {

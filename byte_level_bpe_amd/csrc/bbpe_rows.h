@@ -188,8 +188,8 @@ constexpr uint64_t MAX_GROUPS = 1u << 21;  // workgroups (of up to 1,024) a laun
 // Short rows go to a wave each (where `small` allows it), which has no barrier to
 // wait at: up to 512 pieces always (8,192 rows of 2,048 in bfloat16: log
 // probabilities 12.2 us, by workgroups 29; with 20 alternatives 26 and 76), up to
-// 1,024 where there are more than 512 rows (8,192 rows of 8,192: 30.6 and 34.4,
-// with alternatives 47 and 86; but 512 rows of 5,000: 7.7 and 6.1).
+// 1,024 where there are more than 1,024 rows (8,192 rows of 8,192: 30.6 and 34.4,
+// with alternatives 47 and 86; but 600 rows of 5,000: 7.7 and 6.7).
 //
 // Longer rows go to a workgroup each.  Up to 512 of them would not fill 256 CUs,
 // and go to several, about 1,024 in all, a step each at least, which a second
@@ -203,7 +203,7 @@ struct Cut {
 inline Cut cut_rows(int dtype, uint64_t n_rows, uint32_t vocab, bool small, uint32_t most_parts) {
   const uint32_t per = dtype == BBPE_F32 ? 4 : 8, pieces = most_pieces(dtype, vocab);
   const bool few = n_rows <= 512, step = (vocab + per - 1) / per <= ROW_STEP;  // (a row within one, but for where it begins)
-  Cut c{small && (pieces <= 512 || (step && !few)) ? 1u : ROW_WAVES, 1, 0};
+  Cut c{small && (pieces <= 512 || (step && n_rows > 1024)) ? 1u : ROW_WAVES, 1, 0};
   if (c.waves > 1 && n_rows && few && !step) {
     const uint64_t want = (1024 + n_rows - 1) / n_rows;
     uint64_t most = (pieces + ROW_STEP - 1) / ROW_STEP;

@@ -325,6 +325,60 @@ def test_distill_of_many_rows(n, v, k, dtype):
         near(dev, many(dx[0], n), many(dx[1], n), "dx, in one call")
 
 
+def held_many(x, n, offset):
+    return hold(many(x, n), offset)
+
+
+@pytest.mark.parametrize("n", [160, 512, 513, 1024, 1025])
+@pytest.mark.parametrize("pieces,dtype", [(512, BF), (513, F), (1024, BF), (1024, F), (1025, HF)])
+def test_on_either_side_of_a_cut(pieces, dtype, n):
+    """Counts of rows and of pieces of 16 bytes around which another kernel takes them, rows that begin within a piece."""
+    v = pieces * 16 // torch.empty(0, dtype=dtype).element_size()
+    x, g = logits(6, v, dtype, pieces)
+    x[1] = x[1].round()
+    x[2, 50:] = -INF
+    ids = torch.randint(0, v, (6,), generator=g, dtype=torch.int32)
+    ids[3] = v - 1
+    up = torch.randn(6, generator=g)
+    for k, offset in ((0, 1), (20, 3), (64, 0)):
+        say("cut", n, pieces, dtype, k, offset)
+        dev = held_many(x, n, offset)
+        got = B.token_logprobs(dev, many(ids, n).cuda(), top_k=k)
+        for name, (want, bound) in ref.scores(x, ids, k, 1.0).items():
+            if bound is None:
+                assert torch.equal(getattr(got, name).cpu().long(), many(want, n).long()), name
+            else:
+                near(getattr(got, name), many(want, n), many(bound, n), name)
+        if k == 0:
+            continue
+        for tail in (False, True):
+            say("distill", tail)
+            tops, lp = teacher(x, k, g, tail, 1.0)
+            loss, dx, _ = ref.distill(x, tops, lp, tail, 1.0, up)
+            a = (many(tops, n).cuda(), many(lp, n).cuda())
+            near(B.distill_loss(dev, *a, tail=tail).loss, many(loss[0], n), many(loss[1], n), "loss")
+            out = torch.empty_like(dev)
+            both = B.distill_loss(dev, *a, tail=tail, weights=many(up, n).cuda(), dlogits=out)
+            near(both.loss, many(loss[0], n), many(loss[1], n), "loss, in one call")
+            near(out, many(dx[0], n), many(dx[1], n), "dx, in one call")
+
+
+@pytest.mark.parametrize("v,dtype", [(28672, BF), (28680, BF), (14340, F), (65536, HF), (65544, BF), (32772, F), (4096, F)])
+def test_gradients_of_rows_that_fill_their_waves(v, dtype):
+    """Loss and gradient in one call at the longest rows of so many waves, and a piece longer."""
+    x, g = logits(4, v, dtype, v)
+    w = torch.randn(4, generator=g)
+    for tail in (False, True):
+        say("fill", v, dtype, tail)
+        ids, lp = teacher(x, 64, g, tail, 1.0)
+        n = 160
+        loss, dx, _ = ref.distill(x, ids, lp, tail, 1.0, w)
+        out = torch.empty(n, v, dtype=dtype, device="cuda")
+        both = B.distill_loss(held_many(x, n, 1), many(ids, n).cuda(), many(lp, n).cuda(), tail=tail, weights=many(w, n).cuda(), dlogits=out)
+        near(both.loss, many(loss[0], n), many(loss[1], n), "loss")
+        near(out, many(dx[0], n), many(dx[1], n), "dx")
+
+
 @pytest.mark.parametrize("tail", [False, True])
 def test_distill_odd_rows(tail):
     """No teacher, tokens named twice, ids out of range, teachers and students with no probability for a token,
