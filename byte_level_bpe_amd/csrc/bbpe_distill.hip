@@ -562,7 +562,8 @@ int bbpe_distill_loss_backward(int dtype, const void *logits, int64_t row_stride
                                const float *d_stats, const float *d_grad, void *d_logits, int64_t dl_stride, void *hip_stream) {
   const int rc = check(dtype, logits, row_stride, n_rows, vocab, d_top_ids, d_top_logprobs, top_k, tail, scale);
   if (rc) return rc;
-  if (bad_logits(dtype, d_logits, dl_stride, n_rows, vocab, true) || (n_rows && (!d_stats || !d_grad)) ||
+  if (bad_logits(dtype, d_logits, dl_stride, n_rows, vocab, true) ||
+      crossing(dtype, logits, row_stride, d_logits, dl_stride, n_rows, vocab) || (n_rows && (!d_stats || !d_grad)) ||
       (address(d_stats) & 15) || (address(d_grad) & 3))
     return BBPE_E_INVALID_ARG;
   if (n_rows == 0) return BBPE_OK;
@@ -583,7 +584,8 @@ int bbpe_distill_loss(int dtype, const void *logits, int64_t row_stride, uint64_
   if (rc) return rc;
   if ((n_rows && (!d_loss || !d_lse || !d_stats)) || ((address(d_loss) | address(d_lse) | address(d_weights)) & 3) ||
       (address(d_stats) & 15) || (d_weights == nullptr) != (d_logits == nullptr) ||
-      (d_logits && bad_logits(dtype, d_logits, dl_stride, n_rows, vocab, true)))
+      (d_logits && (bad_logits(dtype, d_logits, dl_stride, n_rows, vocab, true) ||
+                    crossing(dtype, logits, row_stride, d_logits, dl_stride, n_rows, vocab))))
     return BBPE_E_INVALID_ARG;
   if (n_rows == 0) return BBPE_OK;
   const Cut cut = cut_rows(dtype, n_rows, vocab, top_k <= 64, PARTS_MAX);

@@ -228,5 +228,20 @@ inline bool bad_logits(int dtype, const void *x, int64_t stride, uint64_t rows, 
   if (bad_sizes(dtype, rows, vocab) || (rows && (!x || (address(x) & (dtype == BBPE_F32 ? 3 : 1))))) return true;
   return grad && rows > 1 && (stride < 0 ? -stride : stride) < int64_t(vocab);
 }
+// Whether a gradient's rows lie in the logits' other than each in its own place:
+// workgroups would read what others have written.
+inline bool crossing(int dtype, const void *x, int64_t x_stride, const void *dx, int64_t dx_stride, uint64_t rows, uint32_t vocab) {
+  typedef __int128 wide;  // (strides are any numbers)
+  const wide size = dtype == BBPE_F32 ? 4 : 2, row = vocab * size, xs = x_stride * size, ds = dx_stride * size, last = wide(rows) - 1;
+  const wide d = wide(address(dx)) - wide(address(x));
+  if (rows == 0 || (d == 0 && (rows == 1 || xs == ds))) return false;
+  const wide x_from = xs < 0 ? last * xs : 0, x_to = (xs < 0 ? 0 : last * xs) + row;
+  const wide d_from = d + (ds < 0 ? last * ds : 0), d_to = d + (ds < 0 ? 0 : last * ds) + row;
+  if (x_to <= d_from || d_to <= x_from) return false;
+  if (rows == 1 || xs != ds) return true;
+  // rows that take turns with the other matrix's (a gradient's are a row apart at least)
+  const wide s = xs < 0 ? -xs : xs, r = (d % s + s) % s;
+  return r < row || r > s - row;
+}
 
 }  // namespace bbpe

@@ -730,7 +730,9 @@ int bbpe_token_logprobs_backward(int dtype, const void *logits, int64_t row_stri
                                  int64_t dl_stride, void *hip_stream) {
   const int rc = check_scores(dtype, logits, row_stride, n_rows, vocab, top_k, scale);
   if (rc) return rc;
-  if (bad_logits(dtype, d_logits, dl_stride, n_rows, vocab, true)) return BBPE_E_INVALID_ARG;
+  if (bad_logits(dtype, d_logits, dl_stride, n_rows, vocab, true) ||
+      crossing(dtype, logits, row_stride, d_logits, dl_stride, n_rows, vocab))
+    return BBPE_E_INVALID_ARG;
   if (n_rows && (!d_ids || !d_entropy || !d_stats || (g_top && top_k && !d_top_ids))) return BBPE_E_INVALID_ARG;
   if ((address(d_ids) | address(d_entropy) | address(d_top_ids) | address(g_logprobs) | address(g_entropy) | address(g_lse) |
        address(g_top)) & 3 || (address(d_stats) & 7))

@@ -559,7 +559,8 @@ int bbpe_token_logprobs(int dtype, const void *logits, int64_t row_stride, uint6
 /* Its backward pass: from the gradients of d_logprobs, d_entropy, d_lse
  * ([n_rows] float) and d_top_logprobs ([n_rows][top_k]; null: zeros) and what
  * the forward call left, the gradient of the logits, of dtype, rounded once.
- * d_logits may be logits (with the same stride).  A row whose given gradients
+ * d_logits may be logits (with the same stride; rows that lie across the logits'
+ * otherwise are refused).  A row whose given gradients
  * are zeros gets zeros, whatever its logits hold. */
 int bbpe_token_logprobs_backward(int dtype, const void *logits, int64_t row_stride,
                                  uint64_t n_rows, uint32_t vocab, const int32_t *d_ids,
@@ -585,7 +586,7 @@ int bbpe_token_logprobs_backward(int dtype, const void *logits, int64_t row_stri
  *                      gradient; 16-byte aligned);
  *   d_weights[n_rows], d_logits: both or neither: the gradient of the weighted
  *                      sum of the losses, in the same call (as the backward call
- *                      makes it; d_logits may be logits).
+ *                      makes it; d_logits may be logits, as above).
  *
  * A row without a teacher (no entry; without a tail also none above minus
  * infinity) has loss 0 and no gradient, whatever its logits hold.  A listed
@@ -599,7 +600,7 @@ int bbpe_distill_loss(int dtype, const void *logits, int64_t row_stride, uint64_
                       void *d_workspace, uint64_t workspace_bytes, void *hip_stream);
 
 /* Its backward pass, d_grad[n_rows] the gradients of the losses (a row's of 0
- * gives zeros, whatever its logits hold).  d_logits may be logits. */
+ * gives zeros, whatever its logits hold).  d_logits may be logits, as above. */
 int bbpe_distill_loss_backward(int dtype, const void *logits, int64_t row_stride, uint64_t n_rows,
                                uint32_t vocab, const int32_t *d_top_ids,
                                const float *d_top_logprobs, uint32_t top_k, int tail, float scale,

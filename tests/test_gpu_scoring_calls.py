@@ -227,6 +227,54 @@ def test_rows_far_apart():
     assert not store[v:far].any() and not store[far + v:2 * far].any()
 
 
+def test_gradients_between_the_logits_rows():
+    n, v = 40, 5003
+    g = torch.Generator(device="cuda").manual_seed(8)
+    both = torch.randn(n, 2 * v, generator=g, device="cuda")
+    x, dx = both[:, v:], both[:, :v]
+    kept, ids = x.clone(), torch.randint(0, v, (n,), generator=g, device="cuda", dtype=torch.int32)
+    w = torch.randn(n, generator=g, device="cuda")
+    got = B.token_logprobs(x, ids, top_k=6)
+    want = B.token_logprobs_backward(x, ids, got, grad_logprobs=w)
+    B.token_logprobs_backward(x, ids, got, grad_logprobs=w, dlogits=dx)
+    assert torch.equal(dx, want) and torch.equal(x, kept)
+    apart = torch.empty_like(kept)
+    B.distill_loss(x, got.top_ids, got.top_logprobs, tail=True, weights=w, dlogits=apart)
+    B.distill_loss(x, got.top_ids, got.top_logprobs, tail=True, weights=w, dlogits=dx)
+    assert torch.equal(x, kept) and bool((dx - apart).abs().max() <= 1e-6)
+    with pytest.raises(Exception):
+        B.distill_loss(x, got.top_ids, got.top_logprobs, tail=True, weights=w, dlogits=both[:, 1:v + 1])
+
+
+def test_more_rows_than_a_launch_takes():
+    n, v, few = (1 << 21) + 301, 9, 301
+    g = torch.Generator().manual_seed(3)
+    x = torch.randn(few, v, generator=g).to(torch.bfloat16)
+    ids = torch.randint(0, v, (few,), generator=g, dtype=torch.int32)
+    lp, tops = torch.log_softmax(x.float(), 1).topk(3, 1)
+    w = torch.randn(few, generator=g)
+    at = (torch.arange(n) % few).cuda()
+    say("few")
+    small = [t.cuda() for t in (x, ids, tops.int(), lp, w)]
+    large = [t[at] for t in small]
+
+    def run(x, ids, tops, lp, w):
+        a = B.token_logprobs(x, ids, top_k=2)
+        b = B.distill_loss(x, tops, lp, tail=True)
+        out = torch.empty_like(x)
+        c = B.distill_loss(x, tops, lp, tail=True, weights=w, dlogits=out)
+        return [a.logprobs, a.entropy, a.lse, a.ranks, a.top_ids, a.top_logprobs, b.loss, c.loss, out,
+                B.token_logprobs_backward(x, ids, a, grad_logprobs=w), B.distill_loss_backward(w, x, tops, lp, b, tail=True)]
+
+    # (a row's last digits may depend on where it begins in 16 bytes: eight rows of nine elements on, the same)
+    want = run(*[t[(torch.arange(8 * few) % few).cuda()] for t in small])
+    say("many")
+    got = run(*large)
+    at = (torch.arange(n) % (8 * few)).cuda()
+    for i, (p, q) in enumerate(zip(got, want)):
+        assert torch.equal(p, q[at]), i
+
+
 def test_more_tokens_than_bits_at_a_time():
     """A vocabulary of a million and some: the list's bits are set several times in a row, and places pass 2^20."""
     v, k = 1100003, 100

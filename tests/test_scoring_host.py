@@ -94,6 +94,14 @@ def test_distill_backward_refuses(bad):
     assert distill_back_call(**bad) == B.E_INVALID_ARG
 
 
+@pytest.mark.parametrize("call", [scores_back_call, distill_call, distill_back_call])
+@pytest.mark.parametrize("across", [dict(dx=X + 2), dict(dx=X - 198), dict(dx=X + 200), dict(dstride=200), dict(stride=0), dict(dstride=-100),
+                                    dict(stride=150, dstride=150, dx=X + 198), dict(stride=150, dstride=150, dx=X + 102), dict(stride=-100, dx=X),
+                                    dict(n=1, stride=7, dstride=7, dx=X + 14), dict(stride=1 << 62, dx=X + 2)])
+def test_gradients_across_the_logits_are_refused(call, across):
+    assert call(**across) == B.E_INVALID_ARG
+
+
 def test_no_rows_are_nothing_to_do():
     assert scores_call(n=0, x=None, ids=None) == 0 and scores_back_call(n=0, x=None, dx=None) == 0
     assert distill_call(n=0, x=None) == 0 and distill_back_call(n=0, x=None, dx=None) == 0
