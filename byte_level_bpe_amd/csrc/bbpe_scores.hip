@@ -25,7 +25,7 @@ constexpr uint32_t TOP_MAX = 256;   // alternatives at most
 __host__ __device__ constexpr uint32_t with_slack(uint32_t k) { return k + k / 4 + 16; }
 constexpr uint32_t TOP_ROOM = with_slack(TOP_MAX);
 // Alternatives up to which a wave may take a row: of a wave's 256 groups, 96 reach
-// the bar at most, and LDS of 6 KB lets 24 waves onto a CU.
+// the bar at most, and 5.3 KB of LDS let 28 waves (all that its registers do) onto a CU.
 constexpr uint32_t SMALL_TOP = 64;
 constexpr uint32_t KEPT_ROOM = (TOP_ROOM + 63) / 64 * 64;
 constexpr uint32_t JOIN_KEYS = 4096;  // alternatives of all parts at most: 32 KB of LDS in the kernel that joins them
