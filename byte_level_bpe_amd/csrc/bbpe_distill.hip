@@ -8,6 +8,11 @@
 // held against p_r, the student's sum over tokens that are not listed:
 //   loss = sum_t q_t (log q_t - log p_t) + q_r (log q_r - log p_r),
 //   dz_j = p_j (sum q + q_r) - [j not listed] q_r p_j / p_r - sum_{t: t = j} q_t.
+// p_j / p_r is the softmax of the tokens that are not listed by themselves.  Where
+// they lie far below the listed ones, as under a finite mask, p_j and p_r are below
+// any float while that is not: so what concerns it is relative to their own largest
+// element u.  With s = sum w and s_r of theirs, relative to the row's and to u,
+//   dz_j = exp(z_j - u) ((sum q + q_r) exp(u - max) / s - q_r / s_r),   j not listed.
 //
 // One pass over the row for the largest element and the sum of weights relative
 // to it; with a tail, over the tokens that are not listed alone, the listed
@@ -161,20 +166,21 @@ __device__ __forceinline__ void read_list(const DistillArgs &a, const T *x, cons
 // The end of a row, by the wave that has read the list: p holds the weights of the
 // whole row (with a tail: of the tokens that are not listed).
 //
-// stats: the row's maximum and the logarithm of its sum of weights; the factor
-// of p_j in the gradient, of tokens that are not listed; with a tail the listed
-// ones' factor, without one the logarithm of the teacher's sum.
+// stats: the row's maximum, and the logarithm of its sum of weights over the
+// factor of p_j in the gradient.  Without a tail then 0 and the logarithm of the
+// teacher's sum; with one, for tokens that are not listed, their maximum and the
+// factor of weights relative to that.
 template <uint32_t LIST>
-__device__ __forceinline__ float4 end_row(const DistillArgs &a, uint64_t row, Partial p, const ListShared<LIST> &sh) {
+__device__ __forceinline__ float4 end_row(const DistillArgs &a, uint64_t row, bool tail, Partial p, const ListShared<LIST> &sh) {
   const uint32_t lane = threadIdx.x & 63;
   float high = p.max;
-  if (a.tail) {
+  if (tail) {
     for (uint32_t t = lane; t < a.k; t += 64) high = fmaxf(high, sh.own[t]);
     high = wave_max(high);
   }
   const float ref = finite_max(high);
   double others = p.sum, listed = 0.0;
-  if (a.tail) {
+  if (tail) {
     if (p.max != -INFINITY) others *= exp((double(p.max) - ref) * a.scale);
     for (uint32_t t = lane; t < a.k; t += 64) listed += sh.first[t] ? exp((double(sh.own[t]) - ref) * a.scale) : 0.0;
     listed = wave_sum(listed);
@@ -187,31 +193,29 @@ __device__ __forceinline__ float4 end_row(const DistillArgs &a, uint64_t row, Pa
   }
   loss = wave_sum(loss);
   const double rest = sh.rest, mass = sh.mass;
-  double ratio = 0.0;
   if (rest > 0.0) {
-    // log p_r = -log(1 + listed / others): of the ratio, not of two logarithms
-    loss += rest * (log(rest) + log1p(listed / others));
-    ratio = others > 0.0 ? rest * (1.0 + listed / others) : 0.0;
+    // log p_r = -log(1 + listed / others): of the ratio, not of two logarithms, until
+    // it leaves the range of numbers and 1 is nothing beside it
+    // (__any: all lanes hold the same, and a branch leaves one of the logarithms out)
+    loss += rest * (log(rest) + (__any(others > 1e-200) ? log1p(listed / others) : log(listed / p.sum) - (double(p.max) - ref) * a.scale));
   }
   const bool none = high == -INFINITY && sum == 0.0, bad = !(sum == sum) || high == INFINITY;
   const float nan = __uint_as_float(0x7FC00000u);
-  float4 st = make_float4(high, float(log_sum), 0.0f, 0.0f);
+  float4 st = make_float4(high, float(log_sum), 0.0f, float(sh.log_norm));
+  if (tail) {
+    const bool empty = p.max == -INFINITY;  // of tokens that are not listed
+    st.y = float(log_sum - log(mass + rest));
+    st.z = finite_max(p.max);
+    st.w = empty ? 0.0f : float((mass + rest) / sum * (others / p.sum) - rest / p.sum);
+  }
   if (!sh.some) {  // no teacher: no loss and no gradient, whatever the row holds
     loss = 0.0;
     st.x = -INFINITY;
   } else if (bad) {
     loss = nan;
-    st.x = 0.0f;
-    st.y = nan;
+    st = make_float4(0.0f, nan, 0.0f, tail ? nan : st.w);
   } else if (none) {
     loss = INFINITY;
-  }
-  if (a.tail) {
-    st.z = float(mass + rest - ratio);
-    st.w = float(mass + rest);
-  } else {
-    st.z = 1.0f;
-    st.w = float(sh.log_norm);
   }
   if (lane == 0) {
     a.loss[row] = float(loss);
@@ -301,22 +305,23 @@ __device__ __forceinline__ void add_pieces(const DistillArgs &a, const Row<const
 template <typename T, uint32_t WAVES> struct Gradient {
   static constexpr uint32_t THREADS = 64 * WAVES;
   float4 st;
-  float g, inv;
+  float g, inv, base, factor;  // of tokens that are not listed: g * factor * exp(scale * (x - base))
   Exponent x2;
   bool zero;
 
-  __device__ __forceinline__ Gradient(const DistillArgs &a, float4 stats, float grad) : st(stats), g(grad * a.scale), x2(a.x2) {
+  __device__ __forceinline__ Gradient(const DistillArgs &a, bool tail, float4 stats, float grad) : st(stats), g(grad * a.scale), x2(a.x2) {
     zero = st.x == -INFINITY || g == 0.0f;
     inv = __builtin_amdgcn_exp2f(-st.y * LOG2E);
+    base = tail ? st.z : st.x;
+    factor = tail ? st.w : inv;
   }
-  __device__ __forceinline__ float weight(float v) const { return weight_of(v - st.x, x2); }
   __device__ __forceinline__ typename Piece<T>::val of(typename Piece<T>::raw raw) const {
     typename Piece<T>::val v = 0.0f;
     if (zero) return v;
-    const float all = g * st.z * inv;
+    const float all = g * factor;
     v = values<T>(raw);
 #pragma unroll
-    for (uint32_t e = 0; e < Piece<T>::N; ++e) v[e] = weight(v[e]) * all;
+    for (uint32_t e = 0; e < Piece<T>::N; ++e) v[e] = weight_of(v[e] - base, x2) * all;  // (of listed ones anything: they are written once more)
     return v;
   }
   // Pieces [from, to), as out has them.
@@ -347,7 +352,7 @@ template <typename T, uint32_t WAVES> struct Gradient {
         sum = 0.0f;
         for (uint32_t i = 0; i < a.k; ++i) sum += ids[i] == id ? float(q[i]) : 0.0f;
       }
-      out.at[place] = T(g * ((a.tail ? st.w : st.z) * inv * weight(own[t]) - sum));
+      out.at[place] = T(g * (inv * weight_of(own[t] - st.x, x2) - sum));
     }
   }
 };
@@ -379,7 +384,7 @@ __global__ __launch_bounds__(64 * WAVES) void k_distill(DistillArgs a) {
   if (SPLIT) {
     if (threadIdx.x == 0) a.parted[block] = s;
   } else if (threadIdx.x < 64) {
-    end_row(a, row, s, sh.list);
+    end_row(a, row, TAIL, s, sh.list);
   }
 }
 
@@ -434,11 +439,11 @@ __global__ __launch_bounds__(64 * WAVES, 4) void k_distill_step(DistillArgs a) {
   add_pieces<T>(a, r, near, pieces, sh, s);
   s = row_partial<WAVES>(s, a.x2, sh.sums);
   if (tid < 64) {
-    const float4 st = end_row(a, row, s, sh.list);
+    const float4 st = end_row(a, row, TAIL, s, sh.list);
     if (tid == 0) sh.stats = st;
   }
   __syncthreads();
-  const Gradient<T, WAVES> grad(a, sh.stats, weight);
+  const Gradient<T, WAVES> grad(a, TAIL, sh.stats, weight);
   const Row<T> out = r.over(dx);
 #pragma unroll
   for (uint32_t i = 0; i < HELD; ++i) {
@@ -469,7 +474,7 @@ __global__ __launch_bounds__(64) void k_distill_join(DistillArgs a) {
   if (a.tail) read_names<1>(a, 0, sh);
   p = wave_partial(p, a.x2);
   __syncthreads();
-  end_row(a, row, p, sh);
+  end_row(a, row, a.tail, p, sh);
 }
 
 // The gradient by itself: a workgroup a part of a row.
@@ -484,7 +489,7 @@ __global__ __launch_bounds__(64 * WAVES) void k_distill_back(DistillArgs a) {
   const Row<T> r(static_cast<T *>(a.dx) + int64_t(row) * a.dx_stride, a.vocab);
   const uint32_t from = uint32_t(block % a.parts) * a.part, to = min(r.pieces(), from + a.part);
   if (from >= to) return;  // (parts are counted for rows that begin anywhere)
-  const Gradient<T, WAVES> grad(a, a.stats[row], a.grad[row]);
+  const Gradient<T, WAVES> grad(a, a.tail, a.stats[row], a.grad[row]);
   for (uint32_t t = threadIdx.x; t < LIST_MAX; t += THREADS) {
     const int32_t id = t < a.k ? a.ids[row * a.k + t] : -1;
     const bool there = id >= 0 && uint32_t(id) < a.vocab;
