@@ -166,10 +166,11 @@ __device__ __forceinline__ void read_list(const DistillArgs &a, const T *x, cons
 // The end of a row, by the wave that has read the list: p holds the weights of the
 // whole row (with a tail: of the tokens that are not listed).
 //
-// stats: the row's maximum, and the logarithm of its sum of weights over the
-// factor of p_j in the gradient.  Without a tail then 0 and the logarithm of the
-// teacher's sum; with one, for tokens that are not listed, their maximum and the
-// factor of weights relative to that.
+// stats: the row's maximum, and the factor of p_j in the gradient over the row's sum
+// of weights (a quotient, not its logarithm, which in 32 bits would put every
+// probability off by up to a millionth, all the same way).  Without a tail then 0 and
+// the logarithm of the teacher's sum; with one, for tokens that are not listed, their
+// maximum and the factor of weights relative to that.
 template <uint32_t LIST>
 __device__ __forceinline__ float4 end_row(const DistillArgs &a, uint64_t row, bool tail, Partial p, const ListShared<LIST> &sh) {
   const uint32_t lane = threadIdx.x & 63;
@@ -201,10 +202,10 @@ __device__ __forceinline__ float4 end_row(const DistillArgs &a, uint64_t row, bo
   }
   const bool none = high == -INFINITY && sum == 0.0, bad = !(sum == sum) || high == INFINITY;
   const float nan = __uint_as_float(0x7FC00000u);
-  float4 st = make_float4(high, float(log_sum), 0.0f, float(sh.log_norm));
+  float4 st = make_float4(high, float(1.0 / sum), 0.0f, float(sh.log_norm));
   if (tail) {
     const bool empty = p.max == -INFINITY;  // of tokens that are not listed
-    st.y = float(log_sum - log(mass + rest));
+    st.y = float((mass + rest) / sum);
     st.z = finite_max(p.max);
     st.w = empty ? 0.0f : float((mass + rest) / sum * (others / p.sum) - rest / p.sum);
   }
@@ -305,15 +306,14 @@ __device__ __forceinline__ void add_pieces(const DistillArgs &a, const Row<const
 template <typename T, uint32_t WAVES> struct Gradient {
   static constexpr uint32_t THREADS = 64 * WAVES;
   float4 st;
-  float g, inv, base, factor;  // of tokens that are not listed: g * factor * exp(scale * (x - base))
+  float g, base, factor;  // of tokens that are not listed: g * factor * exp(scale * (x - base))
   Exponent x2;
   bool zero;
 
   __device__ __forceinline__ Gradient(const DistillArgs &a, bool tail, float4 stats, float grad) : st(stats), g(grad * a.scale), x2(a.x2) {
     zero = st.x == -INFINITY || g == 0.0f;
-    inv = __builtin_amdgcn_exp2f(-st.y * LOG2E);
     base = tail ? st.z : st.x;
-    factor = tail ? st.w : inv;
+    factor = tail ? st.w : st.y;
   }
   __device__ __forceinline__ typename Piece<T>::val of(typename Piece<T>::raw raw) const {
     typename Piece<T>::val v = 0.0f;
@@ -352,7 +352,7 @@ template <typename T, uint32_t WAVES> struct Gradient {
         sum = 0.0f;
         for (uint32_t i = 0; i < a.k; ++i) sum += ids[i] == id ? float(q[i]) : 0.0f;
       }
-      out.at[place] = T(g * (inv * weight_of(own[t] - st.x, x2) - sum));
+      out.at[place] = T(g * (st.y * weight_of(own[t] - st.x, x2) - sum));
     }
   }
 };

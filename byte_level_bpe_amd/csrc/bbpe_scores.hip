@@ -207,7 +207,7 @@ __device__ __forceinline__ void write_row(const ScoreArgs &a, uint64_t row, cons
   a.ranks[row] = given.there && !end.bad ? above + 1 : 0;
   a.entropy[row] = end.bad ? nan : end.none ? 0.0f : float(end.log_sum - double(end.p.mean) / end.p.sum * a.scale);
   a.lse[row] = end.bad ? nan : end.none ? -INFINITY : float(double(end.p.max) * a.scale + end.log_sum);
-  a.stats[row] = end.bad ? make_float2(0.0f, nan) : make_float2(end.p.max, float(end.log_sum));
+  a.stats[row] = end.bad ? make_float2(0.0f, nan) : make_float2(end.p.max, float(1.0 / end.p.sum));
 }
 template <typename T>
 __device__ __forceinline__ void write_top(const ScoreArgs &a, uint64_t row, uint32_t lead, const RowEnd &end, uint32_t t, uint64_t key) {
@@ -591,8 +591,8 @@ __global__ __launch_bounds__(64 * WAVES) void k_scores_back(ScoreBackArgs a) {
   // p (g + gh (log p + entropy)) = w (alpha + beta t), t = scale log2(e) (x - max), w = exp2(t);
   // t is bounded where w is 0, so that their product is 0
   const bool zero = st.x == -INFINITY || (g == 0.0f && gh == 0.0f && !any);
-  const float inv = a.scale * __builtin_amdgcn_exp2f(-st.y * LOG2E);
-  const float alpha = -inv * (g + gh * (a.entropy[row] - st.y)), beta = -inv * gh * float(LN2);
+  const float inv = a.scale * st.y;
+  const float alpha = -inv * (g + gh * (a.entropy[row] + logf(st.y))), beta = -inv * gh * float(LN2);
   const auto of = [&](float v) {
     const float d = v - st.x, t = fmaxf(__builtin_fmaf(d, a.x2.low, d * a.x2.c), -16384.0f);
     return __builtin_amdgcn_exp2f(t) * (alpha + beta * t);

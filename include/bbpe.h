@@ -546,8 +546,8 @@ int bbpe_tree_attention(const void *q, int64_t q_ts, int64_t q_hs, uint64_t n_to
  *                      without probabilities);
  *   d_top_ids, d_top_logprobs [n_rows][top_k]: the first top_k in that order (a
  *                      row without probabilities: -1 and NaN);
- *   d_stats[n_rows][2]: for the gradient: the row's largest logit, and the
- *                      logarithm of its sum of exp(scale * (logit - largest)). */
+ *   d_stats[n_rows][2]: for the gradient: the row's largest logit, and one over
+ *                      its sum of exp(scale * (logit - largest)). */
 int bbpe_token_logprobs_workspace_bytes(int dtype, uint64_t n_rows, uint32_t vocab,
                                         uint32_t top_k, uint64_t *out_bytes);
 int bbpe_token_logprobs(int dtype, const void *logits, int64_t row_stride, uint64_t n_rows,

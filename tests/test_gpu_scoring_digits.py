@@ -1,0 +1,62 @@
+"""Digits of the gradients between logits and ids, on the GPU: rows whose sums of weights are exact, so that a
+probability is off by what its last few operations round."""
+import math
+
+import pytest
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+import byte_level_bpe_amd as B  # noqa: E402
+from tests.serving_reference import U32  # noqa: E402
+from tests.test_gpu_scoring import F, near  # noqa: E402
+from tests.test_gpu_serving import say  # noqa: E402
+
+SIZES = [300, 1280, 5003, 33001, 50257, 100277, 200005]
+
+
+@pytest.fixture(scope="module", autouse=True)
+def need_gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+
+
+def flat(v):
+    """Rows of one value, of one value in every third place, and of one value up to the middle: weights are 1 or 0."""
+    x = torch.full((3, v), 0.5)
+    x[1, torch.arange(v) % 3 != 0] = -math.inf
+    x[2, v // 2:] = -math.inf
+    return x, torch.exp(x.double() - 0.5) / torch.exp(x.double() - 0.5).sum(1, keepdim=True)
+
+
+@pytest.mark.parametrize("v", SIZES)
+def test_probabilities_in_the_scores_gradient(v):
+    """The log-sum's gradient is p: one over the sum, rounded once, times 1.  The entropy's is 0 where all that can
+    come is alike: of log p + entropy, two numbers up to 13 that are a half step off each, three with their sum."""
+    say("scores", v)
+    x, p = flat(v)
+    dev, ids = x.cuda(), torch.tensor([0, 3, 1], dtype=torch.int32, device="cuda")
+    got, one = B.token_logprobs(dev, ids), torch.ones(3, device="cuda")
+    near(B.token_logprobs_backward(dev, ids, got, grad_lse=one), p, 2 * U32 * p, "p")
+    near(B.token_logprobs_backward(dev, ids, got, grad_entropy=one), 0 * p, 4 * U32 * 13 * p, "entropy")
+
+
+@pytest.mark.parametrize("tail", [False, True])
+@pytest.mark.parametrize("v", SIZES)
+def test_probabilities_in_the_distillation_gradient(v, tail):
+    """Where a token is not listed the gradient is p (times what p_r and the list's remainder make of it): a factor in
+    64 bits, rounded once, times 1."""
+    say("distillation", v, tail)
+    x, p = flat(v)
+    dev = x.cuda()
+    ids = torch.tensor([[0, 3, 6, 9]] * 3, dtype=torch.int32)
+    lp = torch.full((3, 4), math.log(0.125))
+    other = torch.ones(3, v).scatter_(1, ids.long(), 0.0).double()
+    mass = torch.exp(lp.double()).sum(1, keepdim=True)
+    want = p * (1 - (1 - mass) / (p * other).sum(1, keepdim=True)) * other if tail else p * other
+    a, one = (ids.cuda(), lp.cuda()), torch.ones(3, device="cuda")
+    apart = B.distill_loss_backward(one, dev, *a, B.distill_loss(dev, *a, tail=tail), tail=tail)
+    both = torch.empty_like(dev)
+    B.distill_loss(dev, *a, tail=tail, weights=one, dlogits=both)
+    for got, what in ((apart, "apart"), (both, "in one call")):
+        near(got.cpu().double() * other, want, 2 * U32 * want.abs(), what)
