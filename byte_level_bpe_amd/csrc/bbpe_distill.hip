@@ -168,9 +168,10 @@ __device__ __forceinline__ void read_list(const DistillArgs &a, const T *x, cons
 //
 // stats: the row's maximum, and the factor of p_j in the gradient over the row's sum
 // of weights (a quotient, not its logarithm, which in 32 bits would put every
-// probability off by up to a millionth, all the same way).  Without a tail then 0 and
-// the logarithm of the teacher's sum; with one, for tokens that are not listed, their
-// maximum and the factor of weights relative to that.
+// probability off by up to a millionth, all the same way).  Without a tail then the
+// logarithm of the teacher's sum in two parts (any constant may be added to a list:
+// in one, an offset of 10,000 would put all of q off by up to 5e-4); with one, for
+// tokens that are not listed, their maximum and the factor of weights relative to that.
 template <uint32_t LIST>
 __device__ __forceinline__ float4 end_row(const DistillArgs &a, uint64_t row, bool tail, Partial p, const ListShared<LIST> &sh) {
   const uint32_t lane = threadIdx.x & 63;
@@ -202,7 +203,7 @@ __device__ __forceinline__ float4 end_row(const DistillArgs &a, uint64_t row, bo
   }
   const bool none = high == -INFINITY && sum == 0.0, bad = !(sum == sum) || high == INFINITY;
   const float nan = __uint_as_float(0x7FC00000u);
-  float4 st = make_float4(high, float(1.0 / sum), 0.0f, float(sh.log_norm));
+  float4 st = make_float4(high, float(1.0 / sum), float(sh.log_norm), float(sh.log_norm - double(float(sh.log_norm))));
   if (tail) {
     const bool empty = p.max == -INFINITY;  // of tokens that are not listed
     st.y = float((mass + rest) / sum);
@@ -214,7 +215,7 @@ __device__ __forceinline__ float4 end_row(const DistillArgs &a, uint64_t row, bo
     st.x = -INFINITY;
   } else if (bad) {
     loss = nan;
-    st = make_float4(0.0f, nan, 0.0f, tail ? nan : st.w);
+    st = make_float4(0.0f, nan, nan, nan);
   } else if (none) {
     loss = INFINITY;
   }
@@ -478,8 +479,14 @@ __global__ __launch_bounds__(64) void k_distill_join(DistillArgs a) {
 }
 
 // The gradient by itself: a workgroup a part of a row.
+//
+// Bound by the row's read and write (4,096 rows of 100,277 in bfloat16 with a tail: 309
+// us, 5.3 TB/s).  A wave by itself is held to the registers of eight on a SIMD, which the
+// list's exponentials in 64 bits would pass (65,536 rows of 1,280 76.1 us, with seven
+// 83.5; of 1,024 60.3 and 68.8; of 2,048 119.7 and 117.1); workgroups of four are not (those
+// 4,096 rows would take 324 us).
 template <typename T, uint32_t WAVES>
-__global__ __launch_bounds__(64 * WAVES) void k_distill_back(DistillArgs a) {
+__global__ __launch_bounds__(64 * WAVES, WAVES == 1 ? 8 : 1) void k_distill_back(DistillArgs a) {
   constexpr uint32_t THREADS = 64 * WAVES;
   __shared__ alignas(16) int32_t ids[LIST_MAX];
   __shared__ float own[LIST_MAX], q[LIST_MAX];
@@ -490,12 +497,13 @@ __global__ __launch_bounds__(64 * WAVES) void k_distill_back(DistillArgs a) {
   const uint32_t from = uint32_t(block % a.parts) * a.part, to = min(r.pieces(), from + a.part);
   if (from >= to) return;  // (parts are counted for rows that begin anywhere)
   const Gradient<T, WAVES> grad(a, a.tail, a.stats[row], a.grad[row]);
-  for (uint32_t t = threadIdx.x; t < LIST_MAX; t += THREADS) {
+  const double norm = a.tail ? 0.0 : double(grad.st.z) + grad.st.w;
+  for (uint32_t t = threadIdx.x; t < (a.k + 3) / 4 * 4; t += THREADS) {  // (named() reads four at a time)
     const int32_t id = t < a.k ? a.ids[row * a.k + t] : -1;
     const bool there = id >= 0 && uint32_t(id) < a.vocab;
     ids[t] = there ? id : -1;
     if (t >= a.k) continue;
-    q[t] = there ? __builtin_amdgcn_exp2f((a.lp[row * a.k + t] - (a.tail ? 0.0f : grad.st.w)) * LOG2E) : 0.0f;
+    q[t] = there ? float(exp(double(a.lp[row * a.k + t]) - norm)) : 0.0f;
     own[t] = there && (r.lead + uint32_t(id)) / Piece<T>::N - from < to - from ? float(x[id]) : 0.0f;
   }
   __syncthreads();

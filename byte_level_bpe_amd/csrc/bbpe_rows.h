@@ -16,7 +16,6 @@ constexpr uint32_t ROW_THREADS = 256;  // of a workgroup, where it is not a temp
 constexpr uint32_t ROW_WAVES = ROW_THREADS / 64;
 constexpr uint32_t ROW_UNROLL = 4;     // pieces of a thread's step
 constexpr uint32_t ROW_STEP = ROW_THREADS * ROW_UNROLL;  // pieces of a workgroup's step
-constexpr float LOG2E = 1.4426950408889634f;
 constexpr double LN2 = 0.69314718055994530942;
 constexpr float LOWEST = -3.4028234663852886e38f;
 

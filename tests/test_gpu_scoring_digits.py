@@ -60,3 +60,24 @@ def test_probabilities_in_the_distillation_gradient(v, tail):
     B.distill_loss(dev, *a, tail=tail, weights=one, dlogits=both)
     for got, what in ((apart, "apart"), (both, "in one call")):
         near(got.cpu().double() * other, want, 2 * U32 * want.abs(), what)
+
+
+@pytest.mark.parametrize("offset", [0.0, 1.5, 300.0, -1e3, 1e4, -1e4, 1e5])
+@pytest.mark.parametrize("v,k", [(300, 5), (1280, 100), (33001, 256)])
+def test_lists_with_a_constant_added(v, k, offset):
+    """Without a tail a list is made to sum to 1, whatever is added to all of a row.  Listed tokens get p - q: each of the
+    two is in 64 bits and rounded once, then their difference; no bound of the offset, nor of the list's length."""
+    say("constant added", v, k, offset)
+    x, p = flat(v)
+    g = torch.Generator().manual_seed(v + k)
+    ids = torch.stack([torch.randperm(v, generator=g)[:k] for _ in range(3)]).to(torch.int32)
+    lp = (torch.randn(3, k, generator=g) + offset).float()
+    q = torch.softmax(lp.double(), 1)
+    want = p.scatter_add(1, ids.long(), -q)
+    size = p.scatter_add(1, ids.long(), q)
+    dev, a, one = x.cuda(), (ids.cuda(), lp.cuda()), torch.ones(3, device="cuda")
+    apart = B.distill_loss_backward(one, dev, *a, B.distill_loss(dev, *a))
+    both = torch.empty_like(dev)
+    B.distill_loss(dev, *a, weights=one, dlogits=both)
+    for got, what in ((apart, "apart"), (both, "in one call")):
+        near(got, want, 3 * U32 * size, what)
