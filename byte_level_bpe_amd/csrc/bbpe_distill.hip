@@ -28,6 +28,12 @@ namespace bbpe {
 namespace {
 
 constexpr uint32_t LIST_MAX = 256;  // listed tokens at most
+// What a list may leave of 1 by its rounding alone: each of its log probabilities a is
+// off by |a| 2^-24, their q-weighted sum by log(256) 2^-24 at most, and all together by
+// the log-sum that a teacher took off, 2^-18 for one of 64 in a float.  Where the
+// student gives all other tokens minus infinity, as under the teacher's own mask, that
+// much is nothing rather than a divergence of infinity (in every other row or so).
+constexpr double ROUNDING_REST = 0x1p-18;
 // Pieces that a thread holds from the loss to the gradient: 64 of the 128 registers
 // that four waves a SIMD leave it.
 constexpr uint32_t HELD = 16;
@@ -194,7 +200,8 @@ __device__ __forceinline__ float4 end_row(const DistillArgs &a, uint64_t row, bo
     if (sh.q[t] != 0.0) loss += sh.q[t] * (log_q - log_p);
   }
   loss = wave_sum(loss);
-  const double rest = sh.rest, mass = sh.mass;
+  const bool empty = p.max == -INFINITY && p.sum == 0.0;  // of tokens that are not listed
+  const double rest = empty && sh.rest <= ROUNDING_REST ? 0.0 : sh.rest, mass = sh.mass;
   if (rest > 0.0) {
     // log p_r = -log(1 + listed / others): of the ratio, not of two logarithms, until
     // it leaves the range of numbers and 1 is nothing beside it
@@ -205,7 +212,6 @@ __device__ __forceinline__ float4 end_row(const DistillArgs &a, uint64_t row, bo
   const float nan = __uint_as_float(0x7FC00000u);
   float4 st = make_float4(high, float(1.0 / sum), float(sh.log_norm), float(sh.log_norm - double(float(sh.log_norm))));
   if (tail) {
-    const bool empty = p.max == -INFINITY;  // of tokens that are not listed
     st.y = float((mass + rest) / sum);
     st.z = finite_max(p.max);
     st.w = empty ? 0.0f : float((mass + rest) / sum * (others / p.sum) - rest / p.sum);

@@ -581,7 +581,11 @@ int bbpe_token_logprobs_backward(int dtype, const void *logits, int64_t row_stri
  *                      to a row of it), and loss = sum_t q_t (log q_t - log p_t);
  *   tail 1:            q_t = exp(a_t), and what they leave of 1, q_r (0 at
  *                      least), is held against the student's sum p_r over all
- *                      tokens that are not listed: + q_r (log q_r - log p_r);
+ *                      tokens that are not listed: + q_r (log q_r - log p_r).
+ *                      Where those are all minus infinity, a q_r up to 2^-18 is the
+ *                      rounding of the list to float, and none; a larger one makes
+ *                      the loss infinite.  Under a finite mask all of q_r counts,
+ *                      times what the mask takes off: prefer minus infinity;
  *   d_loss[n_rows], d_lse[n_rows] (the student's), d_stats[n_rows][4] (for the
  *                      gradient; 16-byte aligned);
  *   d_weights[n_rows], d_logits: both or neither: the gradient of the weighted

@@ -23,6 +23,11 @@ def need_gpu():
         pytest.skip("no GPU")
 
 
+def as_float(scale):
+    """What the call takes: 0.7 is off by 2^-25 of itself as a float, which differences of near numbers show."""
+    return torch.tensor(scale, dtype=torch.float32).item()
+
+
 def reference(x, ids, lp, scale, weights):
     """((loss, bound), (dx, bound)) of distill_loss with a tail and the gradient of (weights * loss).sum(), every
     log probability from a difference of log-sums; rows that have listed and other tokens, finite in part.
@@ -31,7 +36,7 @@ def reference(x, ids, lp, scale, weights):
     exponential, room for rescaling), the sum of the others' by vocab / 256 + 64 more; the listed ones are in 64 bits, where
     what they leave of 1 keeps 2^-52 for each term."""
     n, v = x.shape
-    k = ids.shape[1]
+    k, scale = ids.shape[1], as_float(scale)
     z = x.double() * scale
     ids = ids.long()
     there = (ids >= 0) & (ids < v)
@@ -145,3 +150,42 @@ def test_gradient_against_differences():
     size = f(x).loss.double().cpu().abs() + 1
     assert bool((slope.abs() > 1e-5).all())
     assert bool(((slope - diff).abs() <= 0.01 * 8 * h * h / 6 + size * 2 * U32 / h + v * U32 * 0.01).all()), (slope, diff)
+
+
+@pytest.mark.parametrize("dtype", [BF, F])
+@pytest.mark.parametrize("n,v,k", [(12, 257, 20), (12, 5003, 64), (12, 33001, 100), (170, 33001, 64), (170, 70001, 256)])
+def test_others_of_minus_infinity(n, v, k, dtype):
+    """A student under the teacher's own mask, which leaves no token but the listed ones: what rounding leaves of 1 is
+    nothing, with all of the list's probability against the student's; what is more than that makes the loss infinite, and
+    no gradient of the masked."""
+    scale, rests = 0.7, [0.0, 1e-7, 3e-6, 1e-5, 0.01, -1e-7]  # of the list, beside its rounding (-: more than 1)
+    g = torch.Generator().manual_seed(v)
+    say("minus infinity", n, v, k, dtype)
+    ids = torch.stack([torch.randperm(v, generator=g)[:k] for _ in range(12)])
+    high = torch.randn(12, k, generator=g).to(dtype)
+    x = torch.full((12, v), -math.inf, dtype=dtype).scatter_(1, ids, high)
+    lp = torch.log_softmax(high.double() * scale + 0.1 * torch.randn(12, k, generator=g, dtype=torch.float64), 1)
+    down = torch.full((k,), -math.inf)
+    lp = torch.stack([torch.nextafter(lp[i].float(), down) if i % 6 == 0 else (lp[i] + math.log1p(-rests[i % 6])).float() for i in range(12)])
+    scale = as_float(scale)
+    q, p, w = torch.exp(lp.double()), torch.softmax(high.double() * scale, 1), torch.randn(12, generator=g)
+    mass = q.sum(1, keepdim=True)
+    left = 1 - mass
+    assert bool((left[::6] > 0).all() and (left[3::6] > 2 ** -18).all() and (left[2::6] < 2 ** -18).all())
+    much = left[:, 0] > 2 ** -18
+    log_p = torch.log(p)
+    loss = (q * (lp.double() - log_p)).sum(1).masked_fill(much, math.inf)
+    loss_tol = (q * (lp.abs() + log_p.abs())).sum(1) * 1e-13 + 2 * U32 * loss.abs()
+    weight = (mass + left * much[:, None]).clamp(min=0)
+    f = w.double()[:, None] * scale
+    dx = torch.zeros(12, v, dtype=torch.float64).scatter_(1, ids, f * (weight * p - q))
+    d = (high.double() - high.double().amax(1, keepdim=True)).abs() * scale
+    bound = torch.zeros(12, v, dtype=torch.float64).scatter_(1, ids, f.abs() * (weight * p * U32 * (8 + 4 * d) + q * 3 * U32))
+    bound = half_step(dtype) * dx.abs() + 2 * bound + torch.finfo(dtype).tiny
+    dev, a, up = many(x, n).cuda(), (many(ids, n).to(torch.int32).cuda(), many(lp, n).cuda()), many(w, n).cuda()
+    got = B.distill_loss(dev, *a, tail=True, scale=scale)
+    near(got.loss, many(loss, n), many(loss_tol, n), "loss")
+    near(B.distill_loss_backward(up, dev, *a, got, tail=True, scale=scale), many(dx, n), many(bound, n), "dx")
+    both = B.distill_loss(dev, *a, tail=True, scale=scale, weights=up, dlogits=dev)
+    near(both.loss, many(loss, n), many(loss_tol, n), "loss, in one call")
+    near(dev, many(dx, n), many(bound, n), "dx, in one call")
