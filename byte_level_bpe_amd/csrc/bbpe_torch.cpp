@@ -2,9 +2,10 @@
 // tensors as documented, on the current device and stream) are checked, their
 // outputs allocated and the library called here, in one step of a microsecond
 // or two where ctypes and tensor methods take fifteen.  Whatever is not plain
-// -- a stream, gradients to be recorded, a mistake -- returns NotImplemented,
+// -- a stream, gradients to be recorded, tangents, a mistake -- returns NotImplemented,
 // and the Python code, which says what is wrong, takes it from the start.
 #include <ATen/ATen.h>
+#include <c10/core/AutogradState.h>
 #include <c10/core/GradMode.h>
 #include <c10/hip/HIPStream.h>
 #include <torch/csrc/Exceptions.h>
@@ -35,8 +36,10 @@ using at::Tensor;
 struct Call {
   bool plain = true;
   int dev = -1;
-  // a call whose inputs require grad is not plain
+  // a call whose inputs require grad is not plain, nor one whose inputs carry
+  // tangents (torch has one level of them)
   bool recorded = c10::GradMode::is_enabled();
+  const bool forward = c10::AutogradState::get_tls_state().get_fw_grad_mode();
 
   // a tensor on the call's device; null where None is allowed and given
   const Tensor *tensor(PyObject *o, bool may_be_none = false) {
@@ -49,7 +52,7 @@ struct Call {
       return nullptr;
     }
     const Tensor &t = THPVariable_Unpack(o);
-    if (!t.is_cuda() || t.layout() != at::kStrided || (recorded && t.requires_grad())) plain = false;
+    if (!t.is_cuda() || t.layout() != at::kStrided || (recorded && t.requires_grad()) || (forward && t._fw_grad(0).defined())) plain = false;
     else if (dev < 0) dev = t.get_device();
     else if (t.get_device() != dev) plain = false;
     return &t;

@@ -20,7 +20,7 @@ from typing import NamedTuple
 import torch
 
 from . import _load
-from .serving import _DTYPES, _On, _bad, _check, _dense, _short, _wants_grad
+from .serving import _DTYPES, _On, _bad, _check, _dense, _no_tangents, _short, _wants_grad
 
 _fns = None
 
@@ -123,12 +123,13 @@ def token_logprobs(logits, ids, top_k: int = 0, scale: float = 1.0, out=None, wo
     rows (bbpe_token_logprobs_workspace_bytes).
 
     Where grad mode is on and logits require grad, logprobs, entropy, lse and
-    top_logprobs carry their gradients (once); into given outputs there are
-    none, and such a call is refused."""
+    top_logprobs carry their gradients (once, backward: inputs with tangents are
+    refused); into given outputs there are none, and such a call is refused."""
     if out is None and workspace is None and stream is None:
         got = _short.token_logprobs(logits, ids, top_k, scale)
         if got is not NotImplemented:
             return tuple.__new__(TokenLogprobs, got)
+    _no_tangents("token_logprobs", logits)
     if _wants_grad(logits):
         if out is not None or workspace is not None:
             _bad("token_logprobs: no gradients into given outputs or workspaces; call it under torch.no_grad()")
@@ -167,6 +168,7 @@ def token_logprobs_backward(logits, ids, scored: TokenLogprobs, grad_logprobs=No
                                              grad_lse, grad_top, scale)
         if got is not NotImplemented:
             return got
+    _no_tangents("token_logprobs_backward", logits, scored.entropy, grad_logprobs, grad_entropy, grad_lse, grad_top)
     dev = logits.device
     with _On(dev, stream, "token_logprobs_backward") as on:
         x = _logits("token_logprobs_backward", logits)
@@ -233,13 +235,15 @@ def distill_loss(logits, top_ids, top_logprobs, tail: bool = False, scale: float
     With weights (float32 [n]) and dlogits (which may be logits) the call also
     writes the gradient of (weights * loss).sum(): one call of a training step
     that knows its weights.  Otherwise, where grad mode is on and logits
-    require grad, loss carries its gradient (once; the teacher has none)."""
+    require grad, loss carries its gradient (once, backward: inputs with tangents
+    are refused; the teacher has none)."""
     if (weights is None) != (dlogits is None):
         _bad("distill_loss: weights and dlogits are given together or not at all")
     if out is None and workspace is None and stream is None:
         got = _short.distill_loss(logits, top_ids, top_logprobs, tail, scale, weights, dlogits)
         if got is not NotImplemented:
             return tuple.__new__(DistillLoss, got)
+    _no_tangents("distill_loss", logits, top_logprobs, weights)
     if _wants_grad(logits, top_logprobs, weights):
         if out is not None or workspace is not None or dlogits is not None or top_logprobs.requires_grad:
             _bad("distill_loss: no gradients into given outputs or workspaces, nor of the teacher or the weights; call it under torch.no_grad()")
@@ -273,6 +277,7 @@ def distill_loss_backward(grad_loss, logits, top_ids, top_logprobs, distilled: D
         got = _short.distill_loss_backward(grad_loss, logits, top_ids, top_logprobs, distilled.stats, tail, scale)
         if got is not NotImplemented:
             return got
+    _no_tangents("distill_loss_backward", grad_loss, logits, top_logprobs)
     dev = logits.device
     with _On(dev, stream, "distill_loss_backward") as on:
         x = _logits("distill_loss_backward", logits)

@@ -22,6 +22,7 @@ import os
 from typing import NamedTuple
 
 import torch
+from torch.autograd import forward_ad
 
 from . import BBPEError, E_INVALID_ARG, HERE, _load
 
@@ -272,6 +273,12 @@ def _norm_args(what, q, k, q_weight, k_weight, positions, inv_freq):
             _dense("positions", positions, torch.int32, (n,), dev), freq)
 
 
+def _no_tangents(what, *tensors):
+    """Refuses inputs of forward-mode differentiation, whose tangents the kernels would drop."""
+    if any(t is not None and forward_ad.unpack_dual(t).tangent is not None for t in tensors):
+        _bad("%s: no forward-mode gradients, and an input carries a tangent; unpack it, or differentiate backward" % what)
+
+
 def _wants_grad(*tensors):
     return torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors)
 
@@ -307,7 +314,7 @@ def qk_norm_rope(q, k, q_weight, k_weight, positions, inv_freq, eps: float = 1e-
     None is ones.
 
     Where grad mode is on and an input requires grad, the outputs carry the
-    gradients of q, k and the weights (once; not those of positions and
+    gradients of q, k and the weights (once, backward; not those of positions and
     inv_freq).  Into a cache or into given outputs there are none: such a call
     is refused."""
     if not (cache is None) == (v is None) == (slots is None):
@@ -319,6 +326,7 @@ def qk_norm_rope(q, k, q_weight, k_weight, positions, inv_freq, eps: float = 1e-
                                    cache._p))
         if got is not NotImplemented:
             return got
+    _no_tangents("qk_norm_rope", q, k, q_weight, k_weight, inv_freq, v)
     if _wants_grad(q, k, q_weight, k_weight, inv_freq, v):
         if cache is not None or q_out is not None or k_out is not None or inv_freq.requires_grad:
             _bad("qk_norm_rope: no gradients into a cache or given outputs, nor of inv_freq; call it under torch.no_grad()")
@@ -361,6 +369,7 @@ def qk_norm_rope_backward(grad_q, grad_k, q, k, q_weight, k_weight, positions, i
         got = _short.qk_norm_rope_backward(q, k, q_weight, k_weight, positions, inv_freq, eps, interleaved, grad_q, grad_k)
         if got is not NotImplemented:
             return got
+    _no_tangents("qk_norm_rope_backward", grad_q, grad_k, q, k, q_weight, k_weight, inv_freq)
     dev, dt = q.device, q.dtype
     with _On(dev, stream, "qk_norm_rope_backward") as on:
         n, hq, hk, dim, rot, ws, pos, freq = _norm_args("qk_norm_rope_backward", q, k, q_weight, k_weight, positions,
@@ -412,6 +421,7 @@ def tree_attention(q, cache: PagedCache, table, q_off, ctx_len, tree_mask=None, 
                                     cache.head_dim ** -0.5 if scale is None else scale, return_lse)
         if got is not NotImplemented:
             return got if return_lse else got[0]
+    _no_tangents("tree_attention", q, cache.k, cache.v)
     if _wants_grad(q, cache.k, cache.v):
         _bad("tree_attention: it has no gradient, and an input requires grad; call it under torch.no_grad()")
     dev, dt = q.device, q.dtype
