@@ -481,6 +481,8 @@ PyObject *distill_loss(PyObject *, PyObject *const *a, Py_ssize_t n_args) {
                            floats(out[0].data_ptr()), floats(out[1].data_ptr()), floats(out[2].data_ptr()), floats(p_w), weights ? d.p : nullptr,
                            weights ? d.t->stride(0) : 0, bytes ? ws.data_ptr() : nullptr, bytes, stream);
   if (rc) return not_plain();
+  // (as torch's own writes into a given tensor do: who has saved it for a backward pass learns of it)
+  if (weights && !d.t->is_inference()) d.t->unsafeGetTensorImpl()->bump_version();
   return tuple_of(out);
   END_HANDLE_TH_ERRORS
 }

@@ -20,7 +20,7 @@ from typing import NamedTuple
 import torch
 
 from . import _load
-from .serving import _DTYPES, _On, _bad, _check, _dense, _no_tangents, _short, _wants_grad
+from .serving import _DTYPES, _On, _bad, _check, _dense, _no_tangents, _short, _wants_grad, _written_to
 
 _fns = None
 
@@ -143,6 +143,7 @@ def token_logprobs(logits, ids, top_k: int = 0, scale: float = 1.0, out=None, wo
         n, f32, i32 = logits.shape[0], torch.float32, torch.int32
         if not 0 <= top_k <= min(256, logits.shape[1]):  # (before anything is allocated)
             _bad("token_logprobs: top_k %d of a vocabulary of %d" % (top_k, logits.shape[1]))
+        given = out or ()
         if out is None:
             shapes = ((n,), f32), ((n,), f32), ((n,), f32), ((n,), i32), ((n, top_k), i32), ((n, top_k), f32), ((n, 2), f32)
             out = TokenLogprobs(*(torch.empty(s, dtype=t, device=dev) for s, t in shapes))
@@ -153,6 +154,7 @@ def token_logprobs(logits, ids, top_k: int = 0, scale: float = 1.0, out=None, wo
             _dense("ranks", out.ranks, i32, (n,), dev), _dense("top_ids", out.top_ids, i32, (n, top_k), dev),
             _dense("top_logprobs", out.top_logprobs, f32, (n, top_k), dev), _dense("stats", out.stats, f32, (n, 2), dev), *space, on.handle)
         _check(st, "token_logprobs")
+        _written_to(*given)
         on.keep(logits, ids, room, *out)
     return out
 
@@ -173,6 +175,7 @@ def token_logprobs_backward(logits, ids, scored: TokenLogprobs, grad_logprobs=No
     with _On(dev, stream, "token_logprobs_backward") as on:
         x = _logits("token_logprobs_backward", logits)
         n, f32, i32, k = logits.shape[0], torch.float32, torch.int32, scored.top_ids.shape[-1]
+        given = dlogits
         if dlogits is None:
             dlogits = torch.empty(logits.shape, dtype=logits.dtype, device=dev)
         st = _lib().bbpe_token_logprobs_backward(
@@ -182,6 +185,7 @@ def token_logprobs_backward(logits, ids, scored: TokenLogprobs, grad_logprobs=No
             _or_none("grad_lse", grad_lse, (n,), dev), _or_none("grad_top", grad_top, (n, k), dev),
             *_gradient("token_logprobs_backward", dlogits, logits), on.handle)
         _check(st, "token_logprobs_backward")
+        _written_to(given)
         on.keep(logits, ids, scored.entropy, scored.top_ids, scored.stats, grad_logprobs, grad_entropy, grad_lse, grad_top, dlogits)
     return dlogits
 
@@ -256,6 +260,7 @@ def distill_loss(logits, top_ids, top_logprobs, tail: bool = False, scale: float
         x = _logits("distill_loss", logits)
         n, f32 = logits.shape[0], torch.float32
         ids, lp, k = _lists("distill_loss", top_ids, top_logprobs, n, dev)
+        given = (dlogits, *(out or ()))
         if out is None:
             out = DistillLoss(*(torch.empty(s, dtype=f32, device=dev) for s in ((n,), (n,), (n, 4))))
         room, *space = _room(_lib().bbpe_distill_loss_workspace_bytes, workspace, dev, "distill_loss", x[0], n, x[4])
@@ -264,6 +269,7 @@ def distill_loss(logits, top_ids, top_logprobs, tail: bool = False, scale: float
             _dense("stats", out.stats, f32, (n, 4), dev), _or_none("weights", weights, (n,), dev),
             *((None, 0) if dlogits is None else _gradient("distill_loss", dlogits, logits)), *space, on.handle)
         _check(st, "distill_loss")
+        _written_to(*given)
         on.keep(logits, top_ids, top_logprobs, weights, dlogits, room, *out)
     return out
 
@@ -283,11 +289,13 @@ def distill_loss_backward(grad_loss, logits, top_ids, top_logprobs, distilled: D
         x = _logits("distill_loss_backward", logits)
         n, f32 = logits.shape[0], torch.float32
         ids, lp, k = _lists("distill_loss_backward", top_ids, top_logprobs, n, dev)
+        given = dlogits
         if dlogits is None:
             dlogits = torch.empty(logits.shape, dtype=logits.dtype, device=dev)
         st = _lib().bbpe_distill_loss_backward(
             *x, ids, lp, k, tail, scale, _dense("stats", distilled.stats, f32, (n, 4), dev),
             _dense("grad_loss", grad_loss, f32, (n,), dev), *_gradient("distill_loss_backward", dlogits, logits), on.handle)
         _check(st, "distill_loss_backward")
+        _written_to(given)
         on.keep(logits, top_ids, top_logprobs, distilled.stats, grad_loss, dlogits)
     return dlogits

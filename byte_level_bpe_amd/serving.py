@@ -279,6 +279,14 @@ def _no_tangents(what, *tensors):
         _bad("%s: no forward-mode gradients, and an input carries a tangent; unpack it, or differentiate backward" % what)
 
 
+def _written_to(*tensors):
+    """Counts the tensors given to write into as changed, as torch does its own: a backward pass that has saved one of
+    them raises instead of reading what is there now."""
+    for t in tensors:
+        if t is not None and not t.is_inference():
+            torch.autograd.graph.increment_version(t)
+
+
 def _wants_grad(*tensors):
     return torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors)
 
@@ -339,6 +347,7 @@ def qk_norm_rope(q, k, q_weight, k_weight, positions, inv_freq, eps: float = 1e-
         n, hq, hk, dim, rot, ws, pos, freq = _norm_args("qk_norm_rope", q, k, q_weight, k_weight, positions, inv_freq)
         if cache is not None and (cache.device != dev or cache.dtype is not dt):
             _bad("qk_norm_rope: the cache is %s on %s, q %s on %s" % (cache.dtype, cache.device, dt, dev))
+        given = q_out, k_out
         if q_out is None:
             q_out = torch.empty((n, hq, dim), dtype=dt, device=dev)
         if k_out is None and cache is None:
@@ -353,6 +362,7 @@ def qk_norm_rope(q, k, q_weight, k_weight, positions, inv_freq, eps: float = 1e-
             None if cache is None else cache._p,
             None if cache is None else _dense("slots", slots, torch.int64, (n,), dev), on.handle)
         _check(st, "qk_norm_rope")
+        _written_to(*given)
         on.keep(q, k, v, q_weight, k_weight, positions, inv_freq, q_out, k_out, slots)
         if cache is not None:
             on.keep(cache.k, cache.v)
@@ -374,6 +384,7 @@ def qk_norm_rope_backward(grad_q, grad_k, q, k, q_weight, k_weight, positions, i
     with _On(dev, stream, "qk_norm_rope_backward") as on:
         n, hq, hk, dim, rot, ws, pos, freq = _norm_args("qk_norm_rope_backward", q, k, q_weight, k_weight, positions,
                                                         inv_freq)
+        given = dq, dk
         if dq is None:
             dq = torch.empty((n, hq, dim), dtype=dt, device=dev)
         if dk is None:
@@ -392,6 +403,7 @@ def qk_norm_rope_backward(grad_q, grad_k, q, k, q_weight, k_weight, positions, i
             None if dws[0] is None else dws[0].data_ptr(), None if dws[1] is None else dws[1].data_ptr(),
             _dense("workspace", workspace, torch.uint8, (None,), dev), workspace.numel(), on.handle)
         _check(st, "qk_norm_rope_backward")
+        _written_to(*given)
         on.keep(grad_q, grad_k, q, k, q_weight, k_weight, positions, inv_freq, dq, dk, workspace, *dws)
     return dq, dk, dws[0], dws[1]
 
@@ -435,6 +447,7 @@ def tree_attention(q, cache: PagedCache, table, q_off, ctx_len, tree_mask=None, 
                 (table.stride(1) != 1 and table.shape[1] > 1) or table.stride(0) < 0:
             _bad("tree_attention: table: an int32 tensor [%d, width] with contiguous rows on %s is wanted, got %s %s on %s"
                  % (n_req, dev, table.dtype, list(table.shape), table.device))
+        given = out, lse
         if out is None:
             out = torch.empty((n, hq, dim), dtype=dt, device=dev)
         if lse is None and return_lse:
@@ -451,5 +464,6 @@ def tree_attention(q, cache: PagedCache, table, q_off, ctx_len, tree_mask=None, 
             None if lse is None else _dense("lse", lse, torch.float32, (n, hq), dev),
             _dense("workspace", workspace, torch.uint8, (None,), dev), workspace.numel(), on.handle)
         _check(st, "tree_attention")
+        _written_to(*given)
         on.keep(q, table, q_off, ctx_len, tree_mask, out, lse, workspace, cache.k, cache.v)
     return (out, lse) if return_lse else out
