@@ -571,8 +571,9 @@ __global__ __launch_bounds__(64 * WAVES) void k_scores_back(ScoreBackArgs a) {
   for (uint32_t t = tid; t < n; t += THREADS) {
     int32_t id = t ? a.top_ids[row * a.k + t - 1] : a.ids[row];
     if (id < 0 || uint32_t(id) >= a.vocab) id = -1;
-    const float *g = t ? a.g_top : a.g_logprobs;
-    const float v = id < 0 || !g ? 0.0f : t ? g[row * a.k + t - 1] : g[row];
+    // (alternatives count without their ids too: a row without probabilities names none, but what it returned depends
+    // on its logits, and its gradient is NaN)
+    const float v = t ? a.g_top[row * a.k + t - 1] : id < 0 || !a.g_logprobs ? 0.0f : a.g_logprobs[row];
     own_id[t] = id;
     own_g[t] = v;
     mine += v;

@@ -81,3 +81,28 @@ def test_lists_with_a_constant_added(v, k, offset):
     B.distill_loss(dev, *a, weights=one, dlogits=both)
     for got, what in ((apart, "apart"), (both, "in one call")):
         near(got, want, 3 * U32 * size, what)
+
+
+@pytest.mark.parametrize("n,v", [(6, 300), (6, 5003), (6, 33001), (1200, 9001)])
+def test_gradient_of_alternatives_without_probabilities(n, v):
+    """A row with a NaN or plus infinity has NaN for its alternatives' log probabilities, and no ids: where a gradient comes
+    back to them alone, the row's is NaN; where zeros do, it is 0, and beside them rows keep theirs."""
+    say("no probabilities", n, v)
+    x = torch.randn(6, v, generator=torch.Generator().manual_seed(v))
+    x[1, 7] = x[2, v - 1] = math.nan
+    x[3, 5] = math.inf
+    rows = torch.arange(n) % 6
+    dev, ids = x[rows].cuda(), torch.full((n,), -1, dtype=torch.int32, device="cuda")
+    g = torch.zeros(6, 4)
+    g[0], g[1], g[3, 2], g[4, 0] = 1.0, 0.5, 1.0, -2.0
+    got = B.token_logprobs(dev, ids, top_k=4)
+    dx = B.token_logprobs_backward(dev, ids, got, grad_top=g[rows].cuda()).cpu()
+    odd = (rows == 1) | (rows == 3)
+    assert bool(dx[odd].isnan().all()) and bool(dx[~odd].isfinite().all()) and not dx[(rows == 2) | (rows == 5)].any()
+    p = torch.softmax(x.double(), 1)
+    for row in (0, 4):
+        want = -p[row] * g[row].sum()
+        want[got.top_ids[row].cpu().long()] += g[row]
+        # the terms, their sum and p's: a few half steps each; its weights' exponents up to 4 |z - max| more
+        bound = U32 * (p[row] * g[row].abs().sum() * (16 + 4 * (x[row] - x[row].max()).abs() + v / 256 + 64) + 8 * want.abs())
+        assert bool(((dx[row] - want).abs() <= bound).all())
