@@ -149,7 +149,7 @@ def token_logprobs(logits, ids, top_k: int = 0, scale: float = 1.0, out=None, wo
             out = TokenLogprobs(*(torch.empty(s, dtype=t, device=dev) for s, t in shapes))
         room, *space = _room(_lib().bbpe_token_logprobs_workspace_bytes, workspace, dev, "token_logprobs", x[0], n, x[4], top_k)
         st = _lib().bbpe_token_logprobs(
-            *x, _dense("ids", ids, i32, (n,), dev), top_k, scale, *(
+            *x, _dense("ids", ids, i32, (n,), dev), top_k, float(scale), *(
                 _dense(name, t, f32, (n,), dev) for name, t in (("logprobs", out.logprobs), ("entropy", out.entropy), ("lse", out.lse))),
             _dense("ranks", out.ranks, i32, (n,), dev), _dense("top_ids", out.top_ids, i32, (n, top_k), dev),
             _dense("top_logprobs", out.top_logprobs, f32, (n, top_k), dev), _dense("stats", out.stats, f32, (n, 2), dev), *space, on.handle)
@@ -179,7 +179,7 @@ def token_logprobs_backward(logits, ids, scored: TokenLogprobs, grad_logprobs=No
         if dlogits is None:
             dlogits = torch.empty(logits.shape, dtype=logits.dtype, device=dev)
         st = _lib().bbpe_token_logprobs_backward(
-            *x, _dense("ids", ids, i32, (n,), dev), k, scale, _dense("entropy", scored.entropy, f32, (n,), dev),
+            *x, _dense("ids", ids, i32, (n,), dev), k, float(scale), _dense("entropy", scored.entropy, f32, (n,), dev),
             _dense("top_ids", scored.top_ids, i32, (n, k), dev), _dense("stats", scored.stats, f32, (n, 2), dev),
             _or_none("grad_logprobs", grad_logprobs, (n,), dev), _or_none("grad_entropy", grad_entropy, (n,), dev),
             _or_none("grad_lse", grad_lse, (n,), dev), _or_none("grad_top", grad_top, (n, k), dev),
@@ -265,7 +265,7 @@ def distill_loss(logits, top_ids, top_logprobs, tail: bool = False, scale: float
             out = DistillLoss(*(torch.empty(s, dtype=f32, device=dev) for s in ((n,), (n,), (n, 4))))
         room, *space = _room(_lib().bbpe_distill_loss_workspace_bytes, workspace, dev, "distill_loss", x[0], n, x[4])
         st = _lib().bbpe_distill_loss(
-            *x, ids, lp, k, tail, scale, _dense("loss", out.loss, f32, (n,), dev), _dense("lse", out.lse, f32, (n,), dev),
+            *x, ids, lp, k, bool(tail), float(scale), _dense("loss", out.loss, f32, (n,), dev), _dense("lse", out.lse, f32, (n,), dev),
             _dense("stats", out.stats, f32, (n, 4), dev), _or_none("weights", weights, (n,), dev),
             *((None, 0) if dlogits is None else _gradient("distill_loss", dlogits, logits)), *space, on.handle)
         _check(st, "distill_loss")
@@ -293,7 +293,7 @@ def distill_loss_backward(grad_loss, logits, top_ids, top_logprobs, distilled: D
         if dlogits is None:
             dlogits = torch.empty(logits.shape, dtype=logits.dtype, device=dev)
         st = _lib().bbpe_distill_loss_backward(
-            *x, ids, lp, k, tail, scale, _dense("stats", distilled.stats, f32, (n, 4), dev),
+            *x, ids, lp, k, bool(tail), float(scale), _dense("stats", distilled.stats, f32, (n, 4), dev),
             _dense("grad_loss", grad_loss, f32, (n,), dev), *_gradient("distill_loss_backward", dlogits, logits), on.handle)
         _check(st, "distill_loss_backward")
         _written_to(given)
