@@ -643,7 +643,7 @@ int bbpe_distill_loss(int dtype, const void *logits, int64_t row_stride, uint64_
       if (pieces <= 64 * HELD && top_k <= 64) by_tail(n_rows, 64, k_distill_step<T, 1, false, 64>, k_distill_step<T, 1, true, 64>);
       else if (pieces <= 224 * HELD) by_tail(n_rows, 256, k_distill_step<T, 4, false, L>, k_distill_step<T, 4, true, L>);
       else if (pieces <= 512 * HELD || sizeof(T) == 2) by_tail(n_rows, 512, k_distill_step<T, 8, false, L>, k_distill_step<T, 8, true, L>);
-      else by_tail(n_rows, 1024, k_distill_step<T, 16, false, L>, k_distill_step<T, 16, true, L>);
+      else if constexpr (sizeof(T) == 4) by_tail(n_rows, 1024, k_distill_step<T, 16, false, L>, k_distill_step<T, 16, true, L>);
     } else if (cut.parts > 1) {
       by_tail(n_rows * cut.parts, ROW_THREADS, k_distill<T, W, false, true, L>, k_distill<T, W, true, true, L>);
       launch(n_rows, k_distill_join<T>, 64);
