@@ -184,18 +184,26 @@ constexpr uint64_t MAX_GROUPS = 1u << 21;  // workgroups (of up to 1,024) a laun
 
 // How rows are cut: waves a workgroup, parts a row and pieces of a part.
 //
-// Short rows go to a wave each (where `small` allows it), which has no barrier to
-// wait at: up to 512 pieces always (8,192 rows of 2,048 in bfloat16: log
-// probabilities 12.2 us, by workgroups 29; with 20 alternatives 26 and 76), up to
-// 1,024 where there are more than 1,024 rows (8,192 rows of 8,192: 30.6 and 34.4,
-// with alternatives 47 and 86; but 600 rows of 5,000: 7.7 and 6.7).
+// Short rows go to a wave each (where `small` allows it), which has no barrier to wait
+// at.  Up to 512 pieces always: from 1,024 rows on it is faster (2,048 rows of 2,048 in
+// bfloat16: log probabilities 6.8 us, by workgroups of four waves 10.6, with 20
+// alternatives 12.8 and 25.4; 8,192 rows 12.6 and 29.7, 26.6 and 76.3), and for fewer
+// rows it is no slower with alternatives (1 row of 1,280: 8.5 us and 9.2; 512 rows: 10.2
+// and 12.1) and the same without (5.4 and 5.4, 6.7 and 6.7), but for distillation of few
+// rows near 512 pieces (1 row of 4,000: 5.6 and 5.0).  Up to 1,024 pieces where there are
+// more than 1,024 rows: with alternatives workgroups win until there (rows of 5,003: 512
+// rows 13.4 us and by waves 14.3, 1,000 15.7 and 15.3, 1,200 17.2 and 16.1, 1,536 24.9 and
+// 16.6; of 8,184: 1,000 16.7 and 16.8, 1,536 25.0 and 18.4), and without until 1,536 or
+// 2,048 (of 5,003: 1,200 8.8 and 9.4, 2,048 11.3 and 10.3; of 8,184: 1,200 9.2 and 10.7,
+// 2,048 12.2 and 12.1, 8,192 38.5 and 31.1).
 //
-// Longer rows go to a workgroup each.  Up to 512 of them would not fill 256 CUs,
-// and go to several, about 1,024 in all, a step each at least, which a second
+// Longer rows go to a workgroup each.  Up to 512 of them would not fill 256 CUs, and
+// go to several, about 1,024 in all and no more than a row has steps, which a second
 // kernel joins (1 row of 100,256: 8.8 us and, by one workgroup, 16; 400 rows: 25 us,
 // with 800 workgroups 26.7, with 2,048 26.7); from 513 rows on the second kernel
 // costs more (1,000 rows: by one each 43 us, by two 49, with 20 alternatives 51
-// and 63).
+// and 63).  Parts are equal, in 64 pieces, not whole steps: a last step may be nearly
+// empty (128 rows of 200,005 in float32: 8 parts of six steps and 128 pieces).
 struct Cut {
   uint32_t waves, parts, part;
 };
@@ -211,6 +219,7 @@ inline Cut cut_rows(int dtype, uint64_t n_rows, uint32_t vocab, bool small, uint
     c.parts = uint32_t(want < most ? want : most);
   }
   c.part = ((pieces + c.parts - 1) / c.parts + 63) / 64 * 64;
+  c.parts = (pieces + c.part - 1) / c.part;  // (of parts rounded up, fewer may do)
   return c;
 }
 
