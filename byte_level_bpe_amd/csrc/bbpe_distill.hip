@@ -282,16 +282,16 @@ __device__ __forceinline__ void add_step(const DistillArgs &a, const typename Pi
     for (uint32_t e = 0; e < P::N; ++e) m = fmaxf(m, v[u][e]);
   }
   if (m > s.max) {
-    if (s.max != -INFINITY) s.sum *= double(weight_of(s.max - m, a.x2));
+    if (s.max != -INFINITY) s.sum *= double(fine_weight(s.max - m, a.x2));
     s.max = m;
   }
   const float ref = finite_max(s.max);
-  float sum = 0.0f;
 #pragma unroll
-  for (uint32_t u = 0; u < ROW_UNROLL; ++u)
+  for (uint32_t u = 0; u < ROW_UNROLL; ++u) {
 #pragma unroll
-    for (uint32_t e = 0; e < P::N; ++e) sum += weight_of(v[u][e] - ref, a.x2);
-  s.sum += double(sum);
+    for (uint32_t e = 0; e < P::N; ++e) v[u][e] = weight_of(v[u][e] - ref, a.x2);
+    s.sum += double(piece_sum<P::N>(v[u]));
+  }
 }
 
 // Adds pieces [first, last) of a row to s; with a tail, their tokens that are not
@@ -359,7 +359,7 @@ template <typename T, uint32_t WAVES> struct Gradient {
         sum = 0.0f;
         for (uint32_t i = 0; i < a.k; ++i) sum += ids[i] == id ? float(q[i]) : 0.0f;
       }
-      out.at[place] = T(g * (st.y * weight_of(own[t] - st.x, x2) - sum));
+      out.at[place] = T(g * (st.y * fine_weight(own[t] - st.x, x2) - sum));
     }
   }
 };

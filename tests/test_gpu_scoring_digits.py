@@ -106,3 +106,29 @@ def test_gradient_of_alternatives_without_probabilities(n, v):
         # the terms, their sum and p's: a few half steps each; its weights' exponents up to 4 |z - max| more
         bound = U32 * (p[row] * g[row].abs().sum() * (16 + 4 * (x[row] - x[row].max()).abs() + v / 256 + 64) + 8 * want.abs())
         assert bool(((dx[row] - want).abs() <= bound).all())
+
+
+@pytest.mark.parametrize("tail", [False, True])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16, F])
+@pytest.mark.parametrize("n,v", [(16, 1280), (16, 4001), (16, 9001), (16, 33001), (1040, 9001), (600, 33001)])
+def test_losses_of_few_digits(n, v, dtype, tail):
+    """One token far above all others, which are alike, and listed: the loss is log(1 + (v - 1) e^-d), a tenth or so.
+
+    Each thread's sum is brought to the row's maximum by one factor, off by three half steps (its exponential's two, and
+    less than one of an exponent up to a half); the largest element's own piece is added in three roundings beside 1,
+    and its thread's other elements, one in 64 or fewer, are off by what their exponents up to 32 are, 24 half steps; the
+    loss is rounded once."""
+    say("few digits", n, v, dtype, tail)
+    d = math.log(10 * v) + torch.arange(16) * 0.13
+    x = torch.zeros(16, v).copy_(-d[:, None]).to(dtype)
+    top = (torch.arange(16) * 997) % v
+    x[torch.arange(16), top] = 0.0
+    others = (v - 1) * torch.exp(x.double().amin(1))
+    want = torch.log1p(others)
+    # (with a tail the list's one probability is 1: nothing is left)
+    rows = torch.arange(n) % 16
+    a = top.to(torch.int32)[rows, None].cuda(), torch.zeros(n, 1, device="cuda")
+    bound = U32 * (3 + others * (3 + 24 / 64) + want) + 1e-12
+    dev, w = x[rows].cuda(), torch.ones(n, device="cuda")
+    near(B.distill_loss(dev, *a, tail=tail).loss, want[rows], bound[rows], "loss")
+    near(B.distill_loss(dev, *a, tail=tail, weights=w, dlogits=torch.empty_like(dev)).loss, want[rows], bound[rows], "in one call")
