@@ -298,22 +298,21 @@ __device__ __forceinline__ void score_pieces(const ScoreArgs &a, uint64_t row, u
     }
     if (m > s.max) {
       const float d = s.max - m;
-      s = s.max == -INFINITY ? Partial{s.sum, m, 0.0f} : scaled(s, m, d, __builtin_amdgcn_exp2f(d * a.x2.c));
+      s = s.max == -INFINITY ? Partial{s.sum, m, 0.0f} : scaled(s, m, d, fine_weight(d, Exponent{a.x2.c, 0.0f}));
       ref = m;
     }
-    float sum = 0.0f;
 #pragma unroll
     for (uint32_t u = 0; u < ROW_UNROLL; ++u) {
       const float bar = p0 + u * THREADS + tid < before_id ? at_least : given.value;
 #pragma unroll
       for (uint32_t e = 0; e < P::N; ++e) {
         const float d = v[u][e] - ref, w = __builtin_amdgcn_exp2f(d * a.x2.c);
-        sum += w;
         s.mean += w * fmaxf(d, LOWEST);  // (0 times minus infinity is to be 0)
         above += uint32_t(__popcll(__ballot(!(v[u][e] <= bar))));
+        v[u][e] = w;
       }
+      s.sum += double(piece_sum<P::N>(v[u]));
     }
-    s.sum += double(sum);
   }
   // (the exponent's second part, to first order: each weight times LN2 * low * (x - max))
   s.sum += LN2 * double(a.x2.low) * double(s.mean);

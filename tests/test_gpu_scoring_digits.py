@@ -132,3 +132,24 @@ def test_losses_of_few_digits(n, v, dtype, tail):
     dev, w = x[rows].cuda(), torch.ones(n, device="cuda")
     near(B.distill_loss(dev, *a, tail=tail).loss, want[rows], bound[rows], "loss")
     near(B.distill_loss(dev, *a, tail=tail, weights=w, dlogits=torch.empty_like(dev)).loss, want[rows], bound[rows], "in one call")
+
+
+@pytest.mark.parametrize("k", [0, 5, 100])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16, F])
+@pytest.mark.parametrize("n,v", [(16, 1280), (16, 4001), (16, 9001), (16, 33001), (1040, 9001), (600, 33001)])
+def test_scores_of_likely_tokens(n, v, dtype, k):
+    """The same rows: the likely token's log probability is -log(1 + (v - 1) e^-d), a tenth or so, with the same bound."""
+    say("likely tokens", n, v, dtype, k)
+    d = math.log(10 * v) + torch.arange(16) * 0.13
+    x = torch.zeros(16, v).copy_(-d[:, None]).to(dtype)
+    top = (torch.arange(16) * 997) % v
+    x[torch.arange(16), top] = 0.0
+    others = (v - 1) * torch.exp(x.double().amin(1))
+    want = -torch.log1p(others)
+    rows = torch.arange(n) % 16
+    bound = U32 * (3 + others * (3 + 24 / 64) - want) + 1e-12
+    got = B.token_logprobs(x[rows].cuda(), top.to(torch.int32)[rows].cuda(), top_k=k)
+    near(got.logprobs, want[rows], bound[rows], "logprobs")
+    near(got.lse, -want[rows], bound[rows], "lse")
+    if k:
+        near(got.top_logprobs[:, 0].contiguous(), want[rows], bound[rows], "top")
