@@ -1,5 +1,4 @@
-"""Digits of the gradients between logits and ids, on the GPU: rows whose sums of weights are exact, so that a
-probability is off by what its last few operations round."""
+"""Digits of what the operators between logits and ids make, on the GPU: rows whose sums of weights are exact, or a 1 and\nmany small ones, so that results are off by what their last few operations round; and scales at their limits."""
 import math
 
 import pytest
@@ -9,7 +8,8 @@ pytestmark = pytest.mark.gpu
 
 import byte_level_bpe_amd as B  # noqa: E402
 from tests.serving_reference import U32  # noqa: E402
-from tests.test_gpu_scoring import F, near  # noqa: E402
+from tests import scoring_reference as ref  # noqa: E402
+from tests.test_gpu_scoring import F, logits, many, near  # noqa: E402
 from tests.test_gpu_serving import say  # noqa: E402
 
 SIZES = [300, 1280, 5003, 33001, 50257, 100277, 200005]
@@ -153,3 +153,28 @@ def test_scores_of_likely_tokens(n, v, dtype, k):
     near(got.lse, -want[rows], bound[rows], "lse")
     if k:
         near(got.top_logprobs[:, 0].contiguous(), want[rows], bound[rows], "top")
+
+
+@pytest.mark.parametrize("scale", [1e30, 1e-30, 1e-3, 1e20])
+@pytest.mark.parametrize("n,v", [(5, 300), (5, 33001), (600, 9001)])
+def test_scores_at_the_scales_limits(n, v, scale):
+    """Logits as small, or as large, as the scale makes up for, with the gradient of every output."""
+    say("limits", n, v, scale)
+    x, g = logits(5, v, F, v)
+    x[1, 5:40] = -math.inf
+    x[2] = x[2].round()
+    x = x / torch.tensor(scale)
+    ids = torch.randint(0, v, (5,), generator=g, dtype=torch.int32)
+    up = dict(g=torch.randn(5, generator=g), gh=torch.randn(5, generator=g), gl=torch.randn(5, generator=g), gt=torch.randn(5, 20, generator=g))
+    as_float = torch.tensor(scale, dtype=torch.float32).item()
+    dev, there = many(x, n).cuda(), many(ids, n).cuda()
+    got = B.token_logprobs(dev, there, top_k=20, scale=scale)
+    for name, (want, bound) in ref.scores(x, ids, 20, as_float).items():
+        if bound is None:
+            assert torch.equal(getattr(got, name).cpu().long(), many(want, n).long()), name
+        else:
+            near(getattr(got, name), many(want, n), many(bound, n), name)
+    args = {name: many(up[a], n).cuda() for a, name in (("g", "grad_logprobs"), ("gh", "grad_entropy"), ("gl", "grad_lse"), ("gt", "grad_top"))}
+    dx = B.token_logprobs_backward(dev, there, got, **args, scale=scale)
+    want, bound = ref.scores_grad(x, ids, 20, as_float, **up)
+    near(dx, many(want, n), many(bound, n), "dx")

@@ -189,3 +189,13 @@ def test_others_of_minus_infinity(n, v, k, dtype):
     both = B.distill_loss(dev, *a, tail=True, scale=scale, weights=up, dlogits=dev)
     near(both.loss, many(loss, n), many(loss_tol, n), "loss, in one call")
     near(dev, many(dx, n), many(bound, n), "dx, in one call")
+
+
+@pytest.mark.parametrize("scale", [1e30, 1e-30, 1e20])
+@pytest.mark.parametrize("n,v,k", [(36, 257, 20), (36, 9001, 64), (170, 33001, 64)])
+def test_scales_at_their_limits(n, v, k, scale):
+    """Logits as small, or as large, as the scale makes up for; the type's lowest value among them."""
+    say("limits", n, v, k, scale)
+    x, ids, lp, w = rows_of(v, k, F, 1.0, v + k)
+    keep = 33  # (the lowest value times 1e30 is past the losses' floats)
+    check(x[:keep] / torch.tensor(scale), ids[:keep], lp[:keep], scale, w[:keep], n, 1)
