@@ -367,7 +367,7 @@ template <typename T, uint32_t WAVES> struct Gradient {
 // The loss: a workgroup a row or, SPLIT, a part of one.
 //
 // Bound by the one read of the row: 4,096 rows of 100,277 in bfloat16 with a tail,
-// 157 us (5.2 TB/s).  The listed tokens' bits cost a word of LDS a piece, and a
+// 160 us (5.1 TB/s).  The listed tokens' bits cost a word of LDS a piece, and a
 // branch that one piece in hundreds takes.
 template <typename T, uint32_t WAVES, bool TAIL, bool SPLIT, uint32_t LIST>
 __global__ __launch_bounds__(64 * WAVES) void k_distill(DistillArgs a) {
@@ -400,11 +400,13 @@ __global__ __launch_bounds__(64 * WAVES) void k_distill(DistillArgs a) {
 // besides is read again.
 //
 // Bound by the read and the write of a row where it is held (4,096 rows of 100,277
-// in bfloat16: 375 us, 4.4 TB/s; the two kernels apart 480), and by what is read
-// again where it is not (2,048 rows of 200,005 in float32, 256 listed: 805 us, 4.1
-// TB/s in two moves; of a row of 800 KB 384 are held or kept).  All of a workgroup loads
-// before any of it stores, so a CU needs workgroups besides: that is why waves are
-// no more than a row needs.  Loading the next row's pieces ahead spilled (936 us for
+// in bfloat16 with a tail, 64 listed: 390 us, 4.2 TB/s; the two kernels apart 479), and by
+// what is read again where it is not (2,048 rows of 200,005 in float32, 256 listed: 811
+// us, 4.0 TB/s in two moves; of a row of 800 KB 384 are held or kept).  All of a
+// workgroup loads before any of it stores, so a CU needs workgroups besides: that is
+// why waves are no more than a row needs.  Rows that are not many times what the card
+// holds at once end in a round that is mostly empty: of 8 waves two workgroups a CU, 512
+// in all, so 1,111 rows take three rounds (68 us, where their bytes take 45).  Loading the next row's pieces ahead spilled (936 us for
 // 403).
 template <typename T, uint32_t WAVES, bool TAIL, uint32_t LIST>
 __global__ __launch_bounds__(64 * WAVES, 4) void k_distill_step(DistillArgs a) {
@@ -631,8 +633,8 @@ int bbpe_distill_loss(int dtype, const void *logits, int64_t row_stride, uint64_
   //   four, up to 3,584 (4,096 rows of 28,000: 104 us, eight 106; of 32,000, 119 and 113);
   //   eight, up to 8,192, and for 16-bit rows of any length (2,048 of 65,536: 115 us,
   //   four 146; of 100,277: 206, sixteen 230);
-  //   sixteen for longer ones of float32 (2,048 of 100,277: 339 us, eight 359; of
-  //   200,005: 771 and 817).
+  //   sixteen for longer ones of float32 (2,048 of 100,277, 64 listed: 340 us, eight 427,
+  //   256 listed 363 and 461; of 200,005: 773 and 955, 817 and 1,000).
   const uint32_t per = dtype == BBPE_F32 ? 4 : 8, pieces = (vocab + per - 1) / per;
   const bool whole = d_logits && (n_rows >= STEP_ROWS || pieces <= 256 * HELD);
   with_element(dtype, [&](auto t) {

@@ -475,7 +475,7 @@ __device__ __forceinline__ void score_pieces(const ScoreArgs &a, uint64_t row, u
 //
 // Bound by the one read of the row: bfloat16, 8,192 rows of 100,277 in 290 us, 5.65
 // TB/s where a sum of as many bytes by itself reaches 3.9 and a copy's two ways 5.0;
-// 4,096 of 200,064 with 20 alternatives 313 us (5.2), float32 580 without and 612
+// 4,096 of 200,064 with 20 alternatives 319 us (5.1), float32 580 without and 612
 // with.  Entropy, rank and the sum in 64 bits fit under the loads: leaving them out
 // changes nothing.  A thread has four loads of 16 bytes in flight and a CU 32 waves
 // (20 with alternatives, for the groups' registers; forced to 24 they spill, 368 us).
@@ -545,7 +545,7 @@ struct ScoreBackArgs {
 };
 
 // One workgroup a part of a row: two steps, so that rows of any length are many
-// workgroups (4,096 rows of 100,277 in bfloat16: 285 us, 5.75 TB/s of what is read
+// workgroups (4,096 rows of 100,277 in bfloat16: 288 us, 5.7 TB/s of what is read
 // and written); a wave a row of up to 512 pieces (65,536 of 1,280: 148 -> 76 us; 512
 // rows of 8,192 7.4 us, by a wave each 11.4).  Elements that have a term of their own are
 // written once more when the part is done, from what was there before (dx may

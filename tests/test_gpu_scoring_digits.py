@@ -1,4 +1,5 @@
-"""Digits of what the operators between logits and ids make, on the GPU: rows whose sums of weights are exact, or a 1 and\nmany small ones, so that results are off by what their last few operations round; and scales at their limits."""
+"""Digits of what the operators between logits and ids make, on the GPU: rows whose sums of weights are exact, or a 1 and
+many small ones, so that results are off by what their last few operations round; and scales at their limits."""
 import math
 
 import pytest
