@@ -405,8 +405,8 @@ __global__ __launch_bounds__(64 * WAVES) void k_distill(DistillArgs a) {
 // us, 4.0 TB/s in two moves; of a row of 800 KB 384 are held or kept).  All of a
 // workgroup loads before any of it stores, so a CU needs workgroups besides: that is
 // why waves are no more than a row needs.  Rows that are not many times what the card
-// holds at once end in a round that is mostly empty: of 8 waves two workgroups a CU, 512
-// in all, so 1,111 rows take three rounds (68 us, where their bytes take 45).  Loading the next row's pieces ahead spilled (936 us for
+// holds at once leave it mostly idle in the end: of 8 waves two workgroups a CU, 512 in
+// all, so 1,111 rows take three turns (68 us, where their bytes take 45).  Loading the next row's pieces ahead spilled (936 us for
 // 403).
 template <typename T, uint32_t WAVES, bool TAIL, uint32_t LIST>
 __global__ __launch_bounds__(64 * WAVES, 4) void k_distill_step(DistillArgs a) {

@@ -203,11 +203,12 @@ template <typename T> struct Given {
 template <typename T>
 __device__ __forceinline__ void write_row(const ScoreArgs &a, uint64_t row, const RowEnd &end, int32_t id, const Given<T> &given, int32_t above) {
   const float nan = __uint_as_float(0x7FC00000u);
+  const double inv = 1.0 / end.p.sum;
   a.logprobs[row] = given.there ? end.logprob(given.value, a.scale) : id < 0 ? 0.0f : nan;
   a.ranks[row] = given.there && !end.bad ? above + 1 : 0;
-  a.entropy[row] = end.bad ? nan : end.none ? 0.0f : float(end.log_sum - double(end.p.mean) / end.p.sum * a.scale);
+  a.entropy[row] = end.bad ? nan : end.none ? 0.0f : float(end.log_sum - double(end.p.mean) * inv * a.scale);
   a.lse[row] = end.bad ? nan : end.none ? -INFINITY : float(double(end.p.max) * a.scale + end.log_sum);
-  a.stats[row] = end.bad ? make_float2(0.0f, nan) : make_float2(end.p.max, float(1.0 / end.p.sum));
+  a.stats[row] = end.bad ? make_float2(0.0f, nan) : make_float2(end.p.max, float(inv));
 }
 template <typename T>
 __device__ __forceinline__ void write_top(const ScoreArgs &a, uint64_t row, uint32_t lead, const RowEnd &end, uint32_t t, uint64_t key) {

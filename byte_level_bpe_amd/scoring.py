@@ -231,8 +231,11 @@ def distill_loss(logits, top_ids, top_logprobs, tail: bool = False, scale: float
     top_logprobs are the teacher's log probabilities at the same temperature
     (token_logprobs' with this scale).  tail False: the list made to sum to 1
     against the student's whole distribution; True: what the list leaves of 1
-    against the student's sum over tokens not listed.  Ids below 0 end a list
-    early; a row with none has loss 0 and no gradient.
+    against the student's sum over tokens not listed (where those are masked by
+    minus infinity, what rounding leaves is none; under a finite mask it counts,
+    times what the mask takes off).  Entries with ids outside the vocabulary are
+    not there: -1 fills up a shorter list; a row with none has loss 0 and no
+    gradient.
 
     workspace: uint8, for few rows (bbpe_distill_loss_workspace_bytes).
 
